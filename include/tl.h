@@ -64,7 +64,8 @@ enum tl_dtype {
   TL_I8 = 1,    /* int8 */
   TL_F16 = 2,   /* IEEE binary16 */
   TL_BF16 = 3,  /* bfloat16 */
-  TL_F32 = 4    /* IEEE binary32 */
+  TL_F32 = 4,   /* IEEE binary32 */
+  TL_F8E4M3 = 5 /* 8-bit float, 4 exponent and 3 mantissa bits, no infinities (paged caches only) */
 };
 
 /* Human-readable name of a tl_status value (static storage). */
@@ -332,6 +333,101 @@ int tl_linear_decode_f32act(const uint8_t* packed, const uint16_t* s, const floa
 int tl_codec_quant(const uint16_t* x, int R, int H, int8_t* q, float* scale, void* stream);
 int tl_codec_dequant_add(const uint16_t* own, const int8_t* q_peers, const float* scale_peers,
                          int npeers, int R, int H, uint16_t* out, void* stream);
+
+/*
+ * A paged key-value cache of one layer. The struct itself is host memory, read
+ * during the call; its pointers are device pointers. Row (page p, head h,
+ * token t of the page) of k starts at element p page_stride + h head_stride +
+ * t token_stride and holds head_dim contiguous elements; v is laid out alike.
+ * So [pages, heads, tokens, dim] and [pages, tokens, heads, dim] are both
+ * described by their strides. Offsets are computed in 64 bits.
+ *   dtype      TL_BF16, TL_F16 or TL_F8E4M3
+ *   k_scale    fp32 [kv_heads], positive, for TL_F8E4M3: an element stands for
+ *   v_scale    its 8-bit value times its head's scale; NULL otherwise
+ * k and v are 16-byte aligned, every stride a positive multiple of 16 bytes,
+ * page_size >= 1, num_pages >= 0; the scales are 4-byte aligned.
+ */
+typedef struct tl_kv_cache {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t page_stride, head_stride, token_stride; /* elements */
+  int dtype;
+  int kv_heads, head_dim, page_size, num_pages;
+} tl_kv_cache;
+
+/*
+ * Appends T tokens' keys and values to a paged cache, with the rotary position
+ * applied to the keys, and to the queries, on the way (the full-attention
+ * layers between the ternary projections; the projections' fused output can be
+ * passed as it lies).
+ *
+ *   k, v       [T, kv_heads, head_dim], dtype TL_BF16 or TL_F16, ldk and ldv
+ *              elements from one token to the next
+ *   q, q_out   [T, q_heads, head_dim] of the same dtype, ldq and ldqo likewise;
+ *              q_out may be q (in place). q = NULL or q_heads = 0: no queries.
+ *   cos_sin    fp32 [max_pos, rot_dim]: row p holds the rot_dim / 2 cosines,
+ *              then the sines, of position p. NULL with rot_dim = 0: the
+ *              tokens are stored as they are.
+ *   rot_dim    channels rotated: 0, or a multiple of 16 up to head_dim; the
+ *              others pass
+ *   interleaved  0: channel i turns with i + rot_dim / 2; 1: 2i with 2i + 1
+ *   positions  int32 [T], in [0, max_pos); may be NULL when rot_dim = 0
+ *   slots      int64 [T]: token t goes to page slots[t] / page_size, row
+ *              slots[t] % page_size; a negative slot (padding) is stored
+ *              nowhere, its query is still rotated
+ * A pair (a, b) becomes (fl(fl(a c) - fl(b s)), fl(fl(b c) + fl(a s))) in fp32,
+ * rounded once to the output type. An 8-bit cache stores the e4m3 value nearest
+ * to fl(y fl(1 / scale)), saturated to +-448 (a NaN stays one), y being the fp32
+ * rotated key, or the value. Other rows of the cache are not touched. Two tokens of one
+ * call must not have the same slot. A position outside [0, max_pos) or a slot past
+ * num_pages * page_size leaves its token out (its q_out row too, for a
+ * position) and records TL_EDATA.
+ * head_dim is a multiple of 16 up to 512, kv_heads and q_heads at most 1024, every
+ * ld a multiple of 8 (0 is allowed for T = 1); anything else is TL_EUNSUPPORTED.
+ */
+int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const void* v, int dtype,
+                 int T, int q_heads, int64_t ldq, int64_t ldk, int64_t ldv, void* q_out,
+                 int64_t ldqo, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                 const int32_t* positions, const int64_t* slots, void* stream);
+
+/*
+ * Attention of one new token per request over its cached keys and values:
+ *   out[b,h] = sum_j p_j V_j / sum_j p_j,  p_j = exp(scale q[b,h] . K_j)
+ * over the request's cached tokens j < lens[b] (window > 0: the last `window` of
+ * them); query head h reads key-value head h / (q_heads / kv_heads). A request
+ * without tokens (lens[b] = 0) gets out = 0 and lse = -inf.
+ *
+ *   q        [B, q_heads, head_dim], dtype TL_BF16 or TL_F16, ldq elements
+ *            from one request to the next; equal to the cache's dtype unless that
+ *            is TL_F8E4M3
+ *   pages    int32 [B, max_pages], ldp entries from one request to the next:
+ *            token j of request b lies in page pages[b][j / page_size]. Entries
+ *            past a request's last page (before a window's first) are not read.
+ *   lens     int32 [B], the new token's own key included
+ *   scale    multiplies q . K (1 / sqrt(head_dim) usually), finite
+ *   out      [B, q_heads, head_dim] of q's dtype, ldo likewise
+ *   lse      optional fp32 [B, q_heads]: log sum_j p_j
+ *   workspace  ws_bytes >= tl_paged_attention_workspace_size. It must hold zeros
+ *            before its first use; every call leaves its counters zero again, so
+ *            one workspace serves any sequence of calls of any shapes that it is
+ *            large enough for. Calls that can overlap on the GPU must not share one.
+ * head_dim is 64, 128 or 256; q_heads a multiple of kv_heads, at most 128 query
+ * heads for each key-value head; q_heads at most 1024. Sums, maxima and scores
+ * are fp32. A length that is negative or above max_pages * page_size, and a page
+ * outside [0, num_pages) among those that a request needs, record TL_EDATA; nothing
+ * is read out of range and that request's output is unspecified. What lies in the pages past a
+ * request's length has no influence, NaN included. The result does not depend on
+ * the order in which the GPU runs its blocks; it may differ in its last bits between batches
+ * of other lengths, which are split elsewhere.
+ */
+int tl_paged_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim,
+                                      size_t* bytes);
+int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B, int q_heads,
+                       int64_t ldq, const int32_t* pages, int max_pages, int64_t ldp,
+                       const int32_t* lens, float scale, int window, void* out, int64_t ldo,
+                       float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Diagnostic: launches one kernel whose bounded wait can never be satisfied (an

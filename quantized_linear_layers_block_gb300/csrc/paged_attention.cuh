@@ -1,0 +1,715 @@
+// Attention of one new token per request over a paged key-value cache.
+//
+//   out[h] = sum_j p_j V_j / sum_j p_j,   p_j = exp(scale q[h] . K_j)
+//
+// Every cached byte is used by the G = q_heads / kv_heads queries that share a
+// key-value head and by nothing else: 2 G flops a 16-bit element, so the cache's bytes bound the kernel
+// and the tensor cores' legacy path (mma.sync, which needs no tensor memory and
+// takes tiles of 8 queries) has room to spare. One pass: the running maximum m,
+// the sum l and the output o of a softmax over the keys seen so far,
+//   m' = max(m, s),  l' = l 2^(m - m') + sum 2^(s - m'),  o' likewise,
+// with s in units of log2(e).
+//
+// Work. A (request, group of query heads) is a segment; its keys are cut into
+// tiles of W * KT keys and the tiles of all segments form one list, cut into
+// equal shares for the blocks of one resident wave. So a batch of ragged lengths
+// needs no plan from the host, which never learns the lengths, and no block waits
+// for the longest request. A segment inside one block's share is finished there;
+// one that is cut leaves a partial (m, l, o) per block in the workspace, and the
+// block that arrives last joins them in block order (the order of arrival does not
+// reach the result). At most two of a block's segments are cut, the first and
+// the last, so the workspace depends on the grid alone.
+//
+// Tiles. Each of a block's W warps streams its own KT keys of a tile through its own ring of STAGES
+// buffers (cp.async, no block barrier in the loop) and keeps its own (m, l, o);
+// the warps meet once per segment. The scores are computed transposed, S^T = K q^T: the
+// keys are the rows of the MMA and 8 NT query heads its columns, so 8 heads need
+// half the MMAs that 16 padded rows would, and S^T and O^T = V^T P^T have their heads on the same
+// lanes, which keeps the rescaling in registers. P^T becomes an operand by an 8x8 transpose (movmatrix).
+// Probabilities are split in two 16-bit numbers, high and low part, so that they count with 16 (bf16)
+// or 22 (f16) bits instead of 8 or 11; the MMAs for it are not what bounds the kernel.
+//
+// An 8-bit cache is widened to f16 in registers (exact); q is then scaled by a
+// power of two of its own per head so that a bf16 query fits f16's range.
+#pragma once
+
+#include "tl_internal.cuh"
+
+#include <cuda_bf16.h>
+
+namespace tl {
+
+enum AttnCache { kCacheBf16 = 0, kCacheF16 = 1, kCacheF8 = 2 };
+
+// n / d for 0 <= n < 2^31 by a multiplication: m = floor(2^(31 + s) / d) + 1 with
+// s = ceil(log2 d) exceeds 2^(31 + s) / d by at most 1, so n m / 2^(31 + s)
+// exceeds n / d by less than 2^-s <= 1 / d.
+struct FastDiv {
+  uint32_t d, m, s;
+  static FastDiv make(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.s) < d) ++f.s;
+    f.m = static_cast<uint32_t>(((1ull << (31 + f.s)) / d) + 1);
+    return f;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return d == 1 ? n : __umulhi(n, m) >> (s - 1);
+  }
+};
+
+struct AttnParams {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t page_stride, head_stride, token_stride;   // bytes
+  int num_pages;
+  FastDiv page;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t ldq, ldo;
+  const int32_t* pages;
+  int64_t ldp;
+  int max_len;              // max_pages * page_size, at most 2^31 - 1
+  const int32_t* lens;
+  float* lse;
+  float scale_log2;
+  int B, q_heads, kv_heads, group, groups_per_kv, window, q_bf16;
+  int* counters;            // one per block
+  float* partials;          // two per block
+  int* status;
+};
+
+constexpr int kAttnWarps = 4;
+constexpr int kAttnMaxBlocksPerSm = 4;
+constexpr int kAttnMaxGrid = 4096;     // counters at the front of the workspace
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// floats of one partial: m and l of each head, then o
+__host__ __device__ constexpr size_t attn_partial_floats(int heads, int dim) {
+  return static_cast<size_t>(heads) * (dim + 2);
+}
+
+cudaError_t launch_attn_bf16(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st);
+cudaError_t launch_attn_f16(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st);
+cudaError_t launch_attn_f8(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st);
+
+namespace attn {
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// d += a b, 16 x 8 x 16
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (BF16)
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// two e4m3 values (low, high byte) as f16, exact
+__device__ __forceinline__ uint32_t widen_lo(uint32_t v) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t v) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int CACHE, int D, int NT>
+struct Traits {
+  static constexpr bool F8 = CACHE == kCacheF8;
+  static constexpr bool BF16 = CACHE == kCacheBf16;      // the MMA's operand type (f16 otherwise)
+  static constexpr int ROW = D * (F8 ? 1 : 2);           // bytes of a key
+  static constexpr int KT = 4096 / ROW > 16 ? 4096 / ROW : 16;   // keys of a warp's buffer: 4 KB of K (8 for 512-byte rows)
+  static constexpr int TILE = kAttnWarps * KT;
+  static constexpr int BUF = 2 * KT * ROW;
+  static constexpr int HEADS = 8 * NT;
+  static constexpr int OPITCH = D + 4;                   // floats; the warps' o meet here, conflict-free
+  static constexpr int MEET = (HEADS * OPITCH + 2 * HEADS) * 4;
+  static constexpr int STAGES = NT == 1 ? 3 : (NT == 2 && D < 256 ? 2 : (D == 256 && !F8 ? 2 : 3));
+  static constexpr int SMEM = kAttnWarps * (STAGES * BUF + MEET);
+  // 2^8 in the probabilities keeps an f16 low part of the small ones out of the subnormals
+  static constexpr float POFF = BF16 ? 0.f : 8.f;
+};
+
+// byte offset of 16-byte chunk c of row r, swizzled so that 8 rows' equal chunks lie in different banks
+template <int ROW>
+__device__ __forceinline__ uint32_t at(int r, int c) {
+  if constexpr (ROW >= 128)
+    return r * ROW + ((c ^ (r & 7)) << 4);
+  else
+    return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+struct Segment {            // where in the list of tiles
+  int b, h, tile, tiles;    // request, group of query heads, tile, tiles of this segment
+  int begin, end;           // first key, one past the last
+};
+
+__device__ __forceinline__ void seg_keys(const AttnParams& p, int len, int tile_keys, Segment& s) {
+  const int n = min(max(len, 0), p.max_len);
+  s.end = n;
+  s.begin = p.window > 0 ? max(0, n - p.window) : 0;
+  s.tiles = max(1, (s.end - s.begin + tile_keys - 1) / tile_keys);
+}
+
+template <int CACHE, int D, int NT>
+__global__ void __launch_bounds__(kAttnWarps * 32)
+paged_attention_kernel(const __grid_constant__ AttnParams p) {
+  using T = Traits<CACHE, D, NT>;
+  constexpr int KT = T::KT, ROW = T::ROW, MT = KT / 16, DT = D / 16, S = T::STAGES;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long s_scan[kAttnWarps];
+  __shared__ Segment s_first;
+  __shared__ int s_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int HG = p.kv_heads * p.groups_per_kv;
+
+  pdl_wait_prior();
+  pdl_launch_dependents();
+
+  // ---- the share of this block: tiles [t0, t1) of `total`
+  const int per = (p.B + blockDim.x - 1) / blockDim.x;
+  long long mine = 0;
+  bool bad = false;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < p.B) {
+      const int len = __ldg(p.lens + b);
+      bad |= len < 0 || len > p.max_len;
+      Segment s;
+      seg_keys(p, len, T::TILE, s);
+      mine += s.tiles;
+    }
+  }
+  if (bad && blockIdx.x == 0) set_status(p.status, TL_EDATA);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  before *= HG;
+  total *= HG;
+  const long long parts = min(total, static_cast<long long>(gridDim.x));
+  if (blockIdx.x >= parts) return;
+  const long long t0 = total * blockIdx.x / parts, t1 = total * (blockIdx.x + 1) / parts;
+  if (t0 >= before && t0 < before + mine * HG) {
+    long long left = t0 - before;
+    for (int i = 0; i < per; ++i) {
+      const int b = tid * per + i;
+      Segment s;
+      seg_keys(p, __ldg(p.lens + b), T::TILE, s);
+      if (left < static_cast<long long>(s.tiles) * HG) {
+        s.b = b;
+        s.h = static_cast<int>(left / s.tiles);
+        s.tile = static_cast<int>(left % s.tiles);
+        s_first = s;
+        break;
+      }
+      left -= static_cast<long long>(s.tiles) * HG;
+    }
+  }
+  __syncthreads();
+  const int count = static_cast<int>(t1 - t0);
+
+  // ---- the warp's ring
+  const uint32_t ring = smem_u32(smem) + warp * S * T::BUF;
+  float* const meet = reinterpret_cast<float*>(smem + kAttnWarps * S * T::BUF);
+
+  constexpr int CPR = ROW / 16;                       // 16-byte chunks of a row
+  constexpr int RPI = 32 / CPR;                       // rows that one instruction of the warp copies
+  constexpr int KPL = (KT + 31) / 32;                 // keys whose address a lane computes
+  Segment ld = s_first;
+  int next_len = 0;                                   // length of the request after ld's
+  int pid[KPL];
+  auto fetch_len = [&]() { next_len = ld.b + 1 < p.B ? __ldg(p.lens + ld.b + 1) : 0; };
+  auto fetch_pages = [&]() {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      const int key = ld.begin + ld.tile * T::TILE + warp * KT + i * 32 + lane;
+      pid[i] = key < ld.end && i * 32 + lane < KT ? __ldg(p.pages + ld.b * p.ldp + p.page.div(key)) : -1;
+    }
+  };
+  fetch_len();
+  fetch_pages();
+  int left = count;                                   // tiles not yet asked for
+  auto load_tile = [&](int stage) {
+    if (left > 0) {
+      const int k0 = ld.begin + ld.tile * T::TILE + warp * KT;
+      if (k0 < ld.end) {
+        const int kvh = ld.h / p.groups_per_kv;
+        int64_t off[KPL];
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) {
+          const int key = k0 + i * 32 + lane;
+          off[i] = -1;
+          if (key < ld.end && i * 32 + lane < KT) {
+            if (static_cast<unsigned>(pid[i]) < static_cast<unsigned>(p.num_pages))
+              off[i] = pid[i] * p.page_stride + kvh * p.head_stride +
+                       static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
+            else
+              set_status(p.status, TL_EDATA);
+          }
+        }
+        const uint32_t kb = ring + stage * T::BUF, vb = kb + KT * ROW;
+        const int c = lane % CPR;
+#pragma unroll
+        for (int i = 0; i < KT / RPI; ++i) {
+          const int r = i * RPI + lane / CPR;
+          const int64_t o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], r & 31);
+          const uint32_t bytes = o < 0 ? 0u : 16u;
+          const int64_t src = (o < 0 ? 0 : o) + c * 16;
+          cp_async16(kb + at<ROW>(r, c), p.k + src, bytes);
+          cp_async16(vb + at<ROW>(r, c), p.v + src, bytes);
+        }
+      }
+      --left;
+      if (++ld.tile == ld.tiles) {
+        ld.tile = 0;
+        if (++ld.h == HG) {
+          ld.h = 0;
+          ++ld.b;
+          seg_keys(p, next_len, T::TILE, ld);
+          fetch_len();
+        }
+      }
+      if (left > 0) fetch_pages();
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) load_tile(i);
+
+  // ---- the segments
+  Segment cur = s_first;
+  int stage = 0, done = 0;
+  bool starts_before = cur.tile > 0;
+  while (done < count) {
+    const int here = min(cur.tiles - cur.tile, count - done);    // tiles of this segment in this block's share
+    const int kvh = cur.h / p.groups_per_kv;
+    const int h0 = kvh * p.group + (cur.h - kvh * p.groups_per_kv) * T::HEADS;
+    const int heads = min(T::HEADS, kvh * p.group + p.group - h0);
+
+    // queries as B operands: k = 16 channels, n = 8 heads. For an 8-bit cache
+    // thread t takes channels 4t .. 4t + 3, as its ldmatrix of K gives them.
+    uint32_t qf[DT][NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint16_t* qr = p.q + cur.b * p.ldq + static_cast<int64_t>(h0 + n * 8 + g) * D;
+      const bool live = n * 8 + g < heads;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        if constexpr (T::F8) {
+          const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(qr + 16 * i + 4 * t)) : make_uint2(0, 0);
+          qf[i][n][0] = w.x;
+          qf[i][n][1] = w.y;
+        } else {
+          qf[i][n][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 2 * t)) : 0u;
+          qf[i][n][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 8 + 2 * t)) : 0u;
+        }
+      }
+    }
+    float sc[NT][2];                                 // log2(e) scale of heads 2t and 2t + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = p.scale_log2;
+    if constexpr (T::F8) {
+      const float ks = __ldg(p.k_scale + kvh);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float up = 1.f;
+        if (p.q_bf16) {
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < DT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 f = unpack2<true>(qf[i][n][e]);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^e <= top < 2^(e + 1); e is kept where both 2^e and 2^-e are normal (an infinite or NaN q stays one)
+          const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
+          up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < DT; ++i) {
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              const float2 f = unpack2<true>(qf[i][n][e2]);
+              qf[i][n][e2] = pack2<false>(f.x * down, f.y * down);
+            }
+          }
+        }
+        sc[n][0] *= ks * __shfl_sync(0xffffffffu, up, 8 * t);        // head 2t is lane group g = 2t
+        sc[n][1] *= ks * __shfl_sync(0xffffffffu, up, 8 * t + 4);
+      }
+    }
+
+    float m[NT][2], l[NT][2], o[DT][NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+    }
+
+    for (int it = 0; it < here; ++it) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      load_tile(stage == 0 ? S - 1 : stage - 1);      // the buffer that the last turn read
+      const int k0 = cur.begin + (cur.tile + it) * T::TILE + warp * KT;
+      const uint32_t kb = ring + stage * T::BUF, vb = kb + KT * ROW;
+      if (k0 < cur.end) {
+        float s[MT][NT][4];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.f;
+          const int r = 16 * j + (lane & 15);
+          if constexpr (T::F8) {
+#pragma unroll
+            for (int i = 0; i < DT; i += 2) {
+              uint32_t w[4];
+              ldsm4(kb + at<ROW>(r, i + (lane >> 4)), w);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t a[4] = {widen_lo(w[2 * e]), widen_lo(w[2 * e + 1]), widen_hi(w[2 * e]), widen_hi(w[2 * e + 1])};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma<false>(s[j][n], a, qf[i + e][n][0], qf[i + e][n][1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < DT; ++i) {
+              uint32_t a[4];
+              ldsm4(kb + at<ROW>(r, 2 * i + (lane >> 4)), a);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma<T::BF16>(s[j][n], a, qf[i][n][0], qf[i][n][1]);
+            }
+          }
+        }
+        // rows 16 j + g (elements 0, 1) and + 8 (2, 3); columns: heads 2t, 2t + 1
+        const int live = cur.end - k0;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][n][e] *= sc[n][e & 1];
+            if (live < KT) {
+              const int r = 16 * j + g;
+              if (r >= live) s[j][n][0] = s[j][n][1] = -INFINITY;
+              if (r + 8 >= live) s[j][n][2] = s[j][n][3] = -INFINITY;
+            }
+          }
+        }
+        bool moved = false;
+        float al[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = m[n][e];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) top = fmaxf(top, fmaxf(s[j][n][e], s[j][n][e + 2]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            moved |= top != m[n][e];
+            // no key seen so far scored above -inf: any finite base will do
+            const float base = top == -INFINITY ? 0.f : top;
+            al[n][e] = exp2_approx(m[n][e] - base);
+            m[n][e] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              s[j][n][e] = exp2_approx(s[j][n][e] - (base - T::POFF));
+              s[j][n][e + 2] = exp2_approx(s[j][n][e + 2] - (base - T::POFF));
+              sum += s[j][n][e] + s[j][n][e + 2];
+            }
+            l[n][e] = l[n][e] * al[n][e] + sum;
+          }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int i = 0; i < DT; ++i) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              o[i][n][0] *= al[n][0];
+              o[i][n][1] *= al[n][1];
+              o[i][n][2] *= al[n][0];
+              o[i][n][3] *= al[n][1];
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x = s[j][n][2 * e], y = s[j][n][2 * e + 1];
+              const uint32_t hi = pack2<T::BF16>(x, y);
+              const float2 back = unpack2<T::BF16>(hi);
+              ph[n][e] = transpose8x8(hi);
+              pl[n][e] = transpose8x8(pack2<T::BF16>(x - back.x, y - back.y));
+            }
+          }
+          if constexpr (T::F8) {
+            const int r = 16 * j + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < DT; i += 2) {
+              uint32_t w[4];
+              ldsm4t(vb + at<ROW>(r, i + (lane >> 4)), w);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // bytes (key 2t: d, d + 1; key 2t + 1: d, d + 1) -> (d of both keys, d + 1 of both keys)
+                const uint32_t x = __byte_perm(w[2 * e], 0, 0x3120), y = __byte_perm(w[2 * e + 1], 0, 0x3120);
+                const uint32_t a[4] = {widen_lo(x), widen_hi(x), widen_lo(y), widen_hi(y)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  mma<false>(o[i + e][n], a, ph[n][0], ph[n][1]);
+                  mma<false>(o[i + e][n], a, pl[n][0], pl[n][1]);
+                }
+              }
+            }
+          } else {
+            const int r = 16 * j + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+            for (int i = 0; i < DT; ++i) {
+              uint32_t a[4];
+              ldsm4t(vb + at<ROW>(r, 2 * i + ((lane >> 3) & 1)), a);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma<T::BF16>(o[i][n], a, ph[n][0], ph[n][1]);
+                mma<T::BF16>(o[i][n], a, pl[n][0], pl[n][1]);
+              }
+            }
+          }
+        }
+      }
+      stage = stage + 1 == S ? 0 : stage + 1;
+    }
+    done += here;
+
+    // ---- the warps meet: each leaves (m, l, o) in shared memory
+    float* const mo = meet + warp * (T::MEET / 4);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+        const int h = 8 * n + 2 * t + e;
+        if (g == 0) {
+          mo[h] = m[n][e];
+          mo[T::HEADS + h] = l[n][e];
+        }
+        float* row = mo + 2 * T::HEADS + h * T::OPITCH;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          if constexpr (T::F8) {
+            *reinterpret_cast<float2*>(row + 16 * i + 2 * g) = make_float2(o[i][n][e], o[i][n][e + 2]);
+          } else {
+            row[16 * i + g] = o[i][n][e];
+            row[16 * i + g + 8] = o[i][n][e + 2];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = !starts_before && cur.tile + here == cur.tiles;
+    const float vs = T::F8 ? __ldg(p.v_scale + kvh) : 1.f;
+    float* const part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + (starts_before ? 0 : 1)) *
+                                         attn_partial_floats(T::HEADS, D);
+    for (int x = tid; x < heads * (D / 2); x += kAttnWarps * 32) {
+      const int h = x / (D / 2), d = 2 * (x % (D / 2));
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, meet[w * (T::MEET / 4) + h]);
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f, ox = 0.f, oy = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float* q = meet + w * (T::MEET / 4);
+        const float f = exp2_approx(q[h] - base);
+        const float2 v = *reinterpret_cast<const float2*>(q + 2 * T::HEADS + h * T::OPITCH + d);
+        sum += f * q[T::HEADS + h];
+        ox += f * v.x;
+        oy += f * v.y;
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : vs / sum;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + cur.b * p.ldo + static_cast<int64_t>(h0 + h) * D + d);
+        *dst = p.q_bf16 ? pack2<true>(ox * inv, oy * inv) : pack2<false>(ox * inv, oy * inv);
+        if (d == 0 && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(cur.b) * p.q_heads + h0 + h] = sum == 0.f ? -INFINITY : (top - T::POFF) * kLn2 + logf(sum);
+      } else {
+        if (d == 0) {
+          part[h] = top;
+          part[T::HEADS + h] = sum;
+        }
+        *reinterpret_cast<float2*>(part + 2 * T::HEADS + h * D + d) = make_float2(ox, oy);
+      }
+    }
+    if (!whole) {
+      // blocks c0 .. c1 share this segment; c0 owns the counter
+      const long long first = t0 + (done - here) - cur.tile, last = first + cur.tiles - 1;
+      const int c0 = static_cast<int>(((first + 1) * parts - 1) / total);
+      const int c1 = static_cast<int>(((last + 1) * parts - 1) / total);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_flag = atomicAdd(p.counters + c0, 1) == c1 - c0;
+      __syncthreads();
+      if (s_flag) {
+        __threadfence();
+        constexpr size_t PF = attn_partial_floats(T::HEADS, D);
+        // block c0 began the segment (its second partial); the others found it begun (their first)
+        const float* const p0 = p.partials + (static_cast<size_t>(c0) * 2 + 1) * PF;
+        const float* const p1 = p.partials + (static_cast<size_t>(c0) * 2 + 2) * PF;
+        const int n = c1 - c0 + 1;
+        for (int x = tid; x < heads * (D / 4); x += kAttnWarps * 32) {
+          const int h = x / (D / 4), d = 4 * (x % (D / 4));
+          float top = -INFINITY;
+          for (int c = 0; c < n; ++c) top = fmaxf(top, __ldcg((c == 0 ? p0 : p1 + (c - 1) * 2 * PF) + h));
+          const float base = top == -INFINITY ? 0.f : top;
+          float sum = 0.f;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int c = 0; c < n; ++c) {
+            const float* q = c == 0 ? p0 : p1 + (c - 1) * 2 * PF;
+            const float f = exp2_approx(__ldcg(q + h) - base);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 2 * T::HEADS + h * D + d));
+            sum += f * __ldcg(q + T::HEADS + h);
+            a.x += f * v.x;
+            a.y += f * v.y;
+            a.z += f * v.z;
+            a.w += f * v.w;
+          }
+          const float inv = sum == 0.f ? 0.f : vs / sum;
+          uint2 r;
+          r.x = p.q_bf16 ? pack2<true>(a.x * inv, a.y * inv) : pack2<false>(a.x * inv, a.y * inv);
+          r.y = p.q_bf16 ? pack2<true>(a.z * inv, a.w * inv) : pack2<false>(a.z * inv, a.w * inv);
+          *reinterpret_cast<uint2*>(p.out + cur.b * p.ldo + static_cast<int64_t>(h0 + h) * D + d) = r;
+          if (d == 0 && p.lse != nullptr)
+            p.lse[static_cast<int64_t>(cur.b) * p.q_heads + h0 + h] = sum == 0.f ? -INFINITY : (top - T::POFF) * kLn2 + logf(sum);
+        }
+        if (tid == 0) p.counters[c0] = 0;
+      }
+    } else {
+      __syncthreads();
+    }
+    starts_before = false;
+    cur.tile = 0;
+    if (++cur.h == HG) {
+      cur.h = 0;
+      ++cur.b;
+      if (done < count) seg_keys(p, __ldg(p.lens + cur.b), T::TILE, cur);
+    }
+  }
+  cp_async_wait<0>();
+}
+
+template <int CACHE, int D, int NT>
+cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
+  using T = Traits<CACHE, D, NT>;
+  static int per_sm[64];                             // blocks per SM, by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int n = __atomic_load_n(&per_sm[dev], __ATOMIC_RELAXED);
+  if (n == 0) {
+    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<CACHE, D, NT>, kAttnWarps * 32, T::SMEM);
+    if (e != cudaSuccess) return e;
+    n = n < 1 ? 1 : n > kAttnMaxBlocksPerSm ? kAttnMaxBlocksPerSm : n;
+    __atomic_store_n(&per_sm[dev], n, __ATOMIC_RELAXED);
+  }
+  const long long keys = p.window > 0 && p.window < p.max_len ? p.window : p.max_len;
+  const long long most = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv *
+                         ((keys + T::TILE - 1) / T::TILE > 0 ? (keys + T::TILE - 1) / T::TILE : 1);
+  long long grid = static_cast<long long>(sms) * n;
+  if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
+  if (grid > most) grid = most;
+  return launch_pdl(paged_attention_kernel<CACHE, D, NT>, dim3(static_cast<unsigned>(grid)), dim3(kAttnWarps * 32),
+                    T::SMEM, st, p);
+}
+
+template <int CACHE>
+cudaError_t launch_dim(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st) {
+  switch (dim) {
+    case 64: return nt == 1 ? launch<CACHE, 64, 1>(p, sms, st) : nt == 2 ? launch<CACHE, 64, 2>(p, sms, st) : launch<CACHE, 64, 4>(p, sms, st);
+    case 128: return nt == 1 ? launch<CACHE, 128, 1>(p, sms, st) : nt == 2 ? launch<CACHE, 128, 2>(p, sms, st) : launch<CACHE, 128, 4>(p, sms, st);
+    case 256: return nt == 1 ? launch<CACHE, 256, 1>(p, sms, st) : launch<CACHE, 256, 2>(p, sms, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace attn
+}  // namespace tl

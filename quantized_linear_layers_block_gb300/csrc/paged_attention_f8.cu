@@ -1,0 +1,10 @@
+// Paged attention over a f8 cache: the instantiations of paged_attention.cuh.
+#include "paged_attention.cuh"
+
+namespace tl {
+
+cudaError_t launch_attn_f8(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st) {
+  return attn::launch_dim<kCacheF8>(p, dim, nt, sms, st);
+}
+
+}  // namespace tl

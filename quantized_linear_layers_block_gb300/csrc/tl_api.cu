@@ -3,7 +3,11 @@
 // errors return without touching the device (and work without a GPU).
 #include "tl_internal.cuh"
 
+#include <atomic>
 #include <mutex>
+
+#include "kv_append.cuh"
+#include "paged_attention.cuh"
 
 namespace {
 
@@ -52,6 +56,56 @@ int check_linear(const void* packed, const void* qT, const void* sw, const void*
 }
 
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
+
+// SMs of the current device (looked up once per device).
+int num_sms(int* out) {
+  static std::atomic<int> sms[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TL_ECUDA;
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return TL_ECUDA;
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return TL_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// rows of `width` elements, `ld` apart, that are read or written as 16-byte vectors of 16-bit elements
+int check_rows(int64_t ld, int64_t width, int64_t rows, int elems16) {
+  if (rows <= 1) return TL_OK;
+  if (ld < 0) return TL_EINVAL;
+  return ld % elems16 == 0 && ld >= width ? TL_OK : TL_EUNSUPPORTED;
+}
+
+int check_cache(const tl_kv_cache* c) {
+  if (c == nullptr || c->kv_heads <= 0 || c->head_dim <= 0 || c->page_size <= 0 || c->num_pages < 0) return TL_EINVAL;
+  if (c->dtype != TL_BF16 && c->dtype != TL_F16 && c->dtype != TL_F8E4M3) return TL_EINVAL;
+  const bool f8 = c->dtype == TL_F8E4M3;
+  if (f8 != (c->k_scale != nullptr) || f8 != (c->v_scale != nullptr)) return TL_EINVAL;
+  if (!aligned4(c->k_scale) || !aligned4(c->v_scale) || !aligned16(c->k) || !aligned16(c->v)) return TL_EINVAL;
+  if (c->num_pages > 0 && (c->k == nullptr || c->v == nullptr)) return TL_EINVAL;
+  const int64_t step = f8 ? 16 : 8;
+  if (c->page_stride <= 0 || c->head_stride <= 0 || c->token_stride <= 0) return TL_EINVAL;
+  if (c->page_stride % step || c->head_stride % step || c->token_stride % step) return TL_EUNSUPPORTED;
+  if (c->kv_heads > 1024) return TL_EUNSUPPORTED;
+  return TL_OK;
+}
+
+// Query heads are taken in groups of 8 NT columns of the MMA: the fewest columns that hold the heads of one
+// key-value head, at most 32 (16 for head_dim 256, whose output fills the registers).
+int attention_columns(int group, int dim) {
+  return group <= 8 ? 1 : group <= 16 || dim == 256 ? 2 : 4;
+}
+
+int check_attention_shape(int B, int q_heads, int kv_heads, int head_dim) {
+  if (B < 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0) return TL_EINVAL;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return TL_EUNSUPPORTED;
+  if (q_heads % kv_heads != 0 || q_heads / kv_heads > 128 || q_heads > 1024) return TL_EUNSUPPORTED;
+  return TL_OK;
+}
 
 // A wait that nothing ends: phase 0 of a fresh mbarrier with no arrival. The
 // bounded wait gives up after limit_ns and records TL_ETIMEOUT, the path every
@@ -275,6 +329,107 @@ int tl_codec_dequant_add(const uint16_t* own, const int8_t* q_peers, const float
                                       as_stream(stream)) == cudaSuccess
              ? TL_OK
              : TL_ECUDA;
+}
+
+int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const void* v, int dtype,
+                 int T, int q_heads, int64_t ldq, int64_t ldk, int64_t ldv, void* q_out,
+                 int64_t ldqo, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                 const int32_t* positions, const int64_t* slots, void* stream) {
+  int r = check_cache(cache);
+  if (r != TL_OK) return r;
+  if (T < 0 || q_heads < 0 || rot_dim < 0 || max_pos < 0 || (interleaved != 0 && interleaved != 1)) return TL_EINVAL;
+  if (dtype != TL_BF16 && dtype != TL_F16) return TL_EINVAL;
+  if (cache->dtype != TL_F8E4M3 && cache->dtype != dtype) return TL_EINVAL;
+  const int d = cache->head_dim;
+  if (d % 16 != 0 || d > 512 || q_heads > 1024 || rot_dim % 16 != 0 || rot_dim > d) return TL_EUNSUPPORTED;
+  if (q == nullptr) q_heads = 0;
+  if (T == 0) return TL_OK;
+  if (!k || !v || !slots || (q_heads > 0 && !q_out)) return TL_EINVAL;
+  if (rot_dim > 0 && (!cos_sin || !positions)) return TL_EINVAL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || (q_heads > 0 && !aligned16(q_out)) || !aligned16(cos_sin) ||
+      !aligned4(positions) || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+    return TL_EINVAL;
+  const int64_t wq = static_cast<int64_t>(q_heads) * d, wk = static_cast<int64_t>(cache->kv_heads) * d;
+  if ((r = check_rows(ldk, wk, T, 8)) != TL_OK || (r = check_rows(ldv, wk, T, 8)) != TL_OK) return r;
+  if (q_heads > 0 && ((r = check_rows(ldq, wq, T, 8)) != TL_OK || (r = check_rows(ldqo, wq, T, 8)) != TL_OK)) return r;
+  int* status = nullptr;
+  if ((r = status_ptr(&status)) != TL_OK) return r;
+  tl::AppendParams p{};
+  p.ck = cache->k, p.cv = cache->v, p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
+  p.page_stride = cache->page_stride, p.head_stride = cache->head_stride, p.token_stride = cache->token_stride;
+  p.num_slots = static_cast<int64_t>(cache->num_pages) * cache->page_size;
+  p.q = static_cast<const uint16_t*>(q), p.k = static_cast<const uint16_t*>(k), p.v = static_cast<const uint16_t*>(v);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.ldq = ldq, p.ldk = ldk, p.ldv = ldv, p.ldqo = ldqo;
+  p.cos_sin = cos_sin, p.positions = positions, p.slots = slots, p.status = status;
+  p.q_heads = q_heads, p.kv_heads = cache->kv_heads, p.dim = d, p.page_size = cache->page_size;
+  p.rot = rot_dim, p.max_pos = max_pos, p.interleaved = interleaved;
+  return tl::launch_kv_append(p, T, dtype == TL_BF16, cache->dtype == TL_F8E4M3, as_stream(stream)) == cudaSuccess
+             ? TL_OK
+             : TL_ECUDA;
+}
+
+int tl_paged_attention_workspace_size(int B, int q_heads, int kv_heads, int head_dim, size_t* bytes) {
+  if (bytes == nullptr) return TL_EINVAL;
+  int r = check_attention_shape(B, q_heads, kv_heads, head_dim);
+  if (r != TL_OK) return r;
+  *bytes = 0;
+  if (B == 0) return TL_OK;
+  int sms = 0;
+  if ((r = num_sms(&sms)) != TL_OK) return r;
+  const long long grid = sms * tl::kAttnMaxBlocksPerSm < tl::kAttnMaxGrid ? sms * tl::kAttnMaxBlocksPerSm : tl::kAttnMaxGrid;
+  const int heads = 8 * attention_columns(q_heads / kv_heads, head_dim);
+  *bytes = tl::kAttnMaxGrid * sizeof(int) + 2 * grid * tl::attn_partial_floats(heads, head_dim) * sizeof(float);
+  return TL_OK;
+}
+
+int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B, int q_heads,
+                       int64_t ldq, const int32_t* pages, int max_pages, int64_t ldp,
+                       const int32_t* lens, float scale, int window, void* out, int64_t ldo,
+                       float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  int r = check_cache(cache);
+  if (r != TL_OK) return r;
+  if (max_pages < 0 || window < 0 || !(scale - scale == 0.f)) return TL_EINVAL;
+  if (dtype != TL_BF16 && dtype != TL_F16) return TL_EINVAL;
+  if (cache->dtype != TL_F8E4M3 && cache->dtype != dtype) return TL_EINVAL;
+  if ((r = check_attention_shape(B, q_heads, cache->kv_heads, cache->head_dim)) != TL_OK) return r;
+  if (B == 0) return TL_OK;
+  if (!q || !out || !lens || !workspace || (max_pages > 0 && !pages)) return TL_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(lens) || !aligned4(pages) || !aligned4(lse))
+    return TL_EINVAL;
+  const int64_t wq = static_cast<int64_t>(q_heads) * cache->head_dim;
+  if ((r = check_rows(ldq, wq, B, 8)) != TL_OK || (r = check_rows(ldo, wq, B, 8)) != TL_OK) return r;
+  if (B > 1 && ldp < max_pages) return TL_EINVAL;
+  size_t need = 0;
+  if ((r = tl_paged_attention_workspace_size(B, q_heads, cache->kv_heads, cache->head_dim, &need)) != TL_OK) return r;
+  if (ws_bytes < need) return TL_ENOSPACE;
+  int sms = 0;
+  int* status = nullptr;
+  if ((r = num_sms(&sms)) != TL_OK || (r = status_ptr(&status)) != TL_OK) return r;
+  const int bytes = cache->dtype == TL_F8E4M3 ? 1 : 2;
+  tl::AttnParams p{};
+  p.k = static_cast<const uint8_t*>(cache->k), p.v = static_cast<const uint8_t*>(cache->v);
+  p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
+  p.page_stride = cache->page_stride * bytes, p.head_stride = cache->head_stride * bytes, p.token_stride = cache->token_stride * bytes;
+  p.num_pages = cache->num_pages;
+  p.page = tl::FastDiv::make(static_cast<uint32_t>(cache->page_size));
+  p.q = static_cast<const uint16_t*>(q), p.out = static_cast<uint16_t*>(out), p.ldq = ldq, p.ldo = ldo;
+  p.pages = pages, p.ldp = ldp, p.lens = lens, p.lse = lse;
+  const int64_t most = static_cast<int64_t>(max_pages) * cache->page_size, limit = 0x7FFF0000;   // keys + a tile stay in an int
+  p.max_len = static_cast<int>(most < limit ? most : limit);
+  p.scale_log2 = scale * tl::kLog2e;
+  p.B = B, p.q_heads = q_heads, p.kv_heads = cache->kv_heads, p.group = q_heads / cache->kv_heads, p.window = window;
+  p.q_bf16 = dtype == TL_BF16;
+  const int nt = attention_columns(p.group, cache->head_dim);
+  p.groups_per_kv = (p.group + 8 * nt - 1) / (8 * nt);
+  p.counters = static_cast<int*>(workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + tl::kAttnMaxGrid * sizeof(int));
+  p.status = status;
+  const cudaStream_t st = as_stream(stream);
+  const cudaError_t e = cache->dtype == TL_BF16  ? tl::launch_attn_bf16(p, cache->head_dim, nt, sms, st)
+                        : cache->dtype == TL_F16 ? tl::launch_attn_f16(p, cache->head_dim, nt, sms, st)
+                                                 : tl::launch_attn_f8(p, cache->head_dim, nt, sms, st);
+  return e == cudaSuccess ? TL_OK : TL_ECUDA;
 }
 
 int tl_selftest_wait_timeout(unsigned int limit_us, void* stream) {

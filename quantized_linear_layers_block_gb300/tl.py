@@ -19,14 +19,27 @@ _lib = None
 _lock = threading.Lock()
 
 TL_OK, TL_EINVAL, TL_EUNSUPPORTED, TL_ECUDA, TL_ETIMEOUT, TL_EDATA, TL_ENOSPACE = range(7)
-TL_I8, TL_F16, TL_BF16, TL_F32 = 1, 2, 3, 4
+TL_I8, TL_F16, TL_BF16, TL_F32, TL_F8E4M3 = 1, 2, 3, 4, 5
 FUSED_DECODE_MAX_K = 8192
 
 # name -> (restype, argtypes)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
+_F = ctypes.c_float
 _PSZ = ctypes.POINTER(ctypes.c_size_t)
+
+
+class tl_kv_cache(ctypes.Structure):
+    """The C struct of the same name (include/tl.h)."""
+
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P),
+                ("page_stride", _L), ("head_stride", _L), ("token_stride", _L),
+                ("dtype", _I), ("kv_heads", _I), ("head_dim", _I), ("page_size", _I), ("num_pages", _I)]
+
+
+_PKV = ctypes.POINTER(tl_kv_cache)
 SIGNATURES = {
     "tl_strerror": (ctypes.c_char_p, [_I]),
     "tl_version": (_I, []),
@@ -43,6 +56,9 @@ SIGNATURES = {
     "tl_linear_decode_f32act": (_I, [_P, _P, _P, _I, _I, _I, _P, _I, _P]),
     "tl_codec_quant": (_I, [_P, _I, _I, _P, _P, _P]),
     "tl_codec_dequant_add": (_I, [_P, _P, _P, _I, _I, _I, _P, _P]),
+    "tl_kv_append": (_I, [_PKV, _P, _P, _P, _I, _I, _I, _L, _L, _L, _P, _L, _P, _I, _I, _I, _P, _P, _P]),
+    "tl_paged_attention_workspace_size": (_I, [_I, _I, _I, _I, _PSZ]),
+    "tl_paged_attention": (_I, [_PKV, _P, _I, _I, _I, _L, _P, _I, _L, _P, _F, _I, _P, _L, _P, _P, _SZ, _P]),
     "tl_selftest_wait_timeout": (_I, [ctypes.c_uint, _P]),
     "tl_get_status": (_I, [_P]),
 }
@@ -90,8 +106,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:    # the current stream's handle without a torch.cuda.Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -294,6 +310,178 @@ def tl_selftest_wait_timeout(limit_us: int = 2000, stream=None) -> None:
 
 def tl_get_status(stream=None) -> int:
     return lib().tl_get_status(_stream(stream))
+
+
+_HALF = {torch.bfloat16: TL_BF16, torch.float16: TL_F16}
+_CACHE_DTYPES = {torch.bfloat16: TL_BF16, torch.float16: TL_F16, torch.float8_e4m3fn: TL_F8E4M3}
+
+
+def _token_rows(t: torch.Tensor, heads: int, dim: int, dtype: torch.dtype, name: str) -> int:
+    """Checks a device tensor [tokens, heads, dim] whose tokens may be any distance apart; returns that distance."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {list(shape)}")
+    if stride[2] != 1 or (stride[1] != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return stride[0]
+
+
+def _ints(t: torch.Tensor, dtype: torch.dtype, n: int, name: str) -> int:
+    """Checks a contiguous device vector of n integers; returns its address."""
+    if not t.is_cuda or t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor [{n}]")
+    return t.data_ptr()
+
+
+class PagedKVCache:
+    """The paged key-value cache of one layer, and the two operators on it.
+
+    k and v are [num_pages, kv_heads, page_size, head_dim] in bf16, fp16 or
+    float8_e4m3fn. They are allocated here (zeros), or passed in with any strides that
+    keep a row's head_dim elements contiguous (a [num_pages, page_size, kv_heads,
+    head_dim] pool is passed as its transpose(1, 2)). An 8-bit element stands for
+    its value times its head's scale (k_scale, v_scale: fp32 [kv_heads]).
+
+    Which pages belong to which request is the caller's: append() takes a slot
+    (page * page_size + row) for each token, attend() a table of pages for each request.
+
+    The cache keeps one workspace for attend(), which joins requests that several
+    blocks share: attend() calls on one cache that can run at the same time on
+    different streams must be ordered by the caller (an event), or use one
+    PagedKVCache over the same k and v for each stream. Its first attend() allocates it.
+    """
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16,
+                 k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None, device="cuda",
+                 k: torch.Tensor | None = None, v: torch.Tensor | None = None):
+        if dtype not in _CACHE_DTYPES:
+            raise ValueError(f"a cache holds {sorted(map(str, _CACHE_DTYPES))}, not {dtype}")
+        if (k is None) != (v is None):
+            raise ValueError("pass both k and v, or neither")
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        if k is None:
+            k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        for t, name in ((k, "k"), (v, "v")):
+            if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be a {dtype} CUDA tensor {list(shape)}")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same strides and contiguous rows")
+        if (dtype == torch.float8_e4m3fn) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("an 8-bit cache needs k_scale and v_scale, a 16-bit one has none")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _dev_tensor(t, torch.float32, name)
+                if tuple(t.shape) != (kv_heads,):
+                    raise ValueError(f"{name} must be [{kv_heads}]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim = shape[0], page_size, kv_heads, head_dim
+        self.dtype, self.device = dtype, k.device
+        self.struct = tl_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), k.stride(1), k.stride(2),
+                                  _CACHE_DTYPES[dtype], kv_heads, head_dim, page_size, num_pages)
+        self._ref = ctypes.pointer(self.struct)
+        self._ws, self._ws_need = None, {}
+
+    def _workspace(self, B: int, q_heads: int):
+        need = self._ws_need.get(q_heads)
+        if need is None:      # does not depend on B, except that B = 0 needs none
+            need = tl_paged_attention_workspace_size(max(B, 1), q_heads, self.kv_heads, self.head_dim)
+            self._ws_need[q_heads] = need
+        if self._ws is None or self._ws.numel() < need:
+            # zeroed once here; every call leaves its counters zero again
+            self._ws = torch.zeros((need,), dtype=torch.uint8, device=self.device)
+        return self._ws
+
+    def append(self, k, v, positions, slots, cos_sin=None, interleaved: bool = False, q=None, q_out=None, stream=None):
+        """tl_kv_append on this cache; returns the rotated queries (None without q)."""
+        return tl_kv_append(self, k, v, positions, slots, cos_sin, interleaved, q, q_out, stream)
+
+    def attend(self, q, pages, lens, scale: float | None = None, window: int = 0, out=None, lse=None, stream=None):
+        """tl_paged_attention on this cache with its own workspace; returns out [requests, q_heads, head_dim]."""
+        return tl_paged_attention(self, q, pages, lens, scale, window, out, lse, None, stream)
+
+
+def tl_kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None, slots: torch.Tensor,
+                 cos_sin: torch.Tensor | None = None, interleaved: bool = False, q: torch.Tensor | None = None,
+                 q_out: torch.Tensor | None = None, stream=None):
+    """k, v [T, kv_heads, head_dim] into the cache's slots int64 [T], and q [T, q_heads, head_dim] into q_out, keys and
+    queries rotated by cos_sin fp32 [max_pos, rot_dim] at positions int32 [T]. Returns q_out (None without q)."""
+    hkv, d = cache.kv_heads, cache.head_dim
+    dt = k.dtype
+    code = _HALF.get(dt)
+    if code is None:
+        raise ValueError(f"k must be bf16 or fp16, got {dt}")
+    ldk, ldv = _token_rows(k, hkv, d, dt, "k"), _token_rows(v, hkv, d, dt, "v")
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same number of tokens")
+    hq = ldq = ldo = 0
+    pq = po = None
+    if q is not None:
+        hq = q.shape[1]
+        ldq = _token_rows(q, hq, d, dt, "q")
+        if q_out is None:
+            q_out = torch.empty((T, hq, d), dtype=dt, device=q.device)
+        ldo = _token_rows(q_out, hq, d, dt, "q_out")
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError("q, q_out and k must have the same number of tokens")
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    rot = max_pos = 0
+    pcs = ppos = None
+    if cos_sin is not None:
+        _dev_tensor(cos_sin, torch.float32, "cos_sin")
+        max_pos, rot = cos_sin.shape
+        pcs, ppos = cos_sin.data_ptr(), _ints(positions, torch.int32, T, "positions")
+    r = lib().tl_kv_append(cache._ref, pq, k.data_ptr(), v.data_ptr(), code, T, hq, ldq, ldk, ldv, po, ldo, pcs, max_pos, rot,
+                           1 if interleaved else 0, ppos, _ints(slots, torch.int64, T, "slots"), _stream(stream))
+    if r != TL_OK:
+        _check(r, "tl_kv_append")
+    return q_out
+
+
+def tl_paged_attention_workspace_size(B: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().tl_paged_attention_workspace_size(B, q_heads, kv_heads, head_dim, ctypes.byref(b)),
+           "tl_paged_attention_workspace_size")
+    return b.value
+
+
+def tl_paged_attention(cache: PagedKVCache, q: torch.Tensor, pages: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
+                       window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q [B, q_heads, head_dim] over the cached tokens that pages int32 [B, max_pages] and lens int32 [B] name -> out of
+    q's shape and dtype; lse fp32 [B, q_heads] when given. scale defaults to head_dim ** -0.5; the workspace to the cache's."""
+    d = cache.head_dim
+    dt = q.dtype
+    code = _HALF.get(dt)
+    if code is None:
+        raise ValueError(f"q must be bf16 or fp16, got {dt}")
+    B, hq = q.shape[0], q.shape[1]
+    ldq = _token_rows(q, hq, d, dt, "q")
+    if out is None:
+        out = torch.empty((B, hq, d), dtype=dt, device=q.device)
+    ldo = _token_rows(out, hq, d, dt, "out")
+    if not pages.is_cuda or pages.dtype is not torch.int32 or pages.dim() != 2 or pages.shape[0] != B or \
+            (pages.shape[1] > 1 and pages.stride(1) != 1):
+        raise ValueError(f"pages must be an int32 CUDA tensor [{B}, max_pages] with contiguous rows")
+    if out.shape[0] != B:
+        raise ValueError("out and q must have the same number of requests")
+    pl = None
+    if lse is not None:
+        _dev_tensor(lse, torch.float32, "lse")
+        if lse.shape != (B, hq):
+            raise ValueError(f"lse must be [{B}, {hq}]")
+        pl = lse.data_ptr()
+    ws = cache._workspace(B, hq) if workspace is None else workspace
+    r = lib().tl_paged_attention(cache._ref, q.data_ptr(), code, B, hq, ldq, pages.data_ptr(), pages.shape[1], pages.stride(0),
+                                 _ints(lens, torch.int32, B, "lens"), d ** -0.5 if scale is None else scale, window,
+                                 out.data_ptr(), ldo, pl, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+    if r != TL_OK:
+        _check(r, "tl_paged_attention")
+    return out
 
 
 class TernaryLinear:
