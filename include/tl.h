@@ -430,6 +430,45 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
                        float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Low-rank adapters of many requests beside a projection (ternary weights cannot
+ * absorb an adapter, so each request's runs beside them):
+ *   y[m] = base[m] + scale[a] B[a] (A[a] x[m]),   a = ids[m]
+ * for every token m of a batch in which each may have another adapter; a
+ * negative id is no adapter (y[m] = base[m]).
+ *
+ * tl_lora_plan sorts a batch's tokens by adapter, once for all the
+ * projections of a step:
+ *   ids     int32 [M]; one of n_adapters or above records TL_EDATA and counts as none
+ *   plan    device memory of tl_lora_plan_size(M, n_adapters) bytes, opaque
+ * M and n_adapters are at most 2^20 and 8192 (more: TL_EUNSUPPORTED).
+ *
+ * tl_lora_apply:
+ *   x       [M, K], dtype TL_BF16 or TL_F16, ldx elements from token to token
+ *   A, B    [n_adapters, rank, K] and [n_adapters, N, rank] of the same dtype, dense
+ *   scale   fp32 [n_adapters]
+ *   plan    of the same M and n_adapters (another one's is refused on the
+ *           device: TL_EDATA, and nothing is written)
+ *   base    [M, N] of y_dtype (TL_BF16, TL_F16 or TL_F32), ldb elements from token to token
+ *   y       [M, N] likewise; may be base (in place, ldy = ldb), must not overlap it otherwise
+ *   workspace  tl_lora_workspace_size(M, rank) bytes, needs no clearing. Calls
+ *           that can overlap on the GPU must not share one.
+ * The products are exact and summed in fp32; A[a] x[m] is kept in fp32 and enters the second product
+ * as the sum of two or three 16-bit numbers, so that it counts with 16 (bf16), 22
+ * (fp16) or, for an fp32 y, 24 bits; base + delta is rounded once to y_dtype. For given
+ * M and n_adapters, a token's result does not depend on the other tokens of the batch.
+ * rank is a multiple of 8 up to 128; K, N (at most 2^22) and the lds multiples of 8;
+ * anything else returns TL_EUNSUPPORTED.
+ */
+int tl_lora_plan_size(int M, int n_adapters, size_t* bytes);
+int tl_lora_plan(const int32_t* ids, int M, int n_adapters, void* plan, size_t plan_bytes,
+                 void* stream);
+int tl_lora_workspace_size(int M, int rank, size_t* bytes);
+int tl_lora_apply(const void* x, int64_t ldx, const void* A, const void* B, const float* scale,
+                  int dtype, int n_adapters, int rank, const void* plan, int M, int N, int K,
+                  const void* base, int64_t ldb, void* y, int64_t ldy, int y_dtype,
+                  void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Diagnostic: launches one kernel whose bounded wait can never be satisfied (an
  * mbarrier phase nothing arrives at) with a limit of limit_us microseconds
  * (1..100000, else TL_EINVAL). The wait gives up and records TL_ETIMEOUT in

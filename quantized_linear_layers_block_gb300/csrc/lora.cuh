@@ -1,0 +1,54 @@
+// What the adapter entry points hand to their kernels, and the layout of a plan.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace tl {
+
+constexpr int kLoraTile = 32;           // most tokens of one item
+constexpr int kLoraMaxM = 1 << 20;
+constexpr int kLoraMaxAdapters = 8192;
+constexpr int kLoraMaxRank = 128;
+
+// A plan: a header, the items (tokens of one adapter, at most kLoraTile of them), and
+// the tokens sorted by adapter, in their own order within one; those without an adapter last.
+struct LoraItem {
+  int adapter, start, count, unused;    // adapter -1: none; start in the sorted order
+};
+struct LoraPlanHeader {
+  int M, n_adapters, items, unused;
+};
+
+// most items that M tokens of n_adapters adapters (and none) can need
+inline int lora_max_items(int M, int n_adapters) {
+  const int bins = n_adapters + 1 < M ? n_adapters + 1 : M;
+  return (M + kLoraTile - 1) / kLoraTile + bins;
+}
+inline size_t lora_plan_bytes(int M, int n_adapters) {
+  return sizeof(LoraPlanHeader) + sizeof(LoraItem) * lora_max_items(M, n_adapters) + sizeof(int) * static_cast<size_t>(M);
+}
+
+struct LoraParams {
+  const uint16_t* x;
+  const uint16_t* A;
+  const uint16_t* B;
+  const float* scale;
+  const LoraPlanHeader* plan;
+  const LoraItem* items;
+  const int* order;
+  float* h;                 // [M, rank], tokens in sorted order
+  const void* base;
+  void* y;
+  int64_t ldx, ldb, ldy;
+  int M, N, K, rank, n_adapters, y_dtype;
+  int copy_bare;            // base and y differ: tokens without an adapter are copied
+  int* status;
+};
+
+cudaError_t launch_lora_plan(const int32_t* ids, int M, int n_adapters, void* plan, int* status, cudaStream_t st);
+cudaError_t launch_lora_apply(const LoraParams& p, bool bf16, int sms, cudaStream_t st);
+
+}  // namespace tl

@@ -59,6 +59,10 @@ SIGNATURES = {
     "tl_kv_append": (_I, [_PKV, _P, _P, _P, _I, _I, _I, _L, _L, _L, _P, _L, _P, _I, _I, _I, _P, _P, _P]),
     "tl_paged_attention_workspace_size": (_I, [_I, _I, _I, _I, _PSZ]),
     "tl_paged_attention": (_I, [_PKV, _P, _I, _I, _I, _L, _P, _I, _L, _P, _F, _I, _P, _L, _P, _P, _SZ, _P]),
+    "tl_lora_plan_size": (_I, [_I, _I, _PSZ]),
+    "tl_lora_plan": (_I, [_P, _I, _I, _P, _SZ, _P]),
+    "tl_lora_workspace_size": (_I, [_I, _I, _PSZ]),
+    "tl_lora_apply": (_I, [_P, _L, _P, _P, _P, _I, _I, _I, _P, _I, _I, _I, _P, _L, _P, _L, _I, _P, _SZ, _P]),
     "tl_selftest_wait_timeout": (_I, [ctypes.c_uint, _P]),
     "tl_get_status": (_I, [_P]),
 }
@@ -481,6 +485,119 @@ def tl_paged_attention(cache: PagedKVCache, q: torch.Tensor, pages: torch.Tensor
                                  out.data_ptr(), ldo, pl, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
     if r != TL_OK:
         _check(r, "tl_paged_attention")
+    return out
+
+
+_OUT_DTYPES = {torch.bfloat16: TL_BF16, torch.float16: TL_F16, torch.float32: TL_F32}
+
+
+def _matrix(t: torch.Tensor, rows: int | None, cols: int, dtype: torch.dtype, name: str) -> int:
+    """Checks a device matrix [rows, cols] with contiguous rows; returns the distance of its rows."""
+    shape, stride = t.shape, t.stride()
+    if not t.is_cuda or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows) or stride[1] != 1:
+        raise ValueError(f"{name} must be [{'tokens' if rows is None else rows}, {cols}] with contiguous rows")
+    return stride[0]
+
+
+def tl_lora_plan_size(M: int, n_adapters: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().tl_lora_plan_size(M, n_adapters, ctypes.byref(b)), "tl_lora_plan_size")
+    return b.value
+
+
+def tl_lora_workspace_size(M: int, rank: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().tl_lora_workspace_size(M, rank, ctypes.byref(b)), "tl_lora_workspace_size")
+    return b.value
+
+
+class LoraPlan:
+    """A batch's tokens sorted by adapter (tl_lora_plan): made once, used by every projection of the step."""
+
+    __slots__ = ("M", "n_adapters", "data")
+
+    def __init__(self, M: int, n_adapters: int, data: torch.Tensor):
+        self.M, self.n_adapters, self.data = M, n_adapters, data
+
+
+def tl_lora_plan(ids: torch.Tensor, n_adapters: int, plan: LoraPlan | None = None, stream=None) -> LoraPlan:
+    """ids int32 [M] (device; negative: no adapter) -> a LoraPlan; `plan` of the same M and n_adapters is rewritten."""
+    if ids.dim() != 1:
+        raise ValueError("ids must be a vector")
+    M = ids.shape[0]
+    p = _ints(ids, torch.int32, M, "ids")
+    if plan is None:
+        plan = LoraPlan(M, n_adapters, torch.empty((tl_lora_plan_size(M, n_adapters),), dtype=torch.uint8, device=ids.device))
+    elif (plan.M, plan.n_adapters) != (M, n_adapters):
+        raise ValueError("the plan is of another number of tokens or adapters")
+    _check(lib().tl_lora_plan(p, M, n_adapters, plan.data.data_ptr(), plan.data.numel(), _stream(stream)), "tl_lora_plan")
+    return plan
+
+
+class LoraBank:
+    """The low-rank adapters beside one projection, of all the requests that may come.
+
+    A [n_adapters, rank, K] and B [n_adapters, N, rank], bf16 or fp16, on the
+    device; scale fp32 [n_adapters] (ones when not given). apply() adds
+    scale[a] B[a] (A[a] x) to each token's output, a being the token's adapter.
+
+    The bank keeps one workspace: apply() calls on one bank that can run at the same time on
+    different streams must be ordered by the caller, or use one LoraBank over the
+    same A and B for each stream. It grows with the largest batch (allocated in apply()).
+    """
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor | None = None):
+        if A.dtype not in _HALF:
+            raise ValueError(f"A must be bf16 or fp16, got {A.dtype}")
+        _dev_tensor(A, A.dtype, "A")
+        _dev_tensor(B, A.dtype, "B")
+        if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[1] != B.shape[2]:
+            raise ValueError("A must be [n_adapters, rank, K] and B [n_adapters, N, rank]")
+        if scale is None:
+            scale = torch.ones((A.shape[0],), dtype=torch.float32, device=A.device)
+        _dev_tensor(scale, torch.float32, "scale")
+        if tuple(scale.shape) != (A.shape[0],):
+            raise ValueError(f"scale must be [{A.shape[0]}]")
+        self.A, self.B, self.scale = A, B, scale
+        self.n_adapters, self.rank, self.K = A.shape
+        self.N = B.shape[1]
+        self.dtype = A.dtype
+        self._fixed = (A.data_ptr(), B.data_ptr(), scale.data_ptr(), _HALF[A.dtype], self.n_adapters, self.rank)
+        self._ws = torch.empty((max(1, tl_lora_workspace_size(64, self.rank)),), dtype=torch.uint8, device=A.device)
+
+    def plan(self, ids: torch.Tensor, plan: LoraPlan | None = None, stream=None) -> LoraPlan:
+        """Sort a batch's tokens by adapter; the plan serves every bank of as many adapters."""
+        return tl_lora_plan(ids, self.n_adapters, plan, stream)
+
+    def apply(self, x: torch.Tensor, base: torch.Tensor, plan: LoraPlan, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """out = base + each token's adapter of x; out may be base (in place). Returns out."""
+        return tl_lora_apply(self, x, base, plan, out, stream)
+
+
+def tl_lora_apply(bank: LoraBank, x: torch.Tensor, base: torch.Tensor, plan: LoraPlan, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """x [M, K] of the bank's dtype, base [M, N] bf16, fp16 or fp32 -> out like base (allocated when not given)."""
+    M = x.shape[0]
+    if plan.M != M or plan.n_adapters != bank.n_adapters:
+        raise ValueError(f"the plan is of {plan.M} tokens and {plan.n_adapters} adapters, not {M} and {bank.n_adapters}")
+    dt = base.dtype
+    code = _OUT_DTYPES.get(dt)
+    if code is None:
+        raise ValueError(f"base must be bf16, fp16 or fp32, got {dt}")
+    ldx = _matrix(x, None, bank.K, bank.dtype, "x")
+    ldb = _matrix(base, M, bank.N, dt, "base")
+    if out is None:
+        out = torch.empty((M, bank.N), dtype=dt, device=base.device)
+    ldo = _matrix(out, M, bank.N, dt, "out")
+    ws = bank._ws
+    if ws.numel() < 4 * M * bank.rank:
+        ws = bank._ws = torch.empty((tl_lora_workspace_size(M, bank.rank),), dtype=torch.uint8, device=bank.A.device)
+    r = lib().tl_lora_apply(x.data_ptr(), ldx, *bank._fixed, plan.data.data_ptr(), M, bank.N, bank.K, base.data_ptr(), ldb,
+                            out.data_ptr(), ldo, code, ws.data_ptr(), ws.numel(), _stream(stream))
+    if r != TL_OK:
+        _check(r, "tl_lora_apply")
     return out
 
 

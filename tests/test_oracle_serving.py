@@ -169,3 +169,33 @@ def test_division_by_multiplication():
         for n in ns:
             if 0 <= n < 2 ** 31:
                 assert (n * m) >> (31 + s) == n // d, (n, d)
+
+
+def test_lora_refusals(lib):
+    ok = 4096
+
+    def call(x=ok, ldx=64, A=ok, B=ok, scale=ok, dtype=tl.TL_BF16, n=2, rank=16, plan=ok, M=3, N=128, K=64, base=ok, ldb=128, y=8192, ldy=128,
+             yd=tl.TL_BF16, ws=ok, wsb=10 ** 6):
+        return lib.tl_lora_apply(x, ldx, A, B, scale, dtype, n, rank, plan, M, N, K, base, ldb, y, ldy, yd, ws, wsb, None)
+
+    for name in ("x", "A", "B", "scale", "plan", "base", "y", "ws"):
+        assert call(**{name: None}) == tl.TL_EINVAL, name
+        assert call(**{name: 4098}) == tl.TL_EINVAL, name
+    assert call(dtype=tl.TL_F32) == tl.TL_EINVAL
+    assert call(yd=tl.TL_F8E4M3) == tl.TL_EINVAL
+    assert call(M=-1) == tl.TL_EINVAL
+    assert call(K=0) == tl.TL_EINVAL
+    for over in (dict(rank=12), dict(rank=136), dict(K=60), dict(N=100), dict(ldx=56), dict(ldy=132), dict(n=9000), dict(M=(1 << 20) + 1),
+                 dict(N=(1 << 22) + 8)):
+        assert call(**over) == tl.TL_EUNSUPPORTED, over
+    assert call(y=ok, ldy=136) == tl.TL_EINVAL               # in place, but the rows lie elsewhere
+    assert call(wsb=100) == tl.TL_ENOSPACE
+    assert call(M=0, x=None, base=None, y=None, ws=None, plan=None) == tl.TL_OK
+    assert call(N=0, x=None, base=None, y=None, ws=None, plan=None) == tl.TL_OK
+    sz = ctypes.c_size_t()
+    assert lib.tl_lora_plan_size(33, 4, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 16 * (2 + 5) + 4 * 33
+    assert lib.tl_lora_plan_size(2, 400, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 16 * (1 + 2) + 4 * 2
+    assert lib.tl_lora_plan(None, 2, 4, ok, 10 ** 6, None) == tl.TL_EINVAL
+    assert lib.tl_lora_plan(ok, 2, 4, ok, 10, None) == tl.TL_ENOSPACE
+    assert lib.tl_lora_plan(ok, 2, 9000, ok, 10 ** 9, None) == tl.TL_EUNSUPPORTED
+    assert lib.tl_lora_plan(None, 0, 4, None, 0, None) == tl.TL_OK
