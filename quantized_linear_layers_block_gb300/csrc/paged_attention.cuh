@@ -75,14 +75,17 @@ struct AttnParams {
   float* lse;
   float scale_log2;
   int B, q_heads, kv_heads, group, groups_per_kv, window, q_bf16;
-  int* counters;            // one per block
+  int runs16;               // page_size is a multiple of 16: 16 keys from a multiple of 16 lie at equal distances
+  int* counters;            // 2 kAttnMaxGrid, zero between calls
   float* partials;          // two per block
   int* status;
 };
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnMaxBlocksPerSm = 4;
-constexpr int kAttnMaxGrid = 4096;     // counters at the front of the workspace
+constexpr int kAttnMaxGrid = 4096;     // the workspace begins with two counters for each block
+constexpr int kJoinWide = 48;          // partials that one block joins at once
+constexpr int kJoinGroup = 16;         // above that: partials joined first
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -99,6 +102,9 @@ namespace attn {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -181,6 +187,7 @@ struct Traits {
   static constexpr int MEET = (HEADS * OPITCH + 2 * HEADS) * 4;
   static constexpr int STAGES = NT == 1 ? 3 : (NT == 2 && D < 256 ? 2 : (D == 256 && !F8 ? 2 : 3));
   static constexpr int SMEM = kAttnWarps * (STAGES * BUF + MEET);
+  static constexpr int BLOCKS = SMEM > 113 * 1024 ? 1 : SMEM > 74 * 1024 ? 2 : 3;     // per SM
   // 2^8 in the probabilities keeps an f16 low part of the small ones out of the subnormals
   static constexpr float POFF = BF16 ? 0.f : 8.f;
 };
@@ -196,83 +203,255 @@ __device__ __forceinline__ uint32_t at(int r, int c) {
 
 struct Segment {            // where in the list of tiles
   int b, h, tile, tiles;    // request, group of query heads, tile, tiles of this segment
-  int begin, end;           // first key, one past the last
+  int begin, first, end;    // where its tiles begin, its first key, one past the last
 };
+
+// 64-bit quotient of non-negative numbers, by the 32-bit division where both fit
+__device__ __forceinline__ long long divide(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return static_cast<unsigned>(n) / static_cast<unsigned>(d);
+  return n / d;
+}
 
 __device__ __forceinline__ void seg_keys(const AttnParams& p, int len, int tile_keys, Segment& s) {
   const int n = min(max(len, 0), p.max_len);
   s.end = n;
-  s.begin = p.window > 0 ? max(0, n - p.window) : 0;
+  s.first = p.window > 0 ? max(0, n - p.window) : 0;
+  s.begin = p.runs16 ? s.first & ~15 : s.first;       // a window's tiles begin with its first key's run
   s.tiles = max(1, (s.end - s.begin + tile_keys - 1) / tile_keys);
 }
 
+// A segment that n blocks share, from block c0 on: c0 began it (its second partial), the others found it
+// begun (their first). Up to kJoinWide partials are joined at once by the last block to
+// arrive; more are joined in groups of kJoinGroup blocks first, each by the last of its group, so that the
+// joins run on many SMs.
+struct Shared {
+  int c0, n, b, h0, heads;
+  float v_scale;
+};
+
+// Four channels of head h of request b, from the joined (m, l, o).
+template <class T>
+__device__ __forceinline__ void write_out(const AttnParams& p, int b, int h, int d, int dim, const float4& o, float m, float l, float vs) {
+  const float inv = l == 0.f ? 0.f : vs / l;
+  uint2 r;
+  r.x = p.q_bf16 ? pack2<true>(o.x * inv, o.y * inv) : pack2<false>(o.x * inv, o.y * inv);
+  r.y = p.q_bf16 ? pack2<true>(o.z * inv, o.w * inv) : pack2<false>(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(p.out + b * p.ldo + static_cast<int64_t>(h) * dim + d) = r;
+  if (d == 0 && p.lse != nullptr)
+    p.lse[static_cast<int64_t>(b) * p.q_heads + h] = l == 0.f ? -INFINITY : (m - T::POFF) * kLn2 + logf(l);
+}
+
+// Called by one thread, after a barrier behind which all of the block's writes lie: counts this block in and
+// says whether it is the last of n. The counter is zero again then, and what the others wrote is visible.
+__device__ __forceinline__ int count_in(int* counter, int n) {
+  __threadfence();
+  const int last = atomicAdd(counter, 1) == n - 1;
+  if (last) {
+    *counter = 0;
+    __threadfence();
+  }
+  return last;
+}
+
+__device__ __forceinline__ int arrive(int* counters, const Shared& s) {
+  if (s.n <= kJoinWide) return count_in(counters + s.c0, s.n);
+  const int first = (static_cast<int>(blockIdx.x) - s.c0) / kJoinGroup * kJoinGroup;
+  return count_in(counters + s.c0 + first, min(kJoinGroup, s.n - first));
+}
+
+// Joins n <= kJoinWide partials, those of blocks first, first + step, ... counted from the segment's first: with
+// LAST, into the segment's result; otherwise into the first of them. One block works alone here, with few
+// warps, so what counts is the number of latencies and of instructions: the partials' o come in
+// bulk copies to the ring, which is free by now (as many at a time as fit), while the warps turn the maxima and
+// sums into one weight per partial and head; then each thread adds up its channels.
+template <class T, int D, bool LAST>
+__device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int first, int step, int n, uint8_t* ring, float* meet,
+                                     uint32_t bar, uint32_t& phase) {
+  constexpr size_t PF = attn_partial_floats(T::HEADS, D);
+  constexpr int THREADS = kAttnWarps * 32, COLS = T::HEADS * D / 4 / THREADS;
+  constexpr int FIT = kAttnWarps * T::STAGES * T::BUF / (T::HEADS * D * 4), ROOM = FIT < 32 ? FIT : 32;   // partials that the ring holds
+  static_assert(ROOM >= 2 && T::HEADS * D / 4 % THREADS == 0 && (kJoinWide + 2) * T::HEADS * 4 <= kAttnWarps * T::MEET, "join");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* const p0 = p.partials + (static_cast<size_t>(s.c0) * 2 + 1) * PF;
+  float* const p1 = p.partials + static_cast<size_t>(s.c0) * 2 * PF;
+  auto part = [&](int i) { return first + i * step == 0 ? p0 : p1 + static_cast<size_t>(first + i * step) * 2 * PF; };
+  const uint32_t bytes = s.heads * D * 4;
+  auto fetch = [&](int i0) {             // warp 0: partials i0 .. i0 + ROOM - 1
+    const int k = min(ROOM, n - i0);
+    if (lane == 0) mbar_arrive_expect_tx(bar, k * bytes);
+    __syncwarp();
+    if (lane < k) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       smem_u32(ring) + lane * (T::HEADS * D * 4)),
+                   "l"(part(i0 + lane) + 2 * T::HEADS), "r"(bytes), "r"(bar)
+                   : "memory");
+    }
+  };
+  if (warp == 0) {
+    // other blocks' ordinary writes, which count_in made visible, before the copies that read them
+    asm volatile("fence.proxy.async;" ::: "memory");
+    fetch(0);
+  }
+  float* const weight = meet;            // [n][HEADS], then the segment's maximum and sum per head
+  float* const all = meet + kJoinWide * T::HEADS;
+  for (int h = warp; h < s.heads; h += kAttnWarps) {
+    float m[kJoinWide / 32 + 1], l[kJoinWide / 32 + 1], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int e = 0; e <= kJoinWide / 32; ++e) {
+      const int i = e * 32 + lane;
+      m[e] = i < n ? __ldcg(part(i) + h) : -INFINITY;
+      l[e] = i < n ? __ldcg(part(i) + T::HEADS + h) : 0.f;
+      top = fmaxf(top, m[e]);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int e = 0; e <= kJoinWide / 32; ++e) {
+      m[e] = exp2_approx(m[e] - base);
+      sum += m[e] * l[e];
+      if (e * 32 + lane < n) weight[(e * 32 + lane) * T::HEADS + h] = m[e];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      all[h] = top;
+      all[T::HEADS + h] = sum;
+    }
+  }
+  __syncthreads();
+  float4 a[COLS];
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += ROOM) {
+    const int k = min(ROOM, n - i0);
+    if (!mbar_wait(bar, phase, nullptr)) set_status(p.status, TL_ETIMEOUT);
+    phase ^= 1;
+    const float4* v = reinterpret_cast<const float4*>(ring) + tid;
+    const float* w = weight + i0 * T::HEADS;
+#pragma unroll 2
+    for (int i = 0; i < k; ++i, v += T::HEADS * D / 4, w += T::HEADS) {
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        const int h = (tid + c * THREADS) / (D / 4);
+        if (h < s.heads) {
+          const float f = w[h];
+          const float4 x = v[c * THREADS];
+          a[c].x += f * x.x;
+          a[c].y += f * x.y;
+          a[c].z += f * x.z;
+          a[c].w += f * x.w;
+        }
+      }
+    }
+    if (i0 + ROOM < n) {
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (warp == 0) fetch(i0 + ROOM);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) {
+    const int x = tid + c * THREADS, h = x / (D / 4), d = 4 * (x % (D / 4));
+    if (h < s.heads) {
+      if constexpr (LAST) {
+        write_out<T>(p, s.b, s.h0 + h, d, D, a[c], all[h], all[T::HEADS + h], s.v_scale);
+      } else {
+        float* const dst = part(0);
+        reinterpret_cast<float4*>(dst + 2 * T::HEADS)[x] = a[c];
+        if (d == 0) {
+          dst[h] = all[h];
+          dst[T::HEADS + h] = all[T::HEADS + h];
+        }
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  __syncthreads();            // `meet` and the ring are free again
+}
+
+// What the last block of a segment, or of a group, does; ring, meet, flag and barrier in shared memory.
+template <class T, int D>
+__device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uint8_t* ring, float* meet, int* flag, uint32_t bar,
+                                       uint32_t& phase) {
+  int step = 1, n = s.n;
+  if (n > kJoinWide) {
+    const int first = (static_cast<int>(blockIdx.x) - s.c0) / kJoinGroup * kJoinGroup;
+    join<T, D, false>(p, s, first, 1, min(kJoinGroup, n - first), ring, meet, bar, phase);
+    step = kJoinGroup;
+    n = (n + kJoinGroup - 1) / kJoinGroup;
+    if (threadIdx.x == 0) *flag = count_in(p.counters + kAttnMaxGrid + s.c0, n);
+    __syncthreads();
+    if (*flag == 0) return;
+  }
+  join<T, D, true>(p, s, 0, step, n, ring, meet, bar, phase);
+}
+
 template <int CACHE, int D, int NT>
-__global__ void __launch_bounds__(kAttnWarps * 32)
+__global__ void __launch_bounds__(kAttnWarps * 32, Traits<CACHE, D, NT>::BLOCKS)
 paged_attention_kernel(const __grid_constant__ AttnParams p) {
   using T = Traits<CACHE, D, NT>;
   constexpr int KT = T::KT, ROW = T::ROW, MT = KT / 16, DT = D / 16, S = T::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_scan[kAttnWarps];
-  __shared__ Segment s_first;
-  __shared__ int s_flag;
+  __shared__ __align__(8) uint64_t s_bar;
+  __shared__ int s_last[2];
+  __shared__ Shared s_pend[2];                        // segments shared with other blocks: the first, the last
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int HG = p.kv_heads * p.groups_per_kv;
 
   pdl_wait_prior();
   pdl_launch_dependents();
 
-  // ---- the share of this block: tiles [t0, t1) of `total`
-  const int per = (p.B + blockDim.x - 1) / blockDim.x;
-  long long mine = 0;
-  bool bad = false;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < p.B) {
-      const int len = __ldg(p.lens + b);
+  // ---- the share of this block: `count` places from t0 of the list, in which a segment has one place for
+  // what it costs besides its tiles, then its tiles. Every warp finds it for itself.
+  long long total = 0;
+  int len = 0;
+  Segment cur;
+  {
+    bool bad = false;
+    for (int base = 0; base < p.B; base += 32) {
+      len = base + lane < p.B ? __ldg(p.lens + base + lane) : 0;
       bad |= len < 0 || len > p.max_len;
-      Segment s;
-      seg_keys(p, len, T::TILE, s);
-      mine += s.tiles;
+      seg_keys(p, len, T::TILE, cur);
+      if (base + lane < p.B) total += cur.tiles + 1;
     }
+    if (bad && blockIdx.x == 0) set_status(p.status, TL_EDATA);
   }
-  if (bad && blockIdx.x == 0) set_status(p.status, TL_EDATA);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
-  before *= HG;
+  // a lane's sum is below 2^50 (2^27 tiles a request, 2^23 requests a lane)
+  total = static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total & 0x1FFFFFF))) +
+          (static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total >> 25))) << 25);
   total *= HG;
-  const long long parts = min(total, static_cast<long long>(gridDim.x));
-  if (blockIdx.x >= parts) return;
-  const long long t0 = total * blockIdx.x / parts, t1 = total * (blockIdx.x + 1) / parts;
-  if (t0 >= before && t0 < before + mine * HG) {
-    long long left = t0 - before;
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      Segment s;
-      seg_keys(p, __ldg(p.lens + b), T::TILE, s);
-      if (left < static_cast<long long>(s.tiles) * HG) {
-        s.b = b;
-        s.h = static_cast<int>(left / s.tiles);
-        s.tile = static_cast<int>(left % s.tiles);
-        s_first = s;
+  const long long share = divide(total + gridDim.x - 1, gridDim.x);
+  const long long t0 = share * blockIdx.x;
+  if (t0 >= total) return;
+  const int count = static_cast<int>(min(share, total - t0));
+  int skip;                                           // places of the first segment that lie before t0
+  {
+    long long run = 0;                                // tiles of the requests before this round's, of one head group
+    for (int base = 0;; base += 32) {
+      if (p.B > 32) len = base + lane < p.B ? __ldg(p.lens + base + lane) : 0;
+      seg_keys(p, len, T::TILE, cur);
+      const unsigned tiles = base + lane < p.B ? cur.tiles + 1 : 0;
+      unsigned incl = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned at = __ballot_sync(0xffffffffu, t0 < HG * (run + incl));
+      if (at != 0) {
+        const int who = __ffs(at) - 1;
+        cur.b = base + who;
+        seg_keys(p, __shfl_sync(0xffffffffu, len, who), T::TILE, cur);
+        const long long left = t0 - HG * (run + __shfl_sync(0xffffffffu, incl - tiles, who));
+        cur.h = static_cast<int>(divide(left, cur.tiles + 1));
+        skip = static_cast<int>(left - cur.h * (cur.tiles + 1ll));
+        cur.tile = max(skip - 1, 0);
         break;
       }
-      left -= static_cast<long long>(s.tiles) * HG;
+      run += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  __syncthreads();
-  const int count = static_cast<int>(t1 - t0);
 
   // ---- the warp's ring
   const uint32_t ring = smem_u32(smem) + warp * S * T::BUF;
@@ -281,53 +460,75 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
   constexpr int CPR = ROW / 16;                       // 16-byte chunks of a row
   constexpr int RPI = 32 / CPR;                       // rows that one instruction of the warp copies
   constexpr int KPL = (KT + 31) / 32;                 // keys whose address a lane computes
-  Segment ld = s_first;
+  Segment ld = cur;
   int next_len = 0;                                   // length of the request after ld's
   int pid[KPL];
+  const int chunk = (lane % CPR) * 16, row0 = lane / CPR;
   auto fetch_len = [&]() { next_len = ld.b + 1 < p.B ? __ldg(p.lens + ld.b + 1) : 0; };
   auto fetch_pages = [&]() {
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
       const int key = ld.begin + ld.tile * T::TILE + warp * KT + i * 32 + lane;
-      pid[i] = key < ld.end && i * 32 + lane < KT ? __ldg(p.pages + ld.b * p.ldp + p.page.div(key)) : -1;
+      pid[i] = key >= ld.first && key < ld.end && i * 32 + lane < KT ? __ldg(p.pages + ld.b * p.ldp + p.page.div(key)) : -1;
     }
   };
   fetch_len();
   fetch_pages();
-  int left = count;                                   // tiles not yet asked for
+  int left = count - (skip == 0);                     // places of the tiles not yet asked for
   auto load_tile = [&](int stage) {
     if (left > 0) {
       const int k0 = ld.begin + ld.tile * T::TILE + warp * KT;
       if (k0 < ld.end) {
         const int kvh = ld.h / p.groups_per_kv;
-        int64_t off[KPL];
+        int64_t off[KPL];                             // bytes from the cache's first row to key i * 32 + lane; -1: no such row
+        bool bad = false;
 #pragma unroll
         for (int i = 0; i < KPL; ++i) {
           const int key = k0 + i * 32 + lane;
           off[i] = -1;
-          if (key < ld.end && i * 32 + lane < KT) {
+          if (key >= ld.first && key < ld.end && i * 32 + lane < KT) {
             if (static_cast<unsigned>(pid[i]) < static_cast<unsigned>(p.num_pages))
               off[i] = pid[i] * p.page_stride + kvh * p.head_stride +
                        static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
             else
-              set_status(p.status, TL_EDATA);
+              bad = true;
           }
         }
-        const uint32_t kb = ring + stage * T::BUF, vb = kb + KT * ROW;
-        const int c = lane % CPR;
+        const uint32_t kb = ring + stage * T::BUF;
+        // a tile of whole pages, or parts of pages, of 16 rows each: one address for 16 rows
+        if (p.runs16 && k0 >= ld.first && k0 + KT <= ld.end && !__any_sync(0xffffffffu, bad)) {
 #pragma unroll
-        for (int i = 0; i < KT / RPI; ++i) {
-          const int r = i * RPI + lane / CPR;
-          const int64_t o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], r & 31);
-          const uint32_t bytes = o < 0 ? 0u : 16u;
-          const int64_t src = (o < 0 ? 0 : o) + c * 16;
-          cp_async16(kb + at<ROW>(r, c), p.k + src, bytes);
-          cp_async16(vb + at<ROW>(r, c), p.v + src, bytes);
+          for (int j = 0; j < MT; ++j) {
+            const int64_t o = __shfl_sync(0xffffffffu, off[j / 2], (16 * j) & 31);
+            const uint8_t* const ks = p.k + o + row0 * p.token_stride + chunk;
+            const uint8_t* const vs = p.v + o + row0 * p.token_stride + chunk;
+#pragma unroll
+            for (int i = 0; i < 16 / RPI; ++i) {
+              const uint32_t dst = kb + at<ROW>(16 * j + i * RPI + row0, chunk >> 4);
+              const int64_t step = static_cast<int64_t>(i * RPI) * p.token_stride;
+              cp_async16(dst, ks + step);
+              cp_async16(dst + KT * ROW, vs + step);
+            }
+          }
+        } else {
+          if (bad) set_status(p.status, TL_EDATA);
+          const int64_t any = 0;
+#pragma unroll
+          for (int i = 0; i < KT / RPI; ++i) {
+            const int r = i * RPI + row0;
+            const int64_t o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], r & 31);
+            const uint32_t bytes = o < 0 ? 0u : 16u;
+            const int64_t src = max(o, any) + chunk;
+            const uint32_t dst = kb + at<ROW>(r, chunk >> 4);
+            cp_async16(dst, p.k + src, bytes);
+            cp_async16(dst + KT * ROW, p.v + src, bytes);
+          }
         }
       }
       --left;
       if (++ld.tile == ld.tiles) {
         ld.tile = 0;
+        --left;
         if (++ld.h == HG) {
           ld.h = 0;
           ++ld.b;
@@ -343,18 +544,21 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
   for (int i = 0; i < S - 1; ++i) load_tile(i);
 
   // ---- the segments
-  Segment cur = s_first;
-  int stage = 0, done = 0;
+  int stage = 0, done = skip == 0;
   bool starts_before = cur.tile > 0;
-  while (done < count) {
-    const int here = min(cur.tiles - cur.tile, count - done);    // tiles of this segment in this block's share
-    const int kvh = cur.h / p.groups_per_kv;
-    const int h0 = kvh * p.group + (cur.h - kvh * p.groups_per_kv) * T::HEADS;
-    const int heads = min(T::HEADS, kvh * p.group + p.group - h0);
-
-    // queries as B operands: k = 16 channels, n = 8 heads. For an 8-bit cache
-    // thread t takes channels 4t .. 4t + 3, as its ldmatrix of K gives them.
-    uint32_t qf[DT][NT][2];
+  // queries as B operands: k = 16 channels, n = 8 heads. For an 8-bit cache thread t takes channels
+  // 4t .. 4t + 3, as its ldmatrix of K gives them. Asked for while the segment before is being finished.
+  uint32_t qf[DT][NT][2];
+  int kvh, h0, heads;
+  float kscale = 1.f, vscale = 1.f;
+  auto fetch_q = [&]() {
+    kvh = cur.h / p.groups_per_kv;
+    h0 = kvh * p.group + (cur.h - kvh * p.groups_per_kv) * T::HEADS;
+    heads = min(T::HEADS, kvh * p.group + p.group - h0);
+    if constexpr (T::F8) {
+      kscale = __ldg(p.k_scale + kvh);
+      vscale = __ldg(p.v_scale + kvh);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const uint16_t* qr = p.q + cur.b * p.ldq + static_cast<int64_t>(h0 + n * 8 + g) * D;
@@ -371,11 +575,21 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
         }
       }
     }
+  };
+  fetch_q();
+  if (tid == 0) {
+    s_pend[0].n = s_pend[1].n = 0;
+    mbar_init(smem_u32(&s_bar), 1);
+    fence_barrier_init();
+  }
+  while (done < count) {
+    const int here = min(cur.tiles - cur.tile, count - done);    // tiles of this segment in this block's share
+
     float sc[NT][2];                                 // log2(e) scale of heads 2t and 2t + 1
 #pragma unroll
     for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = p.scale_log2;
     if constexpr (T::F8) {
-      const float ks = __ldg(p.k_scale + kvh);
+      const float ks = kscale;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float up = 1.f;
@@ -425,11 +639,14 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       const int k0 = cur.begin + (cur.tile + it) * T::TILE + warp * KT;
       const uint32_t kb = ring + stage * T::BUF, vb = kb + KT * ROW;
       if (k0 < cur.end) {
-        float s[MT][NT][4];
+        float s[MT][NT][4], s2[MT][NT][4];            // two chains of dependent MMAs
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) s[j][n][0] = s[j][n][1] = s[j][n][2] = s[j][n][3] = 0.f;
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][n][e] = s2[j][n][e] = 0.f;
+          }
           const int r = 16 * j + (lane & 15);
           if constexpr (T::F8) {
 #pragma unroll
@@ -440,7 +657,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
               for (int e = 0; e < 2; ++e) {
                 const uint32_t a[4] = {widen_lo(w[2 * e]), widen_lo(w[2 * e + 1]), widen_hi(w[2 * e]), widen_hi(w[2 * e + 1])};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma<false>(s[j][n], a, qf[i + e][n][0], qf[i + e][n][1]);
+                for (int n = 0; n < NT; ++n) mma<false>(e ? s2[j][n] : s[j][n], a, qf[i + e][n][0], qf[i + e][n][1]);
               }
             }
           } else {
@@ -449,22 +666,27 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
               uint32_t a[4];
               ldsm4(kb + at<ROW>(r, 2 * i + (lane >> 4)), a);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma<T::BF16>(s[j][n], a, qf[i][n][0], qf[i][n][1]);
+              for (int n = 0; n < NT; ++n) mma<T::BF16>(i & 1 ? s2[j][n] : s[j][n], a, qf[i][n][0], qf[i][n][1]);
             }
           }
         }
         // rows 16 j + g (elements 0, 1) and + 8 (2, 3); columns: heads 2t, 2t + 1
-        const int live = cur.end - k0;
+        const int live = cur.end - k0, early = cur.first - k0;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][n][e] *= sc[n][e & 1];
+            for (int e = 0; e < 4; ++e) s[j][n][e] = (s[j][n][e] + s2[j][n][e]) * sc[n][e & 1];
             if (live < KT) {
               const int r = 16 * j + g;
               if (r >= live) s[j][n][0] = s[j][n][1] = -INFINITY;
               if (r + 8 >= live) s[j][n][2] = s[j][n][3] = -INFINITY;
+            }
+            if (early > 0) {
+              const int r = 16 * j + g;
+              if (r < early) s[j][n][0] = s[j][n][1] = -INFINITY;
+              if (r + 8 < early) s[j][n][2] = s[j][n][3] = -INFINITY;
             }
           }
         }
@@ -532,22 +754,24 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
                 const uint32_t x = __byte_perm(w[2 * e], 0, 0x3120), y = __byte_perm(w[2 * e + 1], 0, 0x3120);
                 const uint32_t a[4] = {widen_lo(x), widen_hi(x), widen_lo(y), widen_hi(y)};
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  mma<false>(o[i + e][n], a, ph[n][0], ph[n][1]);
-                  mma<false>(o[i + e][n], a, pl[n][0], pl[n][1]);
-                }
+                for (int n = 0; n < NT; ++n) mma<false>(o[i + e][n], a, ph[n][0], ph[n][1]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma<false>(o[i + e][n], a, pl[n][0], pl[n][1]);
               }
             }
           } else {
             const int r = 16 * j + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-            for (int i = 0; i < DT; ++i) {
-              uint32_t a[4];
-              ldsm4t(vb + at<ROW>(r, 2 * i + ((lane >> 3) & 1)), a);
+            for (int i = 0; i < DT; i += 4) {         // four independent MMAs before the first dependent one
+              uint32_t a[4][4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) ldsm4t(vb + at<ROW>(r, 2 * (i + e) + ((lane >> 3) & 1)), a[e]);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                mma<T::BF16>(o[i][n], a, ph[n][0], ph[n][1]);
-                mma<T::BF16>(o[i][n], a, pl[n][0], pl[n][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e][n], a[e], ph[n][0], ph[n][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e][n], a[e], pl[n][0], pl[n][1]);
               }
             }
           }
@@ -582,88 +806,12 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
         }
       }
     }
-    __syncthreads();
-    const bool whole = !starts_before && cur.tile + here == cur.tiles;
-    const float vs = T::F8 ? __ldg(p.v_scale + kvh) : 1.f;
-    float* const part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + (starts_before ? 0 : 1)) *
-                                         attn_partial_floats(T::HEADS, D);
-    for (int x = tid; x < heads * (D / 2); x += kAttnWarps * 32) {
-      const int h = x / (D / 2), d = 2 * (x % (D / 2));
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, meet[w * (T::MEET / 4) + h]);
-      const float base = top == -INFINITY ? 0.f : top;
-      float sum = 0.f, ox = 0.f, oy = 0.f;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
-        const float* q = meet + w * (T::MEET / 4);
-        const float f = exp2_approx(q[h] - base);
-        const float2 v = *reinterpret_cast<const float2*>(q + 2 * T::HEADS + h * T::OPITCH + d);
-        sum += f * q[T::HEADS + h];
-        ox += f * v.x;
-        oy += f * v.y;
-      }
-      if (whole) {
-        const float inv = sum == 0.f ? 0.f : vs / sum;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + cur.b * p.ldo + static_cast<int64_t>(h0 + h) * D + d);
-        *dst = p.q_bf16 ? pack2<true>(ox * inv, oy * inv) : pack2<false>(ox * inv, oy * inv);
-        if (d == 0 && p.lse != nullptr)
-          p.lse[static_cast<int64_t>(cur.b) * p.q_heads + h0 + h] = sum == 0.f ? -INFINITY : (top - T::POFF) * kLn2 + logf(sum);
-      } else {
-        if (d == 0) {
-          part[h] = top;
-          part[T::HEADS + h] = sum;
-        }
-        *reinterpret_cast<float2*>(part + 2 * T::HEADS + h * D + d) = make_float2(ox, oy);
-      }
-    }
-    if (!whole) {
-      // blocks c0 .. c1 share this segment; c0 owns the counter
-      const long long first = t0 + (done - here) - cur.tile, last = first + cur.tiles - 1;
-      const int c0 = static_cast<int>(((first + 1) * parts - 1) / total);
-      const int c1 = static_cast<int>(((last + 1) * parts - 1) / total);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_flag = atomicAdd(p.counters + c0, 1) == c1 - c0;
-      __syncthreads();
-      if (s_flag) {
-        __threadfence();
-        constexpr size_t PF = attn_partial_floats(T::HEADS, D);
-        // block c0 began the segment (its second partial); the others found it begun (their first)
-        const float* const p0 = p.partials + (static_cast<size_t>(c0) * 2 + 1) * PF;
-        const float* const p1 = p.partials + (static_cast<size_t>(c0) * 2 + 2) * PF;
-        const int n = c1 - c0 + 1;
-        for (int x = tid; x < heads * (D / 4); x += kAttnWarps * 32) {
-          const int h = x / (D / 4), d = 4 * (x % (D / 4));
-          float top = -INFINITY;
-          for (int c = 0; c < n; ++c) top = fmaxf(top, __ldcg((c == 0 ? p0 : p1 + (c - 1) * 2 * PF) + h));
-          const float base = top == -INFINITY ? 0.f : top;
-          float sum = 0.f;
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int c = 0; c < n; ++c) {
-            const float* q = c == 0 ? p0 : p1 + (c - 1) * 2 * PF;
-            const float f = exp2_approx(__ldcg(q + h) - base);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 2 * T::HEADS + h * D + d));
-            sum += f * __ldcg(q + T::HEADS + h);
-            a.x += f * v.x;
-            a.y += f * v.y;
-            a.z += f * v.z;
-            a.w += f * v.w;
-          }
-          const float inv = sum == 0.f ? 0.f : vs / sum;
-          uint2 r;
-          r.x = p.q_bf16 ? pack2<true>(a.x * inv, a.y * inv) : pack2<false>(a.x * inv, a.y * inv);
-          r.y = p.q_bf16 ? pack2<true>(a.z * inv, a.w * inv) : pack2<false>(a.z * inv, a.w * inv);
-          *reinterpret_cast<uint2*>(p.out + cur.b * p.ldo + static_cast<int64_t>(h0 + h) * D + d) = r;
-          if (d == 0 && p.lse != nullptr)
-            p.lse[static_cast<int64_t>(cur.b) * p.q_heads + h0 + h] = sum == 0.f ? -INFINITY : (top - T::POFF) * kLn2 + logf(sum);
-        }
-        if (tid == 0) p.counters[c0] = 0;
-      }
-    } else {
-      __syncthreads();
-    }
+    const Segment seg = cur;
+    const int sh0 = h0, sheads = heads;
+    const float vs = vscale;
+    const bool whole = !starts_before && seg.tile + here == seg.tiles, second = !starts_before;
+    const long long first = t0 + (done - here) - seg.tile;      // the place of its first tile
+    ++done;                                           // the next segment's first place
     starts_before = false;
     cur.tile = 0;
     if (++cur.h == HG) {
@@ -671,8 +819,60 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       ++cur.b;
       if (done < count) seg_keys(p, __ldg(p.lens + cur.b), T::TILE, cur);
     }
+    if (done < count) fetch_q();
+    __syncthreads();
+    float* const part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + second) * attn_partial_floats(T::HEADS, D);
+    for (int x = tid; x < sheads * (D / 4); x += kAttnWarps * 32) {
+      const int h = x / (D / 4), d = 4 * (x % (D / 4));
+      float mw[kAttnWarps], top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        mw[w] = meet[w * (T::MEET / 4) + h];
+        top = fmaxf(top, mw[w]);
+      }
+      const float base = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float* q = meet + w * (T::MEET / 4) + T::HEADS;
+        const float f = exp2_approx(mw[w] - base);
+        const float4 v = *reinterpret_cast<const float4*>(q + T::HEADS + h * T::OPITCH + d);
+        sum += f * q[h];
+        a.x += f * v.x;
+        a.y += f * v.y;
+        a.z += f * v.z;
+        a.w += f * v.w;
+      }
+      if (whole) {
+        write_out<T>(p, seg.b, sh0 + h, d, D, a, top, sum, vs);
+      } else {
+        if (d == 0) {
+          part[h] = top;
+          part[T::HEADS + h] = sum;
+        }
+        *reinterpret_cast<float4*>(part + 2 * T::HEADS + h * D + d) = a;
+      }
+    }
+    __syncthreads();          // the partial is written, and `meet` is free again
+    if (!whole) {
+      // Blocks c0 .. c0 + n - 1 share this segment. Thread 0 says that this block's partial is there; who
+      // joins them is looked up when the block has nothing else to do.
+      if (tid == 0) {
+        const int c0 = static_cast<int>(divide(first, share));
+        const Shared s{c0, static_cast<int>(divide(first + seg.tiles - 1, share)) - c0 + 1, seg.b, sh0, sheads, vs};
+        s_pend[second] = s;
+        s_last[second] = arrive(p.counters, s);
+      }
+    }
   }
   cp_async_wait<0>();
+  fence_proxy_async_smem();            // joins copy to the ring by the async proxy
+  __syncthreads();
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e)
+    if (s_pend[e].n > 0 && s_last[e]) finish<T, D>(p, s_pend[e], smem, meet, s_last + e, smem_u32(&s_bar), phase);
 }
 
 template <int CACHE, int D, int NT>
@@ -692,8 +892,8 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
     __atomic_store_n(&per_sm[dev], n, __ATOMIC_RELAXED);
   }
   const long long keys = p.window > 0 && p.window < p.max_len ? p.window : p.max_len;
-  const long long most = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv *
-                         ((keys + T::TILE - 1) / T::TILE > 0 ? (keys + T::TILE - 1) / T::TILE : 1);
+  // most places that the list can have; a window's tiles may begin up to 15 keys before it
+  const long long most = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv * ((keys + 15 + T::TILE - 1) / T::TILE + 1);
   long long grid = static_cast<long long>(sms) * n;
   if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
   if (grid > most) grid = most;
