@@ -440,7 +440,7 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
  * projections of a step:
  *   ids     int32 [M]; one of n_adapters or above records TL_EDATA and counts as none
  *   plan    device memory of tl_lora_plan_size(M, n_adapters) bytes, opaque
- * M and n_adapters are at most 2^20 and 8192 (more: TL_EUNSUPPORTED).
+ * M and n_adapters are at most 2^20 and 4096 (more: TL_EUNSUPPORTED).
  *
  * tl_lora_apply:
  *   x       [M, K], dtype TL_BF16 or TL_F16, ldx elements from token to token
@@ -450,8 +450,6 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
  *           device: TL_EDATA, and nothing is written)
  *   base    [M, N] of y_dtype (TL_BF16, TL_F16 or TL_F32), ldb elements from token to token
  *   y       [M, N] likewise; may be base (in place, ldy = ldb), must not overlap it otherwise
- *   workspace  tl_lora_workspace_size(M, rank) bytes, needs no clearing. Calls
- *           that can overlap on the GPU must not share one.
  * The products are exact and summed in fp32; A[a] x[m] is kept in fp32 and enters the second product
  * as the sum of two or three 16-bit numbers, so that it counts with 16 (bf16), 22
  * (fp16) or, for an fp32 y, 24 bits; base + delta is rounded once to y_dtype. For given
@@ -462,11 +460,9 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
 int tl_lora_plan_size(int M, int n_adapters, size_t* bytes);
 int tl_lora_plan(const int32_t* ids, int M, int n_adapters, void* plan, size_t plan_bytes,
                  void* stream);
-int tl_lora_workspace_size(int M, int rank, size_t* bytes);
 int tl_lora_apply(const void* x, int64_t ldx, const void* A, const void* B, const float* scale,
                   int dtype, int n_adapters, int rank, const void* plan, int M, int N, int K,
-                  const void* base, int64_t ldb, void* y, int64_t ldy, int y_dtype,
-                  void* workspace, size_t ws_bytes, void* stream);
+                  const void* base, int64_t ldb, void* y, int64_t ldy, int y_dtype, void* stream);
 
 /*
  * Diagnostic: launches one kernel whose bounded wait can never be satisfied (an

@@ -10,13 +10,14 @@ namespace tl {
 
 constexpr int kLoraTile = 32;           // most tokens of one item
 constexpr int kLoraMaxM = 1 << 20;
-constexpr int kLoraMaxAdapters = 8192;
+constexpr int kLoraMaxAdapters = 4096;
 constexpr int kLoraMaxRank = 128;
 
-// A plan: a header, the items (tokens of one adapter, at most kLoraTile of them), and
-// the tokens sorted by adapter, in their own order within one; those without an adapter last.
+// A plan: a header and the items, each up to kLoraTile tokens of one adapter (or of none), adapter by
+// adapter, the tokens of one in their own order.
 struct LoraItem {
-  int adapter, start, count, unused;    // adapter -1: none; start in the sorted order
+  int adapter, count, unused[2];        // adapter -1: none
+  int token[kLoraTile];
 };
 struct LoraPlanHeader {
   int M, n_adapters, items, unused;
@@ -25,10 +26,10 @@ struct LoraPlanHeader {
 // most items that M tokens of n_adapters adapters (and none) can need
 inline int lora_max_items(int M, int n_adapters) {
   const int bins = n_adapters + 1 < M ? n_adapters + 1 : M;
-  return (M + kLoraTile - 1) / kLoraTile + bins;
+  return (M - bins) / kLoraTile + bins;
 }
 inline size_t lora_plan_bytes(int M, int n_adapters) {
-  return sizeof(LoraPlanHeader) + sizeof(LoraItem) * lora_max_items(M, n_adapters) + sizeof(int) * static_cast<size_t>(M);
+  return sizeof(LoraPlanHeader) + sizeof(LoraItem) * static_cast<size_t>(lora_max_items(M, n_adapters));
 }
 
 struct LoraParams {
@@ -38,8 +39,6 @@ struct LoraParams {
   const float* scale;
   const LoraPlanHeader* plan;
   const LoraItem* items;
-  const int* order;
-  float* h;                 // [M, rank], tokens in sorted order
   const void* base;
   void* y;
   int64_t ldx, ldb, ldy;

@@ -452,33 +452,23 @@ int tl_lora_plan(const int32_t* ids, int M, int n_adapters, void* plan, size_t p
   return tl::launch_lora_plan(ids, M, n_adapters, plan, status, as_stream(stream)) == cudaSuccess ? TL_OK : TL_ECUDA;
 }
 
-int tl_lora_workspace_size(int M, int rank, size_t* bytes) {
-  if (bytes == nullptr || M < 0 || rank <= 0) return TL_EINVAL;
-  if (M > tl::kLoraMaxM || rank > tl::kLoraMaxRank || rank % 8 != 0) return TL_EUNSUPPORTED;
-  *bytes = static_cast<size_t>(M) * rank * sizeof(float);
-  return TL_OK;
-}
-
 int tl_lora_apply(const void* x, int64_t ldx, const void* A, const void* B, const float* scale,
                   int dtype, int n_adapters, int rank, const void* plan, int M, int N, int K,
-                  const void* base, int64_t ldb, void* y, int64_t ldy, int y_dtype,
-                  void* workspace, size_t ws_bytes, void* stream) {
-  if (n_adapters < 0 || N < 0 || K <= 0) return TL_EINVAL;
+                  const void* base, int64_t ldb, void* y, int64_t ldy, int y_dtype, void* stream) {
+  if (n_adapters < 0 || M < 0 || N < 0 || K <= 0 || rank <= 0) return TL_EINVAL;
   if (dtype != TL_BF16 && dtype != TL_F16) return TL_EINVAL;
   if (y_dtype != TL_BF16 && y_dtype != TL_F16 && y_dtype != TL_F32) return TL_EINVAL;
-  size_t need = 0;
-  int r = tl_lora_workspace_size(M, rank, &need);
-  if (r != TL_OK) return r;
+  if (M > tl::kLoraMaxM || rank > tl::kLoraMaxRank || rank % 8 != 0) return TL_EUNSUPPORTED;
   if (n_adapters > tl::kLoraMaxAdapters || N % 8 != 0 || K % 8 != 0 || N > (1 << 22)) return TL_EUNSUPPORTED;
   if (M == 0 || N == 0) return TL_OK;
-  if (!x || !plan || !base || !y || !workspace || (n_adapters > 0 && (!A || !B || !scale))) return TL_EINVAL;
+  if (!x || !plan || !base || !y || (n_adapters > 0 && (!A || !B || !scale))) return TL_EINVAL;
   if (!aligned16(x) || !aligned16(A) || !aligned16(B) || !aligned4(scale) || !aligned16(plan) || !aligned16(base) ||
-      !aligned16(y) || !aligned16(workspace))
+      !aligned16(y))
     return TL_EINVAL;
+  int r;
   if ((r = check_rows(ldx, K, M, 8)) != TL_OK || (r = check_rows(ldb, N, M, 8)) != TL_OK || (r = check_rows(ldy, N, M, 8)) != TL_OK)
     return r;
   if (base == y && M > 1 && ldb != ldy) return TL_EINVAL;
-  if (ws_bytes < need) return TL_ENOSPACE;
   int sms = 0;
   int* status = nullptr;
   if ((r = num_sms(&sms)) != TL_OK || (r = status_ptr(&status)) != TL_OK) return r;
@@ -487,8 +477,6 @@ int tl_lora_apply(const void* x, int64_t ldx, const void* A, const void* B, cons
   p.scale = scale;
   p.plan = static_cast<const tl::LoraPlanHeader*>(plan);
   p.items = reinterpret_cast<const tl::LoraItem*>(p.plan + 1);
-  p.order = reinterpret_cast<const int*>(p.items + tl::lora_max_items(M, n_adapters));
-  p.h = static_cast<float*>(workspace);
   p.base = base, p.y = y, p.ldx = ldx, p.ldb = ldb, p.ldy = ldy;
   p.M = M, p.N = N, p.K = K, p.rank = rank, p.n_adapters = n_adapters, p.y_dtype = y_dtype;
   p.copy_bare = base != y;

@@ -61,8 +61,7 @@ SIGNATURES = {
     "tl_paged_attention": (_I, [_PKV, _P, _I, _I, _I, _L, _P, _I, _L, _P, _F, _I, _P, _L, _P, _P, _SZ, _P]),
     "tl_lora_plan_size": (_I, [_I, _I, _PSZ]),
     "tl_lora_plan": (_I, [_P, _I, _I, _P, _SZ, _P]),
-    "tl_lora_workspace_size": (_I, [_I, _I, _PSZ]),
-    "tl_lora_apply": (_I, [_P, _L, _P, _P, _P, _I, _I, _I, _P, _I, _I, _I, _P, _L, _P, _L, _I, _P, _SZ, _P]),
+    "tl_lora_apply": (_I, [_P, _L, _P, _P, _P, _I, _I, _I, _P, _I, _I, _I, _P, _L, _P, _L, _I, _P]),
     "tl_selftest_wait_timeout": (_I, [ctypes.c_uint, _P]),
     "tl_get_status": (_I, [_P]),
 }
@@ -507,12 +506,6 @@ def tl_lora_plan_size(M: int, n_adapters: int) -> int:
     return b.value
 
 
-def tl_lora_workspace_size(M: int, rank: int) -> int:
-    b = ctypes.c_size_t()
-    _check(lib().tl_lora_workspace_size(M, rank, ctypes.byref(b)), "tl_lora_workspace_size")
-    return b.value
-
-
 class LoraPlan:
     """A batch's tokens sorted by adapter (tl_lora_plan): made once, used by every projection of the step."""
 
@@ -542,10 +535,6 @@ class LoraBank:
     A [n_adapters, rank, K] and B [n_adapters, N, rank], bf16 or fp16, on the
     device; scale fp32 [n_adapters] (ones when not given). apply() adds
     scale[a] B[a] (A[a] x) to each token's output, a being the token's adapter.
-
-    The bank keeps one workspace: apply() calls on one bank that can run at the same time on
-    different streams must be ordered by the caller, or use one LoraBank over the
-    same A and B for each stream. It grows with the largest batch (allocated in apply()).
     """
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor | None = None):
@@ -565,7 +554,6 @@ class LoraBank:
         self.N = B.shape[1]
         self.dtype = A.dtype
         self._fixed = (A.data_ptr(), B.data_ptr(), scale.data_ptr(), _HALF[A.dtype], self.n_adapters, self.rank)
-        self._ws = torch.empty((max(1, tl_lora_workspace_size(64, self.rank)),), dtype=torch.uint8, device=A.device)
 
     def plan(self, ids: torch.Tensor, plan: LoraPlan | None = None, stream=None) -> LoraPlan:
         """Sort a batch's tokens by adapter; the plan serves every bank of as many adapters."""
@@ -591,11 +579,8 @@ def tl_lora_apply(bank: LoraBank, x: torch.Tensor, base: torch.Tensor, plan: Lor
     if out is None:
         out = torch.empty((M, bank.N), dtype=dt, device=base.device)
     ldo = _matrix(out, M, bank.N, dt, "out")
-    ws = bank._ws
-    if ws.numel() < 4 * M * bank.rank:
-        ws = bank._ws = torch.empty((tl_lora_workspace_size(M, bank.rank),), dtype=torch.uint8, device=bank.A.device)
     r = lib().tl_lora_apply(x.data_ptr(), ldx, *bank._fixed, plan.data.data_ptr(), M, bank.N, bank.K, base.data_ptr(), ldb,
-                            out.data_ptr(), ldo, code, ws.data_ptr(), ws.numel(), _stream(stream))
+                            out.data_ptr(), ldo, code, _stream(stream))
     if r != TL_OK:
         _check(r, "tl_lora_apply")
     return out

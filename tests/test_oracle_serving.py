@@ -175,10 +175,10 @@ def test_lora_refusals(lib):
     ok = 4096
 
     def call(x=ok, ldx=64, A=ok, B=ok, scale=ok, dtype=tl.TL_BF16, n=2, rank=16, plan=ok, M=3, N=128, K=64, base=ok, ldb=128, y=8192, ldy=128,
-             yd=tl.TL_BF16, ws=ok, wsb=10 ** 6):
-        return lib.tl_lora_apply(x, ldx, A, B, scale, dtype, n, rank, plan, M, N, K, base, ldb, y, ldy, yd, ws, wsb, None)
+             yd=tl.TL_BF16):
+        return lib.tl_lora_apply(x, ldx, A, B, scale, dtype, n, rank, plan, M, N, K, base, ldb, y, ldy, yd, None)
 
-    for name in ("x", "A", "B", "scale", "plan", "base", "y", "ws"):
+    for name in ("x", "A", "B", "scale", "plan", "base", "y"):
         assert call(**{name: None}) == tl.TL_EINVAL, name
         assert call(**{name: 4098}) == tl.TL_EINVAL, name
     assert call(dtype=tl.TL_F32) == tl.TL_EINVAL
@@ -189,12 +189,11 @@ def test_lora_refusals(lib):
                  dict(N=(1 << 22) + 8)):
         assert call(**over) == tl.TL_EUNSUPPORTED, over
     assert call(y=ok, ldy=136) == tl.TL_EINVAL               # in place, but the rows lie elsewhere
-    assert call(wsb=100) == tl.TL_ENOSPACE
-    assert call(M=0, x=None, base=None, y=None, ws=None, plan=None) == tl.TL_OK
-    assert call(N=0, x=None, base=None, y=None, ws=None, plan=None) == tl.TL_OK
+    assert call(M=0, x=None, base=None, y=None, plan=None) == tl.TL_OK
+    assert call(N=0, x=None, base=None, y=None, plan=None) == tl.TL_OK
     sz = ctypes.c_size_t()
-    assert lib.tl_lora_plan_size(33, 4, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 16 * (2 + 5) + 4 * 33
-    assert lib.tl_lora_plan_size(2, 400, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 16 * (1 + 2) + 4 * 2
+    assert lib.tl_lora_plan_size(33, 4, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 144 * (5 + 0)
+    assert lib.tl_lora_plan_size(2, 400, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 144 * 2
     assert lib.tl_lora_plan(None, 2, 4, ok, 10 ** 6, None) == tl.TL_EINVAL
     assert lib.tl_lora_plan(ok, 2, 4, ok, 10, None) == tl.TL_ENOSPACE
     assert lib.tl_lora_plan(ok, 2, 9000, ok, 10 ** 9, None) == tl.TL_EUNSUPPORTED
