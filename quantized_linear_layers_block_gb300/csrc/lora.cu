@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kLoraWarps = 8;
+constexpr int kLoraMaxCluster = 8;
 
 // ----------------------------------------------------------------- plan
 // Shared memory: for each adapter, and for the tokens without one, a counter and its first item.
@@ -122,21 +123,23 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// base + delta, two 16-bit values
+// base + up d of two 16-bit values; `up` is a power of two, so the fused product is exact
 template <int YD>
-__device__ __forceinline__ uint32_t add2(uint32_t base, float lo, float hi) {
+__device__ __forceinline__ uint32_t add2(uint32_t base, float lo, float hi, float up) {
   uint32_t r;
   if constexpr (YD == TL_BF16) {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(base & 0xFFFF0000u) + hi), "f"(__uint_as_float(base << 16) + lo));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+        : "=r"(r)
+        : "f"(__fmaf_rn(hi, up, __uint_as_float(base & 0xFFFF0000u))), "f"(__fmaf_rn(lo, up, __uint_as_float(base << 16))));
   } else {
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&base));
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b.y + hi), "f"(b.x + lo));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__fmaf_rn(hi, up, b.y)), "f"(__fmaf_rn(lo, up, b.x)));
   }
   return r;
 }
 
 // ----------------------------------------------------------------- the operator
-// Shared memory, in bytes: h's sums [32][RP] in fp32, RP = the rank rounded up to RT 16-row tiles (and to 32); then
+// Shared memory, in bytes: h's sums [32][RP] in fp32, RP = the rank rounded up to 16 (RT = 1) or a multiple of 32; then
 // the warps' sums of one RT [warps][32][16 RT + 4], and in the same place afterwards the parts of h [PARTS][32][136].
 template <bool BF16, int YD, int RT>
 struct Lora {
@@ -145,7 +148,9 @@ struct Lora {
   static constexpr int ROWS = 16 * RT, RPITCH = ROWS + 4, PITCH = kLoraMaxRank + 8;
   static constexpr int RED = kLoraWarps * kLoraTile * RPITCH * 4, HS = PARTS * kLoraTile * PITCH * 2;
   static int smem(int rank) { return kLoraTile * padded(rank) * 4 + (RED > HS ? RED : HS); }
-  __host__ __device__ static int padded(int rank) { return (rank + 31) / 32 * 32; }
+  // the K of the second product: one MMA for ranks up to 16, else pairs of them
+  static constexpr int KSTEP = RT == 1 ? 16 : 32;
+  __host__ __device__ static int padded(int rank) { return (rank + KSTEP - 1) / KSTEP * KSTEP; }
 };
 
 // blockIdx.x = (item * NS + part of the columns) * CS + rank of the block in its cluster
@@ -178,32 +183,52 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   for (int n = 0; n < NT; ++n)
     if (8 * n + g >= count) tok[n] = -1;
 
-  // ---- this warp's columns: groups of 32, g0 + warp, g0 + warp + 8, ... below g1
+  // ---- this warp's columns: groups of 32, col, col + 8, ... below g1. The pointers run ahead of the products.
   const int groups = (p.N + 31) / 32, share = part * CS + me, shares = NS * CS;
   const int g1 = static_cast<int>(static_cast<long long>(groups) * (share + 1) / shares);
   int col = static_cast<int>(static_cast<long long>(groups) * share / shares) + warp;
-  auto load_base = [&](int c, uint4 (&b)[4][V]) {
-    const int n = 32 * c + 8 * t;
+  constexpr int YB = V == 2 ? 4 : 2, STEP = kLoraWarps * 32;
+  int n = 32 * col + 8 * t;                      // this thread's first column of the group asked for next
+  const int n_end = min(32 * g1, p.N);
+  const char* bp[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bp[i] = static_cast<const char*>(p.base) + (tok[i] * p.ldb + n) * YB;
+  // rows of B: columns permuted so that tile j's column c is column 8 (c / 2) + 2 j + c % 2 of the group
+  constexpr int KV = RT == 1 ? 4 : 8;            // elements of a row that a thread takes
+  const int nb0 = 8 * (g >> 1) + (g & 1) - 8 * t;
+  const uint16_t* wp = p.B + (static_cast<int64_t>(adapter) * p.N + n + nb0) * p.rank + KV * t;
+  auto load_base = [&](uint4 (&b)[4][V]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (c < g1 && n < p.N && tok[i] >= 0) {
-        const char* src = static_cast<const char*>(p.base) + (tok[i] * p.ldb + n) * (V == 2 ? 4 : 2);
+      if (n < n_end && tok[i] >= 0) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) b[i][e] = reinterpret_cast<const uint4*>(src)[e];
+        for (int e = 0; e < V; ++e) b[i][e] = reinterpret_cast<const uint4*>(bp[i])[e];
       }
     }
   };
-  auto load_b = [&](int c, int s, uint4 (&b)[4]) {
+  auto load_b = [&](int s, uint4 (&b)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = 32 * c + 8 * (g >> 1) + 2 * j + (g & 1);
-      b[j] = c < g1 && n < p.N && 32 * s + 8 * t < p.rank
-                 ? __ldg(reinterpret_cast<const uint4*>(p.B + (static_cast<int64_t>(adapter) * p.N + n) * p.rank + 32 * s + 8 * t))
-                 : make_uint4(0, 0, 0, 0);
+      b[j] = make_uint4(0, 0, 0, 0);
+      if (n + nb0 + 2 * j < n_end && 32 * s + KV * t < p.rank) {
+        const uint16_t* src = wp + 2 * j * p.rank + 32 * s;
+        if constexpr (RT == 1) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+          b[j].x = w.x, b[j].y = w.y;
+        } else {
+          b[j] = __ldg(reinterpret_cast<const uint4*>(src));
+        }
+      }
     }
   };
+  auto advance = [&]() {
+    n += STEP;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bp[i] += STEP * YB;
+    wp += static_cast<int64_t>(STEP) * p.rank;
+  };
 
-  const int steps = adapter < 0 ? 0 : RP / 32;
+  const int steps = adapter < 0 ? 0 : RP / L::KSTEP;
   uint4 base[4][V], bw[4];
   float up[4] = {};
   if (steps > 0) {
@@ -269,8 +294,8 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       }
     }
     // the first columns' operands arrive while the blocks meet
-    load_base(col, base);
-    load_b(col, 0, bw);
+    load_base(base);
+    load_b(0, bw);
     if (CS > 1) {
       cluster_arrive();
       cluster_wait();
@@ -281,13 +306,14 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     // Lane l has elements 4l .. 4l + 3 of the rank.
     const float sc = __ldg(p.scale + adapter);
     const uint32_t sums = smem_u32(sum);
-    for (int m = warp; m < kLoraTile; m += kLoraWarps) {
+    for (int m = warp; m < count; m += kLoraWarps) {       // rows past the last token may hold anything: they reach no other row
       float v[4] = {};
-      if (m < count && 4 * lane < p.rank) {
-        for (int q = 0; q < CS; ++q) {
-          const float4 f = CS > 1 ? ld_cluster4(sums + (m * RP + 4 * lane) * 4, q) : *reinterpret_cast<const float4*>(sum + m * RP + 4 * lane);
-          v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-        }
+      if (4 * lane < p.rank) {
+        float4 f[kLoraMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kLoraMaxCluster; ++q) f[q] = q < CS ? ld_cluster4(sums + (m * RP + 4 * lane) * 4, q) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < kLoraMaxCluster; ++q) v[0] += f[q].x, v[1] += f[q].y, v[2] += f[q].z, v[3] += f[q].w;
       }
       float top = 0.f;
 #pragma unroll
@@ -300,8 +326,9 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       const int e2 = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
       if (lane == 0) s_up[m] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-      // element 8q + j of 32 (thread q of the quad loads it): MMA j / 4, column 2q + (j & 1) + 8 ((j & 2) / 2)
-      const int q = lane >> 1 & 3, at = 32 * (lane >> 3) + 16 * (lane & 1) + 2 * q;
+      // element 8q + j of 32 (thread q of the quad loads it): MMA j / 4, column 2q + (j & 1) + 8 ((j & 2) / 2);
+      // of 16, for one MMA, element 4q + j
+      const int at = RT == 1 ? 2 * lane : 32 * (lane >> 3) + 16 * (lane & 1) + 2 * (lane >> 1 & 3);
       if (4 * lane < RP) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] *= down;
@@ -324,7 +351,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
             v[2 * e + 1] = isinf(v[2 * e + 1]) ? 0.f : v[2 * e + 1] - hi;
           }
           uint32_t* const dst = reinterpret_cast<uint32_t*>(hs + (h * kLoraTile + m) * PITCH + at);
-          dst[0] = w[0];           // elements j & 2 = 0: columns 2q, 2q + 1
+          dst[0] = w[0];           // j & 2 = 0: columns 2q, 2q + 1
           dst[4] = w[1];           // j & 2 = 2: columns 8 + 2q, 9 + 2q
         }
       }
@@ -334,18 +361,23 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < 4; ++i) up[i] = s_up[8 * i + g];
   } else {
-    load_base(col, base);
+    load_base(base);
   }
 
   // ---- y = base + B h
+  char* yp[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + n) * YB;
   const int mts = count > 16 ? 2 : 1;
   const uint32_t hbase = smem_u32(hs) + ((lane & 15) * PITCH + (lane >> 4) * 8) * 2;
-  for (; col < g1; col += kLoraWarps) {
+  while (col < g1) {
+    const bool live = n < n_end;
     // the next columns' operands: ahead of this one's products where there are registers for them
     uint4 nbase[4][V], nbw[4];
     if constexpr (V == 1) {
-      load_base(col + kLoraWarps, nbase);
-      if (steps > 0) load_b(col + kLoraWarps, 0, nbw);
+      advance();
+      load_base(nbase);
+      if (steps > 0) load_b(0, nbw);
     }
     float acc[2][4][4];
 #pragma unroll
@@ -353,14 +385,24 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
     for (int s = 0; s < steps; ++s) {
-      if (s > 0) load_b(col, s, bw);
+      if (s > 0) {
+        if constexpr (V == 1) {                  // the pointers are a group ahead
+          n -= STEP;
+          wp -= static_cast<int64_t>(STEP) * p.rank;
+        }
+        load_b(s, bw);
+        if constexpr (V == 1) {
+          n += STEP;
+          wp += static_cast<int64_t>(STEP) * p.rank;
+        }
+      }
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (m < mts) {
 #pragma unroll
           for (int h = 0; h < L::PARTS; ++h) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < L::KSTEP / 16; ++half) {
               uint32_t a[4];
               asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                            : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
@@ -374,35 +416,34 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         }
       }
     }
-    // token 8i + g: columns 32 col + 8t + 2j + {0, 1} are elements 2 (i & 1) + {0, 1} of acc[i / 2][j]
-    const int n = 32 * col + 8 * t;
+    // token 8i + g: columns 8t + 2j + {0, 1} of the group are elements 2 (i & 1) + {0, 1} of acc[i / 2][j]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (n < p.N && tok[i] >= 0) {
-        float d[8];
+      if (live && tok[i] >= 0) {
+        uint4 r[V];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          d[2 * j] = acc[i >> 1][j][2 * (i & 1)] * up[i];
-          d[2 * j + 1] = acc[i >> 1][j][2 * (i & 1) + 1] * up[i];
-        }
-        char* dst = static_cast<char*>(p.y) + (tok[i] * p.ldy + n) * (V == 2 ? 4 : 2);
-        uint32_t w[4 * V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          w[4 * e] = base[i][e].x, w[4 * e + 1] = base[i][e].y, w[4 * e + 2] = base[i][e].z, w[4 * e + 3] = base[i][e].w;
-        }
+        for (int e = 0; e < V; ++e) r[e] = base[i][e];
         if (steps > 0) {
-          if constexpr (V == 2) {
+          uint32_t w[4 * V];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) + d[e]);
-          } else {
+          for (int e = 0; e < V; ++e) w[4 * e] = r[e].x, w[4 * e + 1] = r[e].y, w[4 * e + 2] = r[e].z, w[4 * e + 3] = r[e].w;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = add2<YD>(w[e], d[2 * e], d[2 * e + 1]);
+          for (int j = 0; j < 4; ++j) {
+            const float lo = acc[i >> 1][j][2 * (i & 1)], hi = acc[i >> 1][j][2 * (i & 1) + 1];
+            if constexpr (V == 2) {
+              w[2 * j] = __float_as_uint(__fmaf_rn(lo, up[i], __uint_as_float(w[2 * j])));
+              w[2 * j + 1] = __float_as_uint(__fmaf_rn(hi, up[i], __uint_as_float(w[2 * j + 1])));
+            } else {
+              w[j] = add2<YD>(w[j], lo, hi, up[i]);
+            }
           }
+#pragma unroll
+          for (int e = 0; e < V; ++e) r[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        for (int e = 0; e < V; ++e) reinterpret_cast<uint4*>(yp[i])[e] = r[e];
       }
+      yp[i] += STEP * YB;
     }
     if constexpr (V == 1) {
 #pragma unroll
@@ -411,9 +452,11 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         bw[i] = nbw[i];
       }
     } else {
-      load_base(col + kLoraWarps, base);
-      if (steps > 0) load_b(col + kLoraWarps, 0, bw);
+      advance();
+      load_base(base);
+      if (steps > 0) load_b(0, bw);
     }
+    col += kLoraWarps;
   }
   if (steps > 0 && CS > 1) cluster_wait();       // no block leaves while another reads its sums
 }
@@ -431,10 +474,11 @@ cudaError_t apply(const LoraParams& p, int sms, cudaStream_t st) {
     __atomic_store_n(&ready[dev], 1, __ATOMIC_RELAXED);
   }
   const long long items = lora_max_items(p.M, p.n_adapters);
-  // a cluster as large as leaves every warp a piece of K; as many clusters per item as fill the GPU once and
-  // leave every warp columns
-  int cs = 8, ns = 1;
-  while (cs > 1 && (p.K + 31) / 32 < cs * kLoraWarps) cs /= 2;
+  // A cluster as large as leaves every warp a piece of K and all blocks room on the GPU at once (what a block does besides
+  // its columns is worth less the more columns it has); as many clusters per item as fill the GPU once and
+  // leave every warp columns.
+  int cs = kLoraMaxCluster, ns = 1;
+  while (cs > 1 && ((p.K + 31) / 32 < cs * kLoraWarps || items * cs > 2LL * sms)) cs /= 2;
   while (items * cs * ns * 2 <= 2LL * sms && (p.N + 31) / 32 >= 2 * ns * cs * kLoraWarps) ns *= 2;
   return launch_pdl_cluster(lora_kernel<BF16, YD, RT>, dim3(static_cast<unsigned>(items * ns * cs)), dim3(kLoraWarps * 32),
                             L::smem(p.rank), st, cs, p, cs, ns);
