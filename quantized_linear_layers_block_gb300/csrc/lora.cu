@@ -110,6 +110,19 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
   uint32_t remote;
   float4 v;
@@ -139,33 +152,50 @@ __device__ __forceinline__ uint32_t add2(uint32_t base, float lo, float hi, floa
 }
 
 // ----------------------------------------------------------------- the operator
-// Shared memory, in bytes: h's sums [32][RP] in fp32, RP = the rank rounded up to 16 (RT = 1) or a multiple of 32; then
-// the warps' sums of one RT [warps][32][16 RT + 4], and in the same place afterwards the parts of h [PARTS][32][136].
+// Both products stream their operands through rings of cp.async slots in shared memory, each written and
+// read by one thread only, so that no barrier is needed; registers could not hold enough bytes in flight.
+// Shared memory: the first product's ring [RS][slots][threads], then in its place
+// the warps' sums of one RT, then the ring of base [YS][4 V][threads]. Behind that h's sums [32][RP] in fp32, RP
+// the rank rounded up to 16 (RT = 1) or a multiple of 32, and the parts of h [PARTS][32][RP + 8].
 template <bool BF16, int YD, int RT>
 struct Lora {
   static constexpr int PARTS = YD == TL_F32 && BF16 ? 3 : 2;
   static constexpr int V = YD == TL_F32 ? 2 : 1;                // 16-byte vectors of 8 columns
-  static constexpr int ROWS = 16 * RT, RPITCH = ROWS + 4, PITCH = kLoraMaxRank + 8;
-  static constexpr int RED = kLoraWarps * kLoraTile * RPITCH * 4, HS = PARTS * kLoraTile * PITCH * 2;
-  static int smem(int rank) { return kLoraTile * padded(rank) * 4 + (RED > HS ? RED : HS); }
+  static constexpr int ROWS = 16 * RT, RPITCH = ROWS + 4;
+  static constexpr int THREADS = kLoraWarps * 32, VEC = THREADS * 16;
+  static constexpr int SLOTS = 2 * RT + kLoraTile / 8, RS = RT == 4 ? 2 : RT == 2 ? 3 : 4, RING = RS * SLOTS * VEC;
+  static constexpr int YS = V == 1 ? 4 : 2, YRING = YS * 4 * V * VEC;
+  static constexpr int RED = kLoraWarps / 2 * kLoraTile * RPITCH * 4;
+  static_assert(RED <= YRING && YRING <= RING, "layout");
   // the K of the second product: one MMA for ranks up to 16, else pairs of them
   static constexpr int KSTEP = RT == 1 ? 16 : 32;
   __host__ __device__ static int padded(int rank) { return (rank + KSTEP - 1) / KSTEP * KSTEP; }
+  // one pass of the first product (rank <= 16 RT): its ring is free when the sums are written
+  __host__ __device__ static int sum_at(int rank) { return rank <= ROWS ? YRING : RING; }
+  __host__ __device__ static int hs_at(int rank) { return rank <= ROWS ? YRING + kLoraTile * padded(rank) * 4 : YRING; }
+  static int smem(int rank) {
+    const int sum = sum_at(rank) + kLoraTile * padded(rank) * 4, hs = hs_at(rank) + PARTS * kLoraTile * (padded(rank) + 8) * 2;
+    const int most = sum > hs ? sum : hs;
+    // rank > ROWS: hs lies before the sums, in what was the first ring
+    return most > RING ? most : RING;
+  }
 };
 
 // blockIdx.x = (item * NS + part of the columns) * CS + rank of the block in its cluster
 template <bool BF16, int YD, int RT>
 __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_constant__ LoraParams p, int CS, int NS) {
   using L = Lora<BF16, YD, RT>;
-  constexpr int NT = kLoraTile / 8, V = L::V, ROWS = L::ROWS, PITCH = L::PITCH;
+  constexpr int NT = kLoraTile / 8, V = L::V, ROWS = L::ROWS;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float s_up[kLoraTile];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int me = blockIdx.x % CS, part = blockIdx.x / CS % NS, idx = blockIdx.x / CS / NS;
   const int RP = L::padded(p.rank);
-  float* const sum = reinterpret_cast<float*>(smem);
-  float* const red = sum + kLoraTile * RP;
-  uint16_t* const hs = reinterpret_cast<uint16_t*>(red);
+  const int PITCH = RP + 8;
+  float* const sum = reinterpret_cast<float*>(smem + L::sum_at(p.rank));
+  float* const red = reinterpret_cast<float*>(smem);
+  uint16_t* const hs = reinterpret_cast<uint16_t*>(smem + L::hs_at(p.rank));
+  const uint32_t slot0 = smem_u32(smem) + tid * 16;
   pdl_wait_prior();
   pdl_launch_dependents();
   const LoraPlanHeader head = *p.plan;
@@ -195,22 +225,28 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   for (int i = 0; i < 4; ++i) bp[i] = static_cast<const char*>(p.base) + (tok[i] * p.ldb + n) * YB;
   // rows of B: columns permuted so that tile j's column c is column 8 (c / 2) + 2 j + c % 2 of the group
   constexpr int KV = RT == 1 ? 4 : 8;            // elements of a row that a thread takes
-  const int nb0 = 8 * (g >> 1) + (g & 1) - 8 * t;
-  const uint16_t* wp = p.B + (static_cast<int64_t>(adapter) * p.N + n + nb0) * p.rank + KV * t;
-  auto load_base = [&](uint4 (&b)[4][V]) {
+  int nb = 32 * col + 8 * (g >> 1) + (g & 1);                              // its row in tile 0 of the group that wp points to
+  const uint16_t* wp = p.B + (static_cast<int64_t>(adapter) * p.N + nb) * p.rank + KV * t;
+  int asked = 0;                                 // groups of base asked for
+  auto ask_base = [&]() {
+    const uint32_t dst = slot0 + asked % L::YS * (4 * V * L::VEC);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (n < n_end && tok[i] >= 0) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) b[i][e] = reinterpret_cast<const uint4*>(bp[i])[e];
+        for (int e = 0; e < V; ++e) cp_async16(dst + (i * V + e) * L::VEC, bp[i] + 16 * e, 16);
       }
+      bp[i] += STEP * YB;
     }
+    n += STEP;
+    ++asked;
+    cp_async_commit();
   };
   auto load_b = [&](int s, uint4 (&b)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       b[j] = make_uint4(0, 0, 0, 0);
-      if (n + nb0 + 2 * j < n_end && 32 * s + KV * t < p.rank) {
+      if (nb + 2 * j < n_end && 32 * s + KV * t < p.rank) {
         const uint16_t* src = wp + 2 * j * p.rank + 32 * s;
         if constexpr (RT == 1) {
           const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
@@ -221,15 +257,8 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       }
     }
   };
-  auto advance = [&]() {
-    n += STEP;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bp[i] += STEP * YB;
-    wp += static_cast<int64_t>(STEP) * p.rank;
-  };
-
   const int steps = adapter < 0 ? 0 : RP / L::KSTEP;
-  uint4 base[4][V], bw[4];
+  uint4 bw[4];
   float up[4] = {};
   if (steps > 0) {
     // ---- h = A x
@@ -240,7 +269,6 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
 #pragma unroll
     for (int n = 0; n < NT; ++n) xr[n] = p.x + (tok[n] >= 0 ? tok[n] * p.ldx : 0) + 8 * t;
     const int nts = (count + 7) / 8;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
     for (int r0 = 0; r0 < p.rank; r0 += ROWS) {
       const uint16_t* const ar = p.A + (static_cast<int64_t>(adapter) * p.rank + r0 + g) * p.K + 8 * t;
       float acc[RT][NT][4];
@@ -248,60 +276,87 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
-#pragma unroll(RT == 4 ? 1 : 2)
+      auto ask = [&](int c) {
+        if (c < c1) {
+          const int k = 32 * c;
+          const bool in = k + 8 * t < p.K;
+          const uint32_t dst = slot0 + (c - c0) % L::RS * (L::SLOTS * L::VEC);
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool row = in && r0 + 16 * i + 8 * e + g < p.rank;
+              cp_async16(dst + (2 * i + e) * L::VEC, row ? ar + static_cast<int64_t>(16 * i + 8 * e) * p.K + k : p.A, row ? 16 : 0);
+            }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const bool row = in && tok[n] >= 0;
+            if (n < nts) cp_async16(dst + (2 * RT + n) * L::VEC, row ? xr[n] + k : p.x, row ? 16 : 0);
+          }
+        }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int c = 0; c < L::RS - 1; ++c) ask(c0 + c);
       for (int c = c0; c < c1; ++c) {
-        const int k = 32 * c;
-        const bool in = k + 8 * t < p.K;
-        uint4 a[RT][2], b[NT];
+        cp_async_wait<L::RS - 2>();
+        ask(c + L::RS - 1);                      // the slots that the last turn read
+        const uint32_t src = slot0 + (c - c0) % L::RS * (L::SLOTS * L::VEC);
+        uint4 a[RT][2];
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            a[i][e] = in && r0 + 16 * i + 8 * e + g < p.rank
-                          ? __ldg(reinterpret_cast<const uint4*>(ar + static_cast<int64_t>(16 * i + 8 * e) * p.K + k))
-                          : zero;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) b[n] = in && tok[n] >= 0 ? __ldg(reinterpret_cast<const uint4*>(xr[n] + k)) : zero;
+          for (int e = 0; e < 2; ++e) a[i][e] = ld_shared16(src + (2 * i + e) * L::VEC);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if (n < nts) {
+            const uint4 b = ld_shared16(src + (2 * RT + n) * L::VEC);
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              mma16816<BF16>(acc[i][n], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, b[n].x, b[n].y);
-              mma16816<BF16>(acc[i][n], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, b[n].z, b[n].w);
-            }
+            for (int i = 0; i < RT; ++i) mma16816<BF16>(acc[i][n], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, b.x, b.y);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) mma16816<BF16>(acc[i][n], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, b.z, b.w);
           }
         }
       }
-      if (r0 > 0) __syncthreads();               // the warps' sums of the tile before have been read
+      // the warps' sums, two warps to a place
+      float* const mine = red + (warp % (kLoraWarps / 2)) * kLoraTile * L::RPITCH + g;
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int half = 1; half >= 0; --half) {
+        __syncthreads();                         // the rings, or what stood here before, have been read
+        if (warp / (kLoraWarps / 2) == half) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int i = 0; i < RT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            red[(warp * kLoraTile + 8 * n + 2 * t + (e & 1)) * L::RPITCH + 16 * i + g + 8 * (e >> 1)] = acc[i][n][e];
+            for (int n = 0; n < NT; ++n)
+              if (n < nts) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float* const at = mine + (8 * n + 2 * t + (e & 1)) * L::RPITCH + 16 * i + 8 * (e >> 1);
+                  *at = half == 1 ? acc[i][n][e] : *at + acc[i][n][e];
+                }
+              }
+        }
+      }
       __syncthreads();
       for (int x = tid; x < count * (ROWS / 4); x += kLoraWarps * 32) {
         const int m = x / (ROWS / 4), r = 4 * (x % (ROWS / 4));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kLoraWarps; ++w) {
+        for (int w = 0; w < kLoraWarps / 2; ++w) {
           const float4 q = *reinterpret_cast<const float4*>(red + (w * kLoraTile + m) * L::RPITCH + r);
           v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
         }
         if (r0 + r < RP) *reinterpret_cast<float4*>(sum + m * RP + r0 + r) = v;
       }
+      if (r0 + ROWS < p.rank) __syncthreads();   // the next pass's ring lies where the warps' sums do
     }
+    if (CS > 1) cluster_arrive();
+    __syncthreads();                             // the sums have been taken: their place is the ring's
     // the first columns' operands arrive while the blocks meet
-    load_base(base);
+#pragma unroll
+    for (int s = 0; s < L::YS - 1; ++s) ask_base();
     load_b(0, bw);
-    if (CS > 1) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      __syncthreads();
-    }
+    if (CS > 1) cluster_wait();
     // ---- a warp takes a token: sum over the blocks, power of two, then the parts in the K order of the MMAs below.
     // Lane l has elements 4l .. 4l + 3 of the rank.
     const float sc = __ldg(p.scale + adapter);
@@ -361,41 +416,32 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < 4; ++i) up[i] = s_up[8 * i + g];
   } else {
-    load_base(base);
+#pragma unroll
+    for (int s = 0; s < L::YS - 1; ++s) ask_base();
   }
 
   // ---- y = base + B h
   char* yp[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + n) * YB;
+  for (int i = 0; i < 4; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + 32 * col + 8 * t) * YB;
   const int mts = count > 16 ? 2 : 1;
   const uint32_t hbase = smem_u32(hs) + ((lane & 15) * PITCH + (lane >> 4) * 8) * 2;
-  while (col < g1) {
-    const bool live = n < n_end;
-    // the next columns' operands: ahead of this one's products where there are registers for them
-    uint4 nbase[4][V], nbw[4];
-    if constexpr (V == 1) {
-      advance();
-      load_base(nbase);
-      if (steps > 0) load_b(0, nbw);
-    }
+  for (int turn = 0; col < g1; col += kLoraWarps, ++turn) {
+    const bool live = 32 * col + 8 * t < n_end;
     float acc[2][4][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
     for (int s = 0; s < steps; ++s) {
-      if (s > 0) {
-        if constexpr (V == 1) {                  // the pointers are a group ahead
-          n -= STEP;
-          wp -= static_cast<int64_t>(STEP) * p.rank;
-        }
-        load_b(s, bw);
-        if constexpr (V == 1) {
-          n += STEP;
-          wp += static_cast<int64_t>(STEP) * p.rank;
-        }
+      uint4 b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = bw[j];
+      if (s + 1 == steps) {                      // the rows of the next group
+        nb += STEP;
+        wp += static_cast<int64_t>(STEP) * p.rank;
       }
+      load_b(s + 1 == steps ? 0 : s + 1, bw);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (m < mts) {
@@ -410,19 +456,22 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
                            : "memory");
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mma16816<BF16>(acc[m][j], a[0], a[1], a[2], a[3], half ? bw[j].z : bw[j].x, half ? bw[j].w : bw[j].y);
+                mma16816<BF16>(acc[m][j], a[0], a[1], a[2], a[3], half ? b[j].z : b[j].x, half ? b[j].w : b[j].y);
             }
           }
         }
       }
     }
+    cp_async_wait<L::YS - 2>();
+    ask_base();                                  // into the slots that the last turn read
+    const uint32_t src = slot0 + turn % L::YS * (4 * V * L::VEC);
     // token 8i + g: columns 8t + 2j + {0, 1} of the group are elements 2 (i & 1) + {0, 1} of acc[i / 2][j]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (live && tok[i] >= 0) {
         uint4 r[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) r[e] = base[i][e];
+        for (int e = 0; e < V; ++e) r[e] = ld_shared16(src + (i * V + e) * L::VEC);
         if (steps > 0) {
           uint32_t w[4 * V];
 #pragma unroll
@@ -445,19 +494,8 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       }
       yp[i] += STEP * YB;
     }
-    if constexpr (V == 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        base[i][0] = nbase[i][0];
-        bw[i] = nbw[i];
-      }
-    } else {
-      advance();
-      load_base(base);
-      if (steps > 0) load_b(0, bw);
-    }
-    col += kLoraWarps;
   }
+  cp_async_wait<0>();
   if (steps > 0 && CS > 1) cluster_wait();       // no block leaves while another reads its sums
 }
 
