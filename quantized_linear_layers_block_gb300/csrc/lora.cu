@@ -2,7 +2,7 @@
 //   y[m] = base[m] + scale[a] B[a] (A[a] x[m]),  a = ids[m].
 //
 // A plan kernel sorts the tokens by adapter once per step; its items are up
-// to 32 tokens of one adapter, so an adapter's matrices are read once per item,
+// to 16 or 32 tokens of one adapter, so an adapter's matrices are read once per item,
 // by however many tokens use it. One kernel does both products: a cluster of blocks takes an item.
 //
 // First h = A x: the rank is small and K long, so K is cut over all warps of the cluster, whose sums meet through
@@ -33,7 +33,7 @@ constexpr int kLoraMaxCluster = 8;
 // ----------------------------------------------------------------- plan
 // Shared memory: for each adapter, and for the tokens without one, a counter and its first item.
 __global__ void __launch_bounds__(kPlanThreads)
-lora_plan_kernel(const int32_t* __restrict__ ids, int M, int n, LoraPlanHeader* head, LoraItem* items, int* status) {
+lora_plan_kernel(const int32_t* __restrict__ ids, int M, int n, int tile, LoraPlanHeader* head, LoraItem* items, int* status) {
   extern __shared__ int next[];
   int* const first = next + n + 1;
   __shared__ int s_items[kPlanThreads / 32];
@@ -51,7 +51,7 @@ lora_plan_kernel(const int32_t* __restrict__ ids, int M, int n, LoraPlanHeader* 
   // exclusive sum of the items over the bins; a thread owns consecutive bins
   const int per = (n + kPlanThreads) / kPlanThreads;
   int tiles = 0;
-  for (int i = tid * per; i < min(n + 1, (tid + 1) * per); ++i) tiles += (next[i] + kLoraTile - 1) / kLoraTile;
+  for (int i = tid * per; i < min(n + 1, (tid + 1) * per); ++i) tiles += (next[i] + tile - 1) / tile;
   int incl = tiles;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -69,9 +69,9 @@ lora_plan_kernel(const int32_t* __restrict__ ids, int M, int n, LoraPlanHeader* 
     const int c = next[i];
     next[i] = 0;
     first[i] = item;
-    for (int k = 0; k < c; k += kLoraTile, ++item) {
+    for (int k = 0; k < c; k += tile, ++item) {
       items[item].adapter = i < n ? i : -1;
-      items[item].count = min(kLoraTile, c - k);
+      items[item].count = min(tile, c - k);
     }
   }
   if (tid == 0) *head = LoraPlanHeader{M, n, all, 0};
@@ -90,7 +90,7 @@ lora_plan_kernel(const int32_t* __restrict__ ids, int M, int n, LoraPlanHeader* 
           next[b] = at + __popc(same);
         }
         at = __shfl_sync(0xffffffffu, at, leader) + rank;
-        if (b >= 0) items[first[b] + at / kLoraTile].token[at % kLoraTile] = i;
+        if (b >= 0) items[first[b] + at / tile].token[at % tile] = i;
       }
       __syncthreads();
     }
@@ -227,16 +227,20 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   constexpr int KV = RT == 1 ? 4 : 8;            // elements of a row that a thread takes
   int nb = 32 * col + 8 * (g >> 1) + (g & 1);                              // its row in tile 0 of the group that wp points to
   const uint16_t* wp = p.B + (static_cast<int64_t>(adapter) * p.N + nb) * p.rank + KV * t;
+  // up to 16 tokens fill half of a stage: then the ring has twice as many
+  const int mts = count > 16 ? 2 : 1, stages = 2 * L::YS / mts;
   int asked = 0;                                 // groups of base asked for
   auto ask_base = [&]() {
-    const uint32_t dst = slot0 + asked % L::YS * (4 * V * L::VEC);
+    const uint32_t dst = slot0 + (asked & (stages - 1)) * mts * (2 * V * L::VEC);
+    if (n < n_end) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (n < n_end && tok[i] >= 0) {
+      for (int i = 0; i < 4; ++i) {
+        if (tok[i] >= 0) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) cp_async16(dst + (i * V + e) * L::VEC, bp[i] + 16 * e, 16);
+          for (int e = 0; e < V; ++e) cp_async16(dst + (i * V + e) * L::VEC, bp[i] + 16 * e, 16);
+        }
+        bp[i] += STEP * YB;
       }
-      bp[i] += STEP * YB;
     }
     n += STEP;
     ++asked;
@@ -353,14 +357,14 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     if (CS > 1) cluster_arrive();
     __syncthreads();                             // the sums have been taken: their place is the ring's
     // the first columns' operands arrive while the blocks meet
-#pragma unroll
-    for (int s = 0; s < L::YS - 1; ++s) ask_base();
+    for (int s = 0; s < stages - 1; ++s) ask_base();
     load_b(0, bw);
     if (CS > 1) cluster_wait();
     // ---- a warp takes a token: sum over the blocks, power of two, then the parts in the K order of the MMAs below.
     // Lane l has elements 4l .. 4l + 3 of the rank.
     const float sc = __ldg(p.scale + adapter);
     const uint32_t sums = smem_u32(sum);
+#pragma unroll 2
     for (int m = warp; m < count; m += kLoraWarps) {       // rows past the last token may hold anything: they reach no other row
       float v[4] = {};
       if (4 * lane < p.rank) {
@@ -416,15 +420,13 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < 4; ++i) up[i] = s_up[8 * i + g];
   } else {
-#pragma unroll
-    for (int s = 0; s < L::YS - 1; ++s) ask_base();
+    for (int s = 0; s < stages - 1; ++s) ask_base();
   }
 
   // ---- y = base + B h
   char* yp[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + 32 * col + 8 * t) * YB;
-  const int mts = count > 16 ? 2 : 1;
   const uint32_t hbase = smem_u32(hs) + ((lane & 15) * PITCH + (lane >> 4) * 8) * 2;
   for (int turn = 0; col < g1; col += kLoraWarps, ++turn) {
     const bool live = 32 * col + 8 * t < n_end;
@@ -462,9 +464,12 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         }
       }
     }
-    cp_async_wait<L::YS - 2>();
+    if (mts == 2)
+      cp_async_wait<L::YS - 2>();
+    else
+      cp_async_wait<2 * L::YS - 2>();
     ask_base();                                  // into the slots that the last turn read
-    const uint32_t src = slot0 + turn % L::YS * (4 * V * L::VEC);
+    const uint32_t src = slot0 + (turn & (stages - 1)) * mts * (2 * V * L::VEC);
     // token 8i + g: columns 8t + 2j + {0, 1} of the group are elements 2 (i & 1) + {0, 1} of acc[i / 2][j]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -540,7 +545,7 @@ cudaError_t apply_type(const LoraParams& p, int sms, cudaStream_t st) {
 
 cudaError_t launch_lora_plan(const int32_t* ids, int M, int n_adapters, void* plan, int* status, cudaStream_t st) {
   auto* head = static_cast<LoraPlanHeader*>(plan);
-  return launch_pdl(lora_plan_kernel, dim3(1), dim3(kPlanThreads), 2 * sizeof(int) * (n_adapters + 1), st, ids, M, n_adapters, head,
+  return launch_pdl(lora_plan_kernel, dim3(1), dim3(kPlanThreads), 2 * sizeof(int) * (n_adapters + 1), st, ids, M, n_adapters, lora_tile(M), head,
                     reinterpret_cast<LoraItem*>(head + 1), status);
 }
 

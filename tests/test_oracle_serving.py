@@ -192,7 +192,7 @@ def test_lora_refusals(lib):
     assert call(M=0, x=None, base=None, y=None, plan=None) == tl.TL_OK
     assert call(N=0, x=None, base=None, y=None, plan=None) == tl.TL_OK
     sz = ctypes.c_size_t()
-    assert lib.tl_lora_plan_size(33, 4, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 144 * (5 + 0)
+    assert lib.tl_lora_plan_size(33, 4, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 144 * (1 + 5)
     assert lib.tl_lora_plan_size(2, 400, ctypes.byref(sz)) == tl.TL_OK and sz.value == 16 + 144 * 2
     assert lib.tl_lora_plan(None, 2, 4, ok, 10 ** 6, None) == tl.TL_EINVAL
     assert lib.tl_lora_plan(ok, 2, 4, ok, 10, None) == tl.TL_ENOSPACE
