@@ -76,16 +76,15 @@ struct AttnParams {
   float scale_log2;
   int B, q_heads, kv_heads, group, groups_per_kv, window, q_bf16;
   int runs16;               // page_size is a multiple of 16: 16 keys from a multiple of 16 lie at equal distances
-  int* counters;            // 2 kAttnMaxGrid, zero between calls
+  int* counters;            // [kAttnLevels][kAttnMaxGrid], zero between calls
   float* partials;          // two per block
   int* status;
 };
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnMaxBlocksPerSm = 4;
-constexpr int kAttnMaxGrid = 4096;     // the workspace begins with two counters for each block
-constexpr int kJoinWide = 48;          // partials that one block joins at once
-constexpr int kJoinGroup = 16;         // above that: partials joined first
+constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join
+constexpr int kAttnLevels = 6;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -185,8 +184,19 @@ struct Traits {
   static constexpr int HEADS = 8 * NT;
   static constexpr int OPITCH = D + 4;                   // floats; the warps' o meet here, conflict-free
   static constexpr int MEET = (HEADS * OPITCH + 2 * HEADS) * 4;
-  static constexpr int STAGES = NT == 1 ? 3 : (NT == 2 && D < 256 ? 2 : (D == 256 && !F8 ? 2 : 3));
+  // buffers of a warp's ring: up to three where two blocks share an SM (whose 228 KB hold a KB more for each
+  // block), else as many as fit
+  static constexpr int stages() {
+    for (int s = 3; s >= 2; --s)
+      if (kAttnWarps * (s * BUF + MEET) <= 115500) return s;
+    int s = 6;
+    while (kAttnWarps * (s * BUF + MEET) > 231000) --s;
+    return s;
+  }
+  static constexpr int STAGES = stages();
   static constexpr int SMEM = kAttnWarps * (STAGES * BUF + MEET);
+  // partials that one join takes: what the ring holds, and no more than are quick to copy
+  static constexpr int FIT = kAttnWarps * STAGES * BUF / (HEADS * (D + 2) * 4), FAN = FIT < 16 ? FIT : 16;
   static constexpr int BLOCKS = SMEM > 113 * 1024 ? 1 : SMEM > 74 * 1024 ? 2 : 3;     // per SM
   // 2^8 in the probabilities keeps an f16 low part of the small ones out of the subnormals
   static constexpr float POFF = BF16 ? 0.f : 8.f;
@@ -221,11 +231,11 @@ __device__ __forceinline__ void seg_keys(const AttnParams& p, int len, int tile_
 }
 
 // A segment that n blocks share, from block c0 on: c0 began it (its second partial), the others found it
-// begun (their first). Up to kJoinWide partials are joined at once by the last block to
-// arrive; more are joined in groups of kJoinGroup blocks first, each by the last of its group, so that the
-// joins run on many SMs.
+// begun (their first). The partials are joined along a tree: up to `fan` neighbours by the last
+// of them to arrive, their results in the same way, and so on, so that the joins run on many SMs and none
+// reads more than its shared memory holds.
 struct Shared {
-  int c0, n, b, h0, heads;
+  int c0, n, fan, b, h0, heads;
   float v_scale;
 };
 
@@ -253,67 +263,54 @@ __device__ __forceinline__ int count_in(int* counter, int n) {
   return last;
 }
 
-__device__ __forceinline__ int arrive(int* counters, const Shared& s) {
-  if (s.n <= kJoinWide) return count_in(counters + s.c0, s.n);
-  const int first = (static_cast<int>(blockIdx.x) - s.c0) / kJoinGroup * kJoinGroup;
-  return count_in(counters + s.c0 + first, min(kJoinGroup, s.n - first));
+// The group of partials that this block's belongs to when every `step`-th one is left: its first, and how many.
+__device__ __forceinline__ int2 join_group(const Shared& s, int step) {
+  const int first = (static_cast<int>(blockIdx.x) - s.c0) / (step * s.fan) * (step * s.fan);
+  return make_int2(first, min(s.fan, (s.n - first + step - 1) / step));
 }
 
-// Joins n <= kJoinWide partials, those of blocks first, first + step, ... counted from the segment's first: with
-// LAST, into the segment's result; otherwise into the first of them. One block works alone here, with few
-// warps, so what counts is the number of latencies and of instructions: the partials' o come in
-// bulk copies to the ring, which is free by now (as many at a time as fit), while the warps turn the maxima and
-// sums into one weight per partial and head; then each thread adds up its channels.
-template <class T, int D, bool LAST>
-__device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int first, int step, int n, uint8_t* ring, float* meet,
-                                     uint32_t bar, uint32_t& phase) {
+// Joins the k partials of blocks first, first + step, ... counted from the segment's first: with LAST, into the
+// segment's result; otherwise into the first of them. One block works alone here, with few warps, so what
+// counts is the number of latencies and of instructions: bulk copies bring the partials to the
+// ring, which is free by now, the warps turn maxima and sums into one weight per partial and head, and each thread
+// adds up its channels.
+template <class T, int D>
+__device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int first, int step, int k, bool last, uint8_t* ring,
+                                     float* meet, uint32_t bar, uint32_t phase) {
   constexpr size_t PF = attn_partial_floats(T::HEADS, D);
   constexpr int THREADS = kAttnWarps * 32, COLS = T::HEADS * D / 4 / THREADS;
-  constexpr int FIT = kAttnWarps * T::STAGES * T::BUF / (T::HEADS * D * 4), ROOM = FIT < 32 ? FIT : 32;   // partials that the ring holds
-  static_assert(ROOM >= 2 && T::HEADS * D / 4 % THREADS == 0 && (kJoinWide + 2) * T::HEADS * 4 <= kAttnWarps * T::MEET, "join");
+  static_assert(T::FAN >= 2 && T::FAN <= 32 && T::HEADS * D / 4 % THREADS == 0 && (T::FAN + 2) * T::HEADS * 4 <= kAttnWarps * T::MEET, "join");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  float* const p0 = p.partials + (static_cast<size_t>(s.c0) * 2 + 1) * PF;
-  float* const p1 = p.partials + static_cast<size_t>(s.c0) * 2 * PF;
-  auto part = [&](int i) { return first + i * step == 0 ? p0 : p1 + static_cast<size_t>(first + i * step) * 2 * PF; };
-  const uint32_t bytes = s.heads * D * 4;
-  auto fetch = [&](int i0) {             // warp 0: partials i0 .. i0 + ROOM - 1
-    const int k = min(ROOM, n - i0);
-    if (lane == 0) mbar_arrive_expect_tx(bar, k * bytes);
-    __syncwarp();
-    if (lane < k) {
-      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                       smem_u32(ring) + lane * (T::HEADS * D * 4)),
-                   "l"(part(i0 + lane) + 2 * T::HEADS), "r"(bytes), "r"(bar)
-                   : "memory");
-    }
+  auto part = [&](int i) {
+    const int at = first + i * step;
+    return p.partials + static_cast<size_t>(2 * (s.c0 + at) + (at == 0)) * PF;
   };
   if (warp == 0) {
+    const uint32_t bytes = (2 * T::HEADS + s.heads * D) * 4;
     // other blocks' ordinary writes, which count_in made visible, before the copies that read them
     asm volatile("fence.proxy.async;" ::: "memory");
-    fetch(0);
+    if (lane == 0) mbar_arrive_expect_tx(bar, k * bytes);
+    __syncwarp();
+    if (lane < k)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       smem_u32(ring) + lane * static_cast<uint32_t>(PF * 4)),
+                   "l"(part(lane)), "r"(bytes), "r"(bar)
+                   : "memory");
   }
-  float* const weight = meet;            // [n][HEADS], then the segment's maximum and sum per head
-  float* const all = meet + kJoinWide * T::HEADS;
+  if (!mbar_wait(bar, phase, nullptr)) set_status(p.status, TL_ETIMEOUT);
+  const float* const in = reinterpret_cast<const float*>(ring);
+  float* const weight = meet;            // [k][HEADS], then the group's maximum and sum per head
+  float* const all = meet + T::FAN * T::HEADS;
   for (int h = warp; h < s.heads; h += kAttnWarps) {
-    float m[kJoinWide / 32 + 1], l[kJoinWide / 32 + 1], top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int e = 0; e <= kJoinWide / 32; ++e) {
-      const int i = e * 32 + lane;
-      m[e] = i < n ? __ldcg(part(i) + h) : -INFINITY;
-      l[e] = i < n ? __ldcg(part(i) + T::HEADS + h) : 0.f;
-      top = fmaxf(top, m[e]);
-    }
+    const float m = lane < k ? in[lane * PF + h] : -INFINITY, l = lane < k ? in[lane * PF + T::HEADS + h] : 0.f;
+    float top = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-    for (int e = 0; e <= kJoinWide / 32; ++e) {
-      m[e] = exp2_approx(m[e] - base);
-      sum += m[e] * l[e];
-      if (e * 32 + lane < n) weight[(e * 32 + lane) * T::HEADS + h] = m[e];
-    }
+    const float w = exp2_approx(m - (top == -INFINITY ? 0.f : top));
+    float sum = w * l;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane < k) weight[lane * T::HEADS + h] = w;
     if (lane == 0) {
       all[h] = top;
       all[T::HEADS + h] = sum;
@@ -323,38 +320,28 @@ __device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int f
   float4 a[COLS];
 #pragma unroll
   for (int c = 0; c < COLS; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += ROOM) {
-    const int k = min(ROOM, n - i0);
-    if (!mbar_wait(bar, phase, nullptr)) set_status(p.status, TL_ETIMEOUT);
-    phase ^= 1;
-    const float4* v = reinterpret_cast<const float4*>(ring) + tid;
-    const float* w = weight + i0 * T::HEADS;
+  const float4* v = reinterpret_cast<const float4*>(in + 2 * T::HEADS) + tid;
+  const float* w = weight;
 #pragma unroll 2
-    for (int i = 0; i < k; ++i, v += T::HEADS * D / 4, w += T::HEADS) {
+  for (int i = 0; i < k; ++i, v += PF / 4, w += T::HEADS) {
 #pragma unroll
-      for (int c = 0; c < COLS; ++c) {
-        const int h = (tid + c * THREADS) / (D / 4);
-        if (h < s.heads) {
-          const float f = w[h];
-          const float4 x = v[c * THREADS];
-          a[c].x += f * x.x;
-          a[c].y += f * x.y;
-          a[c].z += f * x.z;
-          a[c].w += f * x.w;
-        }
+    for (int c = 0; c < COLS; ++c) {
+      const int h = (tid + c * THREADS) / (D / 4);
+      if (h < s.heads) {
+        const float f = w[h];
+        const float4 x = v[c * THREADS];
+        a[c].x += f * x.x;
+        a[c].y += f * x.y;
+        a[c].z += f * x.z;
+        a[c].w += f * x.w;
       }
-    }
-    if (i0 + ROOM < n) {
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (warp == 0) fetch(i0 + ROOM);
     }
   }
 #pragma unroll
   for (int c = 0; c < COLS; ++c) {
     const int x = tid + c * THREADS, h = x / (D / 4), d = 4 * (x % (D / 4));
     if (h < s.heads) {
-      if constexpr (LAST) {
+      if (last) {
         write_out<T>(p, s.b, s.h0 + h, d, D, a[c], all[h], all[T::HEADS + h], s.v_scale);
       } else {
         float* const dst = part(0);
@@ -370,21 +357,24 @@ __device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int f
   __syncthreads();            // `meet` and the ring are free again
 }
 
-// What the last block of a segment, or of a group, does; ring, meet, flag and barrier in shared memory.
+// What a block does that arrived as the last of its group of partials; ring, meet, flag and barrier in shared memory.
 template <class T, int D>
 __device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uint8_t* ring, float* meet, int* flag, uint32_t bar,
                                        uint32_t& phase) {
-  int step = 1, n = s.n;
-  if (n > kJoinWide) {
-    const int first = (static_cast<int>(blockIdx.x) - s.c0) / kJoinGroup * kJoinGroup;
-    join<T, D, false>(p, s, first, 1, min(kJoinGroup, n - first), ring, meet, bar, phase);
-    step = kJoinGroup;
-    n = (n + kJoinGroup - 1) / kJoinGroup;
-    if (threadIdx.x == 0) *flag = count_in(p.counters + kAttnMaxGrid + s.c0, n);
+  for (int step = 1, level = 0;; ++level) {
+    const int2 g = join_group(s, step);
+    const bool last = g.x == 0 && step * s.fan >= s.n;
+    join<T, D>(p, s, g.x, step, g.y, last, ring, meet, bar, phase);
+    phase ^= 1;
+    if (last) return;
+    step *= s.fan;
+    if (threadIdx.x == 0) {
+      const int2 up = join_group(s, step);
+      *flag = count_in(p.counters + (level + 1) * kAttnMaxGrid + s.c0 + up.x, up.y);
+    }
     __syncthreads();
     if (*flag == 0) return;
   }
-  join<T, D, true>(p, s, 0, step, n, ring, meet, bar, phase);
 }
 
 template <int CACHE, int D, int NT>
@@ -860,9 +850,13 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       // joins them is looked up when the block has nothing else to do.
       if (tid == 0) {
         const int c0 = static_cast<int>(divide(first, share));
-        const Shared s{c0, static_cast<int>(divide(first + seg.tiles - 1, share)) - c0 + 1, seg.b, sh0, sheads, vs};
+        const int n = static_cast<int>(divide(first + seg.tiles - 1, share)) - c0 + 1;
+        // one join of all where they fit, else a tree of two levels, or of more where its joins would not fit
+        const int fan = n <= T::FAN ? n : min(T::FAN, static_cast<int>(ceilf(sqrtf(static_cast<float>(n)))));
+        const Shared s{c0, n, fan, seg.b, sh0, sheads, vs};
         s_pend[second] = s;
-        s_last[second] = arrive(p.counters, s);
+        const int2 g = join_group(s, 1);
+        s_last[second] = count_in(p.counters + c0 + g.x, g.y);
       }
     }
   }

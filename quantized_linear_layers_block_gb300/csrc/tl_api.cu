@@ -380,7 +380,7 @@ int tl_paged_attention_workspace_size(int B, int q_heads, int kv_heads, int head
   if ((r = num_sms(&sms)) != TL_OK) return r;
   const long long grid = sms * tl::kAttnMaxBlocksPerSm < tl::kAttnMaxGrid ? sms * tl::kAttnMaxBlocksPerSm : tl::kAttnMaxGrid;
   const int heads = 8 * attention_columns(q_heads / kv_heads, head_dim);
-  *bytes = 2 * tl::kAttnMaxGrid * sizeof(int) + 2 * grid * tl::attn_partial_floats(heads, head_dim) * sizeof(float);
+  *bytes = tl::kAttnLevels * tl::kAttnMaxGrid * sizeof(int) + 2 * grid * tl::attn_partial_floats(heads, head_dim) * sizeof(float);
   return TL_OK;
 }
 
@@ -425,7 +425,7 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
   const int nt = attention_columns(p.group, cache->head_dim);
   p.groups_per_kv = (p.group + 8 * nt - 1) / (8 * nt);
   p.counters = static_cast<int*>(workspace);
-  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * tl::kAttnMaxGrid * sizeof(int));
+  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + tl::kAttnLevels * tl::kAttnMaxGrid * sizeof(int));
   p.status = status;
   const cudaStream_t st = as_stream(stream);
   const cudaError_t e = cache->dtype == TL_BF16  ? tl::launch_attn_bf16(p, cache->head_dim, nt, sms, st)
