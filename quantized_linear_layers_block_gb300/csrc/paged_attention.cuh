@@ -11,7 +11,7 @@
 // with s in units of log2(e).
 //
 // Work. A (request, group of query heads) is a segment; its keys are cut into
-// tiles of W * KT keys and the tiles of all segments form one list, cut into
+// tiles of 4 KT keys and the tiles of all segments form one list, cut into
 // equal shares for the blocks of one resident wave. So a batch of ragged lengths
 // needs no plan from the host, which never learns the lengths, and no block waits
 // for the longest request. A segment inside one block's share is finished there;
@@ -20,10 +20,11 @@
 // reach the result). At most two of a block's segments are cut, the first and
 // the last, so the workspace depends on the grid alone.
 //
-// Tiles. Each of a block's W warps streams its own KT keys of a tile through its own ring of STAGES
-// buffers (cp.async, no block barrier in the loop) and keeps its own (m, l, o);
-// the warps meet once per segment. The scores are computed transposed, S^T = K q^T: the
-// keys are the rows of the MMA and 8 NT query heads its columns, so 8 heads need
+// Tiles. A tile's keys go through four rings of STAGES buffers (cp.async), KT keys each. A ring has one warp for
+// every 8 query heads of the segment, up to four, which fill it together and read it each for its
+// heads; there is no block barrier in the loop. Each warp keeps its own (m, l, o);
+// the rings meet once per segment. The scores are computed transposed, S^T = K q^T: the
+// keys are the rows of the MMA and 8 query heads its columns, so 8 heads need
 // half the MMAs that 16 padded rows would, and S^T and O^T = V^T P^T have their heads on the same
 // lanes, which keeps the rescaling in registers. P^T becomes an operand by an 8x8 transpose (movmatrix).
 // Probabilities are split in two 16-bit numbers, high and low part, so that they count with 16 (bf16)
@@ -81,8 +82,9 @@ struct AttnParams {
   int* status;
 };
 
-constexpr int kAttnWarps = 4;
+constexpr int kAttnRings = 4;          // rings of key tiles in a block, each with HW warps
 constexpr int kAttnMaxBlocksPerSm = 4;
+constexpr int kAttnCluster = 8;        // blocks that share a segment of a small call
 constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join
 constexpr int kAttnLevels = 6;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -93,9 +95,9 @@ __host__ __device__ constexpr size_t attn_partial_floats(int heads, int dim) {
   return static_cast<size_t>(heads) * (dim + 2);
 }
 
-cudaError_t launch_attn_bf16(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st);
-cudaError_t launch_attn_f16(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st);
-cudaError_t launch_attn_f8(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st);
+cudaError_t launch_attn_bf16(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st);
+cudaError_t launch_attn_f16(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st);
+cudaError_t launch_attn_f8(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st);
 
 namespace attn {
 
@@ -156,6 +158,23 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
   else
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+  uint32_t remote;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote)
+               : "memory");
+  return v;
+}
 // two e4m3 values (low, high byte) as f16, exact
 __device__ __forceinline__ uint32_t widen_lo(uint32_t v) {
   uint32_t r;
@@ -173,31 +192,32 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-template <int CACHE, int D, int NT>
+template <int CACHE, int D, int HW>
 struct Traits {
   static constexpr bool F8 = CACHE == kCacheF8;
   static constexpr bool BF16 = CACHE == kCacheBf16;      // the MMA's operand type (f16 otherwise)
+  static constexpr int THREADS = kAttnRings * HW * 32;
   static constexpr int ROW = D * (F8 ? 1 : 2);           // bytes of a key
-  static constexpr int KT = 4096 / ROW > 16 ? 4096 / ROW : 16;   // keys of a warp's buffer: 4 KB of K (8 for 512-byte rows)
-  static constexpr int TILE = kAttnWarps * KT;
+  static constexpr int KT = 4096 / ROW > 16 ? 4096 / ROW : 16;   // keys of a ring's buffer: 4 KB of K (8 for 512-byte rows)
+  static constexpr int TILE = kAttnRings * KT;
   static constexpr int BUF = 2 * KT * ROW;
-  static constexpr int HEADS = 8 * NT;
+  static constexpr int HEADS = 8 * HW;
   static constexpr int OPITCH = D + 4;                   // floats; the warps' o meet here, conflict-free
   static constexpr int MEET = (HEADS * OPITCH + 2 * HEADS) * 4;
-  // buffers of a warp's ring: up to three where two blocks share an SM (whose 228 KB hold a KB more for each
+  // buffers of a ring: up to three where two blocks share an SM (whose 228 KB hold a KB more for each
   // block), else as many as fit
   static constexpr int stages() {
-    for (int s = 3; s >= 2; --s)
-      if (kAttnWarps * (s * BUF + MEET) <= 115500) return s;
+    for (int s = 3; s >= 2 && HW < 4; --s)             // 512 threads of 128 registers are alone on their SM
+      if (kAttnRings * (s * BUF + MEET) <= 115500) return s;
     int s = 6;
-    while (kAttnWarps * (s * BUF + MEET) > 231000) --s;
+    while (kAttnRings * (s * BUF + MEET) > 231000) --s;
     return s;
   }
   static constexpr int STAGES = stages();
-  static constexpr int SMEM = kAttnWarps * (STAGES * BUF + MEET);
-  // partials that one join takes: what the ring holds, and no more than are quick to copy
-  static constexpr int FIT = kAttnWarps * STAGES * BUF / (HEADS * (D + 2) * 4), FAN = FIT < 16 ? FIT : 16;
-  static constexpr int BLOCKS = SMEM > 113 * 1024 ? 1 : SMEM > 74 * 1024 ? 2 : 3;     // per SM
+  static constexpr int SMEM = kAttnRings * (STAGES * BUF + MEET);
+  // partials that one join takes: what the rings hold, and no more than are quick to copy
+  static constexpr int FIT = kAttnRings * STAGES * BUF / (HEADS * (D + 2) * 4), FAN = FIT < 16 ? FIT : 16;
+  static constexpr int BLOCKS = HW == 4 || SMEM > 115500 ? 1 : SMEM > 75000 ? 2 : 3;     // per SM
   // 2^8 in the probabilities keeps an f16 low part of the small ones out of the subnormals
   static constexpr float POFF = BF16 ? 0.f : 8.f;
 };
@@ -278,8 +298,8 @@ template <class T, int D>
 __device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int first, int step, int k, bool last, uint8_t* ring,
                                      float* meet, uint32_t bar, uint32_t phase) {
   constexpr size_t PF = attn_partial_floats(T::HEADS, D);
-  constexpr int THREADS = kAttnWarps * 32, COLS = T::HEADS * D / 4 / THREADS;
-  static_assert(T::FAN >= 2 && T::FAN <= 32 && T::HEADS * D / 4 % THREADS == 0 && (T::FAN + 2) * T::HEADS * 4 <= kAttnWarps * T::MEET, "join");
+  constexpr int THREADS = T::THREADS, COLS = T::HEADS * D / 4 / THREADS;
+  static_assert(T::FAN >= 2 && T::FAN <= 32 && T::HEADS * D / 4 % THREADS == 0 && (T::FAN + 2) * T::HEADS * 4 <= kAttnRings * T::MEET, "join");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto part = [&](int i) {
     const int at = first + i * step;
@@ -301,7 +321,7 @@ __device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int f
   const float* const in = reinterpret_cast<const float*>(ring);
   float* const weight = meet;            // [k][HEADS], then the group's maximum and sum per head
   float* const all = meet + T::FAN * T::HEADS;
-  for (int h = warp; h < s.heads; h += kAttnWarps) {
+  for (int h = warp; h < s.heads; h += THREADS / 32) {
     const float m = lane < k ? in[lane * PF + h] : -INFINITY, l = lane < k ? in[lane * PF + T::HEADS + h] : 0.f;
     float top = m;
 #pragma unroll
@@ -377,27 +397,44 @@ __device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uin
   }
 }
 
-template <int CACHE, int D, int NT>
-__global__ void __launch_bounds__(kAttnWarps * 32, Traits<CACHE, D, NT>::BLOCKS)
+// What follows the queries, the keys and the values of one segment through a warp; 8 query heads.
+// CL: eight blocks, a cluster, take a segment, and join it through their shared memory.
+template <int CACHE, int D, int HW, bool CL>
+__global__ void __launch_bounds__(kAttnRings * HW * 32, Traits<CACHE, D, HW>::BLOCKS)
 paged_attention_kernel(const __grid_constant__ AttnParams p) {
-  using T = Traits<CACHE, D, NT>;
+  using T = Traits<CACHE, D, HW>;
   constexpr int KT = T::KT, ROW = T::ROW, MT = KT / 16, DT = D / 16, S = T::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_bar;
   __shared__ int s_last[2];
   __shared__ Shared s_pend[2];                        // segments shared with other blocks: the first, the last
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int w = warp / HW, hw = warp % HW;            // the warp's ring, and its 8 heads
   const int HG = p.kv_heads * p.groups_per_kv;
 
   pdl_wait_prior();
   pdl_launch_dependents();
 
-  // ---- the share of this block: `count` places from t0 of the list, in which a segment has one place for
-  // what it costs besides its tiles, then its tiles. Every warp finds it for itself.
-  long long total = 0;
-  int len = 0;
+  long long share = 0, t0 = 0;
+  int count;                                          // places of this block's share
+  int skip;                                           // places of the first segment that lie before t0
   Segment cur;
-  {
+  if constexpr (CL) {
+    // ---- an eighth of a segment's tiles
+    const int seg = blockIdx.x / kAttnCluster, rank = blockIdx.x % kAttnCluster;
+    cur.b = seg / HG;
+    cur.h = seg - cur.b * HG;
+    const int len = __ldg(p.lens + cur.b);
+    if ((len < 0 || len > p.max_len) && tid == 0) set_status(p.status, TL_EDATA);
+    seg_keys(p, len, T::TILE, cur);
+    cur.tile = static_cast<int>(static_cast<long long>(cur.tiles) * rank / kAttnCluster);
+    count = static_cast<int>(static_cast<long long>(cur.tiles) * (rank + 1) / kAttnCluster) - cur.tile;
+    skip = 1;
+  } else {
+    // ---- the share of this block: `count` places from t0 of the list, in which a segment has one place for
+    // what it costs besides its tiles, then its tiles. Every warp finds it for itself.
+    long long total = 0;
+    int len = 0;
     bool bad = false;
     for (int base = 0; base < p.B; base += 32) {
       len = base + lane < p.B ? __ldg(p.lens + base + lane) : 0;
@@ -406,23 +443,20 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       if (base + lane < p.B) total += cur.tiles + 1;
     }
     if (bad && blockIdx.x == 0) set_status(p.status, TL_EDATA);
-  }
-  // a lane's sum is below 2^50 (2^27 tiles a request, 2^23 requests a lane)
-  total = static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total & 0x1FFFFFF))) +
-          (static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total >> 25))) << 25);
-  total *= HG;
-  const long long share = divide(total + gridDim.x - 1, gridDim.x);
-  const long long t0 = share * blockIdx.x;
-  if (t0 >= total) return;
-  const int count = static_cast<int>(min(share, total - t0));
-  int skip;                                           // places of the first segment that lie before t0
-  {
-    long long run = 0;                                // tiles of the requests before this round's, of one head group
+    // a lane's sum is below 2^50 (2^27 tiles a request, 2^23 requests a lane)
+    total = static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total & 0x1FFFFFF))) +
+            (static_cast<long long>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(total >> 25))) << 25);
+    total *= HG;
+    share = divide(total + gridDim.x - 1, gridDim.x);
+    t0 = share * blockIdx.x;
+    if (t0 >= total) return;
+    count = static_cast<int>(min(share, total - t0));
+    long long run = 0;                                // places of the requests before this round's, of one head group
     for (int base = 0;; base += 32) {
       if (p.B > 32) len = base + lane < p.B ? __ldg(p.lens + base + lane) : 0;
       seg_keys(p, len, T::TILE, cur);
-      const unsigned tiles = base + lane < p.B ? cur.tiles + 1 : 0;
-      unsigned incl = tiles;
+      const unsigned places = base + lane < p.B ? cur.tiles + 1 : 0;
+      unsigned incl = places;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -433,7 +467,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
         const int who = __ffs(at) - 1;
         cur.b = base + who;
         seg_keys(p, __shfl_sync(0xffffffffu, len, who), T::TILE, cur);
-        const long long left = t0 - HG * (run + __shfl_sync(0xffffffffu, incl - tiles, who));
+        const long long left = t0 - HG * (run + __shfl_sync(0xffffffffu, incl - places, who));
         cur.h = static_cast<int>(divide(left, cur.tiles + 1));
         skip = static_cast<int>(left - cur.h * (cur.tiles + 1ll));
         cur.tile = max(skip - 1, 0);
@@ -443,31 +477,40 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     }
   }
 
-  // ---- the warp's ring
-  const uint32_t ring = smem_u32(smem) + warp * S * T::BUF;
-  float* const meet = reinterpret_cast<float*>(smem + kAttnWarps * S * T::BUF);
+  // ---- the ring, filled by its HW warps together
+  const uint32_t ring = smem_u32(smem) + w * S * T::BUF;
+  float* const meet = reinterpret_cast<float*>(smem + kAttnRings * S * T::BUF);
+  auto ring_sync = [&]() {
+    if constexpr (HW == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + w), "n"(HW * 32) : "memory");
+  };
 
   constexpr int CPR = ROW / 16;                       // 16-byte chunks of a row
-  constexpr int RPI = 32 / CPR;                       // rows that one instruction of the warp copies
+  constexpr int RPI = 32 / CPR;                       // rows that one instruction of a warp copies
   constexpr int KPL = (KT + 31) / 32;                 // keys whose address a lane computes
+  static_assert(16 / RPI * MT % HW == 0, "rows are shared out evenly");
   Segment ld = cur;
   int next_len = 0;                                   // length of the request after ld's
   int pid[KPL];
   const int chunk = (lane % CPR) * 16, row0 = lane / CPR;
-  auto fetch_len = [&]() { next_len = ld.b + 1 < p.B ? __ldg(p.lens + ld.b + 1) : 0; };
+  auto fetch_len = [&]() {
+    if constexpr (!CL) next_len = ld.b + 1 < p.B ? __ldg(p.lens + ld.b + 1) : 0;
+  };
   auto fetch_pages = [&]() {
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
-      const int key = ld.begin + ld.tile * T::TILE + warp * KT + i * 32 + lane;
+      const int key = ld.begin + ld.tile * T::TILE + w * KT + i * 32 + lane;
       pid[i] = key >= ld.first && key < ld.end && i * 32 + lane < KT ? __ldg(p.pages + ld.b * p.ldp + p.page.div(key)) : -1;
     }
   };
-  fetch_len();
-  fetch_pages();
   int left = count - (skip == 0);                     // places of the tiles not yet asked for
+  fetch_len();
+  if (left > 0) fetch_pages();
   auto load_tile = [&](int stage) {
     if (left > 0) {
-      const int k0 = ld.begin + ld.tile * T::TILE + warp * KT;
+      const int k0 = ld.begin + ld.tile * T::TILE + w * KT;
       if (k0 < ld.end) {
         const int kvh = ld.h / p.groups_per_kv;
         int64_t off[KPL];                             // bytes from the cache's first row to key i * 32 + lane; -1: no such row
@@ -488,27 +531,22 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
         // a tile of whole pages, or parts of pages, of 16 rows each: one address for 16 rows
         if (p.runs16 && k0 >= ld.first && k0 + KT <= ld.end && !__any_sync(0xffffffffu, bad)) {
 #pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            const int64_t o = __shfl_sync(0xffffffffu, off[j / 2], (16 * j) & 31);
-            const uint8_t* const ks = p.k + o + row0 * p.token_stride + chunk;
-            const uint8_t* const vs = p.v + o + row0 * p.token_stride + chunk;
-#pragma unroll
-            for (int i = 0; i < 16 / RPI; ++i) {
-              const uint32_t dst = kb + at<ROW>(16 * j + i * RPI + row0, chunk >> 4);
-              const int64_t step = static_cast<int64_t>(i * RPI) * p.token_stride;
-              cp_async16(dst, ks + step);
-              cp_async16(dst + KT * ROW, vs + step);
-            }
+          for (int x = 0; x < 16 / RPI * MT / HW; ++x) {
+            const int step = x * HW + hw, j = step / (16 / RPI), i = step % (16 / RPI);
+            const int64_t o = __shfl_sync(0xffffffffu, off[KPL == 1 ? 0 : j / 2], (16 * j) & 31) +
+                              static_cast<int64_t>(i * RPI + row0) * p.token_stride + chunk;
+            const uint32_t dst = kb + at<ROW>(step * RPI + row0, chunk >> 4);
+            cp_async16(dst, p.k + o);
+            cp_async16(dst + KT * ROW, p.v + o);
           }
         } else {
           if (bad) set_status(p.status, TL_EDATA);
-          const int64_t any = 0;
 #pragma unroll
-          for (int i = 0; i < KT / RPI; ++i) {
-            const int r = i * RPI + row0;
-            const int64_t o = __shfl_sync(0xffffffffu, off[(i * RPI) / 32], r & 31);
+          for (int x = 0; x < KT / RPI / HW; ++x) {
+            const int r = (x * HW + hw) * RPI + row0;
+            const int64_t o = __shfl_sync(0xffffffffu, off[KPL == 1 ? 0 : (x * HW + hw) * RPI / 32], r & 31);
             const uint32_t bytes = o < 0 ? 0u : 16u;
-            const int64_t src = max(o, any) + chunk;
+            const int64_t src = (o < 0 ? 0 : o) + chunk;
             const uint32_t dst = kb + at<ROW>(r, chunk >> 4);
             cp_async16(dst, p.k + src, bytes);
             cp_async16(dst + KT * ROW, p.v + src, bytes);
@@ -538,116 +576,96 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
   bool starts_before = cur.tile > 0;
   // queries as B operands: k = 16 channels, n = 8 heads. For an 8-bit cache thread t takes channels
   // 4t .. 4t + 3, as its ldmatrix of K gives them. Asked for while the segment before is being finished.
-  uint32_t qf[DT][NT][2];
-  int kvh, h0, heads;
+  uint32_t qf[DT][2];
+  int h0, heads;
   float kscale = 1.f, vscale = 1.f;
   auto fetch_q = [&]() {
-    kvh = cur.h / p.groups_per_kv;
+    const int kvh = cur.h / p.groups_per_kv;
     h0 = kvh * p.group + (cur.h - kvh * p.groups_per_kv) * T::HEADS;
     heads = min(T::HEADS, kvh * p.group + p.group - h0);
     if constexpr (T::F8) {
       kscale = __ldg(p.k_scale + kvh);
       vscale = __ldg(p.v_scale + kvh);
     }
+    const uint16_t* qr = p.q + cur.b * p.ldq + static_cast<int64_t>(h0 + hw * 8 + g) * D;
+    const bool live = hw * 8 + g < heads;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint16_t* qr = p.q + cur.b * p.ldq + static_cast<int64_t>(h0 + n * 8 + g) * D;
-      const bool live = n * 8 + g < heads;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        if constexpr (T::F8) {
-          const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(qr + 16 * i + 4 * t)) : make_uint2(0, 0);
-          qf[i][n][0] = w.x;
-          qf[i][n][1] = w.y;
-        } else {
-          qf[i][n][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 2 * t)) : 0u;
-          qf[i][n][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 8 + 2 * t)) : 0u;
-        }
+    for (int i = 0; i < DT; ++i) {
+      if constexpr (T::F8) {
+        const uint2 x = live ? __ldg(reinterpret_cast<const uint2*>(qr + 16 * i + 4 * t)) : make_uint2(0, 0);
+        qf[i][0] = x.x;
+        qf[i][1] = x.y;
+      } else {
+        qf[i][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 2 * t)) : 0u;
+        qf[i][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 8 + 2 * t)) : 0u;
       }
     }
   };
   fetch_q();
-  if (tid == 0) {
+  if (!CL && tid == 0) {
     s_pend[0].n = s_pend[1].n = 0;
     mbar_init(smem_u32(&s_bar), 1);
     fence_barrier_init();
   }
-  while (done < count) {
-    const int here = min(cur.tiles - cur.tile, count - done);    // tiles of this segment in this block's share
+  while (CL || done < count) {
+    // tiles of this segment in this block's share (none for some blocks of a cluster)
+    const int here = min(cur.tiles - cur.tile, count - done);
 
-    float sc[NT][2];                                 // log2(e) scale of heads 2t and 2t + 1
-#pragma unroll
-    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = p.scale_log2;
+    float sc[2] = {p.scale_log2, p.scale_log2};       // log2(e) scale of heads 2t and 2t + 1
     if constexpr (T::F8) {
-      const float ks = kscale;
+      float up = 1.f;
+      if (p.q_bf16) {
+        float top = 0.f;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float up = 1.f;
-        if (p.q_bf16) {
-          float top = 0.f;
+        for (int i = 0; i < DT; ++i) {
 #pragma unroll
-          for (int i = 0; i < DT; ++i) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 f = unpack2<true>(qf[i][n][e]);
-              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^e <= top < 2^(e + 1); e is kept where both 2^e and 2^-e are normal (an infinite or NaN q stays one)
-          const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
-          up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-          for (int i = 0; i < DT; ++i) {
-#pragma unroll
-            for (int e2 = 0; e2 < 2; ++e2) {
-              const float2 f = unpack2<true>(qf[i][n][e2]);
-              qf[i][n][e2] = pack2<false>(f.x * down, f.y * down);
-            }
+          for (int e = 0; e < 2; ++e) {
+            const float2 f = unpack2<true>(qf[i][e]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
-        sc[n][0] *= ks * __shfl_sync(0xffffffffu, up, 8 * t);        // head 2t is lane group g = 2t
-        sc[n][1] *= ks * __shfl_sync(0xffffffffu, up, 8 * t + 4);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e <= top < 2^(e + 1); e is kept where both 2^e and 2^-e are normal (an infinite or NaN q stays one)
+        const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
+        up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 f = unpack2<true>(qf[i][x]);
+            qf[i][x] = pack2<false>(f.x * down, f.y * down);
+          }
+        }
       }
+      sc[0] *= kscale * __shfl_sync(0xffffffffu, up, 8 * t);         // head 2t is lane group g = 2t
+      sc[1] *= kscale * __shfl_sync(0xffffffffu, up, 8 * t + 4);
     }
 
-    float m[NT][2], l[NT][2], o[DT][NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
-    }
-
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[DT][4] = {};
     for (int it = 0; it < here; ++it) {
       cp_async_wait<S - 2>();
-      __syncwarp();
+      ring_sync();
       load_tile(stage == 0 ? S - 1 : stage - 1);      // the buffer that the last turn read
-      const int k0 = cur.begin + (cur.tile + it) * T::TILE + warp * KT;
+      const int k0 = cur.begin + (cur.tile + it) * T::TILE + w * KT;
       const uint32_t kb = ring + stage * T::BUF, vb = kb + KT * ROW;
       if (k0 < cur.end) {
-        float s[MT][NT][4], s2[MT][NT][4];            // two chains of dependent MMAs
+        float s[MT][4], s2[MT][4];                    // two chains of dependent MMAs
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][n][e] = s2[j][n][e] = 0.f;
-          }
+          for (int e = 0; e < 4; ++e) s[j][e] = s2[j][e] = 0.f;
           const int r = 16 * j + (lane & 15);
           if constexpr (T::F8) {
 #pragma unroll
             for (int i = 0; i < DT; i += 2) {
-              uint32_t w[4];
-              ldsm4(kb + at<ROW>(r, i + (lane >> 4)), w);
+              uint32_t x[4];
+              ldsm4(kb + at<ROW>(r, i + (lane >> 4)), x);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint32_t a[4] = {widen_lo(w[2 * e]), widen_lo(w[2 * e + 1]), widen_hi(w[2 * e]), widen_hi(w[2 * e + 1])};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma<false>(e ? s2[j][n] : s[j][n], a, qf[i + e][n][0], qf[i + e][n][1]);
+                const uint32_t a[4] = {widen_lo(x[2 * e]), widen_lo(x[2 * e + 1]), widen_hi(x[2 * e]), widen_hi(x[2 * e + 1])};
+                mma<false>(e ? s2[j] : s[j], a, qf[i + e][0], qf[i + e][1]);
               }
             }
           } else {
@@ -655,8 +673,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
             for (int i = 0; i < DT; ++i) {
               uint32_t a[4];
               ldsm4(kb + at<ROW>(r, 2 * i + (lane >> 4)), a);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma<T::BF16>(i & 1 ? s2[j][n] : s[j][n], a, qf[i][n][0], qf[i][n][1]);
+              mma<T::BF16>(i & 1 ? s2[j] : s[j], a, qf[i][0], qf[i][1]);
             }
           }
         }
@@ -664,89 +681,74 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
         const int live = cur.end - k0, early = cur.first - k0;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
+          const int r = 16 * j + g;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][n][e] = (s[j][n][e] + s2[j][n][e]) * sc[n][e & 1];
-            if (live < KT) {
-              const int r = 16 * j + g;
-              if (r >= live) s[j][n][0] = s[j][n][1] = -INFINITY;
-              if (r + 8 >= live) s[j][n][2] = s[j][n][3] = -INFINITY;
-            }
-            if (early > 0) {
-              const int r = 16 * j + g;
-              if (r < early) s[j][n][0] = s[j][n][1] = -INFINITY;
-              if (r + 8 < early) s[j][n][2] = s[j][n][3] = -INFINITY;
-            }
+          for (int e = 0; e < 4; ++e) s[j][e] = (s[j][e] + s2[j][e]) * sc[e & 1];
+          if (live < KT) {
+            if (r >= live) s[j][0] = s[j][1] = -INFINITY;
+            if (r + 8 >= live) s[j][2] = s[j][3] = -INFINITY;
+          }
+          if (early > 0) {
+            if (r < early) s[j][0] = s[j][1] = -INFINITY;
+            if (r + 8 < early) s[j][2] = s[j][3] = -INFINITY;
           }
         }
         bool moved = false;
-        float al[NT][2];
+        float al[2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int e = 0; e < 2; ++e) {
+          float top = m[e];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float top = m[n][e];
+          for (int j = 0; j < MT; ++j) top = fmaxf(top, fmaxf(s[j][e], s[j][e + 2]));
 #pragma unroll
-            for (int j = 0; j < MT; ++j) top = fmaxf(top, fmaxf(s[j][n][e], s[j][n][e + 2]));
+          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          moved |= top != m[e];
+          // no key seen so far scored above -inf: any finite base will do
+          const float base = top == -INFINITY ? 0.f : top;
+          al[e] = exp2_approx(m[e] - base);
+          m[e] = top;
+          float sum = 0.f;
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            moved |= top != m[n][e];
-            // no key seen so far scored above -inf: any finite base will do
-            const float base = top == -INFINITY ? 0.f : top;
-            al[n][e] = exp2_approx(m[n][e] - base);
-            m[n][e] = top;
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              s[j][n][e] = exp2_approx(s[j][n][e] - (base - T::POFF));
-              s[j][n][e + 2] = exp2_approx(s[j][n][e + 2] - (base - T::POFF));
-              sum += s[j][n][e] + s[j][n][e + 2];
-            }
-            l[n][e] = l[n][e] * al[n][e] + sum;
+          for (int j = 0; j < MT; ++j) {
+            s[j][e] = exp2_approx(s[j][e] - (base - T::POFF));
+            s[j][e + 2] = exp2_approx(s[j][e + 2] - (base - T::POFF));
+            sum += s[j][e] + s[j][e + 2];
           }
+          l[e] = l[e] * al[e] + sum;
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int i = 0; i < DT; ++i) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              o[i][n][0] *= al[n][0];
-              o[i][n][1] *= al[n][1];
-              o[i][n][2] *= al[n][0];
-              o[i][n][3] *= al[n][1];
-            }
+            o[i][0] *= al[0];
+            o[i][1] *= al[1];
+            o[i][2] *= al[0];
+            o[i][3] *= al[1];
           }
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-          uint32_t ph[NT][2], pl[NT][2];
+          uint32_t ph[2], pl[2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float x = s[j][n][2 * e], y = s[j][n][2 * e + 1];
-              const uint32_t hi = pack2<T::BF16>(x, y);
-              const float2 back = unpack2<T::BF16>(hi);
-              ph[n][e] = transpose8x8(hi);
-              pl[n][e] = transpose8x8(pack2<T::BF16>(x - back.x, y - back.y));
-            }
+          for (int e = 0; e < 2; ++e) {
+            const float x = s[j][2 * e], y = s[j][2 * e + 1];
+            const uint32_t hi = pack2<T::BF16>(x, y);
+            const float2 back = unpack2<T::BF16>(hi);
+            ph[e] = transpose8x8(hi);
+            pl[e] = transpose8x8(pack2<T::BF16>(x - back.x, y - back.y));
           }
           if constexpr (T::F8) {
             const int r = 16 * j + (lane & 15);
 #pragma unroll
             for (int i = 0; i < DT; i += 2) {
-              uint32_t w[4];
-              ldsm4t(vb + at<ROW>(r, i + (lane >> 4)), w);
+              uint32_t x[4];
+              ldsm4t(vb + at<ROW>(r, i + (lane >> 4)), x);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 // bytes (key 2t: d, d + 1; key 2t + 1: d, d + 1) -> (d of both keys, d + 1 of both keys)
-                const uint32_t x = __byte_perm(w[2 * e], 0, 0x3120), y = __byte_perm(w[2 * e + 1], 0, 0x3120);
-                const uint32_t a[4] = {widen_lo(x), widen_hi(x), widen_lo(y), widen_hi(y)};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma<false>(o[i + e][n], a, ph[n][0], ph[n][1]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma<false>(o[i + e][n], a, pl[n][0], pl[n][1]);
+                const uint32_t y = __byte_perm(x[2 * e], 0, 0x3120), z = __byte_perm(x[2 * e + 1], 0, 0x3120);
+                const uint32_t a[4] = {widen_lo(y), widen_hi(y), widen_lo(z), widen_hi(z)};
+                mma<false>(o[i + e], a, ph[0], ph[1]);
+                mma<false>(o[i + e], a, pl[0], pl[1]);
               }
             }
           } else {
@@ -757,12 +759,9 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) ldsm4t(vb + at<ROW>(r, 2 * (i + e) + ((lane >> 3) & 1)), a[e]);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
+              for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e], a[e], ph[0], ph[1]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e][n], a[e], ph[n][0], ph[n][1]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e][n], a[e], pl[n][0], pl[n][1]);
-              }
+              for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e], a[e], pl[0], pl[1]);
             }
           }
         }
@@ -772,61 +771,63 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     done += here;
 
     // ---- the warps meet: each leaves (m, l, o) in shared memory
-    float* const mo = meet + warp * (T::MEET / 4);
+    float* const mo = meet + w * (T::MEET / 4);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+      const int h = 8 * hw + 2 * t + e;
+      if (g == 0) {
+        mo[h] = m[e];
+        mo[T::HEADS + h] = l[e];
+      }
+      float* row = mo + 2 * T::HEADS + h * T::OPITCH;
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
-        const int h = 8 * n + 2 * t + e;
-        if (g == 0) {
-          mo[h] = m[n][e];
-          mo[T::HEADS + h] = l[n][e];
-        }
-        float* row = mo + 2 * T::HEADS + h * T::OPITCH;
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-          if constexpr (T::F8) {
-            *reinterpret_cast<float2*>(row + 16 * i + 2 * g) = make_float2(o[i][n][e], o[i][n][e + 2]);
-          } else {
-            row[16 * i + g] = o[i][n][e];
-            row[16 * i + g + 8] = o[i][n][e + 2];
-          }
+      for (int i = 0; i < DT; ++i) {
+        if constexpr (T::F8) {
+          *reinterpret_cast<float2*>(row + 16 * i + 2 * g) = make_float2(o[i][e], o[i][e + 2]);
+        } else {
+          row[16 * i + g] = o[i][e];
+          row[16 * i + g + 8] = o[i][e + 2];
         }
       }
     }
     const Segment seg = cur;
     const int sh0 = h0, sheads = heads;
     const float vs = vscale;
-    const bool whole = !starts_before && seg.tile + here == seg.tiles, second = !starts_before;
+    const bool whole = !CL && !starts_before && seg.tile + here == seg.tiles, second = !starts_before;
     const long long first = t0 + (done - here) - seg.tile;      // the place of its first tile
-    ++done;                                           // the next segment's first place
-    starts_before = false;
-    cur.tile = 0;
-    if (++cur.h == HG) {
-      cur.h = 0;
-      ++cur.b;
-      if (done < count) seg_keys(p, __ldg(p.lens + cur.b), T::TILE, cur);
+    if constexpr (CL) {
+      cp_async_wait<0>();                             // the ring is where the block's result goes
+    } else {
+      ++done;                                         // the next segment's first place
+      starts_before = false;
+      cur.tile = 0;
+      if (++cur.h == HG) {
+        cur.h = 0;
+        ++cur.b;
+        if (done < count) seg_keys(p, __ldg(p.lens + cur.b), T::TILE, cur);
+      }
+      if (done < count) fetch_q();
     }
-    if (done < count) fetch_q();
     __syncthreads();
-    float* const part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + second) * attn_partial_floats(T::HEADS, D);
-    for (int x = tid; x < sheads * (D / 4); x += kAttnWarps * 32) {
+    float* const part = CL ? reinterpret_cast<float*>(smem)
+                           : p.partials + (static_cast<size_t>(blockIdx.x) * 2 + second) * attn_partial_floats(T::HEADS, D);
+    for (int x = tid; x < sheads * (D / 4); x += T::THREADS) {
       const int h = x / (D / 4), d = 4 * (x % (D / 4));
-      float mw[kAttnWarps], top = -INFINITY;
+      float mw[kAttnRings], top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
-        mw[w] = meet[w * (T::MEET / 4) + h];
-        top = fmaxf(top, mw[w]);
+      for (int r = 0; r < kAttnRings; ++r) {
+        mw[r] = meet[r * (T::MEET / 4) + h];
+        top = fmaxf(top, mw[r]);
       }
       const float base = top == -INFINITY ? 0.f : top;
       float sum = 0.f;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
-        const float* q = meet + w * (T::MEET / 4) + T::HEADS;
-        const float f = exp2_approx(mw[w] - base);
+      for (int r = 0; r < kAttnRings; ++r) {
+        const float* q = meet + r * (T::MEET / 4) + T::HEADS;
+        const float f = exp2_approx(mw[r] - base);
         const float4 v = *reinterpret_cast<const float4*>(q + T::HEADS + h * T::OPITCH + d);
         sum += f * q[h];
         a.x += f * v.x;
@@ -844,20 +845,50 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
         *reinterpret_cast<float4*>(part + 2 * T::HEADS + h * D + d) = a;
       }
     }
+    if constexpr (CL) {
+      // ---- the cluster's blocks join: each takes an eighth of the channels
+      cluster_sync();
+      const uint32_t mine = smem_u32(smem), rank = blockIdx.x % kAttnCluster;
+      for (int x = rank * T::THREADS + tid; x < sheads * (D / 4); x += kAttnCluster * T::THREADS) {
+        const int h = x / (D / 4), d = 4 * (x % (D / 4));
+        float mr[kAttnCluster], lr[kAttnCluster], top = -INFINITY;
+        float4 v[kAttnCluster];
+#pragma unroll
+        for (int r = 0; r < kAttnCluster; ++r) {
+          mr[r] = ld_cluster(mine + 4 * h, r);
+          lr[r] = ld_cluster(mine + 4 * (T::HEADS + h), r);
+          v[r] = ld_cluster4(mine + 4 * (2 * T::HEADS + h * D + d), r);
+          top = fmaxf(top, mr[r]);
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < kAttnCluster; ++r) {
+          const float f = exp2_approx(mr[r] - base);
+          sum += f * lr[r];
+          a.x += f * v[r].x;
+          a.y += f * v[r].y;
+          a.z += f * v[r].z;
+          a.w += f * v[r].w;
+        }
+        write_out<T>(p, seg.b, sh0 + h, d, D, a, top, sum, vs);
+      }
+      cluster_sync();                                 // no block leaves while another reads its result
+      return;
+    }
     __syncthreads();          // the partial is written, and `meet` is free again
-    if (!whole) {
+    if (!whole && tid == 0) {
       // Blocks c0 .. c0 + n - 1 share this segment. Thread 0 says that this block's partial is there; who
       // joins them is looked up when the block has nothing else to do.
-      if (tid == 0) {
-        const int c0 = static_cast<int>(divide(first, share));
-        const int n = static_cast<int>(divide(first + seg.tiles - 1, share)) - c0 + 1;
-        // one join of all where they fit, else a tree of two levels, or of more where its joins would not fit
-        const int fan = n <= T::FAN ? n : min(T::FAN, static_cast<int>(ceilf(sqrtf(static_cast<float>(n)))));
-        const Shared s{c0, n, fan, seg.b, sh0, sheads, vs};
-        s_pend[second] = s;
-        const int2 g = join_group(s, 1);
-        s_last[second] = count_in(p.counters + c0 + g.x, g.y);
-      }
+      const int c0 = static_cast<int>(divide(first, share));
+      const int n = static_cast<int>(divide(first + seg.tiles - 1, share)) - c0 + 1;
+      // one join of all where they fit, else a tree of two levels, or of more where its joins would not fit
+      const int fan = n <= T::FAN ? n : min(T::FAN, static_cast<int>(ceilf(sqrtf(static_cast<float>(n)))));
+      const Shared s{c0, n, fan, seg.b, sh0, sheads, vs};
+      s_pend[second] = s;
+      const int2 group = join_group(s, 1);
+      s_last[second] = count_in(p.counters + c0 + group.x, group.y);
     }
   }
   cp_async_wait<0>();
@@ -869,38 +900,44 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     if (s_pend[e].n > 0 && s_last[e]) finish<T, D>(p, s_pend[e], smem, meet, s_last + e, smem_u32(&s_bar), phase);
 }
 
-template <int CACHE, int D, int NT>
+template <int CACHE, int D, int HW>
 cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
-  using T = Traits<CACHE, D, NT>;
+  using T = Traits<CACHE, D, HW>;
   static int per_sm[64];                             // blocks per SM, by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int n = __atomic_load_n(&per_sm[dev], __ATOMIC_RELAXED);
   if (n == 0) {
-    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, HW, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<CACHE, D, NT>, kAttnWarps * 32, T::SMEM);
+    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, HW, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    if (e != cudaSuccess) return e;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<CACHE, D, HW, false>, T::THREADS, T::SMEM);
     if (e != cudaSuccess) return e;
     n = n < 1 ? 1 : n > kAttnMaxBlocksPerSm ? kAttnMaxBlocksPerSm : n;
     __atomic_store_n(&per_sm[dev], n, __ATOMIC_RELAXED);
   }
   const long long keys = p.window > 0 && p.window < p.max_len ? p.window : p.max_len;
-  // most places that the list can have; a window's tiles may begin up to 15 keys before it
-  const long long most = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv * ((keys + 15 + T::TILE - 1) / T::TILE + 1);
+  const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv;
   long long grid = static_cast<long long>(sms) * n;
   if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
+  // Few and short segments: a cluster for each, while they all fit on half of the GPU at once and a block has two tiles at most
+  if (segments * kAttnCluster * 2 <= grid && keys <= 2ll * kAttnCluster * T::TILE)
+    return launch_pdl_cluster(paged_attention_kernel<CACHE, D, HW, true>, dim3(static_cast<unsigned>(segments * kAttnCluster)),
+                              dim3(T::THREADS), T::SMEM, st, kAttnCluster, p);
+  // most places that the list can have; a window's tiles may begin up to 15 keys before it
+  const long long most = segments * ((keys + 15 + T::TILE - 1) / T::TILE + 1);
   if (grid > most) grid = most;
-  return launch_pdl(paged_attention_kernel<CACHE, D, NT>, dim3(static_cast<unsigned>(grid)), dim3(kAttnWarps * 32),
-                    T::SMEM, st, p);
+  return launch_pdl(paged_attention_kernel<CACHE, D, HW, false>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
 }
 
 template <int CACHE>
-cudaError_t launch_dim(const AttnParams& p, int dim, int nt, int sms, cudaStream_t st) {
+cudaError_t launch_dim(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st) {
   switch (dim) {
-    case 64: return nt == 1 ? launch<CACHE, 64, 1>(p, sms, st) : nt == 2 ? launch<CACHE, 64, 2>(p, sms, st) : launch<CACHE, 64, 4>(p, sms, st);
-    case 128: return nt == 1 ? launch<CACHE, 128, 1>(p, sms, st) : nt == 2 ? launch<CACHE, 128, 2>(p, sms, st) : launch<CACHE, 128, 4>(p, sms, st);
-    case 256: return nt == 1 ? launch<CACHE, 256, 1>(p, sms, st) : launch<CACHE, 256, 2>(p, sms, st);
+    case 64: return hw == 1 ? launch<CACHE, 64, 1>(p, sms, st) : hw == 2 ? launch<CACHE, 64, 2>(p, sms, st) : launch<CACHE, 64, 4>(p, sms, st);
+    case 128: return hw == 1 ? launch<CACHE, 128, 1>(p, sms, st) : hw == 2 ? launch<CACHE, 128, 2>(p, sms, st) : launch<CACHE, 128, 4>(p, sms, st);
+    case 256: return hw == 1 ? launch<CACHE, 256, 1>(p, sms, st) : launch<CACHE, 256, 2>(p, sms, st);
     default: return cudaErrorInvalidValue;
   }
 }

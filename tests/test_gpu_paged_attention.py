@@ -119,6 +119,15 @@ def test_one_request_split_over_blocks(d, cache, n):
     assert torch.equal(a, b)        # the order in which blocks arrive does not reach the result
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cache", ["bf16", "f8"])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (6, 1), (12, 1), (20, 2), (33, 1)])
+def test_few_short_requests(d, cache, hq, hkv):
+    """Small calls, in which a cluster of blocks shares each segment."""
+    for lens, window in (([1], 0), ([0, 70], 0), ([700, 64], 0), ([900], 100), ([33, 0], 1)):
+        check(*build(d + hq + len(lens), lens, hq, hkv, d, 16, cache), lens, window=window)
+
+
 def test_many_requests_and_workspace_reuse():
     rng = np.random.default_rng(3)
     lens = [int(x) for x in rng.integers(0, 40, 700)]
