@@ -20,8 +20,8 @@
 // reach the result). At most two of a block's segments are cut, the first and
 // the last, so the workspace depends on the grid alone.
 //
-// Tiles. A tile's keys go through four rings of STAGES buffers (cp.async), KT keys each. A ring has one warp for
-// every 8 query heads of the segment, up to four, which fill it together and read it each for its
+// Tiles. A tile's keys go through four rings of STAGES buffers (cp.async), KT keys each. A ring has a warp for
+// up to 8 or 16 query heads of the segment, or two warps, which fill it together and read it each for its
 // heads; there is no block barrier in the loop. Each warp keeps its own (m, l, o);
 // the rings meet once per segment. The scores are computed transposed, S^T = K q^T: the
 // keys are the rows of the MMA and 8 query heads its columns, so 8 heads need
@@ -95,9 +95,9 @@ __host__ __device__ constexpr size_t attn_partial_floats(int heads, int dim) {
   return static_cast<size_t>(heads) * (dim + 2);
 }
 
-cudaError_t launch_attn_bf16(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st);
-cudaError_t launch_attn_f16(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st);
-cudaError_t launch_attn_f8(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st);
+cudaError_t launch_attn_bf16(const AttnParams& p, int dim, int columns, int sms, cudaStream_t st);
+cudaError_t launch_attn_f16(const AttnParams& p, int dim, int columns, int sms, cudaStream_t st);
+cudaError_t launch_attn_f8(const AttnParams& p, int dim, int columns, int sms, cudaStream_t st);
 
 namespace attn {
 
@@ -192,7 +192,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-template <int CACHE, int D, int HW>
+// HW warps to a ring, 8 NT query heads to a warp
+template <int CACHE, int D, int HW, int NT>
 struct Traits {
   static constexpr bool F8 = CACHE == kCacheF8;
   static constexpr bool BF16 = CACHE == kCacheBf16;      // the MMA's operand type (f16 otherwise)
@@ -201,13 +202,13 @@ struct Traits {
   static constexpr int KT = 4096 / ROW > 16 ? 4096 / ROW : 16;   // keys of a ring's buffer: 4 KB of K (8 for 512-byte rows)
   static constexpr int TILE = kAttnRings * KT;
   static constexpr int BUF = 2 * KT * ROW;
-  static constexpr int HEADS = 8 * HW;
+  static constexpr int HEADS = 8 * HW * NT;
   static constexpr int OPITCH = D + 4;                   // floats; the warps' o meet here, conflict-free
   static constexpr int MEET = (HEADS * OPITCH + 2 * HEADS) * 4;
   // buffers of a ring: up to three where two blocks share an SM (whose 228 KB hold a KB more for each
   // block), else as many as fit
   static constexpr int stages() {
-    for (int s = 3; s >= 2 && HW < 4; --s)             // 512 threads of 128 registers are alone on their SM
+    for (int s = 3; s >= 2 && HW * NT < 4; --s)        // 256 threads of 255 registers are alone on their SM
       if (kAttnRings * (s * BUF + MEET) <= 115500) return s;
     int s = 6;
     while (kAttnRings * (s * BUF + MEET) > 231000) --s;
@@ -217,7 +218,7 @@ struct Traits {
   static constexpr int SMEM = kAttnRings * (STAGES * BUF + MEET);
   // partials that one join takes: what the rings hold, and no more than are quick to copy
   static constexpr int FIT = kAttnRings * STAGES * BUF / (HEADS * (D + 2) * 4), FAN = FIT < 16 ? FIT : 16;
-  static constexpr int BLOCKS = HW == 4 || SMEM > 115500 ? 1 : SMEM > 75000 ? 2 : 3;     // per SM
+  static constexpr int BLOCKS = HW * NT == 4 || SMEM > 115500 ? 1 : SMEM > 75000 ? 2 : 3;     // per SM
   // 2^8 in the probabilities keeps an f16 low part of the small ones out of the subnormals
   static constexpr float POFF = BF16 ? 0.f : 8.f;
 };
@@ -397,19 +398,18 @@ __device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uin
   }
 }
 
-// What follows the queries, the keys and the values of one segment through a warp; 8 query heads.
 // CL: eight blocks, a cluster, take a segment, and join it through their shared memory.
-template <int CACHE, int D, int HW, bool CL>
-__global__ void __launch_bounds__(kAttnRings * HW * 32, Traits<CACHE, D, HW>::BLOCKS)
+template <int CACHE, int D, int HW, int NT, bool CL>
+__global__ void __launch_bounds__(kAttnRings * HW * 32, Traits<CACHE, D, HW, NT>::BLOCKS)
 paged_attention_kernel(const __grid_constant__ AttnParams p) {
-  using T = Traits<CACHE, D, HW>;
+  using T = Traits<CACHE, D, HW, NT>;
   constexpr int KT = T::KT, ROW = T::ROW, MT = KT / 16, DT = D / 16, S = T::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_bar;
   __shared__ int s_last[2];
   __shared__ Shared s_pend[2];                        // segments shared with other blocks: the first, the last
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int w = warp / HW, hw = warp % HW;            // the warp's ring, and its 8 heads
+  const int w = warp / HW, hw = warp % HW;            // the warp's ring, and its 8 NT heads
   const int HG = p.kv_heads * p.groups_per_kv;
 
   pdl_wait_prior();
@@ -576,7 +576,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
   bool starts_before = cur.tile > 0;
   // queries as B operands: k = 16 channels, n = 8 heads. For an 8-bit cache thread t takes channels
   // 4t .. 4t + 3, as its ldmatrix of K gives them. Asked for while the segment before is being finished.
-  uint32_t qf[DT][2];
+  uint32_t qf[DT][NT][2];
   int h0, heads;
   float kscale = 1.f, vscale = 1.f;
   auto fetch_q = [&]() {
@@ -587,17 +587,21 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       kscale = __ldg(p.k_scale + kvh);
       vscale = __ldg(p.v_scale + kvh);
     }
-    const uint16_t* qr = p.q + cur.b * p.ldq + static_cast<int64_t>(h0 + hw * 8 + g) * D;
-    const bool live = hw * 8 + g < heads;
 #pragma unroll
-    for (int i = 0; i < DT; ++i) {
-      if constexpr (T::F8) {
-        const uint2 x = live ? __ldg(reinterpret_cast<const uint2*>(qr + 16 * i + 4 * t)) : make_uint2(0, 0);
-        qf[i][0] = x.x;
-        qf[i][1] = x.y;
-      } else {
-        qf[i][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 2 * t)) : 0u;
-        qf[i][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 8 + 2 * t)) : 0u;
+    for (int n = 0; n < NT; ++n) {
+      const int h = 8 * (hw * NT + n) + g;
+      const uint16_t* qr = p.q + cur.b * p.ldq + static_cast<int64_t>(h0 + h) * D;
+      const bool live = h < heads;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        if constexpr (T::F8) {
+          const uint2 x = live ? __ldg(reinterpret_cast<const uint2*>(qr + 16 * i + 4 * t)) : make_uint2(0, 0);
+          qf[i][n][0] = x.x;
+          qf[i][n][1] = x.y;
+        } else {
+          qf[i][n][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 2 * t)) : 0u;
+          qf[i][n][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * i + 8 + 2 * t)) : 0u;
+        }
       }
     }
   };
@@ -611,39 +615,50 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     // tiles of this segment in this block's share (none for some blocks of a cluster)
     const int here = min(cur.tiles - cur.tile, count - done);
 
-    float sc[2] = {p.scale_log2, p.scale_log2};       // log2(e) scale of heads 2t and 2t + 1
-    if constexpr (T::F8) {
-      float up = 1.f;
-      if (p.q_bf16) {
-        float top = 0.f;
+    float sc[NT][2];                                  // log2(e) scale of heads 2t and 2t + 1
 #pragma unroll
-        for (int i = 0; i < DT; ++i) {
+    for (int n = 0; n < NT; ++n) {
+      sc[n][0] = sc[n][1] = p.scale_log2;
+      if constexpr (T::F8) {
+        float up = 1.f;
+        if (p.q_bf16) {
+          float top = 0.f;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 f = unpack2<true>(qf[i][e]);
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          for (int i = 0; i < DT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 f = unpack2<true>(qf[i][n][e]);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^e <= top < 2^(e + 1); e is kept where both 2^e and 2^-e are normal (an infinite or NaN q stays one)
+          const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
+          up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < DT; ++i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float2 f = unpack2<true>(qf[i][n][x]);
+              qf[i][n][x] = pack2<false>(f.x * down, f.y * down);
+            }
           }
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e <= top < 2^(e + 1); e is kept where both 2^e and 2^-e are normal (an infinite or NaN q stays one)
-        const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
-        up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float2 f = unpack2<true>(qf[i][x]);
-            qf[i][x] = pack2<false>(f.x * down, f.y * down);
-          }
-        }
+        sc[n][0] *= kscale * __shfl_sync(0xffffffffu, up, 8 * t);    // head 2t is lane group g = 2t
+        sc[n][1] *= kscale * __shfl_sync(0xffffffffu, up, 8 * t + 4);
       }
-      sc[0] *= kscale * __shfl_sync(0xffffffffu, up, 8 * t);         // head 2t is lane group g = 2t
-      sc[1] *= kscale * __shfl_sync(0xffffffffu, up, 8 * t + 4);
     }
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {}, o[DT][4] = {};
+    float m[NT][2], l[NT][2], o[DT][NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+    }
     for (int it = 0; it < here; ++it) {
       cp_async_wait<S - 2>();
       ring_sync();
@@ -651,11 +666,13 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       const int k0 = cur.begin + (cur.tile + it) * T::TILE + w * KT;
       const uint32_t kb = ring + stage * T::BUF, vb = kb + KT * ROW;
       if (k0 < cur.end) {
-        float s[MT][4], s2[MT][4];                    // two chains of dependent MMAs
+        float s[MT][NT][4], s2[MT][NT][4];            // two chains of dependent MMAs
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[j][e] = s2[j][e] = 0.f;
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][n][e] = s2[j][n][e] = 0.f;
           const int r = 16 * j + (lane & 15);
           if constexpr (T::F8) {
 #pragma unroll
@@ -665,7 +682,8 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const uint32_t a[4] = {widen_lo(x[2 * e]), widen_lo(x[2 * e + 1]), widen_hi(x[2 * e]), widen_hi(x[2 * e + 1])};
-                mma<false>(e ? s2[j] : s[j], a, qf[i + e][0], qf[i + e][1]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma<false>(e ? s2[j][n] : s[j][n], a, qf[i + e][n][0], qf[i + e][n][1]);
               }
             }
           } else {
@@ -673,68 +691,78 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
             for (int i = 0; i < DT; ++i) {
               uint32_t a[4];
               ldsm4(kb + at<ROW>(r, 2 * i + (lane >> 4)), a);
-              mma<T::BF16>(i & 1 ? s2[j] : s[j], a, qf[i][0], qf[i][1]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma<T::BF16>(i & 1 ? s2[j][n] : s[j][n], a, qf[i][n][0], qf[i][n][1]);
             }
           }
         }
         // rows 16 j + g (elements 0, 1) and + 8 (2, 3); columns: heads 2t, 2t + 1
         const int live = cur.end - k0, early = cur.first - k0;
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const int r = 16 * j + g;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[j][e] = (s[j][e] + s2[j][e]) * sc[e & 1];
-          if (live < KT) {
-            if (r >= live) s[j][0] = s[j][1] = -INFINITY;
-            if (r + 8 >= live) s[j][2] = s[j][3] = -INFINITY;
-          }
-          if (early > 0) {
-            if (r < early) s[j][0] = s[j][1] = -INFINITY;
-            if (r + 8 < early) s[j][2] = s[j][3] = -INFINITY;
-          }
-        }
         bool moved = false;
-        float al[2];
+        float al[NT][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float top = m[e];
-#pragma unroll
-          for (int j = 0; j < MT; ++j) top = fmaxf(top, fmaxf(s[j][e], s[j][e + 2]));
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          moved |= top != m[e];
-          // no key seen so far scored above -inf: any finite base will do
-          const float base = top == -INFINITY ? 0.f : top;
-          al[e] = exp2_approx(m[e] - base);
-          m[e] = top;
-          float sum = 0.f;
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int j = 0; j < MT; ++j) {
-            s[j][e] = exp2_approx(s[j][e] - (base - T::POFF));
-            s[j][e + 2] = exp2_approx(s[j][e + 2] - (base - T::POFF));
-            sum += s[j][e] + s[j][e + 2];
+            const int r = 16 * j + g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][n][e] = (s[j][n][e] + s2[j][n][e]) * sc[n][e & 1];
+            if (live < KT) {
+              if (r >= live) s[j][n][0] = s[j][n][1] = -INFINITY;
+              if (r + 8 >= live) s[j][n][2] = s[j][n][3] = -INFINITY;
+            }
+            if (early > 0) {
+              if (r < early) s[j][n][0] = s[j][n][1] = -INFINITY;
+              if (r + 8 < early) s[j][n][2] = s[j][n][3] = -INFINITY;
+            }
           }
-          l[e] = l[e] * al[e] + sum;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = m[n][e];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) top = fmaxf(top, fmaxf(s[j][n][e], s[j][n][e + 2]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            moved |= top != m[n][e];
+            // no key seen so far scored above -inf: any finite base will do
+            const float base = top == -INFINITY ? 0.f : top;
+            al[n][e] = exp2_approx(m[n][e] - base);
+            m[n][e] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              s[j][n][e] = exp2_approx(s[j][n][e] - (base - T::POFF));
+              s[j][n][e + 2] = exp2_approx(s[j][n][e + 2] - (base - T::POFF));
+              sum += s[j][n][e] + s[j][n][e + 2];
+            }
+            l[n][e] = l[n][e] * al[n][e] + sum;
+          }
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int i = 0; i < DT; ++i) {
-            o[i][0] *= al[0];
-            o[i][1] *= al[1];
-            o[i][2] *= al[0];
-            o[i][3] *= al[1];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              o[i][n][0] *= al[n][0];
+              o[i][n][1] *= al[n][1];
+              o[i][n][2] *= al[n][0];
+              o[i][n][3] *= al[n][1];
+            }
           }
         }
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-          uint32_t ph[2], pl[2];
+          uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = s[j][2 * e], y = s[j][2 * e + 1];
-            const uint32_t hi = pack2<T::BF16>(x, y);
-            const float2 back = unpack2<T::BF16>(hi);
-            ph[e] = transpose8x8(hi);
-            pl[e] = transpose8x8(pack2<T::BF16>(x - back.x, y - back.y));
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x = s[j][n][2 * e], y = s[j][n][2 * e + 1];
+              const uint32_t hi = pack2<T::BF16>(x, y);
+              const float2 back = unpack2<T::BF16>(hi);
+              ph[n][e] = transpose8x8(hi);
+              pl[n][e] = transpose8x8(pack2<T::BF16>(x - back.x, y - back.y));
+            }
           }
           if constexpr (T::F8) {
             const int r = 16 * j + (lane & 15);
@@ -742,13 +770,19 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
             for (int i = 0; i < DT; i += 2) {
               uint32_t x[4];
               ldsm4t(vb + at<ROW>(r, i + (lane >> 4)), x);
+              uint32_t a[2][4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 // bytes (key 2t: d, d + 1; key 2t + 1: d, d + 1) -> (d of both keys, d + 1 of both keys)
                 const uint32_t y = __byte_perm(x[2 * e], 0, 0x3120), z = __byte_perm(x[2 * e + 1], 0, 0x3120);
-                const uint32_t a[4] = {widen_lo(y), widen_hi(y), widen_lo(z), widen_hi(z)};
-                mma<false>(o[i + e], a, ph[0], ph[1]);
-                mma<false>(o[i + e], a, pl[0], pl[1]);
+                a[e][0] = widen_lo(y), a[e][1] = widen_hi(y), a[e][2] = widen_lo(z), a[e][3] = widen_hi(z);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mma<false>(o[i + e][n], a[e], ph[n][0], ph[n][1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mma<false>(o[i + e][n], a[e], pl[n][0], pl[n][1]);
               }
             }
           } else {
@@ -759,9 +793,12 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) ldsm4t(vb + at<ROW>(r, 2 * (i + e) + ((lane >> 3) & 1)), a[e]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e], a[e], ph[0], ph[1]);
+              for (int n = 0; n < NT; ++n) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e], a[e], pl[0], pl[1]);
+                for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e][n], a[e], ph[n][0], ph[n][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma<T::BF16>(o[i + e][n], a[e], pl[n][0], pl[n][1]);
+              }
             }
           }
         }
@@ -773,22 +810,25 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     // ---- the warps meet: each leaves (m, l, o) in shared memory
     float* const mo = meet + w * (T::MEET / 4);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
-      const int h = 8 * hw + 2 * t + e;
-      if (g == 0) {
-        mo[h] = m[e];
-        mo[T::HEADS + h] = l[e];
-      }
-      float* row = mo + 2 * T::HEADS + h * T::OPITCH;
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        if constexpr (T::F8) {
-          *reinterpret_cast<float2*>(row + 16 * i + 2 * g) = make_float2(o[i][e], o[i][e + 2]);
-        } else {
-          row[16 * i + g] = o[i][e];
-          row[16 * i + g + 8] = o[i][e + 2];
+        for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+        const int h = 8 * (hw * NT + n) + 2 * t + e;
+        if (g == 0) {
+          mo[h] = m[n][e];
+          mo[T::HEADS + h] = l[n][e];
+        }
+        float* row = mo + 2 * T::HEADS + h * T::OPITCH;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          if constexpr (T::F8) {
+            *reinterpret_cast<float2*>(row + 16 * i + 2 * g) = make_float2(o[i][n][e], o[i][n][e + 2]);
+          } else {
+            row[16 * i + g] = o[i][n][e];
+            row[16 * i + g + 8] = o[i][n][e + 2];
+          }
         }
       }
     }
@@ -900,20 +940,20 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     if (s_pend[e].n > 0 && s_last[e]) finish<T, D>(p, s_pend[e], smem, meet, s_last + e, smem_u32(&s_bar), phase);
 }
 
-template <int CACHE, int D, int HW>
+template <int CACHE, int D, int HW, int NT>
 cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
-  using T = Traits<CACHE, D, HW>;
+  using T = Traits<CACHE, D, HW, NT>;
   static int per_sm[64];                             // blocks per SM, by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int n = __atomic_load_n(&per_sm[dev], __ATOMIC_RELAXED);
   if (n == 0) {
-    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, HW, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, HW, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, HW, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, HW, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<CACHE, D, HW, false>, T::THREADS, T::SMEM);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<CACHE, D, HW, NT, false>, T::THREADS, T::SMEM);
     if (e != cudaSuccess) return e;
     n = n < 1 ? 1 : n > kAttnMaxBlocksPerSm ? kAttnMaxBlocksPerSm : n;
     __atomic_store_n(&per_sm[dev], n, __ATOMIC_RELAXED);
@@ -924,20 +964,28 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
   if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
   // Few and short segments: a cluster for each, while they all fit on half of the GPU at once and a block has two tiles at most
   if (segments * kAttnCluster * 2 <= grid && keys <= 2ll * kAttnCluster * T::TILE)
-    return launch_pdl_cluster(paged_attention_kernel<CACHE, D, HW, true>, dim3(static_cast<unsigned>(segments * kAttnCluster)),
+    return launch_pdl_cluster(paged_attention_kernel<CACHE, D, HW, NT, true>, dim3(static_cast<unsigned>(segments * kAttnCluster)),
                               dim3(T::THREADS), T::SMEM, st, kAttnCluster, p);
   // most places that the list can have; a window's tiles may begin up to 15 keys before it
   const long long most = segments * ((keys + 15 + T::TILE - 1) / T::TILE + 1);
   if (grid > most) grid = most;
-  return launch_pdl(paged_attention_kernel<CACHE, D, HW, false>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
+  return launch_pdl(paged_attention_kernel<CACHE, D, HW, NT, false>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
 }
 
+// `columns`: 1, 2 or 4 times 8 query heads to a segment. A warp that takes 16 heads reads K and V half as often as two
+// that take 8 each, and has the registers for it up to 128 channels.
 template <int CACHE>
-cudaError_t launch_dim(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st) {
+cudaError_t launch_dim(const AttnParams& p, int dim, int columns, int sms, cudaStream_t st) {
   switch (dim) {
-    case 64: return hw == 1 ? launch<CACHE, 64, 1>(p, sms, st) : hw == 2 ? launch<CACHE, 64, 2>(p, sms, st) : launch<CACHE, 64, 4>(p, sms, st);
-    case 128: return hw == 1 ? launch<CACHE, 128, 1>(p, sms, st) : hw == 2 ? launch<CACHE, 128, 2>(p, sms, st) : launch<CACHE, 128, 4>(p, sms, st);
-    case 256: return hw == 1 ? launch<CACHE, 256, 1>(p, sms, st) : launch<CACHE, 256, 2>(p, sms, st);
+    case 64:
+      return columns == 1 ? launch<CACHE, 64, 1, 1>(p, sms, st)
+             : columns == 2 ? launch<CACHE, 64, 1, 2>(p, sms, st)
+                            : launch<CACHE, 64, 2, 2>(p, sms, st);
+    case 128:
+      return columns == 1 ? launch<CACHE, 128, 1, 1>(p, sms, st)
+             : columns == 2 ? launch<CACHE, 128, 1, 2>(p, sms, st)
+                            : launch<CACHE, 128, 2, 2>(p, sms, st);
+    case 256: return columns == 1 ? launch<CACHE, 256, 1, 1>(p, sms, st) : launch<CACHE, 256, 2, 1>(p, sms, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -3,8 +3,8 @@
 
 namespace tl {
 
-cudaError_t launch_attn_f16(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st) {
-  return attn::launch_dim<kCacheF16>(p, dim, hw, sms, st);
+cudaError_t launch_attn_f16(const AttnParams& p, int dim, int columns, int sms, cudaStream_t st) {
+  return attn::launch_dim<kCacheF16>(p, dim, columns, sms, st);
 }
 
 }  // namespace tl

@@ -3,8 +3,8 @@
 
 namespace tl {
 
-cudaError_t launch_attn_f8(const AttnParams& p, int dim, int hw, int sms, cudaStream_t st) {
-  return attn::launch_dim<kCacheF8>(p, dim, hw, sms, st);
+cudaError_t launch_attn_f8(const AttnParams& p, int dim, int columns, int sms, cudaStream_t st) {
+  return attn::launch_dim<kCacheF8>(p, dim, columns, sms, st);
 }
 
 }  // namespace tl

@@ -95,9 +95,9 @@ int check_cache(const tl_kv_cache* c) {
   return TL_OK;
 }
 
-// Query heads are taken in groups of 8 for each warp of a ring: the fewest of 1, 2 or 4 warps that hold the heads of one
-// key-value head, at most 2 for head_dim 256, whose output fills the registers.
-int attention_warps(int group, int dim) {
+// Query heads are taken in groups of 8, 16 or 32, columns of the MMA: the fewest that hold the heads of one
+// key-value head, at most 16 for head_dim 256, whose output fills the registers.
+int attention_columns(int group, int dim) {
   return group <= 8 ? 1 : group <= 16 || dim == 256 ? 2 : 4;
 }
 
@@ -379,7 +379,7 @@ int tl_paged_attention_workspace_size(int B, int q_heads, int kv_heads, int head
   int sms = 0;
   if ((r = num_sms(&sms)) != TL_OK) return r;
   const long long grid = sms * tl::kAttnMaxBlocksPerSm < tl::kAttnMaxGrid ? sms * tl::kAttnMaxBlocksPerSm : tl::kAttnMaxGrid;
-  const int heads = 8 * attention_warps(q_heads / kv_heads, head_dim);
+  const int heads = 8 * attention_columns(q_heads / kv_heads, head_dim);
   *bytes = tl::kAttnLevels * tl::kAttnMaxGrid * sizeof(int) + 2 * grid * tl::attn_partial_floats(heads, head_dim) * sizeof(float);
   return TL_OK;
 }
@@ -422,15 +422,15 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
   p.B = B, p.q_heads = q_heads, p.kv_heads = cache->kv_heads, p.group = q_heads / cache->kv_heads, p.window = window;
   p.q_bf16 = dtype == TL_BF16;
   p.runs16 = cache->page_size % 16 == 0;
-  const int hw = attention_warps(p.group, cache->head_dim);
-  p.groups_per_kv = (p.group + 8 * hw - 1) / (8 * hw);
+  const int columns = attention_columns(p.group, cache->head_dim);
+  p.groups_per_kv = (p.group + 8 * columns - 1) / (8 * columns);
   p.counters = static_cast<int*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + tl::kAttnLevels * tl::kAttnMaxGrid * sizeof(int));
   p.status = status;
   const cudaStream_t st = as_stream(stream);
-  const cudaError_t e = cache->dtype == TL_BF16  ? tl::launch_attn_bf16(p, cache->head_dim, hw, sms, st)
-                        : cache->dtype == TL_F16 ? tl::launch_attn_f16(p, cache->head_dim, hw, sms, st)
-                                                 : tl::launch_attn_f8(p, cache->head_dim, hw, sms, st);
+  const cudaError_t e = cache->dtype == TL_BF16  ? tl::launch_attn_bf16(p, cache->head_dim, columns, sms, st)
+                        : cache->dtype == TL_F16 ? tl::launch_attn_f16(p, cache->head_dim, columns, sms, st)
+                                                 : tl::launch_attn_f8(p, cache->head_dim, columns, sms, st);
   return e == cudaSuccess ? TL_OK : TL_ECUDA;
 }
 
