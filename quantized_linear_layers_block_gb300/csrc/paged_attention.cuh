@@ -85,8 +85,9 @@ struct AttnParams {
 constexpr int kAttnRings = 4;          // rings of key tiles in a block, each with HW warps
 constexpr int kAttnMaxBlocksPerSm = 4;
 constexpr int kAttnCluster = 8;        // blocks that share a segment of a small call
-constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join
-constexpr int kAttnLevels = 6;
+constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join tree
+constexpr int kAttnLevels = 2;
+constexpr int kJoinBytes = 320 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -216,8 +217,8 @@ struct Traits {
   }
   static constexpr int STAGES = stages();
   static constexpr int SMEM = kAttnRings * (STAGES * BUF + MEET);
-  // partials that one join takes: what the rings hold, and no more than are quick to copy
-  static constexpr int FIT = kAttnRings * STAGES * BUF / (HEADS * (D + 2) * 4), FAN = FIT < 16 ? FIT : 16;
+  // partials that the rings hold, at most a warp's lanes
+  static constexpr int HOLD = kAttnRings * STAGES * BUF / (HEADS * (D + 2) * 4), FIT = HOLD < 32 ? HOLD : 32;
   static constexpr int BLOCKS = HW * NT == 4 || SMEM > 115500 ? 1 : SMEM > 75000 ? 2 : 3;     // per SM
   // 2^8 in the probabilities keeps an f16 low part of the small ones out of the subnormals
   static constexpr float POFF = BF16 ? 0.f : 8.f;
@@ -252,9 +253,8 @@ __device__ __forceinline__ void seg_keys(const AttnParams& p, int len, int tile_
 }
 
 // A segment that n blocks share, from block c0 on: c0 began it (its second partial), the others found it
-// begun (their first). The partials are joined along a tree: up to `fan` neighbours by the last
-// of them to arrive, their results in the same way, and so on, so that the joins run on many SMs and none
-// reads more than its shared memory holds.
+// begun (their first). The partials are joined by the last block to arrive; where they are many, `fan` neighbours
+// by the last of them, and their results in the same way, so that the joins run on many SMs.
 struct Shared {
   int c0, n, fan, b, h0, heads;
   float v_scale;
@@ -275,87 +275,101 @@ __device__ __forceinline__ void write_out(const AttnParams& p, int b, int h, int
 // Called by one thread, after a barrier behind which all of the block's writes lie: counts this block in and
 // says whether it is the last of n. The counter is zero again then, and what the others wrote is visible.
 __device__ __forceinline__ int count_in(int* counter, int n) {
-  __threadfence();
-  const int last = atomicAdd(counter, 1) == n - 1;
-  if (last) {
-    *counter = 0;
-    __threadfence();
-  }
-  return last;
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  if (before != n - 1) return 0;
+  *counter = 0;
+  return 1;
 }
 
-// The group of partials that this block's belongs to when every `step`-th one is left: its first, and how many.
+// The group of partials that this block's belongs to when every `step`-th one is left (fan^2 >= n): its first, and how many.
 __device__ __forceinline__ int2 join_group(const Shared& s, int step) {
   const int first = (static_cast<int>(blockIdx.x) - s.c0) / (step * s.fan) * (step * s.fan);
   return make_int2(first, min(s.fan, (s.n - first + step - 1) / step));
 }
 
-// Joins the k partials of blocks first, first + step, ... counted from the segment's first: with LAST, into the
+// Joins the n partials of blocks first, first + step, ... counted from the segment's first: with LAST, into the
 // segment's result; otherwise into the first of them. One block works alone here, with few warps, so what
 // counts is the number of latencies and of instructions: bulk copies bring the partials to the
-// ring, which is free by now, the warps turn maxima and sums into one weight per partial and head, and each thread
-// adds up its channels.
+// ring, which is free by now, as many at a time as fit; the warps turn maxima and sums into one weight per
+// partial and head, and each thread adds up its channels.
 template <class T, int D>
-__device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int first, int step, int k, bool last, uint8_t* ring,
-                                     float* meet, uint32_t bar, uint32_t phase) {
+__device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int first, int step, int n, bool last, uint8_t* ring,
+                                     float* meet, uint32_t bar, uint32_t& phase) {
   constexpr size_t PF = attn_partial_floats(T::HEADS, D);
   constexpr int THREADS = T::THREADS, COLS = T::HEADS * D / 4 / THREADS;
-  static_assert(T::FAN >= 2 && T::FAN <= 32 && T::HEADS * D / 4 % THREADS == 0 && (T::FAN + 2) * T::HEADS * 4 <= kAttnRings * T::MEET, "join");
+  static_assert(T::FIT >= 2 && T::FIT <= 32 && T::HEADS * D / 4 % THREADS == 0 && (T::FIT + 3) * T::HEADS * 4 <= kAttnRings * T::MEET, "join");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto part = [&](int i) {
     const int at = first + i * step;
     return p.partials + static_cast<size_t>(2 * (s.c0 + at) + (at == 0)) * PF;
   };
-  if (warp == 0) {
-    const uint32_t bytes = (2 * T::HEADS + s.heads * D) * 4;
-    // other blocks' ordinary writes, which count_in made visible, before the copies that read them
-    asm volatile("fence.proxy.async;" ::: "memory");
-    if (lane == 0) mbar_arrive_expect_tx(bar, k * bytes);
-    __syncwarp();
-    if (lane < k)
-      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                       smem_u32(ring) + lane * static_cast<uint32_t>(PF * 4)),
-                   "l"(part(lane)), "r"(bytes), "r"(bar)
-                   : "memory");
-  }
-  if (!mbar_wait(bar, phase, nullptr)) set_status(p.status, TL_ETIMEOUT);
   const float* const in = reinterpret_cast<const float*>(ring);
-  float* const weight = meet;            // [k][HEADS], then the group's maximum and sum per head
-  float* const all = meet + T::FAN * T::HEADS;
-  for (int h = warp; h < s.heads; h += THREADS / 32) {
-    const float m = lane < k ? in[lane * PF + h] : -INFINITY, l = lane < k ? in[lane * PF + T::HEADS + h] : 0.f;
-    float top = m;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float w = exp2_approx(m - (top == -INFINITY ? 0.f : top));
-    float sum = w * l;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane < k) weight[lane * T::HEADS + h] = w;
-    if (lane == 0) {
-      all[h] = top;
-      all[T::HEADS + h] = sum;
-    }
-  }
-  __syncthreads();
+  // [k + 1][HEADS]: of this round's partials, and of the rounds before; then the maximum and sum per head so far
+  float* const weight = meet;
+  float* const all = meet + (T::FIT + 1) * T::HEADS;
   float4 a[COLS];
 #pragma unroll
   for (int c = 0; c < COLS; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* v = reinterpret_cast<const float4*>(in + 2 * T::HEADS) + tid;
-  const float* w = weight;
-#pragma unroll 2
-  for (int i = 0; i < k; ++i, v += PF / 4, w += T::HEADS) {
+  for (int i0 = 0; i0 < n; i0 += T::FIT) {
+    const int k = min(T::FIT, n - i0);
+    if (warp == 0) {
+      const uint32_t bytes = (2 * T::HEADS + s.heads * D) * 4;
+      // other blocks' ordinary writes, which count_in made visible, before the copies that read them
+      asm volatile("fence.proxy.async;" ::: "memory");
+      if (lane == 0) mbar_arrive_expect_tx(bar, k * bytes);
+      __syncwarp();
+      if (lane < k)
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem_u32(ring) + lane * static_cast<uint32_t>(PF * 4)),
+                     "l"(part(i0 + lane)), "r"(bytes), "r"(bar)
+                     : "memory");
+    }
+    if (!mbar_wait(bar, phase, nullptr)) set_status(p.status, TL_ETIMEOUT);
+    phase ^= 1;
+    for (int h = warp; h < s.heads; h += THREADS / 32) {
+      const float m = lane < k ? in[lane * PF + h] : -INFINITY, l = lane < k ? in[lane * PF + T::HEADS + h] : 0.f;
+      const float m0 = i0 > 0 ? all[h] : -INFINITY, l0 = i0 > 0 ? all[T::HEADS + h] : 0.f;
+      float top = fmaxf(m, m0);
 #pragma unroll
-    for (int c = 0; c < COLS; ++c) {
-      const int h = (tid + c * THREADS) / (D / 4);
-      if (h < s.heads) {
-        const float f = w[h];
+      for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float base = top == -INFINITY ? 0.f : top, w = exp2_approx(m - base), w0 = exp2_approx(m0 - base);
+      float sum = w * l;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane < k) weight[lane * T::HEADS + h] = w;
+      if (lane == 0) {
+        weight[T::FIT * T::HEADS + h] = w0;
+        all[h] = top;
+        all[T::HEADS + h] = sum + w0 * l0;
+      }
+    }
+    __syncthreads();
+    const float4* v = reinterpret_cast<const float4*>(in + 2 * T::HEADS) + tid;
+    const float* w = weight;
+    if (i0 > 0) {
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        const float f = weight[T::FIT * T::HEADS + (tid + c * THREADS) / (D / 4)];
+        a[c].x *= f, a[c].y *= f, a[c].z *= f, a[c].w *= f;
+      }
+    }
+    // (heads past s.heads add up whatever lies there, which is not written out: no branches)
+#pragma unroll 4
+    for (int i = 0; i < k; ++i, v += PF / 4, w += T::HEADS) {
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        const float f = w[(tid + c * THREADS) / (D / 4)];
         const float4 x = v[c * THREADS];
         a[c].x += f * x.x;
         a[c].y += f * x.y;
         a[c].z += f * x.z;
         a[c].w += f * x.w;
       }
+    }
+    if (i0 + T::FIT < n) {
+      fence_proxy_async_smem();
+      __syncthreads();
     }
   }
 #pragma unroll
@@ -386,7 +400,6 @@ __device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uin
     const int2 g = join_group(s, step);
     const bool last = g.x == 0 && step * s.fan >= s.n;
     join<T, D>(p, s, g.x, step, g.y, last, ring, meet, bar, phase);
-    phase ^= 1;
     if (last) return;
     step *= s.fan;
     if (threadIdx.x == 0) {
@@ -923,8 +936,8 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       // joins them is looked up when the block has nothing else to do.
       const int c0 = static_cast<int>(divide(first, share));
       const int n = static_cast<int>(divide(first + seg.tiles - 1, share)) - c0 + 1;
-      // one join of all where they fit, else a tree of two levels, or of more where its joins would not fit
-      const int fan = n <= T::FAN ? n : min(T::FAN, static_cast<int>(ceilf(sqrtf(static_cast<float>(n)))));
+      // One join of all up to kJoinBytes, which cost about what a second level of the tree does (3 us); else two levels.
+      const int fan = static_cast<long long>(n) * sheads * D * 4 <= kJoinBytes ? n : static_cast<int>(ceilf(sqrtf(static_cast<float>(n))));
       const Shared s{c0, n, fan, seg.b, sh0, sheads, vs};
       s_pend[second] = s;
       const int2 group = join_group(s, 1);
