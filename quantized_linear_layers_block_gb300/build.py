@@ -1,26 +1,30 @@
-"""Build the CUDA library libtl_gb300.so in-tree (sm_103a only).
+"""Build the CUDA library libtl_gb300.so in-tree (sm_103a only), and _tensors.so, the Python module that hands
+torch tensors to it (only where torch is installed; the library does not need it).
 
 Usage: python -m quantized_linear_layers_block_gb300.build   (or build() from Python)
 
-Each translation unit under csrc/ is compiled in parallel with
+Each CUDA translation unit under csrc/ is compiled in parallel with
 `nvcc -gencode arch=compute_103a,code=sm_103a -lineinfo -O3`, then linked
-into a shared library next to this file. Objects go to _build/ at the
+into a shared library next to this file; tensors.cpp with g++ against torch's headers. Objects go to _build/ at the
 repository root; both are git-ignored.
 """
 
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtl_gb300.so")
+TENSORS = os.path.join(PKG, "_tensors.so")
 SOURCES = ["tl_api.cu", "pack.cu", "rotate_quant.cu", "decode.cu", "decode_fused_m.cu", "prefill.cu", "codec.cu",
            "decode_f32.cu", "decode_tc.cu", "kv_append.cu", "paged_attention_bf16.cu", "paged_attention_f16.cu",
            "paged_attention_f8.cu", "lora.cu"]
@@ -35,8 +39,13 @@ def _nvcc() -> str:
     return cand
 
 
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or (_torch_dir() is not None and not os.path.exists(TENSORS)):
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "tl.h"), __file__]
@@ -60,14 +69,41 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stdout.write(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    torch_dir = _torch_dir()
+
+    def compile_tensors() -> str | None:
+        if torch_dir is None:
+            return None
+        obj = os.path.join(OBJDIR, "tensors.o")
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+        dirs = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), cuda]
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{d}" for d in dirs),
+               "-c", os.path.join(CSRC, "tensors.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for tensors.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        tensors = ex.submit(compile_tensors)
         objs = list(ex.map(compile_one, SOURCES))
+        tensors_obj = tensors.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if tensors_obj is not None:
+        tmp = TENSORS + ".tmp"
+        libs = os.path.join(torch_dir, "lib")
+        cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, tensors_obj, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+               "-lc10", f"-L{PKG}", "-l:libtl_gb300.so", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link of _tensors.so failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, TENSORS)
     return LIB
 
 

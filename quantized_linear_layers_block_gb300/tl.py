@@ -319,25 +319,25 @@ _HALF = {torch.bfloat16: TL_BF16, torch.float16: TL_F16}
 _CACHE_DTYPES = {torch.bfloat16: TL_BF16, torch.float16: TL_F16, torch.float8_e4m3fn: TL_F8E4M3}
 
 
-def _token_rows(t: torch.Tensor, heads: int, dim: int, dtype: torch.dtype, name: str) -> int:
-    """Checks a device tensor [tokens, heads, dim] whose tokens may be any distance apart; returns that distance."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {list(shape)}")
-    if stride[2] != 1 or (stride[1] != dim and heads > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return stride[0]
+_ext = None
 
 
-def _ints(t: torch.Tensor, dtype: torch.dtype, n: int, name: str) -> int:
-    """Checks a contiguous device vector of n integers; returns its address."""
-    if not t.is_cuda or t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor [{n}]")
-    return t.data_ptr()
+def _tensors():
+    """The module that checks the tensors of the calls below and hands them to the C ABI (csrc/tensors.cpp)."""
+    global _ext
+    if _ext is None:
+        lib()
+        try:
+            from . import _tensors as m
+        except ImportError as e:
+            raise RuntimeError("_tensors.so is missing or of another torch: build it with "
+                               "`python -m quantized_linear_layers_block_gb300.build --force`") from e
+        _ext = m
+    return _ext
+
+
+def _raw_stream(stream):
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 class PagedKVCache:
@@ -383,19 +383,19 @@ class PagedKVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = shape[0], page_size, kv_heads, head_dim
         self.dtype, self.device = dtype, k.device
+        self.scale = head_dim ** -0.5      # of attend(), unless it is given another
         self.struct = tl_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), k.stride(1), k.stride(2),
                                   _CACHE_DTYPES[dtype], kv_heads, head_dim, page_size, num_pages)
-        self._ref = ctypes.pointer(self.struct)
-        self._ws, self._ws_need = None, {}
+        self._address = ctypes.addressof(self.struct)
+        self._ws, self._ws_heads = None, ()
 
-    def _workspace(self, B: int, q_heads: int):
-        need = self._ws_need.get(q_heads)
-        if need is None:      # does not depend on B, except that B = 0 needs none
-            need = tl_paged_attention_workspace_size(max(B, 1), q_heads, self.kv_heads, self.head_dim)
-            self._ws_need[q_heads] = need
+    def _workspace(self, q_heads: int) -> torch.Tensor:
+        # its size does not depend on the number of requests
+        need = tl_paged_attention_workspace_size(1, q_heads, self.kv_heads, self.head_dim)
         if self._ws is None or self._ws.numel() < need:
             # zeroed once here; every call leaves its counters zero again
             self._ws = torch.zeros((need,), dtype=torch.uint8, device=self.device)
+        self._ws_heads += (q_heads,)
         return self._ws
 
     def append(self, k, v, positions, slots, cos_sin=None, interleaved: bool = False, q=None, q_out=None, stream=None):
@@ -412,34 +412,9 @@ def tl_kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, position
                  q_out: torch.Tensor | None = None, stream=None):
     """k, v [T, kv_heads, head_dim] into the cache's slots int64 [T], and q [T, q_heads, head_dim] into q_out, keys and
     queries rotated by cos_sin fp32 [max_pos, rot_dim] at positions int32 [T]. Returns q_out (None without q)."""
-    hkv, d = cache.kv_heads, cache.head_dim
-    dt = k.dtype
-    code = _HALF.get(dt)
-    if code is None:
-        raise ValueError(f"k must be bf16 or fp16, got {dt}")
-    ldk, ldv = _token_rows(k, hkv, d, dt, "k"), _token_rows(v, hkv, d, dt, "v")
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError("k and v must have the same number of tokens")
-    hq = ldq = ldo = 0
-    pq = po = None
-    if q is not None:
-        hq = q.shape[1]
-        ldq = _token_rows(q, hq, d, dt, "q")
-        if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=dt, device=q.device)
-        ldo = _token_rows(q_out, hq, d, dt, "q_out")
-        if q.shape[0] != T or q_out.shape[0] != T:
-            raise ValueError("q, q_out and k must have the same number of tokens")
-        pq, po = q.data_ptr(), q_out.data_ptr()
-    rot = max_pos = 0
-    pcs = ppos = None
-    if cos_sin is not None:
-        _dev_tensor(cos_sin, torch.float32, "cos_sin")
-        max_pos, rot = cos_sin.shape
-        pcs, ppos = cos_sin.data_ptr(), _ints(positions, torch.int32, T, "positions")
-    r = lib().tl_kv_append(cache._ref, pq, k.data_ptr(), v.data_ptr(), code, T, hq, ldq, ldk, ldv, po, ldo, pcs, max_pos, rot,
-                           1 if interleaved else 0, ppos, _ints(slots, torch.int64, T, "slots"), _stream(stream))
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    r = (_ext or _tensors()).kv_append(cache._address, k, v, positions, slots, cos_sin, interleaved, q, q_out, _raw_stream(stream))
     if r != TL_OK:
         _check(r, "tl_kv_append")
     return q_out
@@ -457,47 +432,16 @@ def tl_paged_attention(cache: PagedKVCache, q: torch.Tensor, pages: torch.Tensor
                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [B, q_heads, head_dim] over the cached tokens that pages int32 [B, max_pages] and lens int32 [B] name -> out of
     q's shape and dtype; lse fp32 [B, q_heads] when given. scale defaults to head_dim ** -0.5; the workspace to the cache's."""
-    d = cache.head_dim
-    dt = q.dtype
-    code = _HALF.get(dt)
-    if code is None:
-        raise ValueError(f"q must be bf16 or fp16, got {dt}")
-    B, hq = q.shape[0], q.shape[1]
-    ldq = _token_rows(q, hq, d, dt, "q")
     if out is None:
-        out = torch.empty((B, hq, d), dtype=dt, device=q.device)
-    ldo = _token_rows(out, hq, d, dt, "out")
-    if not pages.is_cuda or pages.dtype is not torch.int32 or pages.dim() != 2 or pages.shape[0] != B or \
-            (pages.shape[1] > 1 and pages.stride(1) != 1):
-        raise ValueError(f"pages must be an int32 CUDA tensor [{B}, max_pages] with contiguous rows")
-    if out.shape[0] != B:
-        raise ValueError("out and q must have the same number of requests")
-    pl = None
-    if lse is not None:
-        _dev_tensor(lse, torch.float32, "lse")
-        if lse.shape != (B, hq):
-            raise ValueError(f"lse must be [{B}, {hq}]")
-        pl = lse.data_ptr()
-    ws = cache._workspace(B, hq) if workspace is None else workspace
-    r = lib().tl_paged_attention(cache._ref, q.data_ptr(), code, B, hq, ldq, pages.data_ptr(), pages.shape[1], pages.stride(0),
-                                 _ints(lens, torch.int32, B, "lens"), d ** -0.5 if scale is None else scale, window,
-                                 out.data_ptr(), ldo, pl, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if workspace is None:
+        heads = q.shape[1] if q.dim() == 3 else 0
+        workspace = cache._ws if heads in cache._ws_heads else cache._workspace(heads)
+    r = (_ext or _tensors()).paged_attention(cache._address, q, pages, lens, cache.scale if scale is None else scale, window, out, lse,
+                                             workspace, _raw_stream(stream))
     if r != TL_OK:
         _check(r, "tl_paged_attention")
     return out
-
-
-_OUT_DTYPES = {torch.bfloat16: TL_BF16, torch.float16: TL_F16, torch.float32: TL_F32}
-
-
-def _matrix(t: torch.Tensor, rows: int | None, cols: int, dtype: torch.dtype, name: str) -> int:
-    """Checks a device matrix [rows, cols] with contiguous rows; returns the distance of its rows."""
-    shape, stride = t.shape, t.stride()
-    if not t.is_cuda or t.dtype is not dtype:
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
-    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows) or stride[1] != 1:
-        raise ValueError(f"{name} must be [{'tokens' if rows is None else rows}, {cols}] with contiguous rows")
-    return stride[0]
 
 
 def tl_lora_plan_size(M: int, n_adapters: int) -> int:
@@ -517,15 +461,15 @@ class LoraPlan:
 
 def tl_lora_plan(ids: torch.Tensor, n_adapters: int, plan: LoraPlan | None = None, stream=None) -> LoraPlan:
     """ids int32 [M] (device; negative: no adapter) -> a LoraPlan; `plan` of the same M and n_adapters is rewritten."""
+    _dev_tensor(ids, torch.int32, "ids")
     if ids.dim() != 1:
         raise ValueError("ids must be a vector")
     M = ids.shape[0]
-    p = _ints(ids, torch.int32, M, "ids")
     if plan is None:
         plan = LoraPlan(M, n_adapters, torch.empty((tl_lora_plan_size(M, n_adapters),), dtype=torch.uint8, device=ids.device))
     elif (plan.M, plan.n_adapters) != (M, n_adapters):
         raise ValueError("the plan is of another number of tokens or adapters")
-    _check(lib().tl_lora_plan(p, M, n_adapters, plan.data.data_ptr(), plan.data.numel(), _stream(stream)), "tl_lora_plan")
+    _check(lib().tl_lora_plan(_ptr(ids), M, n_adapters, plan.data.data_ptr(), plan.data.numel(), _stream(stream)), "tl_lora_plan")
     return plan
 
 
@@ -553,7 +497,6 @@ class LoraBank:
         self.n_adapters, self.rank, self.K = A.shape
         self.N = B.shape[1]
         self.dtype = A.dtype
-        self._fixed = (A.data_ptr(), B.data_ptr(), scale.data_ptr(), _HALF[A.dtype], self.n_adapters, self.rank)
 
     def plan(self, ids: torch.Tensor, plan: LoraPlan | None = None, stream=None) -> LoraPlan:
         """Sort a batch's tokens by adapter; the plan serves every bank of as many adapters."""
@@ -567,20 +510,11 @@ class LoraBank:
 def tl_lora_apply(bank: LoraBank, x: torch.Tensor, base: torch.Tensor, plan: LoraPlan, out: torch.Tensor | None = None,
                   stream=None) -> torch.Tensor:
     """x [M, K] of the bank's dtype, base [M, N] bf16, fp16 or fp32 -> out like base (allocated when not given)."""
-    M = x.shape[0]
-    if plan.M != M or plan.n_adapters != bank.n_adapters:
-        raise ValueError(f"the plan is of {plan.M} tokens and {plan.n_adapters} adapters, not {M} and {bank.n_adapters}")
-    dt = base.dtype
-    code = _OUT_DTYPES.get(dt)
-    if code is None:
-        raise ValueError(f"base must be bf16, fp16 or fp32, got {dt}")
-    ldx = _matrix(x, None, bank.K, bank.dtype, "x")
-    ldb = _matrix(base, M, bank.N, dt, "base")
+    if plan.n_adapters != bank.n_adapters:
+        raise ValueError(f"the plan is of {plan.n_adapters} adapters, not {bank.n_adapters}")
     if out is None:
-        out = torch.empty((M, bank.N), dtype=dt, device=base.device)
-    ldo = _matrix(out, M, bank.N, dt, "out")
-    r = lib().tl_lora_apply(x.data_ptr(), ldx, *bank._fixed, plan.data.data_ptr(), M, bank.N, bank.K, base.data_ptr(), ldb,
-                            out.data_ptr(), ldo, code, _stream(stream))
+        out = torch.empty(base.shape, dtype=base.dtype, device=base.device)
+    r = (_ext or _tensors()).lora_apply(bank.A, bank.B, bank.scale, plan.data, plan.M, x, base, out, _raw_stream(stream))
     if r != TL_OK:
         _check(r, "tl_lora_apply")
     return out
