@@ -25,6 +25,6 @@ struct AppendParams {
   int q_heads, kv_heads, dim, page_size, rot, max_pos, interleaved;
 };
 
-cudaError_t launch_kv_append(const AppendParams& p, int T, bool bf16, bool f8, cudaStream_t st);
+cudaError_t launch_kv_append(const AppendParams& p, int T, bool bf16, bool f8, int sms, cudaStream_t st);
 
 }  // namespace tl

@@ -353,8 +353,9 @@ int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const v
   const int64_t wq = static_cast<int64_t>(q_heads) * d, wk = static_cast<int64_t>(cache->kv_heads) * d;
   if ((r = check_rows(ldk, wk, T, 8)) != TL_OK || (r = check_rows(ldv, wk, T, 8)) != TL_OK) return r;
   if (q_heads > 0 && ((r = check_rows(ldq, wq, T, 8)) != TL_OK || (r = check_rows(ldqo, wq, T, 8)) != TL_OK)) return r;
+  int sms = 0;
   int* status = nullptr;
-  if ((r = status_ptr(&status)) != TL_OK) return r;
+  if ((r = num_sms(&sms)) != TL_OK || (r = status_ptr(&status)) != TL_OK) return r;
   tl::AppendParams p{};
   p.ck = cache->k, p.cv = cache->v, p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
   p.page_stride = cache->page_stride, p.head_stride = cache->head_stride, p.token_stride = cache->token_stride;
@@ -365,7 +366,7 @@ int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const v
   p.cos_sin = cos_sin, p.positions = positions, p.slots = slots, p.status = status;
   p.q_heads = q_heads, p.kv_heads = cache->kv_heads, p.dim = d, p.page_size = cache->page_size;
   p.rot = rot_dim, p.max_pos = max_pos, p.interleaved = interleaved;
-  return tl::launch_kv_append(p, T, dtype == TL_BF16, cache->dtype == TL_F8E4M3, as_stream(stream)) == cudaSuccess
+  return tl::launch_kv_append(p, T, dtype == TL_BF16, cache->dtype == TL_F8E4M3, sms, as_stream(stream)) == cudaSuccess
              ? TL_OK
              : TL_ECUDA;
 }

@@ -91,7 +91,7 @@ def test_matches_the_formula(dtype, cache, interleaved, hq, hkv, d, rot):
     case(37, hq, hkv, d, 16, dtype, cache, rot, interleaved)
 
 
-@pytest.mark.parametrize("T", [1, 2, 24, 301])
+@pytest.mark.parametrize("T", [1, 2, 24, 301, 1300])
 @pytest.mark.parametrize("page", [1, 7, 64])
 @pytest.mark.parametrize("layout", ["heads", "tokens"])
 def test_lengths_pages_and_layouts(T, page, layout):
