@@ -155,7 +155,7 @@ __device__ __forceinline__ uint32_t add2(uint32_t base, float lo, float hi, floa
 // Both products stream their operands through rings of cp.async slots in shared memory, each written and
 // read by one thread only, so that no barrier is needed; registers could not hold enough bytes in flight.
 // Shared memory: the first product's ring [RS][slots][threads], then in its place
-// the warps' sums of one RT, then the ring of base [YS][4 V][threads]. Behind that h's sums [32][RP] in fp32, RP
+// the warps' sums of one RT, then the second product's ring [YS][4][threads]. Behind that h's sums [32][RP] in fp32, RP
 // the rank rounded up to 16 (RT = 1) or a multiple of 32, and the parts of h [PARTS][32][RP + 8].
 template <bool BF16, int YD, int RT>
 struct Lora {
@@ -164,7 +164,10 @@ struct Lora {
   static constexpr int ROWS = 16 * RT, RPITCH = ROWS + 4;
   static constexpr int THREADS = kLoraWarps * 32, VEC = THREADS * 16;
   static constexpr int SLOTS = 2 * RT + kLoraTile / 8, RS = RT == 4 ? 2 : RT == 2 ? 3 : 4, RING = RS * SLOTS * VEC;
-  static constexpr int YS = V == 1 ? 4 : 2, YRING = YS * 4 * V * VEC;
+  // The second product's ring. Up to rank 16, a thread's part of B is 8 bytes a row and goes to registers, one group
+  // ahead (8-byte slots in the ring: 4096 tokens 112 us instead of 103); above, B has stages of its own.
+  static constexpr bool REG_B = RT == 1;
+  static constexpr int YS = RT == 2 ? 6 : 4, YSTAGE = 4 * VEC, YRING = YS * YSTAGE;
   static constexpr int RED = kLoraWarps / 2 * kLoraTile * RPITCH * 4;
   static_assert(RED <= YRING && YRING <= RING, "layout");
   // the K of the second product: one MMA for ranks up to 16, else pairs of them
@@ -196,8 +199,9 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   float* const red = reinterpret_cast<float*>(smem);
   uint16_t* const hs = reinterpret_cast<uint16_t*>(smem + L::hs_at(p.rank));
   const uint32_t slot0 = smem_u32(smem) + tid * 16;
+  // No early start for the next kernel: its clusters would be placed where the first SMs fall free, two blocks
+  // on some and none on others (515 tokens of rank 64, calls back to back: 29 us with it, 22 without).
   pdl_wait_prior();
-  pdl_launch_dependents();
   const LoraPlanHeader head = *p.plan;
   const LoraItem* const item = p.items + idx;
   const int adapter = item->adapter, count = item->count;
@@ -213,56 +217,73 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   for (int n = 0; n < NT; ++n)
     if (8 * n + g >= count) tok[n] = -1;
 
-  // ---- this warp's columns: groups of 32, col, col + 8, ... below g1. The pointers run ahead of the products.
+  // ---- this warp's columns: groups of 32, col, col + 8, ... below g1. Each passes through the ring as `steps`
+  // stages with B's rows for one K step (none up to rank 16), then one or two with base; the pointers run
+  // ahead of the products.
   const int groups = (p.N + 31) / 32, share = part * CS + me, shares = NS * CS;
   const int g1 = static_cast<int>(static_cast<long long>(groups) * (share + 1) / shares);
   int col = static_cast<int>(static_cast<long long>(groups) * share / shares) + warp;
   constexpr int YB = V == 2 ? 4 : 2, STEP = kLoraWarps * 32;
-  int n = 32 * col + 8 * t;                      // this thread's first column of the group asked for next
   const int n_end = min(32 * g1, p.N);
+  int n = 32 * col + 8 * t;                      // this thread's first column of the group asked for
   const char* bp[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) bp[i] = static_cast<const char*>(p.base) + (tok[i] * p.ldb + n) * YB;
   // rows of B: columns permuted so that tile j's column c is column 8 (c / 2) + 2 j + c % 2 of the group
   constexpr int KV = RT == 1 ? 4 : 8;            // elements of a row that a thread takes
-  int nb = 32 * col + 8 * (g >> 1) + (g & 1);                              // its row in tile 0 of the group that wp points to
+  int nb = 32 * col + 8 * (g >> 1) + (g & 1);    // its row in tile 0 of the group that wp points to
   const uint16_t* wp = p.B + (static_cast<int64_t>(adapter) * p.N + nb) * p.rank + KV * t;
-  // up to 16 tokens fill half of a stage: then the ring has twice as many
-  const int mts = count > 16 ? 2 : 1, stages = 2 * L::YS / mts;
-  int asked = 0;                                 // groups of base asked for
-  auto ask_base = [&]() {
-    const uint32_t dst = slot0 + (asked & (stages - 1)) * mts * (2 * V * L::VEC);
-    if (n < n_end) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (tok[i] >= 0) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) cp_async16(dst + (i * V + e) * L::VEC, bp[i] + 16 * e, 16);
-        }
-        bp[i] += STEP * YB;
-      }
-    }
-    n += STEP;
-    ++asked;
-    cp_async_commit();
-  };
-  auto load_b = [&](int s, uint4 (&b)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      b[j] = make_uint4(0, 0, 0, 0);
-      if (nb + 2 * j < n_end && 32 * s + KV * t < p.rank) {
-        const uint16_t* src = wp + 2 * j * p.rank + 32 * s;
-        if constexpr (RT == 1) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-          b[j].x = w.x, b[j].y = w.y;
-        } else {
-          b[j] = __ldg(reinterpret_cast<const uint4*>(src));
-        }
-      }
-    }
-  };
   const int steps = adapter < 0 ? 0 : RP / L::KSTEP;
-  uint4 bw[4];
+  const int mts = count > 16 ? 2 : 1, halves = V == 2 && mts == 2 ? 2 : 1;      // stages with base
+  const int b_stages = L::REG_B ? 0 : steps;
+  int kind = 0, ask_at = 0, take_at = 0;         // which of a group's stages is asked for next; places in the ring
+  auto ask_next = [&]() {
+    const uint32_t dst = slot0 + ask_at * L::YSTAGE;
+    if (n - 8 * t < n_end) {
+      if (kind < b_stages) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = nb + 2 * j < n_end && 32 * kind + KV * t < p.rank;
+          cp_async16(dst + j * L::VEC, in ? wp + 2 * j * p.rank + 32 * kind : p.B, in ? 16 : 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // V = 1: token 8i + g; V = 2: the two vectors of tokens 8 (i / 2) + g, and 16 more in the second stage
+          const int half = kind - b_stages, r = V == 1 ? i : (i >> 1) + 2 * half;
+          const char* const src = V == 1 ? bp[i] : (half == 0 ? bp[i >> 1] : bp[2 + (i >> 1)]) + 16 * (i & 1);
+          if (n < n_end && 8 * r + g < count) cp_async16(dst + i * L::VEC, src, 16);
+        }
+      }
+    }
+    cp_async_commit();
+    if (++kind == b_stages + halves) {
+      kind = 0;
+      n += STEP;
+      if constexpr (!L::REG_B) {
+        nb += STEP;
+        wp += static_cast<int64_t>(STEP) * p.rank;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bp[i] += STEP * YB;
+    }
+    ask_at = ask_at + 1 == L::YS ? 0 : ask_at + 1;
+  };
+  uint2 bw[4] = {};                              // REG_B: B's rows of the group taken next
+  auto load_b = [&]() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      bw[j] = nb + 2 * j < n_end && KV * t < p.rank ? __ldg(reinterpret_cast<const uint2*>(wp + 2 * j * p.rank)) : make_uint2(0, 0);
+    nb += STEP;
+    wp += static_cast<int64_t>(STEP) * p.rank;
+  };
+  auto take_next = [&]() {
+    cp_async_wait<L::YS - 2>();
+    ask_next();                                  // into the slots that the last turn read
+    const uint32_t src = slot0 + take_at * L::YSTAGE;
+    take_at = take_at + 1 == L::YS ? 0 : take_at + 1;
+    return src;
+  };
   float up[4] = {};
   if (steps > 0) {
     // ---- h = A x
@@ -357,8 +378,9 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     if (CS > 1) cluster_arrive();
     __syncthreads();                             // the sums have been taken: their place is the ring's
     // the first columns' operands arrive while the blocks meet
-    for (int s = 0; s < stages - 1; ++s) ask_base();
-    load_b(0, bw);
+#pragma unroll 1
+    for (int s = 0; s < L::YS - 1; ++s) ask_next();
+    if constexpr (L::REG_B) load_b();
     if (CS > 1) cluster_wait();
     // ---- a warp takes a token: sum over the blocks, power of two, then the parts in the K order of the MMAs below.
     // Lane l has elements 4l .. 4l + 3 of the rank.
@@ -420,7 +442,8 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < 4; ++i) up[i] = s_up[8 * i + g];
   } else {
-    for (int s = 0; s < stages - 1; ++s) ask_base();
+#pragma unroll 1
+    for (int s = 0; s < L::YS - 1; ++s) ask_next();
   }
 
   // ---- y = base + B h
@@ -428,7 +451,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
 #pragma unroll
   for (int i = 0; i < 4; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + 32 * col + 8 * t) * YB;
   const uint32_t hbase = smem_u32(hs) + ((lane & 15) * PITCH + (lane >> 4) * 8) * 2;
-  for (int turn = 0; col < g1; col += kLoraWarps, ++turn) {
+  for (; col < g1; col += kLoraWarps) {
     const bool live = 32 * col + 8 * t < n_end;
     float acc[2][4][4];
 #pragma unroll
@@ -437,13 +460,15 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       for (int j = 0; j < 4; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
     for (int s = 0; s < steps; ++s) {
       uint4 b[4];
+      if constexpr (L::REG_B) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = bw[j];
-      if (s + 1 == steps) {                      // the rows of the next group
-        nb += STEP;
-        wp += static_cast<int64_t>(STEP) * p.rank;
+        for (int j = 0; j < 4; ++j) b[j] = make_uint4(bw[j].x, bw[j].y, 0, 0);
+        load_b();
+      } else {
+        const uint32_t at = take_next();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = ld_shared16(at + j * L::VEC);
       }
-      load_b(s + 1 == steps ? 0 : s + 1, bw);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (m < mts) {
@@ -464,19 +489,15 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         }
       }
     }
-    if (mts == 2)
-      cp_async_wait<L::YS - 2>();
-    else
-      cp_async_wait<2 * L::YS - 2>();
-    ask_base();                                  // into the slots that the last turn read
-    const uint32_t src = slot0 + (turn & (stages - 1)) * mts * (2 * V * L::VEC);
+    uint32_t src = take_next();
     // token 8i + g: columns 8t + 2j + {0, 1} of the group are elements 2 (i & 1) + {0, 1} of acc[i / 2][j]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      if (V == 2 && i == 2 && mts == 2) src = take_next();
       if (live && tok[i] >= 0) {
         uint4 r[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) r[e] = ld_shared16(src + (i * V + e) * L::VEC);
+        for (int e = 0; e < V; ++e) r[e] = ld_shared16(src + (V == 1 ? i : 2 * (i & 1) + e) * L::VEC);
         if (steps > 0) {
           uint32_t w[4 * V];
 #pragma unroll
