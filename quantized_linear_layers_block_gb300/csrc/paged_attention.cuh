@@ -87,6 +87,7 @@ constexpr int kAttnMaxBlocksPerSm = 4;
 constexpr int kAttnCluster = 8;        // blocks that share a segment of a small call
 constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join tree
 constexpr int kAttnLevels = 2;
+constexpr int kJoinFew = 4;
 constexpr int kJoinBytes = 320 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -392,10 +393,49 @@ __device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int f
   __syncthreads();            // `meet` and the ring are free again
 }
 
+// The same of up to kJoinFew partials, all of a segment's: every thread reads what it needs at once, one latency.
+template <class T, int D>
+__device__ __forceinline__ void join_few(const AttnParams& p, const Shared& s) {
+  constexpr size_t PF = attn_partial_floats(T::HEADS, D);
+  for (int x = threadIdx.x; x < s.heads * (D / 4); x += T::THREADS) {
+    const int h = x / (D / 4);
+    float m[kJoinFew], l[kJoinFew], top = -INFINITY;
+    float4 v[kJoinFew];
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      m[i] = -INFINITY, l[i] = 0.f, v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < s.n) {
+        const float* const q = p.partials + static_cast<size_t>(2 * (s.c0 + i) + (i == 0)) * PF;
+        m[i] = __ldcg(q + h);
+        l[i] = __ldcg(q + T::HEADS + h);
+        v[i] = __ldcg(reinterpret_cast<const float4*>(q + 2 * T::HEADS) + x);
+      }
+      top = fmaxf(top, m[i]);
+    }
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kJoinFew; ++i) {
+      const float f = exp2_approx(m[i] - base);
+      sum += f * l[i];
+      a.x += f * v[i].x;
+      a.y += f * v[i].y;
+      a.z += f * v[i].z;
+      a.w += f * v[i].w;
+    }
+    write_out<T>(p, s.b, s.h0 + h, 4 * (x % (D / 4)), D, a, top, sum, s.v_scale);
+  }
+}
+
 // What a block does that arrived as the last of its group of partials; ring, meet, flag and barrier in shared memory.
 template <class T, int D>
 __device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uint8_t* ring, float* meet, int* flag, uint32_t bar,
                                        uint32_t& phase) {
+  if (s.n <= kJoinFew) {
+    join_few<T, D>(p, s);
+    return;
+  }
   for (int step = 1, level = 0;; ++level) {
     const int2 g = join_group(s, step);
     const bool last = g.x == 0 && step * s.fan >= s.n;
@@ -426,7 +466,6 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
   const int HG = p.kv_heads * p.groups_per_kv;
 
   pdl_wait_prior();
-  pdl_launch_dependents();
 
   long long share = 0, t0 = 0;
   int count;                                          // places of this block's share
@@ -851,6 +890,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     const bool whole = !CL && !starts_before && seg.tile + here == seg.tiles, second = !starts_before;
     const long long first = t0 + (done - here) - seg.tile;      // the place of its first tile
     if constexpr (CL) {
+      pdl_launch_dependents();
       cp_async_wait<0>();                             // the ring is where the block's result goes
     } else {
       ++done;                                         // the next segment's first place
@@ -944,6 +984,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       s_last[second] = count_in(p.counters + c0 + group.x, group.y);
     }
   }
+  pdl_launch_dependents();             // the stream is over: the next kernel may begin its own beside the joins
   cp_async_wait<0>();
   fence_proxy_async_smem();            // joins copy to the ring by the async proxy
   __syncthreads();
