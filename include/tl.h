@@ -366,7 +366,7 @@ typedef struct tl_kv_cache {
  *   k, v       [T, kv_heads, head_dim], dtype TL_BF16 or TL_F16, ldk and ldv
  *              elements from one token to the next
  *   q, q_out   [T, q_heads, head_dim] of the same dtype, ldq and ldqo likewise;
- *              q_out may be q (in place). q = NULL or q_heads = 0: no queries.
+ *              q_out may be q (in place, ldqo = ldq). q = NULL or q_heads = 0: no queries.
  *   cos_sin    fp32 [max_pos, rot_dim]: row p holds the rot_dim / 2 cosines,
  *              then the sines, of position p. NULL with rot_dim = 0: the
  *              tokens are stored as they are.

@@ -139,7 +139,7 @@ const char* tl_strerror(int status) {
   }
 }
 
-int tl_version(void) { return 10000; }
+int tl_version(void) { return 10100; }
 
 int tl_packed_sizes(int N, int K, size_t* packed_bytes, size_t* qT_bytes, size_t* sw_bytes) {
   const int r = check_nk(N, K);
@@ -353,6 +353,7 @@ int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const v
   const int64_t wq = static_cast<int64_t>(q_heads) * d, wk = static_cast<int64_t>(cache->kv_heads) * d;
   if ((r = check_rows(ldk, wk, T, 8)) != TL_OK || (r = check_rows(ldv, wk, T, 8)) != TL_OK) return r;
   if (q_heads > 0 && ((r = check_rows(ldq, wq, T, 8)) != TL_OK || (r = check_rows(ldqo, wq, T, 8)) != TL_OK)) return r;
+  if (q_heads > 0 && q == q_out && T > 1 && ldq != ldqo) return TL_EINVAL;      // in place, but the rows lie elsewhere
   int sms = 0;
   int* status = nullptr;
   if ((r = num_sms(&sms)) != TL_OK || (r = status_ptr(&status)) != TL_OK) return r;

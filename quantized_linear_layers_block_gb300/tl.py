@@ -340,6 +340,14 @@ def _raw_stream(stream):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
+def _allocate(make, shape, dtype, device, stream):
+    """A tensor that the kernels of `stream` are the first to use: allocated, and filled, in that stream's order."""
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            return make(shape, dtype=dtype, device=device)
+    return make(shape, dtype=dtype, device=device)
+
+
 class PagedKVCache:
     """The paged key-value cache of one layer, and the two operators on it.
 
@@ -355,7 +363,8 @@ class PagedKVCache:
     The cache keeps one workspace for attend(), which joins requests that several
     blocks share: attend() calls on one cache that can run at the same time on
     different streams must be ordered by the caller (an event), or use one
-    PagedKVCache over the same k and v for each stream. Its first attend() allocates it.
+    PagedKVCache over the same k and v for each stream. The first attend() with a number of
+    query heads allocates it: call it once before capturing a graph.
     """
 
     def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16,
@@ -387,16 +396,17 @@ class PagedKVCache:
         self.struct = tl_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), k.stride(1), k.stride(2),
                                   _CACHE_DTYPES[dtype], kv_heads, head_dim, page_size, num_pages)
         self._address = ctypes.addressof(self.struct)
-        self._ws, self._ws_heads = None, ()
+        self._ws = {}      # by the number of query heads; never replaced, as a captured graph holds its address
 
-    def _workspace(self, q_heads: int) -> torch.Tensor:
+    def _workspace(self, q_heads: int, stream) -> torch.Tensor:
         # its size does not depend on the number of requests
         need = tl_paged_attention_workspace_size(1, q_heads, self.kv_heads, self.head_dim)
-        if self._ws is None or self._ws.numel() < need:
+        ws = next((w for w in self._ws.values() if w.numel() >= need), None)
+        if ws is None:
             # zeroed once here; every call leaves its counters zero again
-            self._ws = torch.zeros((need,), dtype=torch.uint8, device=self.device)
-        self._ws_heads += (q_heads,)
-        return self._ws
+            ws = _allocate(torch.zeros, (need,), torch.uint8, self.device, stream)
+        self._ws[q_heads] = ws
+        return ws
 
     def append(self, k, v, positions, slots, cos_sin=None, interleaved: bool = False, q=None, q_out=None, stream=None):
         """tl_kv_append on this cache; returns the rotated queries (None without q)."""
@@ -413,7 +423,7 @@ def tl_kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, position
     """k, v [T, kv_heads, head_dim] into the cache's slots int64 [T], and q [T, q_heads, head_dim] into q_out, keys and
     queries rotated by cos_sin fp32 [max_pos, rot_dim] at positions int32 [T]. Returns q_out (None without q)."""
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _allocate(torch.empty, q.shape, q.dtype, q.device, stream)
     r = (_ext or _tensors()).kv_append(cache._address, k, v, positions, slots, cos_sin, interleaved, q, q_out, _raw_stream(stream))
     if r != TL_OK:
         _check(r, "tl_kv_append")
@@ -433,10 +443,12 @@ def tl_paged_attention(cache: PagedKVCache, q: torch.Tensor, pages: torch.Tensor
     """q [B, q_heads, head_dim] over the cached tokens that pages int32 [B, max_pages] and lens int32 [B] name -> out of
     q's shape and dtype; lse fp32 [B, q_heads] when given. scale defaults to head_dim ** -0.5; the workspace to the cache's."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _allocate(torch.empty, q.shape, q.dtype, q.device, stream)
     if workspace is None:
         heads = q.shape[1] if q.dim() == 3 else 0
-        workspace = cache._ws if heads in cache._ws_heads else cache._workspace(heads)
+        workspace = cache._ws.get(heads)
+        if workspace is None:
+            workspace = cache._workspace(heads, stream)
     r = (_ext or _tensors()).paged_attention(cache._address, q, pages, lens, cache.scale if scale is None else scale, window, out, lse,
                                              workspace, _raw_stream(stream))
     if r != TL_OK:
@@ -466,7 +478,7 @@ def tl_lora_plan(ids: torch.Tensor, n_adapters: int, plan: LoraPlan | None = Non
         raise ValueError("ids must be a vector")
     M = ids.shape[0]
     if plan is None:
-        plan = LoraPlan(M, n_adapters, torch.empty((tl_lora_plan_size(M, n_adapters),), dtype=torch.uint8, device=ids.device))
+        plan = LoraPlan(M, n_adapters, _allocate(torch.empty, (tl_lora_plan_size(M, n_adapters),), torch.uint8, ids.device, stream))
     elif (plan.M, plan.n_adapters) != (M, n_adapters):
         raise ValueError("the plan is of another number of tokens or adapters")
     _check(lib().tl_lora_plan(_ptr(ids), M, n_adapters, plan.data.data_ptr(), plan.data.numel(), _stream(stream)), "tl_lora_plan")
@@ -513,7 +525,7 @@ def tl_lora_apply(bank: LoraBank, x: torch.Tensor, base: torch.Tensor, plan: Lor
     if plan.n_adapters != bank.n_adapters:
         raise ValueError(f"the plan is of {plan.n_adapters} adapters, not {bank.n_adapters}")
     if out is None:
-        out = torch.empty(base.shape, dtype=base.dtype, device=base.device)
+        out = _allocate(torch.empty, base.shape, base.dtype, base.device, stream)
     r = (_ext or _tensors()).lora_apply(bank.A, bank.B, bank.scale, plan.data, plan.M, x, base, out, _raw_stream(stream))
     if r != TL_OK:
         _check(r, "tl_lora_apply")

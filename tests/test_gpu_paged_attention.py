@@ -178,6 +178,23 @@ def test_strided_query_and_output_on_another_stream():
     assert bool((hold[:, 0] == 5).all()) and bool((hold[:, 7] == 5).all())
 
 
+def test_another_stream_without_its_context():
+    """The outputs and the workspace that a call allocates belong to the stream that it is given."""
+    lens = [3000, 20]
+    kv, q, table, k64, v64 = build(21, lens, 8, 2, 128, 16)
+    qd, td, ld = q.cuda(), torch.tensor(table).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.empty((1 << 28,), dtype=torch.float32, device="cuda")
+    for _ in range(20):
+        busy.fill_(1.0)                  # the current stream is behind
+    y = kv.attend(qd, td, ld, stream=st)
+    st.synchronize()
+    got = y.clone()
+    torch.cuda.synchronize()
+    assert torch.equal(got, check(kv, q, table, k64, v64, lens))
+
+
 def test_rows_past_the_32_bit_range():
     """A cache of over 2^31 elements, whose offsets in bytes pass 2^32, the request's pages at its end."""
     page, hkv, d = 64, 8, 128

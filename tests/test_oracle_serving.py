@@ -120,6 +120,7 @@ def test_append_refusals(lib):
     assert call(ldv=-128) == tl.TL_EINVAL
     assert call(q=ok, hq=4, ldq=256, qo=None) == tl.TL_EINVAL
     assert call(q=ok, hq=4, ldq=250, qo=ok, ldo=256) == tl.TL_EUNSUPPORTED
+    assert call(q=ok, hq=4, ldq=256, qo=ok, ldo=264) == tl.TL_EINVAL      # in place, but the rows lie elsewhere
     assert call(T=0, k=None, v=None, slots=None) == tl.TL_OK
 
 
