@@ -382,17 +382,20 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     for (int s = 0; s < L::YS - 1; ++s) ask_next();
     if constexpr (L::REG_B) load_b();
     if (CS > 1) cluster_wait();
-    // ---- a warp takes a token: sum over the blocks, power of two, then the parts in the K order of the MMAs below.
-    // Lane l has elements 4l .. 4l + 3 of the rank.
+    // ---- some lanes take a token: sum over the blocks, power of two, then the parts in the K order of the MMAs below.
+    // A lane has four elements of the rank; 32 / wide tokens to a warp.
     const float sc = __ldg(p.scale + adapter);
     const uint32_t sums = smem_u32(sum);
-#pragma unroll 2
-    for (int m = warp; m < count; m += kLoraWarps) {       // rows past the last token may hold anything: they reach no other row
+    int wide = 4;
+    while (4 * wide < RP) wide *= 2;
+    const int sub = lane & (wide - 1), per_warp = 32 / wide;
+    for (int m0 = warp * per_warp; m0 < count; m0 += kLoraWarps * per_warp) {     // rows past the last token may hold anything: they reach no other row
+      const int m = m0 + lane / wide;
       float v[4] = {};
-      if (4 * lane < p.rank) {
+      if (m < count && 4 * sub < p.rank) {
         float4 f[kLoraMaxCluster];
 #pragma unroll
-        for (int q = 0; q < kLoraMaxCluster; ++q) f[q] = q < CS ? ld_cluster4(sums + (m * RP + 4 * lane) * 4, q) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < kLoraMaxCluster; ++q) f[q] = q < CS ? ld_cluster4(sums + (m * RP + 4 * sub) * 4, q) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int q = 0; q < kLoraMaxCluster; ++q) v[0] += f[q].x, v[1] += f[q].y, v[2] += f[q].z, v[3] += f[q].w;
       }
@@ -402,15 +405,14 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         v[e] *= sc;
         top = fmaxf(top, fabsf(v[e]));
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e2 = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-      if (lane == 0) s_up[m] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+      if (sub == 0 && m < kLoraTile) s_up[m] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
       // element 8q + j of 32 (thread q of the quad loads it): MMA j / 4, column 2q + (j & 1) + 8 ((j & 2) / 2);
       // of 16, for one MMA, element 4q + j
-      const int at = RT == 1 ? 2 * lane : 32 * (lane >> 3) + 16 * (lane & 1) + 2 * (lane >> 1 & 3);
-      if (4 * lane < RP) {
+      const int at = RT == 1 ? 2 * sub : 32 * (sub >> 3) + 16 * (sub & 1) + 2 * (sub >> 1 & 3);
+      if (m < count && 4 * sub < RP) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] *= down;
 #pragma unroll
