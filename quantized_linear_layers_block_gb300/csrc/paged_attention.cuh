@@ -83,7 +83,7 @@ struct AttnParams {
 };
 
 constexpr int kAttnRings = 4;          // rings of key tiles in a block, each with HW warps
-constexpr int kAttnMaxBlocksPerSm = 4;
+constexpr int kAttnMaxBlocksPerSm = 2;
 constexpr int kAttnCluster = 8;        // blocks that share a segment of a small call
 constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join tree
 constexpr int kAttnLevels = 2;
@@ -220,7 +220,7 @@ struct Traits {
   static constexpr int SMEM = kAttnRings * (STAGES * BUF + MEET);
   // partials that the rings hold, at most a warp's lanes
   static constexpr int HOLD = kAttnRings * STAGES * BUF / (HEADS * (D + 2) * 4), FIT = HOLD < 32 ? HOLD : 32;
-  static constexpr int BLOCKS = HW * NT == 4 || SMEM > 115500 ? 1 : SMEM > 75000 ? 2 : 3;     // per SM
+  static constexpr int BLOCKS = HW * NT == 4 || SMEM > 115500 ? 1 : kAttnMaxBlocksPerSm;     // per SM
   // 2^8 in the probabilities keeps an f16 low part of the small ones out of the subnormals
   static constexpr float POFF = BF16 ? 0.f : 8.f;
 };

@@ -363,8 +363,7 @@ class PagedKVCache:
     The cache keeps one workspace for attend(), which joins requests that several
     blocks share: attend() calls on one cache that can run at the same time on
     different streams must be ordered by the caller (an event), or use one
-    PagedKVCache over the same k and v for each stream. The first attend() with a number of
-    query heads allocates it: call it once before capturing a graph.
+    PagedKVCache over the same k and v for each stream.
     """
 
     def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16,
@@ -396,17 +395,12 @@ class PagedKVCache:
         self.struct = tl_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), k.stride(1), k.stride(2),
                                   _CACHE_DTYPES[dtype], kv_heads, head_dim, page_size, num_pages)
         self._address = ctypes.addressof(self.struct)
-        self._ws = {}      # by the number of query heads; never replaced, as a captured graph holds its address
-
-    def _workspace(self, q_heads: int, stream) -> torch.Tensor:
-        # its size does not depend on the number of requests
-        need = tl_paged_attention_workspace_size(1, q_heads, self.kv_heads, self.head_dim)
-        ws = next((w for w in self._ws.values() if w.numel() >= need), None)
-        if ws is None:
-            # zeroed once here; every call leaves its counters zero again
-            ws = _allocate(torch.zeros, (need,), torch.uint8, self.device, stream)
-        self._ws[q_heads] = ws
-        return ws
+        # attend()'s workspace: of the most query heads to a key-value head that take one (17), as its size depends
+        # neither on the requests nor on more heads. Zeroed once here; every call leaves its counters zero again.
+        self._ws = None
+        if head_dim in (64, 128, 256) and kv_heads <= 1024:
+            need = tl_paged_attention_workspace_size(1, kv_heads * min(17, 1024 // kv_heads), kv_heads, head_dim)
+            self._ws = torch.zeros((need,), dtype=torch.uint8, device=k.device)
 
     def append(self, k, v, positions, slots, cos_sin=None, interleaved: bool = False, q=None, q_out=None, stream=None):
         """tl_kv_append on this cache; returns the rotated queries (None without q)."""
@@ -445,10 +439,9 @@ def tl_paged_attention(cache: PagedKVCache, q: torch.Tensor, pages: torch.Tensor
     if out is None:
         out = _allocate(torch.empty, q.shape, q.dtype, q.device, stream)
     if workspace is None:
-        heads = q.shape[1] if q.dim() == 3 else 0
-        workspace = cache._ws.get(heads)
-        if workspace is None:
-            workspace = cache._workspace(heads, stream)
+        if cache._ws is None:
+            raise TLError(TL_EUNSUPPORTED, "tl_paged_attention")
+        workspace = cache._ws
     r = (_ext or _tensors()).paged_attention(cache._address, q, pages, lens, cache.scale if scale is None else scale, window, out, lse,
                                              workspace, _raw_stream(stream))
     if r != TL_OK:
