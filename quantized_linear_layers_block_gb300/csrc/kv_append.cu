@@ -8,7 +8,9 @@
 // read and written once: bound by HBM for prompts, by the launch and one chain of loads (slot
 // and position, angles, data) for the few tokens of a decode step. One block takes one token: a thread owns
 // 16 channels (two 16-byte vectors, which hold both halves of their 8 pairs in either pairing) at a
-// fixed place of the head and walks over the heads, so it reads its angles once for all of them.
+// fixed place of the head and walks over the heads, so it reads its angles once for all of them. Measured on
+// GB300: 16000 tokens of 40 + 16 heads of 128, fp16: 72 us, 6.5 TB/s, 0.95 of the copy rate; 24 tokens of 24 + 8 heads of 256:
+// 2.4 us, about what an empty kernel between others takes.
 #include "tl_internal.cuh"
 
 #include <cuda_bf16.h>

@@ -1,13 +1,13 @@
 // Low-rank adapters of many requests beside a projection:
 //   y[m] = base[m] + scale[a] B[a] (A[a] x[m]),  a = ids[m].
 //
-// A plan kernel sorts the tokens by adapter once per step; its items are up
-// to 16 or 32 tokens of one adapter, so an adapter's matrices are read once per item,
+// A plan kernel sorts the tokens by adapter once per step; an item is up to 16 or 32
+// tokens of one adapter, so an adapter's matrices are read once per item,
 // by however many tokens use it. One kernel does both products: a cluster of blocks takes an item.
 //
 // First h = A x: the rank is small and K long, so K is cut over all warps of the cluster, whose sums meet through
 // distributed shared memory in a fixed order; h never goes to memory. The adapter's rows are the 16
-// rows of the MMA and the item's tokens its 8 columns. Nothing is used twice but through registers, so
+// rows of the MMA, 8 of the item's tokens its columns. Nothing is used twice but through registers, so
 // the operands come straight from global memory: with the K axis permuted alike on both sides
 // (thread t of a quad takes the 8 consecutive elements 8t .. 8t + 7 of 32) every load is 16 bytes.
 //
@@ -18,6 +18,12 @@
 //
 // A few items leave most SMs idle, and the expansion long: then several clusters take
 // an item's columns, and each forms h for itself (its A is in L2 by then).
+//
+// Measured on GB300: 4096 tokens, rank 16, K = 5120, N = 34816, bf16: 102 us, 6.05 TB/s, 0.89 of the copy rate (two kernels
+// with h in memory: 169 us). 515 tokens, rank 64, K = 17408, N = 5120, fp32 out: 22 us, of which the first
+// product takes 8 (96 MB of x and A per item into the SMs, 83 B/ns each), the second 4.5 and the chain
+// around them (plan, sums, two meetings of the cluster, parts) the rest. 48 tokens of 32 adapters, rank 32, K = N = 5120:
+// 8.3 us; one token, rank 16, N = 17408: 5.5 us, all of it that chain.
 #include "lora.cuh"
 #include "tl_internal.cuh"
 
@@ -153,7 +159,9 @@ __device__ __forceinline__ uint32_t add2(uint32_t base, float lo, float hi, floa
 
 // ----------------------------------------------------------------- the operator
 // Both products stream their operands through rings of cp.async slots in shared memory, each written and
-// read by one thread only, so that no barrier is needed; registers could not hold enough bytes in flight.
+// read by one thread only, so that no barrier is needed; registers could not hold enough bytes in flight
+// (4096 tokens: 134 us with operands a step ahead in registers). A stage of the first ring is a whole K step: finer
+// stages keep more bytes on their way and took longer, by their own instructions.
 // Shared memory: the first product's ring [RS][slots][threads], then in its place
 // the warps' sums of one RT, then the second product's ring [YS][4][threads]. Behind that h's sums [32][RP] in fp32, RP
 // the rank rounded up to 16 (RT = 1) or a multiple of 32, and the parts of h [PARTS][32][RP + 8].
