@@ -9,8 +9,8 @@
 // and position, angles, data) for the few tokens of a decode step. One block takes one token: a thread owns
 // 16 channels (two 16-byte vectors, which hold both halves of their 8 pairs in either pairing) at a
 // fixed place of the head and walks over the heads, so it reads its angles once for all of them. Measured on
-// GB300: 16000 tokens of 40 + 16 heads of 128, fp16: 72 us, 6.5 TB/s, 0.95 of the copy rate; 24 tokens of 24 + 8 heads of 256:
-// 2.4 us, about what an empty kernel between others takes.
+// GB300: 16000 tokens of 40 + 16 heads of 128, fp16: 72 us, 6.5 TB/s, 0.96 of the copy rate; 24 tokens of 24 + 8 heads of 256:
+// 2.3 us, about what an empty kernel between others takes.
 #include "tl_internal.cuh"
 
 #include <cuda_bf16.h>
@@ -19,8 +19,6 @@
 
 namespace tl {
 namespace {
-
-constexpr int kAppendMaxThreads = 512;
 
 template <bool BF16>
 __device__ __forceinline__ void widen8(const uint4& v, float (&f)[8]) {
@@ -62,19 +60,32 @@ __device__ __forceinline__ uint2 narrow8_e4m3(const float (&f)[8], float inv) {
 }
 
 // lanes = head_dim / 16 threads cover a head; `rows` heads are taken at a time
-template <bool BF16, bool F8>
-__global__ void __launch_bounds__(kAppendMaxThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
+template <bool BF16, bool F8, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 64 ? 20 : THREADS == 256 ? 4 : 1) kv_append_kernel(const __grid_constant__ AppendParams p) {
   const int lanes = p.dim >> 4;
   const int row = threadIdx.x / lanes, j = threadIdx.x - row * lanes;
   const int rows = blockDim.x / lanes;
   const int tok = blockIdx.x;
   pdl_wait_prior();
-  pdl_launch_dependents();
+  // (no early start for the next kernel, whose blocks would take this one's room: 1500 tokens, calls back to back, 12 us with it,
+  // 6.5 without; 512 tokens 4.1 and 3.7)
   const int64_t slot = __ldg(p.slots + tok);
   const bool turn = 16 * j < p.rot;
   // the thread's two vectors of 8 channels: pairs (a[i], b[i]), or pairs of neighbours in a, then in b
   const int c0 = turn && !p.interleaved ? 8 * j : 16 * j;
   const int c1 = turn && !p.interleaved ? 8 * j + (p.rot >> 1) : 16 * j + 8;
+  // q may be q_out: not the read-only path
+  auto load = [&](int h, uint4& v0, uint4& v1) {
+    const bool is_v = h >= p.q_heads + p.kv_heads;
+    const uint16_t* src = h < p.q_heads ? p.q + tok * p.ldq + h * p.dim
+                          : is_v        ? p.v + tok * p.ldv + (h - p.q_heads - p.kv_heads) * p.dim
+                                        : p.k + tok * p.ldk + (h - p.q_heads) * p.dim;
+    v0 = *reinterpret_cast<const uint4*>(src + c0);
+    v1 = *reinterpret_cast<const uint4*>(src + c1);
+  };
+  // the first head's data wait for neither slot nor angles
+  uint4 first0 = make_uint4(0, 0, 0, 0), first1 = first0;
+  if (row < p.q_heads + 2 * p.kv_heads) load(row, first0, first1);
   bool ok = true;
   float cs[8], sn[8];
   if (p.rot > 0) {
@@ -102,14 +113,9 @@ __global__ void __launch_bounds__(kAppendMaxThreads) kv_append_kernel(const __gr
     cell = page * p.page_stride + (slot - page * p.page_size) * p.token_stride;
   }
   const int heads = p.q_heads + (keep ? 2 * p.kv_heads : 0);
-#pragma unroll 2
-  for (int h = row; h < heads; h += rows) {
+  auto store = [&](int h, const uint4& v0, const uint4& v1) {
     const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
     const int kh = h - p.q_heads - (is_v ? p.kv_heads : 0);
-    const uint16_t* src = is_q ? p.q + tok * p.ldq + h * p.dim
-                               : (is_v ? p.v + tok * p.ldv : p.k + tok * p.ldk) + kh * p.dim;
-    const uint4 v0 = *reinterpret_cast<const uint4*>(src + c0);     // q may be q_out: not the read-only path
-    const uint4 v1 = *reinterpret_cast<const uint4*>(src + c1);
     uint4 r0 = v0, r1 = v1;
     float a[8], b[8];
     const bool turned = turn && !is_v;
@@ -159,7 +165,25 @@ __global__ void __launch_bounds__(kAppendMaxThreads) kv_append_kernel(const __gr
         *reinterpret_cast<uint4*>(dst + c1) = r1;
       }
     }
+  };
+  if (row < heads) store(row, first0, first1);
+#pragma unroll 2
+  for (int h = row + rows; h < heads; h += rows) {
+    uint4 v0, v1;
+    load(h, v0, v1);
+    store(h, v0, v1);
   }
+}
+
+template <int THREADS>
+cudaError_t launch(const AppendParams& p, int T, bool bf16, bool f8, cudaStream_t st) {
+  const int lanes = p.dim / 16;
+  const dim3 grid(static_cast<unsigned>(T)), block(static_cast<unsigned>(THREADS / lanes * lanes));
+  if (bf16)
+    return f8 ? launch_pdl(kv_append_kernel<true, true, THREADS>, grid, block, 0, st, p)
+              : launch_pdl(kv_append_kernel<true, false, THREADS>, grid, block, 0, st, p);
+  return f8 ? launch_pdl(kv_append_kernel<false, true, THREADS>, grid, block, 0, st, p)
+            : launch_pdl(kv_append_kernel<false, false, THREADS>, grid, block, 0, st, p);
 }
 
 }  // namespace
@@ -168,14 +192,8 @@ cudaError_t launch_kv_append(const AppendParams& p, int T, bool bf16, bool f8, i
   // One block for each token. Few tokens: all their heads at once, as the latency of one pass is the time (24 tokens of 32
   // heads of 256: 2.4 us with 512 threads, 3.0 with 128, 4.2 with 64). Many: small blocks, which start and end
   // out of step and so keep the memory busy (16000 tokens of 56 heads of 128: 141 us with 512, 87 with 256, 75 with 128, 72 with 64,
-  // 0.95 of the copy rate; 512 tokens: 4.9, 4.0, 4.1 and 5.3).
-  const int threads = T <= sms ? 512 : T < 8 * sms ? 256 : 64, lanes = p.dim / 16;
-  const dim3 grid(static_cast<unsigned>(T)), block(static_cast<unsigned>(threads / lanes * lanes));
-  if (bf16)
-    return f8 ? launch_pdl(kv_append_kernel<true, true>, grid, block, 0, st, p)
-              : launch_pdl(kv_append_kernel<true, false>, grid, block, 0, st, p);
-  return f8 ? launch_pdl(kv_append_kernel<false, true>, grid, block, 0, st, p)
-            : launch_pdl(kv_append_kernel<false, false>, grid, block, 0, st, p);
+  // 0.96 of the copy rate; 512 tokens: 4.9, 3.7, 4.1 and 5.3; 1000 tokens: 5.8 with 256, 5.5 with 64).
+  return T <= sms ? launch<512>(p, T, bf16, f8, st) : T < 4 * sms ? launch<256>(p, T, bf16, f8, st) : launch<64>(p, T, bf16, f8, st);
 }
 
 }  // namespace tl
