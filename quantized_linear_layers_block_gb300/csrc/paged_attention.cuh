@@ -33,8 +33,8 @@
 // An 8-bit cache is widened to f16 in registers (exact); q is then scaled by a
 // power of two of its own per head so that a bf16 query fits f16's range.
 //
-// Few and short segments take the same way with a cluster of eight blocks each, which join through their shared
-// memory: no list, no workspace, no atomics.
+// Few segments of some hundred keys take the same way with a cluster of eight blocks each, which join through their shared
+// memory; segments of few keys with a ring each: no list, no workspace, no atomics.
 //
 // Measured on GB300 (copy rate 6.79 TB/s): the loop streams at 7.4-7.7 TB/s. 160 requests of 512-16384 tokens, 8 heads of 128
 // channels, 8 bits: 222 us, 6.8 TB/s of 1.51 GB. 24 requests of 40-9000 tokens, 4 heads of 256, bf16: 37 us, 4.7 TB/s;
@@ -462,11 +462,18 @@ __device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uin
   }
 }
 
-// CL: eight blocks, a cluster, take a segment, and join it through their shared memory.
-template <int CACHE, int D, int HW, int NT, bool CL>
+enum AttnMode {
+  kList,      // the list of tiles, in equal shares
+  kCluster,   // eight blocks, a cluster, take a segment, and join it through their shared memory
+  kSolo       // each ring takes whole segments for itself, of KT keys a tile: no meetings, no joins
+};
+
+template <int CACHE, int D, int HW, int NT, AttnMode MODE>
 __global__ void __launch_bounds__(kAttnRings * HW * 32, Traits<CACHE, D, HW, NT>::BLOCKS)
 paged_attention_kernel(const __grid_constant__ AttnParams p) {
   using T = Traits<CACHE, D, HW, NT>;
+  constexpr bool CL = MODE == kCluster, SOLO = MODE == kSolo;
+  constexpr int TILE = SOLO ? T::KT : T::TILE;        // keys of a tile, of the whole block or of one ring
   constexpr int KT = T::KT, ROW = T::ROW, MT = KT / 16, DT = D / 16, S = T::STAGES;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_bar;
@@ -489,9 +496,24 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     cur.h = seg - cur.b * HG;
     const int len = __ldg(p.lens + cur.b);
     if ((len < 0 || len > p.max_len) && tid == 0) set_status(p.status, TL_EDATA);
-    seg_keys(p, len, T::TILE, cur);
+    seg_keys(p, len, TILE, cur);
     cur.tile = static_cast<int>(static_cast<long long>(cur.tiles) * rank / kAttnCluster);
     count = static_cast<int>(static_cast<long long>(cur.tiles) * (rank + 1) / kAttnCluster) - cur.tile;
+    skip = 1;
+  } else if constexpr (SOLO) {
+    // ---- the block's segments, shared out to its rings; `count` of them, whole
+    const long long segments = static_cast<long long>(p.B) * HG;
+    const long long s0 = segments * blockIdx.x / gridDim.x;
+    const int n = static_cast<int>(segments * (blockIdx.x + 1) / gridDim.x - s0);
+    const long long mine = s0 + static_cast<long long>(n) * w / kAttnRings;
+    count = static_cast<int>(s0 + static_cast<long long>(n) * (w + 1) / kAttnRings - mine);
+    if (count == 0) return;
+    cur.b = static_cast<int>(divide(mine, HG));
+    cur.h = static_cast<int>(mine - static_cast<long long>(cur.b) * HG);
+    const int len = __ldg(p.lens + cur.b);
+    if ((len < 0 || len > p.max_len) && lane == 0) set_status(p.status, TL_EDATA);
+    seg_keys(p, len, TILE, cur);
+    cur.tile = 0;
     skip = 1;
   } else {
     // ---- the share of this block: `count` places from t0 of the list, in which a segment has one place for
@@ -502,7 +524,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     for (int base = 0; base < p.B; base += 32) {
       len = base + lane < p.B ? __ldg(p.lens + base + lane) : 0;
       bad |= len < 0 || len > p.max_len;
-      seg_keys(p, len, T::TILE, cur);
+      seg_keys(p, len, TILE, cur);
       if (base + lane < p.B) total += cur.tiles + 1;
     }
     if (bad && blockIdx.x == 0) set_status(p.status, TL_EDATA);
@@ -517,7 +539,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     long long run = 0;                                // places of the requests before this round's, of one head group
     for (int base = 0;; base += 32) {
       if (p.B > 32) len = base + lane < p.B ? __ldg(p.lens + base + lane) : 0;
-      seg_keys(p, len, T::TILE, cur);
+      seg_keys(p, len, TILE, cur);
       const unsigned places = base + lane < p.B ? cur.tiles + 1 : 0;
       unsigned incl = places;
 #pragma unroll
@@ -529,7 +551,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       if (at != 0) {
         const int who = __ffs(at) - 1;
         cur.b = base + who;
-        seg_keys(p, __shfl_sync(0xffffffffu, len, who), T::TILE, cur);
+        seg_keys(p, __shfl_sync(0xffffffffu, len, who), TILE, cur);
         const long long left = t0 - HG * (run + __shfl_sync(0xffffffffu, incl - places, who));
         cur.h = static_cast<int>(divide(left, cur.tiles + 1));
         skip = static_cast<int>(left - cur.h * (cur.tiles + 1ll));
@@ -550,6 +572,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       asm volatile("bar.sync %0, %1;" ::"r"(1 + w), "n"(HW * 32) : "memory");
   };
 
+  const int at0 = SOLO ? 0 : w * KT;                  // the ring's first key of a tile
   constexpr int CPR = ROW / 16;                       // 16-byte chunks of a row
   constexpr int RPI = 32 / CPR;                       // rows that one instruction of a warp copies
   constexpr int KPL = (KT + 31) / 32;                 // keys whose address a lane computes
@@ -564,16 +587,16 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
   auto fetch_pages = [&]() {
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
-      const int key = ld.begin + ld.tile * T::TILE + w * KT + i * 32 + lane;
+      const int key = ld.begin + ld.tile * TILE + at0 + i * 32 + lane;
       pid[i] = key >= ld.first && key < ld.end && i * 32 + lane < KT ? __ldg(p.pages + ld.b * p.ldp + p.page.div(key)) : -1;
     }
   };
-  int left = count - (skip == 0);                     // places of the tiles not yet asked for
+  int left = count - (skip == 0);                     // places of the tiles (kSolo: segments) not yet asked for
   fetch_len();
   if (left > 0) fetch_pages();
   auto load_tile = [&](int stage) {
     if (left > 0) {
-      const int k0 = ld.begin + ld.tile * T::TILE + w * KT;
+      const int k0 = ld.begin + ld.tile * TILE + at0;
       if (k0 < ld.end) {
         const int kvh = ld.h / p.groups_per_kv;
         int64_t off[KPL];                             // bytes from the cache's first row to key i * 32 + lane; -1: no such row
@@ -616,14 +639,15 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
           }
         }
       }
-      --left;
+      if constexpr (!SOLO) --left;
       if (++ld.tile == ld.tiles) {
         ld.tile = 0;
         --left;
         if (++ld.h == HG) {
           ld.h = 0;
           ++ld.b;
-          seg_keys(p, next_len, T::TILE, ld);
+          if (SOLO && (next_len < 0 || next_len > p.max_len) && left > 0 && lane == 0) set_status(p.status, TL_EDATA);
+          seg_keys(p, next_len, TILE, ld);
           fetch_len();
         }
       }
@@ -669,14 +693,14 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     }
   };
   fetch_q();
-  if (!CL && tid == 0) {
+  if (MODE == kList && tid == 0) {
     s_pend[0].n = s_pend[1].n = 0;
     mbar_init(smem_u32(&s_bar), 1);
     fence_barrier_init();
   }
   while (CL || done < count) {
     // tiles of this segment in this block's share (none for some blocks of a cluster)
-    const int here = min(cur.tiles - cur.tile, count - done);
+    const int here = SOLO ? cur.tiles : min(cur.tiles - cur.tile, count - done);
 
     float sc[NT][2];                                  // log2(e) scale of heads 2t and 2t + 1
 #pragma unroll
@@ -726,7 +750,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       cp_async_wait<S - 2>();
       ring_sync();
       load_tile(stage == 0 ? S - 1 : stage - 1);      // the buffer that the last turn read
-      const int k0 = cur.begin + (cur.tile + it) * T::TILE + w * KT;
+      const int k0 = cur.begin + (cur.tile + it) * TILE + at0;
       const uint32_t kb = ring + stage * T::BUF, vb = kb + KT * ROW;
       if (k0 < cur.end) {
         float s[MT][NT][4], s2[MT][NT][4];            // two chains of dependent MMAs
@@ -868,7 +892,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       }
       stage = stage + 1 == S ? 0 : stage + 1;
     }
-    done += here;
+    done += SOLO ? 1 : here;
 
     // ---- the warps meet: each leaves (m, l, o) in shared memory
     float* const mo = meet + w * (T::MEET / 4);
@@ -898,6 +922,25 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
     const Segment seg = cur;
     const int sh0 = h0, sheads = heads;
     const float vs = vscale;
+    if constexpr (SOLO) {
+      // a warp alone: its heads pass through its part of the ring's place of meeting to whole rows
+      cur.tile = 0;
+      if (++cur.h == HG) {
+        cur.h = 0;
+        ++cur.b;
+        if (done < count) seg_keys(p, __ldg(p.lens + cur.b), TILE, cur);
+      }
+      if (done < count) fetch_q();
+      __syncwarp();
+      const int first_head = 8 * NT * hw, live = min(8 * NT, sheads - first_head);
+      for (int x = lane; x < live * (D / 4); x += 32) {
+        const int h = first_head + x / (D / 4), d = 4 * (x % (D / 4));
+        const float4 v = *reinterpret_cast<const float4*>(mo + 2 * T::HEADS + h * T::OPITCH + d);
+        write_out<T>(p, seg.b, sh0 + h, d, D, v, mo[h], mo[T::HEADS + h], vs);
+      }
+      __syncwarp();
+      continue;
+    }
     const bool whole = !CL && !starts_before && seg.tile + here == seg.tiles, second = !starts_before;
     const long long first = t0 + (done - here) - seg.tile;      // the place of its first tile
     if constexpr (CL) {
@@ -910,7 +953,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       if (++cur.h == HG) {
         cur.h = 0;
         ++cur.b;
-        if (done < count) seg_keys(p, __ldg(p.lens + cur.b), T::TILE, cur);
+        if (done < count) seg_keys(p, __ldg(p.lens + cur.b), TILE, cur);
       }
       if (done < count) fetch_q();
     }
@@ -995,6 +1038,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       s_last[second] = count_in(p.counters + c0 + group.x, group.y);
     }
   }
+  if constexpr (SOLO) return;
   pdl_launch_dependents();             // the stream is over: the next kernel may begin its own beside the joins
   cp_async_wait<0>();
   fence_proxy_async_smem();            // joins copy to the ring by the async proxy
@@ -1014,11 +1058,12 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int n = __atomic_load_n(&per_sm[dev], __ATOMIC_RELAXED);
   if (n == 0) {
-    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, HW, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(paged_attention_kernel<CACHE, D, HW, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
-    if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<CACHE, D, HW, NT, false>, T::THREADS, T::SMEM);
+    for (auto* kernel : {paged_attention_kernel<CACHE, D, HW, NT, kList>, paged_attention_kernel<CACHE, D, HW, NT, kCluster>,
+                         paged_attention_kernel<CACHE, D, HW, NT, kSolo>}) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+      if (e != cudaSuccess) return e;
+    }
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<CACHE, D, HW, NT, kList>, T::THREADS, T::SMEM);
     if (e != cudaSuccess) return e;
     n = n < 1 ? 1 : n > kAttnMaxBlocksPerSm ? kAttnMaxBlocksPerSm : n;
     __atomic_store_n(&per_sm[dev], n, __ATOMIC_RELAXED);
@@ -1027,14 +1072,20 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
   const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv;
   long long grid = static_cast<long long>(sms) * n;
   if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
-  // Few and short segments: a cluster for each, while they all fit on half of the GPU at once and a block has two tiles at most
-  if (segments * kAttnCluster * 2 <= grid && keys <= 2ll * kAttnCluster * T::TILE)
-    return launch_pdl_cluster(paged_attention_kernel<CACHE, D, HW, NT, true>, dim3(static_cast<unsigned>(segments * kAttnCluster)),
+  // Short segments: a ring for each, while that is one step or two, or as long as there are segments for all rings
+  // (1216 of one key 11.2 -> 4.1 us; but 76 of up to 123 keys, of 128 channels, 7.6 -> 10.0 us).
+  // Few and longer ones: a cluster each, while they all fit on half of the GPU at once and a block has two tiles at most.
+  if (keys <= (segments < grid * kAttnRings ? 2 : 8) * T::KT)
+    return launch_pdl(paged_attention_kernel<CACHE, D, HW, NT, kSolo>, dim3(static_cast<unsigned>(segments < grid ? segments : grid)),
+                      dim3(T::THREADS), T::SMEM, st, p);
+  const bool few = segments * kAttnCluster * 2 <= grid;
+  if (few && keys <= 2ll * kAttnCluster * T::TILE)
+    return launch_pdl_cluster(paged_attention_kernel<CACHE, D, HW, NT, kCluster>, dim3(static_cast<unsigned>(segments * kAttnCluster)),
                               dim3(T::THREADS), T::SMEM, st, kAttnCluster, p);
   // most places that the list can have; a window's tiles may begin up to 15 keys before it
   const long long most = segments * ((keys + 15 + T::TILE - 1) / T::TILE + 1);
   if (grid > most) grid = most;
-  return launch_pdl(paged_attention_kernel<CACHE, D, HW, NT, false>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
+  return launch_pdl(paged_attention_kernel<CACHE, D, HW, NT, kList>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
 }
 
 // `columns`: 1, 2 or 4 times 8 query heads to a segment. A warp that takes 16 heads reads K and V half as often as two

@@ -128,6 +128,29 @@ def test_few_short_requests(d, cache, hq, hkv):
         check(*build(d + hq + len(lens), lens, hq, hkv, d, 16, cache), lens, window=window)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cache,qtype", [("bf16", None), ("f16", None), ("f8", "bf16"), ("f8", "f16")])
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 1), (24, 2), (20, 1), (40, 1)])
+def test_many_short_requests(d, cache, qtype, hq, hkv):
+    """Segments of few keys, which a ring of a block takes whole: one for each ring, and several."""
+    for b, hi, window in ((40, 95, 0), (700, 30, 0), (100, 110, 9), (3, 15, 0)):
+        lens = [int(x) for x in np.random.default_rng(b + d).integers(0, hi + 1, b)]
+        check(*build(d + hq + b, lens, hq, hkv, d, 16, cache, qtype), lens, window=window)
+
+
+def test_bad_lengths_among_short_requests():
+    lens = [5, 9, 3, 7] * 30
+    kv, q, table, k64, v64 = build(22, lens, 4, 2, 64, 16)
+    good = check(kv, q, table, k64, v64, lens)
+    wrong = list(lens)
+    wrong[50], wrong[51] = -3, 1000
+    safe = np.where(table < 0, 0, table)
+    y = kv.attend(q.cuda(), torch.tensor(safe).cuda(), torch.tensor(wrong, dtype=torch.int32).cuda())
+    assert tl.tl_get_status() == tl.TL_EDATA
+    keep = [i for i in range(120) if i not in (50, 51)]
+    assert torch.equal(y[keep], good[keep])
+
+
 def test_many_requests_and_workspace_reuse():
     rng = np.random.default_rng(3)
     lens = [int(x) for x in rng.integers(0, 40, 700)]
