@@ -12,15 +12,15 @@
 // (thread t of a quad takes the 8 consecutive elements 8t .. 8t + 7 of 32) every load is 16 bytes.
 //
 // Then y = base + scale B h: every block has h and takes its part of the columns. Tokens are the rows of the MMA, the
-// columns of B are permuted so that a thread ends with 8 consecutive ones of a token: 16-byte loads
-// of base and stores of y, whose bytes bound the kernel for many tokens. h is scaled by a
+// columns of B are permuted so that a thread ends with 8 of a token, in 16-byte pieces side by side with its
+// quad's: loads of base and stores of y, whose bytes bound the kernel for many tokens. h is scaled by a
 // power of two of its own per token (the f16 range) and split in 16-bit parts, so that it keeps 16 bits or more.
 //
 // A few items leave most SMs idle, and the expansion long: then several clusters take
 // an item's columns, and each forms h for itself (its A is in L2 by then).
 //
 // Measured on GB300: 4096 tokens, rank 16, K = 5120, N = 34816, bf16: 102 us, 6.05 TB/s, 0.89 of the copy rate (two kernels
-// with h in memory: 169 us). 515 tokens, rank 64, K = 17408, N = 5120, fp32 out: 22 us, of which the first
+// with h in memory: 169 us). 515 tokens, rank 64, K = 17408, N = 5120, fp32 out: 21 us, of which the first
 // product takes 8 (96 MB of x and A per item into the SMs, 83 B/ns each), the second 4.5 and the chain
 // around them (plan, sums, two meetings of the cluster, parts) the rest. 48 tokens of 32 adapters, rank 32, K = N = 5120:
 // 8.3 us; one token, rank 16, N = 17408: 5.5 us, all of it that chain.
@@ -231,15 +231,19 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   const int groups = (p.N + 31) / 32, share = part * CS + me, shares = NS * CS;
   const int g1 = static_cast<int>(static_cast<long long>(groups) * (share + 1) / shares);
   int col = static_cast<int>(static_cast<long long>(groups) * share / shares) + warp;
-  constexpr int YB = V == 2 ? 4 : 2, STEP = kLoraWarps * 32;
+  // A thread has 8 columns of a group of 32: 8t .. 8t + 7 of 16-bit rows, 4t .. 4t + 3 of each half of fp32 rows, so that
+  // every 16-byte access of a quad covers 64 bytes (8 consecutive columns in fp32 touch each sector twice: 1743 tokens,
+  // rank 8, N = 33688: 153 us).
+  constexpr int YB = V == 2 ? 4 : 2, SIDE = 8 / V, STEP = kLoraWarps * 32;
   const int n_end = min(32 * g1, p.N);
-  int n = 32 * col + 8 * t;                      // this thread's first column of the group asked for
+  int n = 32 * col + SIDE * t;                   // this thread's first column of the group asked for
   const char* bp[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) bp[i] = static_cast<const char*>(p.base) + (tok[i] * p.ldb + n) * YB;
-  // rows of B: columns permuted so that tile j's column c is column 8 (c / 2) + 2 j + c % 2 of the group
+  // rows of B: columns permuted so that tile j's column c is column SIDE (c / 2) + tile_col(j) + c % 2 of the group
+  auto tile_col = [](int j) { return V == 2 ? 2 * (j & 1) + 16 * (j >> 1) : 2 * j; };
   constexpr int KV = RT == 1 ? 4 : 8;            // elements of a row that a thread takes
-  int nb = 32 * col + 8 * (g >> 1) + (g & 1);    // its row in tile 0 of the group that wp points to
+  int nb = 32 * col + SIDE * (g >> 1) + (g & 1);    // its row in tile 0 of the group that wp points to
   const uint16_t* wp = p.B + (static_cast<int64_t>(adapter) * p.N + nb) * p.rank + KV * t;
   const int steps = adapter < 0 ? 0 : RP / L::KSTEP;
   const int mts = count > 16 ? 2 : 1, halves = V == 2 && mts == 2 ? 2 : 1;      // stages with base
@@ -247,20 +251,20 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   int kind = 0, ask_at = 0, take_at = 0;         // which of a group's stages is asked for next; places in the ring
   auto ask_next = [&]() {
     const uint32_t dst = slot0 + ask_at * L::YSTAGE;
-    if (n - 8 * t < n_end) {
+    if (n - SIDE * t < n_end) {
       if (kind < b_stages) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool in = nb + 2 * j < n_end && 32 * kind + KV * t < p.rank;
-          cp_async16(dst + j * L::VEC, in ? wp + 2 * j * p.rank + 32 * kind : p.B, in ? 16 : 0);
+          const bool in = nb + tile_col(j) < n_end && 32 * kind + KV * t < p.rank;
+          cp_async16(dst + j * L::VEC, in ? wp + tile_col(j) * p.rank + 32 * kind : p.B, in ? 16 : 0);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // V = 1: token 8i + g; V = 2: the two vectors of tokens 8 (i / 2) + g, and 16 more in the second stage
           const int half = kind - b_stages, r = V == 1 ? i : (i >> 1) + 2 * half;
-          const char* const src = V == 1 ? bp[i] : (half == 0 ? bp[i >> 1] : bp[2 + (i >> 1)]) + 16 * (i & 1);
-          if (n < n_end && 8 * r + g < count) cp_async16(dst + i * L::VEC, src, 16);
+          const char* const src = V == 1 ? bp[i] : (half == 0 ? bp[i >> 1] : bp[2 + (i >> 1)]) + 64 * (i & 1);
+          if (n + (V == 1 ? 0 : 16 * (i & 1)) < n_end && 8 * r + g < count) cp_async16(dst + i * L::VEC, src, 16);
         }
       }
     }
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   auto load_b = [&]() {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      bw[j] = nb + 2 * j < n_end && KV * t < p.rank ? __ldg(reinterpret_cast<const uint2*>(wp + 2 * j * p.rank)) : make_uint2(0, 0);
+      bw[j] = nb + tile_col(j) < n_end && KV * t < p.rank ? __ldg(reinterpret_cast<const uint2*>(wp + tile_col(j) * p.rank)) : make_uint2(0, 0);
     nb += STEP;
     wp += static_cast<int64_t>(STEP) * p.rank;
   };
@@ -459,10 +463,10 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   // ---- y = base + B h
   char* yp[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + 32 * col + 8 * t) * YB;
+  for (int i = 0; i < 4; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + 32 * col + SIDE * t) * YB;
   const uint32_t hbase = smem_u32(hs) + ((lane & 15) * PITCH + (lane >> 4) * 8) * 2;
   for (; col < g1; col += kLoraWarps) {
-    const bool live = 32 * col + 8 * t < n_end;
+    const int left = n_end - 32 * col - SIDE * t;              // columns from this thread's first to the end
     float acc[2][4][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -500,11 +504,11 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       }
     }
     uint32_t src = take_next();
-    // token 8i + g: columns 8t + 2j + {0, 1} of the group are elements 2 (i & 1) + {0, 1} of acc[i / 2][j]
+    // token 8i + g: columns SIDE t + tile_col(j) + {0, 1} of the group are elements 2 (i & 1) + {0, 1} of acc[i / 2][j]
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (V == 2 && i == 2 && mts == 2) src = take_next();
-      if (live && tok[i] >= 0) {
+      if (left > 0 && tok[i] >= 0) {
         uint4 r[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) r[e] = ld_shared16(src + (V == 1 ? i : 2 * (i & 1) + e) * L::VEC);
@@ -526,7 +530,8 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
           for (int e = 0; e < V; ++e) r[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) reinterpret_cast<uint4*>(yp[i])[e] = r[e];
+        for (int e = 0; e < V; ++e)
+          if (16 * e < left) reinterpret_cast<uint4*>(yp[i])[4 * e] = r[e];
       }
       yp[i] += STEP * YB;
     }
