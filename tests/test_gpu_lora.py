@@ -80,6 +80,17 @@ def test_few_and_many_adapters():
     check(*make(5, 33, 256, 128, 16, 2, ids=[0] * 16 + [1] + [-1] * 16), in_place=True)
 
 
+@pytest.mark.parametrize("M", [39, 45, 52, 70, 90, 140, 305])
+def test_clusters_of_every_size(M):
+    check(*make(100 + M, M, 2056, 1000, 24, M, ids=np.arange(M)))
+
+
+@pytest.mark.parametrize("M", [1, 3, 7, 11])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_columns_of_an_item_over_several_clusters(M, out):
+    check(*make(200 + M, M, 600, 20008, 40, M, out=out, ids=np.arange(M)), out=out)
+
+
 def test_in_place_strided_and_another_stream():
     for out in ("bf16", "f32"):
         check(*make(6, 45, 264, 200, 16, 3, out=out), out=out, in_place=True)
