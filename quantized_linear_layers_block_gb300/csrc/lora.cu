@@ -165,27 +165,29 @@ __device__ __forceinline__ uint32_t add2(uint32_t base, float lo, float hi, floa
 // Shared memory: the first product's ring [RS][slots][threads], then in its place
 // the warps' sums of one RT, then the second product's ring [YS][4][threads]. Behind that h's sums [32][RP] in fp32, RP
 // the rank rounded up to 16 (RT = 1) or a multiple of 32, and the parts of h [PARTS][32][RP + 8].
-template <bool BF16, int YD, int RT>
+template <bool BF16, int YD, int RT, int TILE>
 struct Lora {
   static constexpr int PARTS = YD == TL_F32 && BF16 ? 3 : 2;
   static constexpr int V = YD == TL_F32 ? 2 : 1;                // 16-byte vectors of 8 columns
   static constexpr int ROWS = 16 * RT, RPITCH = ROWS + 4;
   static constexpr int THREADS = kLoraWarps * 32, VEC = THREADS * 16;
-  static constexpr int SLOTS = 2 * RT + kLoraTile / 8, RS = RT == 4 ? 2 : RT == 2 ? 3 : 4, RING = RS * SLOTS * VEC;
+  static constexpr int SLOTS = 2 * RT + TILE / 8, RS = RT == 4 ? 2 : RT == 2 && TILE == 32 ? 3 : 4, RING = RS * SLOTS * VEC;
   // The second product's ring. Up to rank 16, a thread's part of B is 8 bytes a row and goes to registers, one group
   // ahead (8-byte slots in the ring: 4096 tokens 112 us instead of 103); above, B has stages of its own.
   static constexpr bool REG_B = RT == 1;
-  static constexpr int YS = RT == 2 ? 6 : 4, YSTAGE = 4 * VEC, YRING = YS * YSTAGE;
-  static constexpr int RED = kLoraWarps / 2 * kLoraTile * RPITCH * 4;
+  static constexpr int BASES = V == 1 ? TILE / 8 : 4;          // vectors of base in a stage
+  static constexpr int YSLOTS = REG_B ? BASES : 4;
+  static constexpr int YS = REG_B ? 16 / YSLOTS : RT == 2 ? 6 : 4, YSTAGE = YSLOTS * VEC, YRING = YS * YSTAGE;
+  static constexpr int RED = kLoraWarps / 2 * TILE * RPITCH * 4;
   static_assert(RED <= YRING && YRING <= RING, "layout");
   // the K of the second product: one MMA for ranks up to 16, else pairs of them
   static constexpr int KSTEP = RT == 1 ? 16 : 32;
   __host__ __device__ static int padded(int rank) { return (rank + KSTEP - 1) / KSTEP * KSTEP; }
   // one pass of the first product (rank <= 16 RT): its ring is free when the sums are written
   __host__ __device__ static int sum_at(int rank) { return rank <= ROWS ? YRING : RING; }
-  __host__ __device__ static int hs_at(int rank) { return rank <= ROWS ? YRING + kLoraTile * padded(rank) * 4 : YRING; }
+  __host__ __device__ static int hs_at(int rank) { return rank <= ROWS ? YRING + TILE * padded(rank) * 4 : YRING; }
   static int smem(int rank) {
-    const int sum = sum_at(rank) + kLoraTile * padded(rank) * 4, hs = hs_at(rank) + PARTS * kLoraTile * (padded(rank) + 8) * 2;
+    const int sum = sum_at(rank) + TILE * padded(rank) * 4, hs = hs_at(rank) + PARTS * TILE * (padded(rank) + 8) * 2;
     const int most = sum > hs ? sum : hs;
     // rank > ROWS: hs lies before the sums, in what was the first ring
     return most > RING ? most : RING;
@@ -193,12 +195,12 @@ struct Lora {
 };
 
 // blockIdx.x = (item * NS + part of the columns) * CS + rank of the block in its cluster
-template <bool BF16, int YD, int RT>
+template <bool BF16, int YD, int RT, int TILE>
 __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_constant__ LoraParams p, int CS, int NS) {
-  using L = Lora<BF16, YD, RT>;
-  constexpr int NT = kLoraTile / 8, V = L::V, ROWS = L::ROWS;
+  using L = Lora<BF16, YD, RT, TILE>;
+  constexpr int NT = TILE / 8, V = L::V, ROWS = L::ROWS;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float s_up[kLoraTile];
+  __shared__ float s_up[TILE];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int me = blockIdx.x % CS, part = blockIdx.x / CS % NS, idx = blockIdx.x / CS / NS;
   const int RP = L::padded(p.rank);
@@ -237,16 +239,16 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   constexpr int YB = V == 2 ? 4 : 2, SIDE = 8 / V, STEP = kLoraWarps * 32;
   const int n_end = min(32 * g1, p.N);
   int n = 32 * col + SIDE * t;                   // this thread's first column of the group asked for
-  const char* bp[4];
+  const char* bp[NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bp[i] = static_cast<const char*>(p.base) + (tok[i] * p.ldb + n) * YB;
+  for (int i = 0; i < NT; ++i) bp[i] = static_cast<const char*>(p.base) + (tok[i] * p.ldb + n) * YB;
   // rows of B: columns permuted so that tile j's column c is column SIDE (c / 2) + tile_col(j) + c % 2 of the group
   auto tile_col = [](int j) { return V == 2 ? 2 * (j & 1) + 16 * (j >> 1) : 2 * j; };
   constexpr int KV = RT == 1 ? 4 : 8;            // elements of a row that a thread takes
   int nb = 32 * col + SIDE * (g >> 1) + (g & 1);    // its row in tile 0 of the group that wp points to
   const uint16_t* wp = p.B + (static_cast<int64_t>(adapter) * p.N + nb) * p.rank + KV * t;
   const int steps = adapter < 0 ? 0 : RP / L::KSTEP;
-  const int mts = count > 16 ? 2 : 1, halves = V == 2 && mts == 2 ? 2 : 1;      // stages with base
+  const int mts = TILE > 16 && count > 16 ? 2 : 1, halves = V == 2 && mts == 2 ? 2 : 1;      // stages with base
   const int b_stages = L::REG_B ? 0 : steps;
   int kind = 0, ask_at = 0, take_at = 0;         // which of a group's stages is asked for next; places in the ring
   auto ask_next = [&]() {
@@ -260,10 +262,10 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < L::BASES; ++i) {
           // V = 1: token 8i + g; V = 2: the two vectors of tokens 8 (i / 2) + g, and 16 more in the second stage
           const int half = kind - b_stages, r = V == 1 ? i : (i >> 1) + 2 * half;
-          const char* const src = V == 1 ? bp[i] : (half == 0 ? bp[i >> 1] : bp[2 + (i >> 1)]) + 64 * (i & 1);
+          const char* const src = V == 1 ? bp[i] : (half == 0 ? bp[i >> 1] : bp[(NT - 2) + (i >> 1)]) + 64 * (i & 1);
           if (n + (V == 1 ? 0 : 16 * (i & 1)) < n_end && 8 * r + g < count) cp_async16(dst + i * L::VEC, src, 16);
         }
       }
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         wp += static_cast<int64_t>(STEP) * p.rank;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bp[i] += STEP * YB;
+      for (int i = 0; i < NT; ++i) bp[i] += STEP * YB;
     }
     ask_at = ask_at + 1 == L::YS ? 0 : ask_at + 1;
   };
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     take_at = take_at + 1 == L::YS ? 0 : take_at + 1;
     return src;
   };
-  float up[4] = {};
+  float up[NT] = {};
   if (steps > 0) {
     // ---- h = A x
     const int chunks = (p.K + 31) / 32, workers = CS * kLoraWarps, worker = me * kLoraWarps + warp;
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         }
       }
       // the warps' sums, two warps to a place
-      float* const mine = red + (warp % (kLoraWarps / 2)) * kLoraTile * L::RPITCH + g;
+      float* const mine = red + (warp % (kLoraWarps / 2)) * TILE * L::RPITCH + g;
 #pragma unroll
       for (int half = 1; half >= 0; --half) {
         __syncthreads();                         // the rings, or what stood here before, have been read
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kLoraWarps / 2; ++w) {
-          const float4 q = *reinterpret_cast<const float4*>(red + (w * kLoraTile + m) * L::RPITCH + r);
+          const float4 q = *reinterpret_cast<const float4*>(red + (w * TILE + m) * L::RPITCH + r);
           v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
         }
         if (r0 + r < RP) *reinterpret_cast<float4*>(sum + m * RP + r0 + r) = v;
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e2 = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-      if (sub == 0 && m < kLoraTile) s_up[m] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+      if (sub == 0 && m < TILE) s_up[m] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
       // element 8q + j of 32 (thread q of the quad loads it): MMA j / 4, column 2q + (j & 1) + 8 ((j & 2) / 2);
       // of 16, for one MMA, element 4q + j
       const int at = RT == 1 ? 2 * sub : 32 * (sub >> 3) + 16 * (sub & 1) + 2 * (sub >> 1 & 3);
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
             v[2 * e] = isinf(v[2 * e]) ? 0.f : v[2 * e] - lo;
             v[2 * e + 1] = isinf(v[2 * e + 1]) ? 0.f : v[2 * e + 1] - hi;
           }
-          uint32_t* const dst = reinterpret_cast<uint32_t*>(hs + (h * kLoraTile + m) * PITCH + at);
+          uint32_t* const dst = reinterpret_cast<uint32_t*>(hs + (h * TILE + m) * PITCH + at);
           dst[0] = w[0];           // j & 2 = 0: columns 2q, 2q + 1
           dst[4] = w[1];           // j & 2 = 2: columns 8 + 2q, 9 + 2q
         }
@@ -454,22 +456,22 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     if (CS > 1) cluster_arrive();                // this block has read the others' sums
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) up[i] = s_up[8 * i + g];
+    for (int i = 0; i < NT; ++i) up[i] = s_up[8 * i + g];
   } else {
 #pragma unroll 1
     for (int s = 0; s < L::YS - 1; ++s) ask_next();
   }
 
   // ---- y = base + B h
-  char* yp[4];
+  char* yp[NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + 32 * col + SIDE * t) * YB;
+  for (int i = 0; i < NT; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + 32 * col + SIDE * t) * YB;
   const uint32_t hbase = smem_u32(hs) + ((lane & 15) * PITCH + (lane >> 4) * 8) * 2;
   for (; col < g1; col += kLoraWarps) {
     const int left = n_end - 32 * col - SIDE * t;              // columns from this thread's first to the end
-    float acc[2][4][4];
+    float acc[NT / 2][4][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < NT / 2; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.f;
     for (int s = 0; s < steps; ++s) {
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
         for (int j = 0; j < 4; ++j) b[j] = ld_shared16(at + j * L::VEC);
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
+      for (int m = 0; m < NT / 2; ++m) {
         if (m < mts) {
 #pragma unroll
           for (int h = 0; h < L::PARTS; ++h) {
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
               uint32_t a[4];
               asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                            : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
-                           : "r"(hbase + ((h * kLoraTile + 16 * m) * PITCH + 32 * s + 16 * half) * 2)
+                           : "r"(hbase + ((h * TILE + 16 * m) * PITCH + 32 * s + 16 * half) * 2)
                            : "memory");
 #pragma unroll
               for (int j = 0; j < 4; ++j)
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     uint32_t src = take_next();
     // token 8i + g: columns SIDE t + tile_col(j) + {0, 1} of the group are elements 2 (i & 1) + {0, 1} of acc[i / 2][j]
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NT; ++i) {
       if (V == 2 && i == 2 && mts == 2) src = take_next();
       if (left > 0 && tok[i] >= 0) {
         uint4 r[V];
@@ -540,15 +542,15 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   if (steps > 0 && CS > 1) cluster_wait();       // no block leaves while another reads its sums
 }
 
-template <bool BF16, int YD, int RT>
+template <bool BF16, int YD, int RT, int TILE>
 cudaError_t apply(const LoraParams& p, int sms, cudaStream_t st) {
-  using L = Lora<BF16, YD, RT>;
+  using L = Lora<BF16, YD, RT, TILE>;
   static int ready[64];                            // the shared memory limit is set, by device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (__atomic_load_n(&ready[dev], __ATOMIC_RELAXED) == 0) {
-    e = cudaFuncSetAttribute(lora_kernel<BF16, YD, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(kLoraMaxRank));
+    e = cudaFuncSetAttribute(lora_kernel<BF16, YD, RT, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(kLoraMaxRank));
     if (e != cudaSuccess) return e;
     __atomic_store_n(&ready[dev], 1, __ATOMIC_RELAXED);
   }
@@ -561,21 +563,28 @@ cudaError_t apply(const LoraParams& p, int sms, cudaStream_t st) {
   int cs = kLoraMaxCluster, ns = 1;
   while (cs > 1 && ((p.K + 31) / 32 < cs * kLoraWarps || items * cs > 2LL * sms)) --cs;
   while (items * cs * (ns + 1) <= 2LL * sms && (p.N + 31) / 32 >= (ns + 1) * cs * kLoraWarps) ++ns;
-  return launch_pdl_cluster(lora_kernel<BF16, YD, RT>, dim3(static_cast<unsigned>(items * ns * cs)), dim3(kLoraWarps * 32),
+  return launch_pdl_cluster(lora_kernel<BF16, YD, RT, TILE>, dim3(static_cast<unsigned>(items * ns * cs)), dim3(kLoraWarps * 32),
                             L::smem(p.rank), st, cs, p, cs, ns);
 }
 
-template <bool BF16, int YD>
+template <bool BF16, int YD, int TILE>
 cudaError_t apply_rank(const LoraParams& p, int sms, cudaStream_t st) {
-  return p.rank <= 16 ? apply<BF16, YD, 1>(p, sms, st) : p.rank <= 32 ? apply<BF16, YD, 2>(p, sms, st) : apply<BF16, YD, 4>(p, sms, st);
+  return p.rank <= 16   ? apply<BF16, YD, 1, TILE>(p, sms, st)
+         : p.rank <= 32 ? apply<BF16, YD, 2, TILE>(p, sms, st)
+                        : apply<BF16, YD, 4, TILE>(p, sms, st);
+}
+
+template <bool BF16, int YD>
+cudaError_t apply_tile(const LoraParams& p, int sms, cudaStream_t st) {
+  return lora_tile(p.M) == 16 ? apply_rank<BF16, YD, 16>(p, sms, st) : apply_rank<BF16, YD, 32>(p, sms, st);
 }
 
 template <bool BF16>
 cudaError_t apply_type(const LoraParams& p, int sms, cudaStream_t st) {
   switch (p.y_dtype) {
-    case TL_BF16: return apply_rank<BF16, TL_BF16>(p, sms, st);
-    case TL_F16: return apply_rank<BF16, TL_F16>(p, sms, st);
-    default: return apply_rank<BF16, TL_F32>(p, sms, st);
+    case TL_BF16: return apply_tile<BF16, TL_BF16>(p, sms, st);
+    case TL_F16: return apply_tile<BF16, TL_F16>(p, sms, st);
+    default: return apply_tile<BF16, TL_F32>(p, sms, st);
   }
 }
 

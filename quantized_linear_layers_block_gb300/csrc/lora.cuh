@@ -23,10 +23,12 @@ struct LoraPlanHeader {
   int M, n_adapters, items, unused;
 };
 
-// Tokens of an item. 32 read an adapter's matrices half as often as 16; 16 leave twice as many
-// items, which clusters of blocks share the SMs more evenly with (rank 64, K = 17408, N = 5120: 515 tokens 28 us
-// with 16 and 34 us with 32), and which a GPU full of items does not need.
-inline int lora_tile(int M) { return M >= 2048 ? 32 : 16; }
+// Tokens of an item. 32 read an adapter's matrices half as often as 16 and fill the matrix instructions' rows as
+// well; 16 leave twice as many items, which blocks share the SMs more evenly with, and a shorter chain. The plan
+// serves adapters of any rank and width, and both sides meet at about the same M for all of them (K = 5120, N = 17408,
+// 4 adapters, 16 against 32 tokens, us: rank 8: 512 tokens 12.8, 16.6; 1024: 24.4, 19.9; 2048: 43, 33;
+// rank 128: 512 tokens 35, 52; 1024: 54, 53; 2048: 96, 83).
+inline int lora_tile(int M) { return M >= 1024 ? 32 : 16; }
 
 // most items that M tokens of n_adapters adapters (and none) can need
 inline int lora_max_items(int M, int n_adapters) {

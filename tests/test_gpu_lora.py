@@ -85,6 +85,13 @@ def test_clusters_of_every_size(M):
     check(*make(100 + M, M, 2056, 1000, 24, M, ids=np.arange(M)))
 
 
+@pytest.mark.parametrize("M", [1023, 1024, 1100])
+@pytest.mark.parametrize("rank", [8, 32, 128])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_both_sizes_of_items(M, rank, out):
+    check(*make(300 + M + rank, M, 392, 296, rank, 5, out=out), out=out)
+
+
 @pytest.mark.parametrize("M", [1, 3, 7, 11])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_columns_of_an_item_over_several_clusters(M, out):
