@@ -163,8 +163,9 @@ __device__ __forceinline__ uint32_t add2(uint32_t base, float lo, float hi, floa
 // (4096 tokens: 134 us with operands a step ahead in registers). A stage of the first ring is a whole K step: finer
 // stages keep more bytes on their way and took longer, by their own instructions.
 // Shared memory: the first product's ring [RS][slots][threads], then in its place
-// the warps' sums of one RT, then the second product's ring [YS][4][threads]. Behind that h's sums [32][RP] in fp32, RP
-// the rank rounded up to 16 (RT = 1) or a multiple of 32, and the parts of h [PARTS][32][RP + 8].
+// the warps' sums, then the second product's ring [YS][slots][threads]. Behind the larger of these two h's sums
+// [TILE][RP] in fp32, RP the rank rounded up to 16 (RT = 1) or a multiple of 32, and the parts of h [PARTS][TILE][RP + 8].
+// A rank above 64 is cut over the two halves of the warps, which share K among four then.
 template <bool BF16, int YD, int RT, int TILE>
 struct Lora {
   static constexpr int PARTS = YD == TL_F32 && BF16 ? 3 : 2;
@@ -178,19 +179,16 @@ struct Lora {
   static constexpr int BASES = V == 1 ? TILE / 8 : 4;          // vectors of base in a stage
   static constexpr int YSLOTS = REG_B ? BASES : 4;
   static constexpr int YS = REG_B ? 16 / YSLOTS : RT == 2 ? 6 : 4, YSTAGE = YSLOTS * VEC, YRING = YS * YSTAGE;
-  static constexpr int RED = kLoraWarps / 2 * TILE * RPITCH * 4;
-  static_assert(RED <= YRING && YRING <= RING, "layout");
+  static constexpr int RED = kLoraWarps * TILE * RPITCH * 4;
+  static constexpr int AREA = RED > YRING ? RED : YRING;
+  static_assert(YRING <= RING, "layout");
   // the K of the second product: one MMA for ranks up to 16, else pairs of them
   static constexpr int KSTEP = RT == 1 ? 16 : 32;
   __host__ __device__ static int padded(int rank) { return (rank + KSTEP - 1) / KSTEP * KSTEP; }
-  // one pass of the first product (rank <= 16 RT): its ring is free when the sums are written
-  __host__ __device__ static int sum_at(int rank) { return rank <= ROWS ? YRING : RING; }
-  __host__ __device__ static int hs_at(int rank) { return rank <= ROWS ? YRING + TILE * padded(rank) * 4 : YRING; }
+  __host__ __device__ static int hs_at(int rank) { return AREA + TILE * padded(rank) * 4; }
   static int smem(int rank) {
-    const int sum = sum_at(rank) + TILE * padded(rank) * 4, hs = hs_at(rank) + PARTS * TILE * (padded(rank) + 8) * 2;
-    const int most = sum > hs ? sum : hs;
-    // rank > ROWS: hs lies before the sums, in what was the first ring
-    return most > RING ? most : RING;
+    const int hs = hs_at(rank) + PARTS * TILE * (padded(rank) + 8) * 2;
+    return hs > RING ? hs : RING;
   }
 };
 
@@ -205,7 +203,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   const int me = blockIdx.x % CS, part = blockIdx.x / CS % NS, idx = blockIdx.x / CS / NS;
   const int RP = L::padded(p.rank);
   const int PITCH = RP + 8;
-  float* const sum = reinterpret_cast<float*>(smem + L::sum_at(p.rank));
+  float* const sum = reinterpret_cast<float*>(smem + L::AREA);
   float* const red = reinterpret_cast<float*>(smem);
   uint16_t* const hs = reinterpret_cast<uint16_t*>(smem + L::hs_at(p.rank));
   const uint32_t slot0 = smem_u32(smem) + tid * 16;
@@ -227,6 +225,96 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   for (int n = 0; n < NT; ++n)
     if (8 * n + g >= count) tok[n] = -1;
 
+  const int steps = adapter < 0 ? 0 : RP / L::KSTEP;
+  if (steps > 0) {
+    // ---- h = A x
+    const bool two = RT == 4 && p.rank > ROWS;                                    // the upper warps take ranks 64 and up
+    const int per_block = two ? kLoraWarps / 2 : kLoraWarps, r0 = two ? warp / (kLoraWarps / 2) * ROWS : 0;
+    const int chunks = (p.K + 31) / 32, workers = CS * per_block, worker = me * per_block + (warp & (per_block - 1));
+    const int c0 = static_cast<int>(static_cast<long long>(chunks) * worker / workers);
+    const int c1 = static_cast<int>(static_cast<long long>(chunks) * (worker + 1) / workers);
+    const uint16_t* xr[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xr[n] = p.x + (tok[n] >= 0 ? tok[n] * p.ldx : 0) + 8 * t;
+    const int nts = (count + 7) / 8;
+    const uint16_t* const ar = p.A + (static_cast<int64_t>(adapter) * p.rank + r0 + g) * p.K + 8 * t;
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+    auto ask = [&](int c) {
+      if (c < c1) {
+        const int k = 32 * c;
+        const bool in = k + 8 * t < p.K;
+        const uint32_t dst = slot0 + (c - c0) % L::RS * (L::SLOTS * L::VEC);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool row = in && r0 + 16 * i + 8 * e + g < p.rank;
+            cp_async16(dst + (2 * i + e) * L::VEC, row ? ar + static_cast<int64_t>(16 * i + 8 * e) * p.K + k : p.A, row ? 16 : 0);
+          }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const bool row = in && tok[n] >= 0;
+          if (n < nts) cp_async16(dst + (2 * RT + n) * L::VEC, row ? xr[n] + k : p.x, row ? 16 : 0);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int c = 0; c < L::RS - 1; ++c) ask(c0 + c);
+    for (int c = c0; c < c1; ++c) {
+      cp_async_wait<L::RS - 2>();
+      ask(c + L::RS - 1);                      // the slots that the last turn read
+      const uint32_t src = slot0 + (c - c0) % L::RS * (L::SLOTS * L::VEC);
+      uint4 a[RT][2];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) a[i][e] = ld_shared16(src + (2 * i + e) * L::VEC);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n < nts) {
+          const uint4 b = ld_shared16(src + (2 * RT + n) * L::VEC);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) mma16816<BF16>(acc[i][n], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, b.x, b.y);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) mma16816<BF16>(acc[i][n], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, b.z, b.w);
+        }
+      }
+    }
+    // the warps' sums
+    __syncthreads();                             // the rings have been read
+    float* const mine = red + warp * TILE * L::RPITCH + g;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (n < nts) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mine[(8 * n + 2 * t + (e & 1)) * L::RPITCH + 16 * i + 8 * (e >> 1)] = acc[i][n][e];
+        }
+    __syncthreads();
+    constexpr int W = ROWS / 4;
+    for (int x = tid; x < count * (two ? 2 * W : W); x += kLoraWarps * 32) {
+      const int m = two ? x / (2 * W) : x / W, r = 4 * (two ? x % (2 * W) : x % W);
+      const float* const from = red + ((r / ROWS) * (kLoraWarps / 2) * TILE + m) * L::RPITCH + r % ROWS;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kLoraWarps; ++w) {
+        if (w < per_block) {
+          const float4 q = *reinterpret_cast<const float4*>(from + w * TILE * L::RPITCH);
+          v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+        }
+      }
+      if (r < RP) *reinterpret_cast<float4*>(sum + m * RP + r) = v;
+    }
+    if (CS > 1) cluster_arrive();
+    __syncthreads();                             // the sums have been taken: their place is the ring's
+  }
+
   // ---- this warp's columns: groups of 32, col, col + 8, ... below g1. Each passes through the ring as `steps`
   // stages with B's rows for one K step (none up to rank 16), then one or two with base; the pointers run
   // ahead of the products.
@@ -247,7 +335,6 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   constexpr int KV = RT == 1 ? 4 : 8;            // elements of a row that a thread takes
   int nb = 32 * col + SIDE * (g >> 1) + (g & 1);    // its row in tile 0 of the group that wp points to
   const uint16_t* wp = p.B + (static_cast<int64_t>(adapter) * p.N + nb) * p.rank + KV * t;
-  const int steps = adapter < 0 ? 0 : RP / L::KSTEP;
   const int mts = TILE > 16 && count > 16 ? 2 : 1, halves = V == 2 && mts == 2 ? 2 : 1;      // stages with base
   const int b_stages = L::REG_B ? 0 : steps;
   int kind = 0, ask_at = 0, take_at = 0;         // which of a group's stages is asked for next; places in the ring
@@ -283,11 +370,12 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     }
     ask_at = ask_at + 1 == L::YS ? 0 : ask_at + 1;
   };
-  uint2 bw[4] = {};                              // REG_B: B's rows of the group taken next
-  auto load_b = [&]() {
+  // REG_B: B's rows of the groups in turn; two sets by name, for a set that is moved waits for its loads
+  uint2 b_even[4] = {}, b_odd[4] = {};
+  auto load_b = [&](uint2 (&w)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      bw[j] = nb + tile_col(j) < n_end && KV * t < p.rank ? __ldg(reinterpret_cast<const uint2*>(wp + tile_col(j) * p.rank)) : make_uint2(0, 0);
+      w[j] = nb + tile_col(j) < n_end && KV * t < p.rank ? __ldg(reinterpret_cast<const uint2*>(wp + tile_col(j) * p.rank)) : make_uint2(0, 0);
     nb += STEP;
     wp += static_cast<int64_t>(STEP) * p.rank;
   };
@@ -298,103 +386,14 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     take_at = take_at + 1 == L::YS ? 0 : take_at + 1;
     return src;
   };
+  // the first columns' operands arrive while the blocks meet
+#pragma unroll 1
+  for (int s = 0; s < L::YS - 1; ++s) ask_next();
+  if constexpr (L::REG_B) {
+    if (steps > 0) load_b(b_even);
+  }
   float up[NT] = {};
   if (steps > 0) {
-    // ---- h = A x
-    const int chunks = (p.K + 31) / 32, workers = CS * kLoraWarps, worker = me * kLoraWarps + warp;
-    const int c0 = static_cast<int>(static_cast<long long>(chunks) * worker / workers);
-    const int c1 = static_cast<int>(static_cast<long long>(chunks) * (worker + 1) / workers);
-    const uint16_t* xr[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) xr[n] = p.x + (tok[n] >= 0 ? tok[n] * p.ldx : 0) + 8 * t;
-    const int nts = (count + 7) / 8;
-    for (int r0 = 0; r0 < p.rank; r0 += ROWS) {
-      const uint16_t* const ar = p.A + (static_cast<int64_t>(adapter) * p.rank + r0 + g) * p.K + 8 * t;
-      float acc[RT][NT][4];
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
-      auto ask = [&](int c) {
-        if (c < c1) {
-          const int k = 32 * c;
-          const bool in = k + 8 * t < p.K;
-          const uint32_t dst = slot0 + (c - c0) % L::RS * (L::SLOTS * L::VEC);
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool row = in && r0 + 16 * i + 8 * e + g < p.rank;
-              cp_async16(dst + (2 * i + e) * L::VEC, row ? ar + static_cast<int64_t>(16 * i + 8 * e) * p.K + k : p.A, row ? 16 : 0);
-            }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const bool row = in && tok[n] >= 0;
-            if (n < nts) cp_async16(dst + (2 * RT + n) * L::VEC, row ? xr[n] + k : p.x, row ? 16 : 0);
-          }
-        }
-        cp_async_commit();
-      };
-#pragma unroll
-      for (int c = 0; c < L::RS - 1; ++c) ask(c0 + c);
-      for (int c = c0; c < c1; ++c) {
-        cp_async_wait<L::RS - 2>();
-        ask(c + L::RS - 1);                      // the slots that the last turn read
-        const uint32_t src = slot0 + (c - c0) % L::RS * (L::SLOTS * L::VEC);
-        uint4 a[RT][2];
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) a[i][e] = ld_shared16(src + (2 * i + e) * L::VEC);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n < nts) {
-            const uint4 b = ld_shared16(src + (2 * RT + n) * L::VEC);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) mma16816<BF16>(acc[i][n], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, b.x, b.y);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) mma16816<BF16>(acc[i][n], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, b.z, b.w);
-          }
-        }
-      }
-      // the warps' sums, two warps to a place
-      float* const mine = red + (warp % (kLoraWarps / 2)) * TILE * L::RPITCH + g;
-#pragma unroll
-      for (int half = 1; half >= 0; --half) {
-        __syncthreads();                         // the rings, or what stood here before, have been read
-        if (warp / (kLoraWarps / 2) == half) {
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              if (n < nts) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float* const at = mine + (8 * n + 2 * t + (e & 1)) * L::RPITCH + 16 * i + 8 * (e >> 1);
-                  *at = half == 1 ? acc[i][n][e] : *at + acc[i][n][e];
-                }
-              }
-        }
-      }
-      __syncthreads();
-      for (int x = tid; x < count * (ROWS / 4); x += kLoraWarps * 32) {
-        const int m = x / (ROWS / 4), r = 4 * (x % (ROWS / 4));
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kLoraWarps / 2; ++w) {
-          const float4 q = *reinterpret_cast<const float4*>(red + (w * TILE + m) * L::RPITCH + r);
-          v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
-        }
-        if (r0 + r < RP) *reinterpret_cast<float4*>(sum + m * RP + r0 + r) = v;
-      }
-      if (r0 + ROWS < p.rank) __syncthreads();   // the next pass's ring lies where the warps' sums do
-    }
-    if (CS > 1) cluster_arrive();
-    __syncthreads();                             // the sums have been taken: their place is the ring's
-    // the first columns' operands arrive while the blocks meet
-#pragma unroll 1
-    for (int s = 0; s < L::YS - 1; ++s) ask_next();
-    if constexpr (L::REG_B) load_b();
     if (CS > 1) cluster_wait();
     // ---- some lanes take a token: sum over the blocks, power of two, then the parts in the K order of the MMAs below.
     // A lane has four elements of the rank; 32 / wide tokens to a warp.
@@ -457,9 +456,6 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NT; ++i) up[i] = s_up[8 * i + g];
-  } else {
-#pragma unroll 1
-    for (int s = 0; s < L::YS - 1; ++s) ask_next();
   }
 
   // ---- y = base + B h
@@ -467,7 +463,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
 #pragma unroll
   for (int i = 0; i < NT; ++i) yp[i] = static_cast<char*>(p.y) + (tok[i] * p.ldy + 32 * col + SIDE * t) * YB;
   const uint32_t hbase = smem_u32(hs) + ((lane & 15) * PITCH + (lane >> 4) * 8) * 2;
-  for (; col < g1; col += kLoraWarps) {
+  auto group = [&](const uint2 (&mine)[4], uint2 (&next)[4]) {
     const int left = n_end - 32 * col - SIDE * t;              // columns from this thread's first to the end
     float acc[NT / 2][4][4];
 #pragma unroll
@@ -478,8 +474,8 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       uint4 b[4];
       if constexpr (L::REG_B) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = make_uint4(bw[j].x, bw[j].y, 0, 0);
-        load_b();
+        for (int j = 0; j < 4; ++j) b[j] = make_uint4(mine[j].x, mine[j].y, 0, 0);
+        load_b(next);
       } else {
         const uint32_t at = take_next();
 #pragma unroll
@@ -537,6 +533,13 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       }
       yp[i] += STEP * YB;
     }
+    col += kLoraWarps;
+  };
+  while (col < g1) {
+    group(b_even, b_odd);
+    if constexpr (L::REG_B) {
+      if (col < g1) group(b_odd, b_even);
+    }
   }
   cp_async_wait<0>();
   if (steps > 0 && CS > 1) cluster_wait();       // no block leaves while another reads its sums
@@ -561,7 +564,8 @@ cudaError_t apply(const LoraParams& p, int sms, cudaStream_t st) {
   // tokens, rank 64, K = 4096, N = 14336: 2 blocks an item 75 us, 3 blocks 54; 428 tokens, rank 128, K = 936,
   // N = 29200: 256 blocks in all 56 us, 288 blocks 50).
   int cs = kLoraMaxCluster, ns = 1;
-  while (cs > 1 && ((p.K + 31) / 32 < cs * kLoraWarps || items * cs > 2LL * sms)) --cs;
+  const int per_block = p.rank > L::ROWS ? kLoraWarps / 2 : kLoraWarps;           // warps that share K
+  while (cs > 1 && ((p.K + 31) / 32 < cs * per_block || items * cs > 2LL * sms)) --cs;
   while (items * cs * (ns + 1) <= 2LL * sms && (p.N + 31) / 32 >= (ns + 1) * cs * kLoraWarps) ++ns;
   return launch_pdl_cluster(lora_kernel<BF16, YD, RT, TILE>, dim3(static_cast<unsigned>(items * ns * cs)), dim3(kLoraWarps * 32),
                             L::smem(p.rank), st, cs, p, cs, ns);
