@@ -27,6 +27,8 @@
 #include "lora.cuh"
 #include "tl_internal.cuh"
 
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 namespace tl {
@@ -557,16 +559,26 @@ cudaError_t apply(const LoraParams& p, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     __atomic_store_n(&ready[dev], 1, __ATOMIC_RELAXED);
   }
+  // Blocks of a cluster (cs) share an item's K and clusters of an item (ns) repeat that; both share its columns.
+  // All blocks run at once, two to an SM at most, and the SM with most of them sets the time: taken is the pair with the
+  // fewest bytes into it, of those that leave every warp a piece of K and columns. A block alone takes in 1 / 0.75 of
+  // what each of two does (0.5 to 0.85 tried). Bound to powers of two, 3000 tokens, rank 64, K = 4096,
+  // N = 14336: 75 us, so 54; with the largest cs and then the largest ns, 256 tokens, rank 128, K = 5120, N = 17408:
+  // 32 us, so 25.
   const long long items = lora_max_items(p.M, p.n_adapters);
-  // A cluster as large as leaves every warp a piece of K and all blocks room on the GPU at once (what a block does besides
-  // its columns is worth less the more columns it has); as many clusters per item as that room holds, with
-  // columns for every warp. Neither is held to a power of two, for the SM with most blocks sets the time (3000
-  // tokens, rank 64, K = 4096, N = 14336: 2 blocks an item 75 us, 3 blocks 54; 428 tokens, rank 128, K = 936,
-  // N = 29200: 256 blocks in all 56 us, 288 blocks 50).
-  int cs = kLoraMaxCluster, ns = 1;
   const int per_block = p.rank > L::ROWS ? kLoraWarps / 2 : kLoraWarps;           // warps that share K
-  while (cs > 1 && ((p.K + 31) / 32 < cs * per_block || items * cs > 2LL * sms)) --cs;
-  while (items * cs * (ns + 1) <= 2LL * sms && (p.N + 31) / 32 >= (ns + 1) * cs * kLoraWarps) ++ns;
+  const int chunks = (p.K + 31) / 32, groups = (p.N + 31) / 32;
+  int cs = 1, ns = 1;
+  float best = 0.f;
+  for (int c = 1; c <= kLoraMaxCluster && (c == 1 || (chunks >= c * per_block && items * c <= 2LL * sms)); ++c) {
+    for (int full = 1; full <= 2; ++full) {
+      const int fit = static_cast<int>(full * static_cast<long long>(sms) / (items * c)), most = groups / (c * kLoraWarps);
+      const int n = std::max(1, std::min(fit, most));
+      const float a = 2.f * p.K * (p.rank + TILE), b = 2.f * p.N * (p.rank + 2 * L::V * TILE);   // x and A; B, base and y
+      const float bytes = (a + b / n) / c * (items * c * n <= sms ? 0.75f : 1.f);
+      if (c + full == 2 || bytes <= best) best = bytes, cs = c, ns = n;
+    }
+  }
   return launch_pdl_cluster(lora_kernel<BF16, YD, RT, TILE>, dim3(static_cast<unsigned>(items * ns * cs)), dim3(kLoraWarps * 32),
                             L::smem(p.rank), st, cs, p, cs, ns);
 }
