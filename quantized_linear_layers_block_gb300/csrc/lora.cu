@@ -141,6 +141,16 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t rank, uint32_t v) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster2(uint32_t addr, uint32_t rank, uint32_t a, uint32_t b) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(remote), "r"(a), "r"(b) : "memory");
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -187,6 +197,7 @@ struct Lora {
   // the K of the second product: one MMA for ranks up to 16, else pairs of them
   static constexpr int KSTEP = RT == 1 ? 16 : 32;
   __host__ __device__ static int padded(int rank) { return (rank + KSTEP - 1) / KSTEP * KSTEP; }
+  static constexpr bool SHARED = RT == 4;        // each block sums some tokens for all
   __host__ __device__ static int hs_at(int rank) { return AREA + TILE * padded(rank) * 4; }
   static int smem(int rank) {
     const int hs = hs_at(rank) + PARTS * TILE * (padded(rank) + 8) * 2;
@@ -398,14 +409,18 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   if (steps > 0) {
     if (CS > 1) cluster_wait();
     // ---- some lanes take a token: sum over the blocks, power of two, then the parts in the K order of the MMAs below.
-    // A lane has four elements of the rank; 32 / wide tokens to a warp.
+    // A lane has four elements of the rank; 32 / wide tokens to a warp. Up to rank 32 every block does this for all tokens.
+    // Above, what they read from one another would take longest (rank 128, 8 blocks: 64 KB each at 27 B/ns, 2.5 us): a
+    // block sums the tokens me, me + CS, ... and stores their parts to every block, which costs a second meeting.
+    constexpr bool SHARED = L::SHARED;
     const float sc = __ldg(p.scale + adapter);
     const uint32_t sums = smem_u32(sum);
     int wide = 4;
     while (4 * wide < RP) wide *= 2;
     const int sub = lane & (wide - 1), per_warp = 32 / wide;
-    for (int m0 = warp * per_warp; m0 < count; m0 += kLoraWarps * per_warp) {     // rows past the last token may hold anything: they reach no other row
-      const int m = m0 + lane / wide;
+    const int m_first = SHARED ? me : 0, m_step = SHARED ? CS : 1;
+    for (int j0 = warp * per_warp; m_first + j0 * m_step < count; j0 += kLoraWarps * per_warp) {     // rows past the last token may hold anything: they reach no other row
+      const int m = m_first + (j0 + lane / wide) * m_step;
       float v[4] = {};
       if (m < count && 4 * sub < p.rank) {
         float4 f[kLoraMaxCluster];
@@ -423,39 +438,57 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e2 = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-      if (sub == 0 && m < TILE) s_up[m] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+      const uint32_t back = static_cast<uint32_t>(127 + e2) << 23;
       // element 8q + j of 32 (thread q of the quad loads it): MMA j / 4, column 2q + (j & 1) + 8 ((j & 2) / 2);
       // of 16, for one MMA, element 4q + j
       const int at = RT == 1 ? 2 * sub : 32 * (sub >> 3) + 16 * (sub & 1) + 2 * (sub >> 1 & 3);
-      if (m < count && 4 * sub < RP) {
+      const bool live = m < count && 4 * sub < RP;
+      if (live && sub == 0) {
+        if (SHARED && CS > 1) {
+          for (int q = 0; q < CS; ++q) st_cluster(smem_u32(&s_up[m]), q, back);
+        } else {
+          s_up[m] = __uint_as_float(back);
+        }
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= down;
+      for (int e = 0; e < 4; ++e) v[e] *= down;
 #pragma unroll
-        for (int h = 0; h < L::PARTS; ++h) {
-          uint32_t w[2];
+      for (int h = 0; h < L::PARTS; ++h) {
+        uint32_t w[2];                           // j & 2 = 0: columns 2q, 2q + 1; j & 2 = 2: columns 8 + 2q, 9 + 2q
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float lo, hi;
-            if constexpr (BF16) {
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
-              lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xFFFF0000u);
-            } else {
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-              lo = f.x, hi = f.y;
-            }
-            // an infinity is in the first part alone
-            v[2 * e] = isinf(v[2 * e]) ? 0.f : v[2 * e] - lo;
-            v[2 * e + 1] = isinf(v[2 * e + 1]) ? 0.f : v[2 * e + 1] - hi;
+        for (int e = 0; e < 2; ++e) {
+          float lo, hi;
+          if constexpr (BF16) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+            lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xFFFF0000u);
+          } else {
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+            lo = f.x, hi = f.y;
           }
-          uint32_t* const dst = reinterpret_cast<uint32_t*>(hs + (h * TILE + m) * PITCH + at);
-          dst[0] = w[0];           // j & 2 = 0: columns 2q, 2q + 1
-          dst[4] = w[1];           // j & 2 = 2: columns 8 + 2q, 9 + 2q
+          // an infinity is in the first part alone
+          v[2 * e] = isinf(v[2 * e]) ? 0.f : v[2 * e] - lo;
+          v[2 * e + 1] = isinf(v[2 * e + 1]) ? 0.f : v[2 * e + 1] - hi;
+        }
+        uint16_t* const row = hs + (h * TILE + m) * PITCH;
+        if (SHARED && CS > 1) {
+          // with the lane of the next q: one takes the lower columns of both, the other the upper
+          const bool upper = sub & 2;
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[1], 2);
+          const uint32_t to = smem_u32(row + at + (upper ? 6 : 0));
+          if (live)
+            for (int q = 0; q < CS; ++q) st_cluster2(to, q, upper ? other : w[0], upper ? w[1] : other);
+        } else if (live) {
+          *reinterpret_cast<uint32_t*>(row + at) = w[0];
+          *reinterpret_cast<uint32_t*>(row + at + 8) = w[1];
         }
       }
     }
-    if (CS > 1) cluster_arrive();                // this block has read the others' sums
-    __syncthreads();
+    if (CS > 1) cluster_arrive();                // this block has read the others' sums, and written to them
+    if (SHARED && CS > 1)
+      cluster_wait();
+    else
+      __syncthreads();
 #pragma unroll
     for (int i = 0; i < NT; ++i) up[i] = s_up[8 * i + g];
   }
@@ -544,7 +577,7 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
     }
   }
   cp_async_wait<0>();
-  if (steps > 0 && CS > 1) cluster_wait();       // no block leaves while another reads its sums
+  if (!L::SHARED && steps > 0 && CS > 1) cluster_wait();        // no block leaves while another reads its sums
 }
 
 template <bool BF16, int YD, int RT, int TILE>
