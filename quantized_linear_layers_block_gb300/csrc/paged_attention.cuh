@@ -1072,10 +1072,12 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
   const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv;
   long long grid = static_cast<long long>(sms) * n;
   if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
-  // Short segments: a ring for each, while that is one step or two, or as long as there are segments for all rings
-  // (1216 of one key 11.2 -> 4.1 us; but 76 of up to 123 keys, of 128 channels, 7.6 -> 10.0 us).
+  // Short segments: a ring for each, while that is one step or two, or eight where the blocks would have one and a half
+  // segments each or more (1216 of one key 11.2 -> 4.1 us; bf16, 128 channels, 60 keys, 4 steps: 456 segments 7.4 -> 6.4 us,
+  // but 304 5.4 -> 6.3; 120 keys: 456 9.8 -> 9.5, 912 13.1 -> 10.0, but 304 6.4 -> 9.3; the one loss known is 256 channels in 16
+  // bits, where a block has an SM: 304 of 120 keys 10.9 -> 12.0).
   // Few and longer ones: a cluster each, while they all fit on half of the GPU at once and a block has two tiles at most.
-  if (keys <= (segments < grid * kAttnRings ? 2 : 8) * T::KT)
+  if (keys <= (2 * segments < 3 * grid ? 2 : 8) * T::KT)
     return launch_pdl(paged_attention_kernel<CACHE, D, HW, NT, kSolo>, dim3(static_cast<unsigned>(segments < grid ? segments : grid)),
                       dim3(T::THREADS), T::SMEM, st, p);
   const bool few = segments * kAttnCluster * 2 <= grid;
