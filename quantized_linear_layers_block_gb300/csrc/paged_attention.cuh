@@ -33,8 +33,8 @@
 // An 8-bit cache is widened to f16 in registers (exact); q is then scaled by a
 // power of two of its own per head so that a bf16 query fits f16's range.
 //
-// Few segments of some hundred keys take the same way with a cluster of eight blocks each, which join through their shared
-// memory; segments of few keys with a ring each: no list, no workspace, no atomics.
+// Few segments of up to some thousand keys take the same way with a cluster of two to eight blocks each, which join
+// through their shared memory; segments of few keys with a ring each: no list, no workspace, no atomics.
 //
 // Measured on GB300 (copy rate 6.79 TB/s): the loop streams at 7.4-7.7 TB/s. 160 requests of 512-16384 tokens, 8 heads of 128
 // channels, 8 bits: 222 us, 6.8 TB/s of 1.51 GB. 24 requests of 40-9000 tokens, 4 heads of 256, bf16: 37 us, 4.7 TB/s;
@@ -88,6 +88,7 @@ struct AttnParams {
   float scale_log2;
   int B, q_heads, kv_heads, group, groups_per_kv, window, q_bf16;
   int runs16;               // page_size is a multiple of 16: 16 keys from a multiple of 16 lie at equal distances
+  int cluster_log;          // kCluster: 2^cluster_log blocks share a segment, up to kAttnCluster
   int* counters;            // [kAttnLevels][kAttnMaxGrid], zero between calls
   float* partials;          // two per block
   int* status;
@@ -95,7 +96,7 @@ struct AttnParams {
 
 constexpr int kAttnRings = 4;          // rings of key tiles in a block, each with HW warps
 constexpr int kAttnMaxBlocksPerSm = 2;
-constexpr int kAttnCluster = 8;        // blocks that share a segment of a small call
+constexpr int kAttnCluster = 8;        // most blocks that share a segment of a small call
 constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join tree
 constexpr int kAttnLevels = 2;
 constexpr int kJoinFew = 4;
@@ -464,7 +465,7 @@ __device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uin
 
 enum AttnMode {
   kList,      // the list of tiles, in equal shares
-  kCluster,   // eight blocks, a cluster, take a segment, and join it through their shared memory
+  kCluster,   // a cluster of blocks takes a segment, and joins it through its shared memory
   kSolo       // each ring takes whole segments for itself, of KT keys a tile: no meetings, no joins
 };
 
@@ -490,15 +491,15 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
   int skip;                                           // places of the first segment that lie before t0
   Segment cur;
   if constexpr (CL) {
-    // ---- an eighth of a segment's tiles
-    const int seg = blockIdx.x / kAttnCluster, rank = blockIdx.x % kAttnCluster;
+    // ---- an equal part of a segment's tiles
+    const int seg = blockIdx.x >> p.cluster_log, rank = blockIdx.x & ((1 << p.cluster_log) - 1);
     cur.b = seg / HG;
     cur.h = seg - cur.b * HG;
     const int len = __ldg(p.lens + cur.b);
     if ((len < 0 || len > p.max_len) && tid == 0) set_status(p.status, TL_EDATA);
     seg_keys(p, len, TILE, cur);
-    cur.tile = static_cast<int>(static_cast<long long>(cur.tiles) * rank / kAttnCluster);
-    count = static_cast<int>(static_cast<long long>(cur.tiles) * (rank + 1) / kAttnCluster) - cur.tile;
+    cur.tile = static_cast<int>(static_cast<long long>(cur.tiles) * rank >> p.cluster_log);
+    count = static_cast<int>(static_cast<long long>(cur.tiles) * (rank + 1) >> p.cluster_log) - cur.tile;
     skip = 1;
   } else if constexpr (SOLO) {
     // ---- the block's segments, shared out to its rings; `count` of them, whole
@@ -993,18 +994,20 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       }
     }
     if constexpr (CL) {
-      // ---- the cluster's blocks join: each takes an eighth of the channels
+      // ---- the cluster's blocks join: each takes an equal part of the channels
       cluster_sync();
-      const uint32_t mine = smem_u32(smem), rank = blockIdx.x % kAttnCluster;
-      for (int x = rank * T::THREADS + tid; x < sheads * (D / 4); x += kAttnCluster * T::THREADS) {
+      const int size = 1 << p.cluster_log, rank = blockIdx.x & (size - 1);
+      const uint32_t mine = smem_u32(smem);
+      for (int x = rank * T::THREADS + tid; x < sheads * (D / 4); x += size * T::THREADS) {
         const int h = x / (D / 4), d = 4 * (x % (D / 4));
         float mr[kAttnCluster], lr[kAttnCluster], top = -INFINITY;
         float4 v[kAttnCluster];
 #pragma unroll
         for (int r = 0; r < kAttnCluster; ++r) {
-          mr[r] = ld_cluster(mine + 4 * h, r);
-          lr[r] = ld_cluster(mine + 4 * (T::HEADS + h), r);
-          v[r] = ld_cluster4(mine + 4 * (2 * T::HEADS + h * D + d), r);
+          const int from = r & (size - 1);            // past the cluster's size the same again, at no weight: no branches
+          mr[r] = ld_cluster(mine + 4 * h, from);
+          lr[r] = ld_cluster(mine + 4 * (T::HEADS + h), from);
+          v[r] = ld_cluster4(mine + 4 * (2 * T::HEADS + h * D + d), from);
           top = fmaxf(top, mr[r]);
         }
         const float base = top == -INFINITY ? 0.f : top;
@@ -1012,7 +1015,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int r = 0; r < kAttnCluster; ++r) {
-          const float f = exp2_approx(mr[r] - base);
+          const float f = r < size ? exp2_approx(mr[r] - base) : 0.f;
           sum += f * lr[r];
           a.x += f * v[r].x;
           a.y += f * v[r].y;
@@ -1076,14 +1079,24 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
   // segments each or more (1216 of one key 11.2 -> 4.1 us; bf16, 128 channels, 60 keys, 4 steps: 456 segments 7.4 -> 6.4 us,
   // but 304 5.4 -> 6.3; 120 keys: 456 9.8 -> 9.5, 912 13.1 -> 10.0, but 304 6.4 -> 9.3; the one loss known is 256 channels in 16
   // bits, where a block has an SM: 304 of 120 keys 10.9 -> 12.0).
-  // Few and longer ones: a cluster each, while they all fit on half of the GPU at once and a block has two tiles at most.
   if (keys <= (2 * segments < 3 * grid ? 2 : 8) * T::KT)
     return launch_pdl(paged_attention_kernel<CACHE, D, HW, NT, kSolo>, dim3(static_cast<unsigned>(segments < grid ? segments : grid)),
                       dim3(T::THREADS), T::SMEM, st, p);
-  const bool few = segments * kAttnCluster * 2 <= grid;
-  if (few && keys <= 2ll * kAttnCluster * T::TILE)
-    return launch_pdl_cluster(paged_attention_kernel<CACHE, D, HW, NT, kCluster>, dim3(static_cast<unsigned>(segments * kAttnCluster)),
-                              dim3(T::THREADS), T::SMEM, st, kAttnCluster, p);
+  // Few and longer ones: a cluster each, the largest of which all run at once, while a block has eight tiles at most, and
+  // half as many would have more than one.
+  // Pairs fill all places; fours and eights leave some free, and eights with an SM to a block near half of them (there 16 segments
+  // of 1000 keys, 256 channels: list 10.5 us, eights 11.5, fours 8.8). bf16, 128 channels, list against clusters: 36
+  // segments of 2000 keys 12.1, 9.0; 56 of 600 9.9, 7.5; 152 of 600 14.2, 10.2; 4 of 4000 14.5, 10.1, of 8000 16.4, 16.5;
+  // 152 of 300 to 2400 keys 21.4, 24.5.
+  for (int log = 3; log > 0; --log) {
+    const int c = 1 << log;
+    if (segments * c > (c == 2 ? grid : c == 8 && n == 1 ? grid / 2 : grid * 19 / 20) || 2 * keys <= c * T::TILE) continue;
+    if (keys > 8ll * c * T::TILE) break;
+    AttnParams shared = p;
+    shared.cluster_log = log;
+    return launch_pdl_cluster(paged_attention_kernel<CACHE, D, HW, NT, kCluster>, dim3(static_cast<unsigned>(segments * c)),
+                              dim3(T::THREADS), T::SMEM, st, c, shared);
+  }
   // most places that the list can have; a window's tiles may begin up to 15 keys before it
   const long long most = segments * ((keys + 15 + T::TILE - 1) / T::TILE + 1);
   if (grid > most) grid = most;

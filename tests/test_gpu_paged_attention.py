@@ -128,6 +128,16 @@ def test_few_short_requests(d, cache, hq, hkv):
         check(*build(d + hq + len(lens), lens, hq, hkv, d, 16, cache), lens, window=window)
 
 
+@pytest.mark.parametrize("d,cache", [(64, "bf16"), (128, "f16"), (128, "f8"), (256, "bf16"), (256, "f8")])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (16, 1), (40, 2)])
+@pytest.mark.parametrize("batch,longest", [(2, 2040), (9, 1500), (14, 1000), (30, 700), (75, 460)])
+def test_clusters_of_every_size(d, cache, hq, hkv, batch, longest):
+    """From eight blocks to a segment down to two, with requests of no token and of one among them."""
+    rng = np.random.default_rng(batch + d)
+    lens = [longest, 0, 1] + [int(n) for n in rng.integers(2, longest, batch)]
+    check(*build(batch + d + hq, lens[:batch], hq, hkv, d, 16, cache), lens[:batch])
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("cache,qtype", [("bf16", None), ("f16", None), ("f8", "bf16"), ("f8", "f16")])
 @pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 1), (24, 2), (20, 1), (40, 1)])
