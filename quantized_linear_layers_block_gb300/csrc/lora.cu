@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kLoraWarps = 8;
-constexpr int kLoraMaxCluster = 8;
+constexpr int kLoraMaxCluster = 16;
 
 // ----------------------------------------------------------------- plan
 // Shared memory: for each adapter, and for the tokens without one, a counter and its first item.
@@ -423,11 +423,13 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
       const int m = m_first + (j0 + lane / wide) * m_step;
       float v[4] = {};
       if (m < count && 4 * sub < p.rank) {
-        float4 f[kLoraMaxCluster];
+        for (int q0 = 0; q0 < (SHARED ? CS : 1); q0 += 8) {       // (eight blocks at most if not SHARED)
+          float4 f[8];
 #pragma unroll
-        for (int q = 0; q < kLoraMaxCluster; ++q) f[q] = q < CS ? ld_cluster4(sums + (m * RP + 4 * sub) * 4, q) : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int q = 0; q < 8; ++q) f[q] = q0 + q < CS ? ld_cluster4(sums + (m * RP + 4 * sub) * 4, q0 + q) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int q = 0; q < kLoraMaxCluster; ++q) v[0] += f[q].x, v[1] += f[q].y, v[2] += f[q].z, v[3] += f[q].w;
+          for (int q = 0; q < 8; ++q) v[0] += f[q].x, v[1] += f[q].y, v[2] += f[q].z, v[3] += f[q].w;
+        }
       }
       float top = 0.f;
 #pragma unroll
@@ -590,6 +592,10 @@ cudaError_t apply(const LoraParams& p, int sms, cudaStream_t st) {
   if (__atomic_load_n(&ready[dev], __ATOMIC_RELAXED) == 0) {
     e = cudaFuncSetAttribute(lora_kernel<BF16, YD, RT, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::smem(kLoraMaxRank));
     if (e != cudaSuccess) return e;
+    if (L::SHARED) {
+      e = cudaFuncSetAttribute(lora_kernel<BF16, YD, RT, TILE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+    }
     __atomic_store_n(&ready[dev], 1, __ATOMIC_RELAXED);
   }
   // Blocks of a cluster (cs) share an item's K and clusters of an item (ns) repeat that; both share its columns.
@@ -597,15 +603,18 @@ cudaError_t apply(const LoraParams& p, int sms, cudaStream_t st) {
   // fewest bytes into it, of those that leave every warp a piece of K and columns. A block alone takes in 1 / 0.75 of
   // what each of two does (0.5 to 0.85 tried). Bound to powers of two, 3000 tokens, rank 64, K = 4096,
   // N = 14336: 75 us, so 54; with the largest cs and then the largest ns, 256 tokens, rank 128, K = 5120, N = 17408:
-  // 32 us, so 25.
+  // 32 us, so 25. Sixteen blocks, above rank 32, find room on four fifths of the GPU or less (2 tokens of 2 adapters, rank 128,
+  // K = 8488, N = 33832: at most eight 18.1 us, so 13.3; ten and twelve as well: 200 tokens, rank 64, 17.0 us, so 11.4).
   const long long items = lora_max_items(p.M, p.n_adapters);
   const int per_block = p.rank > L::ROWS ? kLoraWarps / 2 : kLoraWarps;           // warps that share K
   const int chunks = (p.K + 31) / 32, groups = (p.N + 31) / 32;
   int cs = 1, ns = 1;
   float best = 0.f;
-  for (int c = 1; c <= kLoraMaxCluster && (c == 1 || (chunks >= c * per_block && items * c <= 2LL * sms)); ++c) {
+  for (int c = 1; c <= (L::SHARED ? kLoraMaxCluster : 8); c = c < 8 ? c + 1 : 2 * c) {
+    const int room = c > 8 ? sms * 4 / 5 : sms;
+    if (c > 1 && (chunks < c * per_block || items * c > 2LL * room)) break;
     for (int full = 1; full <= 2; ++full) {
-      const int fit = static_cast<int>(full * static_cast<long long>(sms) / (items * c)), most = groups / (c * kLoraWarps);
+      const int fit = static_cast<int>(full * static_cast<long long>(room) / (items * c)), most = groups / (c * kLoraWarps);
       const int n = std::max(1, std::min(fit, most));
       const float a = 2.f * p.K * (p.rank + TILE), b = 2.f * p.N * (p.rank + 2 * L::V * TILE);   // x and A; B, base and y
       const float bytes = (a + b / n) / c * (items * c * n <= sms ? 0.75f : 1.f);

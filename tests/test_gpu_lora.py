@@ -85,6 +85,13 @@ def test_clusters_of_every_size(M):
     check(*make(100 + M, M, 2056, 1000, 24, M, ids=np.arange(M)))
 
 
+@pytest.mark.parametrize("rank", [40, 64, 96, 128])
+@pytest.mark.parametrize("M,n", [(1, 1), (5, 5), (20, 1), (60, 4)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16")])
+def test_few_items_of_large_adapters(rank, M, n, dtype, out):
+    check(*make(400 + M + rank, M, 6152, 2056, rank, n, dtype, out, ids=np.arange(M) % n), dtype, out)
+
+
 @pytest.mark.parametrize("M", [1023, 1024, 1100])
 @pytest.mark.parametrize("rank", [8, 32, 128])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
