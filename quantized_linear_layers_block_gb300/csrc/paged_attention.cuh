@@ -33,8 +33,8 @@
 // An 8-bit cache is widened to f16 in registers (exact); q is then scaled by a
 // power of two of its own per head so that a bf16 query fits f16's range.
 //
-// Few segments of up to some thousand keys take the same way with a cluster of two to eight blocks each, which join
-// through their shared memory; segments of few keys with a ring each: no list, no workspace, no atomics.
+// Few segments of up to some thousand keys take the same way with one to eight blocks each, a cluster, which join
+// through their shared memory; many segments of few keys with a ring each: no list, no workspace, no atomics.
 //
 // Measured on GB300 (copy rate 6.79 TB/s): the loop streams at 7.4-7.7 TB/s. 160 requests of 512-16384 tokens, 8 heads of 128
 // channels, 8 bits: 222 us, 6.8 TB/s of 1.51 GB. 24 requests of 40-9000 tokens, 4 heads of 256, bf16: 37 us, 4.7 TB/s;
@@ -942,7 +942,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       __syncwarp();
       continue;
     }
-    const bool whole = !CL && !starts_before && seg.tile + here == seg.tiles, second = !starts_before;
+    const bool whole = CL ? p.cluster_log == 0 : !starts_before && seg.tile + here == seg.tiles, second = !starts_before;
     const long long first = t0 + (done - here) - seg.tile;      // the place of its first tile
     if constexpr (CL) {
       pdl_launch_dependents();
@@ -994,6 +994,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       }
     }
     if constexpr (CL) {
+      if (whole) return;
       // ---- the cluster's blocks join: each takes an equal part of the channels
       cluster_sync();
       const int size = 1 << p.cluster_log, rank = blockIdx.x & (size - 1);
@@ -1075,28 +1076,29 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
   const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv;
   long long grid = static_cast<long long>(sms) * n;
   if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
-  // Short segments: a ring for each, while that is one step or two, or eight where the blocks would have one and a half
-  // segments each or more (1216 of one key 11.2 -> 4.1 us; bf16, 128 channels, 60 keys, 4 steps: 456 segments 7.4 -> 6.4 us,
-  // but 304 5.4 -> 6.3; 120 keys: 456 9.8 -> 9.5, 912 13.1 -> 10.0, but 304 6.4 -> 9.3; the one loss known is 256 channels in 16
-  // bits, where a block has an SM: 304 of 120 keys 10.9 -> 12.0).
-  if (keys <= (2 * segments < 3 * grid ? 2 : 8) * T::KT)
-    return launch_pdl(paged_attention_kernel<CACHE, D, HW, NT, kSolo>, dim3(static_cast<unsigned>(segments < grid ? segments : grid)),
-                      dim3(T::THREADS), T::SMEM, st, p);
-  // Few and longer ones: a cluster each, the largest of which all run at once, while a block has eight tiles at most, and
-  // half as many would have more than one.
-  // Pairs fill all places; fours and eights leave some free, and eights with an SM to a block near half of them (there 16 segments
-  // of 1000 keys, 256 channels: list 10.5 us, eights 11.5, fours 8.8). bf16, 128 channels, list against clusters: 36
-  // segments of 2000 keys 12.1, 9.0; 56 of 600 9.9, 7.5; 152 of 600 14.2, 10.2; 4 of 4000 14.5, 10.1, of 8000 16.4, 16.5;
-  // 152 of 300 to 2400 keys 21.4, 24.5.
-  for (int log = 3; log > 0; --log) {
+  // Few segments: a cluster each, of 8, 4, 2 or 1 blocks, the most of which all run at once, while a block has eight tiles
+  // at most and a smaller cluster would not have next to none. One or two blocks fill all places; fours and eights leave some
+  // free, and eights with an SM to a block near half of them (there 16 segments of 1000 keys, 256 channels: list 10.5 us, eights 11.5,
+  // fours 8.8). bf16, 128 channels, list against clusters: 4 segments of 4000 keys 14.5, 10.1, of 8000 16.4, 16.5; 36 of 2000
+  // 12.1, 9.0; 56 of 600 9.9, 7.5; 152 of 600 14.2, 10.2; 300 of 200 8.6, 6.9, of 50 to 400 12.8, 8.7, of 100 to 800 16.8,
+  // 15.3, of 187 to 1500 24.7, 27.4. Pairs against single blocks: 152 of 200 6.7, 5.9, of 400 8.3, 9.0.
+  for (int log = 3; log >= 0; --log) {
     const int c = 1 << log;
-    if (segments * c > (c == 2 ? grid : c == 8 && n == 1 ? grid / 2 : grid * 19 / 20) || 2 * keys <= c * T::TILE) continue;
-    if (keys > 8ll * c * T::TILE) break;
+    const long long tiles = (keys + T::TILE - 1) / T::TILE;
+    if (segments * c > (c <= 2 ? grid : c == 8 && n == 1 ? grid / 2 : grid * 19 / 20)) continue;
+    if (tiles <= (c == 8 || c == 2 ? 4 : c == 4 ? 2 : 0)) continue;
+    if (tiles > 8 * c) break;
     AttnParams shared = p;
     shared.cluster_log = log;
     return launch_pdl_cluster(paged_attention_kernel<CACHE, D, HW, NT, kCluster>, dim3(static_cast<unsigned>(segments * c)),
                               dim3(T::THREADS), T::SMEM, st, c, shared);
   }
+  // Many short ones: a ring for each, while that is one step or two, or eight where the blocks would have one and a half
+  // segments each or more (bf16, 128 channels, 456 segments of 60 keys, 4 steps: 7.4 -> 6.4 us, of 120 9.8 -> 9.5; 912 of 120 13.1 ->
+  // 10.0; the one loss known is 256 channels in 16 bits, where a block has an SM: 304 of 120 keys 10.9 -> 12.0).
+  if (keys <= (2 * segments < 3 * grid ? 2 : 8) * T::KT)
+    return launch_pdl(paged_attention_kernel<CACHE, D, HW, NT, kSolo>, dim3(static_cast<unsigned>(segments < grid ? segments : grid)),
+                      dim3(T::THREADS), T::SMEM, st, p);
   // most places that the list can have; a window's tiles may begin up to 15 keys before it
   const long long most = segments * ((keys + 15 + T::TILE - 1) / T::TILE + 1);
   if (grid > most) grid = most;

@@ -130,9 +130,9 @@ def test_few_short_requests(d, cache, hq, hkv):
 
 @pytest.mark.parametrize("d,cache", [(64, "bf16"), (128, "f16"), (128, "f8"), (256, "bf16"), (256, "f8")])
 @pytest.mark.parametrize("hq,hkv", [(4, 1), (16, 1), (40, 2)])
-@pytest.mark.parametrize("batch,longest", [(2, 2040), (9, 1500), (14, 1000), (30, 700), (75, 460)])
+@pytest.mark.parametrize("batch,longest", [(2, 2040), (9, 1500), (14, 1000), (30, 700), (75, 460), (150, 250), (150, 30)])
 def test_clusters_of_every_size(d, cache, hq, hkv, batch, longest):
-    """From eight blocks to a segment down to two, with requests of no token and of one among them."""
+    """From eight blocks to a segment down to one, with requests of no token and of one among them."""
     rng = np.random.default_rng(batch + d)
     lens = [longest, 0, 1] + [int(n) for n in rng.integers(2, longest, batch)]
     check(*build(batch + d + hq, lens[:batch], hq, hkv, d, 16, cache), lens[:batch])
