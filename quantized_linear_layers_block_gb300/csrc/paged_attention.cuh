@@ -33,14 +33,14 @@
 // An 8-bit cache is widened to f16 in registers (exact); q is then scaled by a
 // power of two of its own per head so that a bf16 query fits f16's range.
 //
-// Few segments of up to some thousand keys take the same way with one to eight blocks each, a cluster, which join
+// Few segments of up to some thousand keys take the same way with one to sixteen blocks each, a cluster, which join
 // through their shared memory; many segments of few keys with a ring each: no list, no workspace, no atomics.
 //
 // Measured on GB300 (copy rate 6.79 TB/s): the loop streams at 7.4-7.7 TB/s. 160 requests of 512-16384 tokens, 8 heads of 128
 // channels, 8 bits: 222 us, 6.8 TB/s of 1.51 GB. 24 requests of 40-9000 tokens, 4 heads of 256, bf16: 37 us, 4.7 TB/s;
 // 23 us of it stream, 3.4 us pass before the first loads are out (lengths, place in the list, page
 // table) and 8 us in meetings and joins. One request of 80001: 61 us, 5.3 TB/s. 577 tokens of
-// one request: 6.3 us. The 16-bit loop takes 1.3 us for a tile of 64 KB per SM whatever is left out of its
+// one request: 5.6 us. The 16-bit loop takes 1.3 us for a tile of 64 KB per SM whatever is left out of its
 // arithmetic; above 16 query heads to a key-value head it is the arithmetic that bounds (32 heads of 128
 // channels: 103 us where the bytes take 50).
 #pragma once
@@ -88,7 +88,7 @@ struct AttnParams {
   float scale_log2;
   int B, q_heads, kv_heads, group, groups_per_kv, window, q_bf16;
   int runs16;               // page_size is a multiple of 16: 16 keys from a multiple of 16 lie at equal distances
-  int cluster_log;          // kCluster: 2^cluster_log blocks share a segment, up to kAttnCluster
+  int cluster_log;          // kCluster: 2^cluster_log blocks share a segment
   int* counters;            // [kAttnLevels][kAttnMaxGrid], zero between calls
   float* partials;          // two per block
   int* status;
@@ -96,7 +96,7 @@ struct AttnParams {
 
 constexpr int kAttnRings = 4;          // rings of key tiles in a block, each with HW warps
 constexpr int kAttnMaxBlocksPerSm = 2;
-constexpr int kAttnCluster = 8;        // most blocks that share a segment of a small call
+constexpr int kAttnClusterLog = 4;     // of the most blocks that share a segment of a small call
 constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join tree
 constexpr int kAttnLevels = 2;
 constexpr int kJoinFew = 4;
@@ -1001,27 +1001,31 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       const uint32_t mine = smem_u32(smem);
       for (int x = rank * T::THREADS + tid; x < sheads * (D / 4); x += size * T::THREADS) {
         const int h = x / (D / 4), d = 4 * (x % (D / 4));
-        float mr[kAttnCluster], lr[kAttnCluster], top = -INFINITY;
-        float4 v[kAttnCluster];
-#pragma unroll
-        for (int r = 0; r < kAttnCluster; ++r) {
-          const int from = r & (size - 1);            // past the cluster's size the same again, at no weight: no branches
-          mr[r] = ld_cluster(mine + 4 * h, from);
-          lr[r] = ld_cluster(mine + 4 * (T::HEADS + h), from);
-          v[r] = ld_cluster4(mine + 4 * (2 * T::HEADS + h * D + d), from);
-          top = fmaxf(top, mr[r]);
-        }
-        const float base = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
+        float top = -INFINITY, sum = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r0 = 0; r0 < size; r0 += 8) {
+          float mr[8], lr[8], most = top;
+          float4 v[8];
 #pragma unroll
-        for (int r = 0; r < kAttnCluster; ++r) {
-          const float f = r < size ? exp2_approx(mr[r] - base) : 0.f;
-          sum += f * lr[r];
-          a.x += f * v[r].x;
-          a.y += f * v[r].y;
-          a.z += f * v[r].z;
-          a.w += f * v[r].w;
+          for (int r = 0; r < 8; ++r) {
+            const int from = (r0 + r) & (size - 1);     // past the cluster's size the same again, at no weight: no branches
+            mr[r] = ld_cluster(mine + 4 * h, from);
+            lr[r] = ld_cluster(mine + 4 * (T::HEADS + h), from);
+            v[r] = ld_cluster4(mine + 4 * (2 * T::HEADS + h * D + d), from);
+            most = fmaxf(most, mr[r]);
+          }
+          const float base = most == -INFINITY ? 0.f : most, f0 = exp2_approx(top - base);
+          top = most;
+          sum *= f0, a.x *= f0, a.y *= f0, a.z *= f0, a.w *= f0;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float f = r < size ? exp2_approx(mr[r] - base) : 0.f;
+            sum += f * lr[r];
+            a.x += f * v[r].x;
+            a.y += f * v[r].y;
+            a.z += f * v[r].z;
+            a.w += f * v[r].w;
+          }
         }
         write_out<T>(p, seg.b, sh0 + h, d, D, a, top, sum, vs);
       }
@@ -1056,37 +1060,54 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
 template <int CACHE, int D, int HW, int NT>
 cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
   using T = Traits<CACHE, D, HW, NT>;
-  static int per_sm[64];                             // blocks per SM, by device
+  // by device: blocks per SM, and how many clusters of 2^i blocks run at once
+  static int per_sm[64], at_once[64][kAttnClusterLog + 1];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  int n = __atomic_load_n(&per_sm[dev], __ATOMIC_RELAXED);
+  int n = __atomic_load_n(&per_sm[dev], __ATOMIC_ACQUIRE);
   if (n == 0) {
     for (auto* kernel : {paged_attention_kernel<CACHE, D, HW, NT, kList>, paged_attention_kernel<CACHE, D, HW, NT, kCluster>,
                          paged_attention_kernel<CACHE, D, HW, NT, kSolo>}) {
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
       if (e != cudaSuccess) return e;
     }
+    auto* const kernel = paged_attention_kernel<CACHE, D, HW, NT, kCluster>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attention_kernel<CACHE, D, HW, NT, kList>, T::THREADS, T::SMEM);
     if (e != cudaSuccess) return e;
     n = n < 1 ? 1 : n > kAttnMaxBlocksPerSm ? kAttnMaxBlocksPerSm : n;
-    __atomic_store_n(&per_sm[dev], n, __ATOMIC_RELAXED);
+    __atomic_store_n(&at_once[dev][0], sms * n, __ATOMIC_RELAXED);
+    for (int log = 1; log <= kAttnClusterLog; ++log) {
+      cudaLaunchAttribute size;
+      size.id = cudaLaunchAttributeClusterDimension;
+      size.val.clusterDim.x = 1 << log, size.val.clusterDim.y = size.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1 << log), cfg.blockDim = dim3(T::THREADS), cfg.dynamicSmemBytes = T::SMEM;
+      cfg.attrs = &size, cfg.numAttrs = 1;
+      int clusters = 0;
+      e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      __atomic_store_n(&at_once[dev][log], clusters, __ATOMIC_RELAXED);
+    }
+    __atomic_store_n(&per_sm[dev], n, __ATOMIC_RELEASE);
   }
   const long long keys = p.window > 0 && p.window < p.max_len ? p.window : p.max_len;
   const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.groups_per_kv;
   long long grid = static_cast<long long>(sms) * n;
   if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
-  // Few segments: a cluster each, of 8, 4, 2 or 1 blocks, the most of which all run at once, while a block has eight tiles
-  // at most and a smaller cluster would not have next to none. One or two blocks fill all places; fours and eights leave some
-  // free, and eights with an SM to a block near half of them (there 16 segments of 1000 keys, 256 channels: list 10.5 us, eights 11.5,
-  // fours 8.8). bf16, 128 channels, list against clusters: 4 segments of 4000 keys 14.5, 10.1, of 8000 16.4, 16.5; 36 of 2000
-  // 12.1, 9.0; 56 of 600 9.9, 7.5; 152 of 600 14.2, 10.2; 300 of 200 8.6, 6.9, of 50 to 400 12.8, 8.7, of 100 to 800 16.8,
-  // 15.3, of 187 to 1500 24.7, 27.4. Pairs against single blocks: 152 of 200 6.7, 5.9, of 400 8.3, 9.0.
-  for (int log = 3; log >= 0; --log) {
+  // Few segments: a cluster each, of 16 to 1 blocks, the most of which all run at once (sixteens on SMs of their own), while a
+  // block has eight tiles at most and a smaller cluster would not have next to none. bf16, 128 channels, list against clusters:
+  // 4 segments of 4000 keys 14.5, 10.1 (7.5 with sixteens), 5 of 8000 14.5, 11.1; 36 of 2000 12.1, 9.0; 56 of 600 9.9, 7.5; 152 of
+  // 600 14.2, 10.2; 300 of 200 8.6, 6.9, of 50 to 400 12.8, 8.7, of 100 to 800 16.8, 15.3, of 187 to 1500 24.7, 27.4. Pairs
+  // against single blocks: 152 of 200 6.7, 5.9, of 400 8.3, 9.0. Clusters that do not all run at once lose (256
+  // channels, 16 eights: list 10.5, eights 11.5).
+  const long long tiles = (keys + T::TILE - 1) / T::TILE;
+  for (int log = kAttnClusterLog; log >= 0; --log) {
     const int c = 1 << log;
-    const long long tiles = (keys + T::TILE - 1) / T::TILE;
-    if (segments * c > (c <= 2 ? grid : c == 8 && n == 1 ? grid / 2 : grid * 19 / 20)) continue;
-    if (tiles <= (c == 8 || c == 2 ? 4 : c == 4 ? 2 : 0)) continue;
+    if (segments > __atomic_load_n(&at_once[dev][log], __ATOMIC_RELAXED) / (c == 16 ? n : 1)) continue;
+    if (tiles <= (c == 16 ? 8 : c == 8 || c == 2 ? 4 : c == 4 ? 2 : 0)) continue;
     if (tiles > 8 * c) break;
     AttnParams shared = p;
     shared.cluster_log = log;
