@@ -45,6 +45,7 @@
 // channels: 103 us where the bytes take 50).
 #pragma once
 
+#include "attention_join.h"
 #include "tl_internal.cuh"
 
 #include <cuda_bf16.h>
@@ -89,7 +90,7 @@ struct AttnParams {
   int B, q_heads, kv_heads, group, groups_per_kv, window, q_bf16;
   int runs16;               // page_size is a multiple of 16: 16 keys from a multiple of 16 lie at equal distances
   int cluster_log;          // kCluster: 2^cluster_log blocks share a segment
-  int* counters;            // [kAttnLevels][kAttnMaxGrid], zero between calls
+  int* counters;            // [kAttnLevels][kAttnMaxGrid] (attention_join.h), zero between calls
   float* partials;          // two per block
   int* status;
 };
@@ -97,10 +98,7 @@ struct AttnParams {
 constexpr int kAttnRings = 4;          // rings of key tiles in a block, each with HW warps
 constexpr int kAttnMaxBlocksPerSm = 2;
 constexpr int kAttnClusterLog = 4;     // of the most blocks that share a segment of a small call
-constexpr int kAttnMaxGrid = 4096;     // the workspace begins with a counter for each block and level of a join tree
-constexpr int kAttnLevels = 2;
 constexpr int kJoinFew = 4;
-constexpr int kJoinBytes = 320 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -286,19 +284,15 @@ __device__ __forceinline__ void write_out(const AttnParams& p, int b, int h, int
 }
 
 // Called by one thread, after a barrier behind which all of the block's writes lie: counts this block in and
-// says whether it is the last of n. The counter is zero again then, and what the others wrote is visible.
-__device__ __forceinline__ int count_in(int* counter, int n) {
+// says whether it is the last of its group. The counter is zero again then, and what the others wrote is visible.
+__device__ __forceinline__ int count_in(const AttnParams& p, const JoinGroup& g) {
+  if (g.counter < 0) return 1;
+  int* const counter = p.counters + g.counter;
   int before;
   asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
-  if (before != n - 1) return 0;
+  if (before != g.size - 1) return 0;
   *counter = 0;
   return 1;
-}
-
-// The group of partials that this block's belongs to when every `step`-th one is left (fan^2 >= n): its first, and how many.
-__device__ __forceinline__ int2 join_group(const Shared& s, int step) {
-  const int first = (static_cast<int>(blockIdx.x) - s.c0) / (step * s.fan) * (step * s.fan);
-  return make_int2(first, min(s.fan, (s.n - first + step - 1) / step));
 }
 
 // Joins the n partials of blocks first, first + step, ... counted from the segment's first: with LAST, into the
@@ -449,15 +443,12 @@ __device__ __forceinline__ void finish(const AttnParams& p, const Shared& s, uin
     return;
   }
   for (int step = 1, level = 0;; ++level) {
-    const int2 g = join_group(s, step);
-    const bool last = g.x == 0 && step * s.fan >= s.n;
-    join<T, D>(p, s, g.x, step, g.y, last, ring, meet, bar, phase);
+    const JoinGroup g = join_group(static_cast<int>(blockIdx.x), s.c0, s.n, s.fan, step, level);
+    const bool last = g.first == 0 && step * s.fan >= s.n;
+    join<T, D>(p, s, g.first, step, g.size, last, ring, meet, bar, phase);
     if (last) return;
     step *= s.fan;
-    if (threadIdx.x == 0) {
-      const int2 up = join_group(s, step);
-      *flag = count_in(p.counters + (level + 1) * kAttnMaxGrid + s.c0 + up.x, up.y);
-    }
+    if (threadIdx.x == 0) *flag = count_in(p, join_group(static_cast<int>(blockIdx.x), s.c0, s.n, s.fan, step, level + 1));
     __syncthreads();
     if (*flag == 0) return;
   }
@@ -1038,12 +1029,9 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
       // joins them is looked up when the block has nothing else to do.
       const int c0 = static_cast<int>(divide(first, share));
       const int n = static_cast<int>(divide(first + seg.tiles - 1, share)) - c0 + 1;
-      // One join of all up to kJoinBytes, which cost about what a second level of the tree does (3 us); else two levels.
-      const int fan = static_cast<long long>(n) * sheads * D * 4 <= kJoinBytes ? n : static_cast<int>(ceilf(sqrtf(static_cast<float>(n))));
-      const Shared s{c0, n, fan, seg.b, sh0, sheads, vs};
-      s_pend[second] = s;
-      const int2 group = join_group(s, 1);
-      s_last[second] = count_in(p.counters + c0 + group.x, group.y);
+      const int fan = join_fan(n, sheads * D * 4);
+      s_pend[second] = Shared{c0, n, fan, seg.b, sh0, sheads, vs};
+      s_last[second] = count_in(p, join_group(static_cast<int>(blockIdx.x), c0, n, fan, 1, 0));
     }
   }
   if constexpr (SOLO) return;
