@@ -226,15 +226,23 @@ __global__ void __launch_bounds__(kLoraWarps * 32, 2) lora_kernel(const __grid_c
   pdl_wait_prior();
   const LoraPlanHeader head = *p.plan;
   const LoraItem* const item = p.items + idx;
-  const int adapter = item->adapter, count = item->count;
-  int tok[NT];
+  int adapter, count, tok[NT];
+  auto read_item = [&]() {
+    adapter = item->adapter;
+    count = item->count;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) tok[n] = item->token[8 * n + g];
+    for (int n = 0; n < NT; ++n) tok[n] = item->token[8 * n + g];
+  };
+  // Every plan has a first item, which is read beside the header; another one's place may lie past the end of a plan of
+  // fewer tokens or adapters, so the header is asked first.
+  if (idx == 0) read_item();
   if (head.M != p.M || head.n_adapters != p.n_adapters) {
     if (tid == 0) set_status(p.status, TL_EDATA);
     return;
   }
-  if (idx >= head.items || (adapter < 0 && !p.copy_bare)) return;         // whole clusters leave
+  if (idx >= head.items) return;                                          // whole clusters leave
+  if (idx > 0) read_item();
+  if (adapter < 0 && !p.copy_bare) return;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
     if (8 * n + g >= count) tok[n] = -1;
