@@ -28,7 +28,8 @@
 // half the MMAs that 16 padded rows would, and S^T and O^T = V^T P^T have their heads on the same
 // lanes, which keeps the rescaling in registers. P^T becomes an operand by an 8x8 transpose (movmatrix).
 // Probabilities are split in two 16-bit numbers, high and low part, so that they count with 16 (bf16)
-// or 22 (f16) bits instead of 8 or 11; the MMAs for it are not what bounds the kernel.
+// or 22 (f16) bits instead of 8 or 11; the MMAs for it are not what bounds the kernel. Both parts are positive, and never zero,
+// so that an infinite value makes its channel infinite: a low part of either sign, or a zero, would make it NaN.
 //
 // An 8-bit cache is widened to f16 in registers (exact); q is then scaled by a
 // power of two of its own per head so that a bf16 query fits f16's range.
@@ -47,6 +48,8 @@
 
 #include "attention_join.h"
 #include "tl_internal.cuh"
+
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -163,6 +166,25 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Towards zero, and then at least the least positive number (f16) or normal number (bf16): the parts of a probability.
+template <bool BF16>
+__device__ __forceinline__ uint32_t above_zero(uint32_t v) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x00800080));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x00010001));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2_down(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return above_zero<BF16>(r);
+}
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
   if constexpr (BF16)
@@ -204,6 +226,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// 2^x, by which sums of earlier keys or of another share are scaled down; no infinity among them may meet a zero.
+__device__ __forceinline__ float faded(float x) { return fmaxf(exp2_approx(x), 0x1p-126f); }
+
 // HW warps to a ring, 8 NT query heads to a warp
 template <int CACHE, int D, int HW, int NT>
 struct Traits {
@@ -231,8 +256,9 @@ struct Traits {
   // partials that the rings hold, at most a warp's lanes
   static constexpr int HOLD = kAttnRings * STAGES * BUF / (HEADS * (D + 2) * 4), FIT = HOLD < 32 ? HOLD : 32;
   static constexpr int BLOCKS = HW * NT == 4 || SMEM > 115500 ? 1 : kAttnMaxBlocksPerSm;     // per SM
-  // 2^8 in the probabilities keeps an f16 low part of the small ones out of the subnormals
-  static constexpr float POFF = BF16 ? 0.f : 8.f;
+  // 2^15 in the probabilities keeps an f16 low part of the small ones out of the subnormals, and makes the least f16 number,
+  // which every key with a value at least counts with, 2^-39 of the largest probability
+  static constexpr float POFF = BF16 ? 0.f : 15.f;
 };
 
 // byte offset of 16-byte chunk c of row r, swizzled so that 8 rows' equal chunks lie in different banks
@@ -340,7 +366,7 @@ __device__ __forceinline__ void join(const AttnParams& p, const Shared& s, int f
       float top = fmaxf(m, m0);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float base = top == -INFINITY ? 0.f : top, w = exp2_approx(m - base), w0 = exp2_approx(m0 - base);
+      const float base = top == -INFINITY ? 0.f : top, w = faded(m - base), w0 = faded(m0 - base);
       float sum = w * l;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -423,7 +449,7 @@ __device__ __forceinline__ void join_few(const AttnParams& p, const Shared& s) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kJoinFew; ++i) {
-      const float f = exp2_approx(m[i] - base);
+      const float f = faded(m[i] - base);
       sum += f * l[i];
       a.x += f * v[i].x;
       a.y += f * v[i].y;
@@ -805,7 +831,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
             moved |= top != m[n][e];
             // no key seen so far scored above -inf: any finite base will do
             const float base = top == -INFINITY ? 0.f : top;
-            al[n][e] = exp2_approx(m[n][e] - base);
+            al[n][e] = faded(m[n][e] - base);
             m[n][e] = top;
             float sum = 0.f;
 #pragma unroll
@@ -837,10 +863,12 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float x = s[j][n][2 * e], y = s[j][n][2 * e + 1];
-              const uint32_t hi = pack2<T::BF16>(x, y);
+              // e4m3 has no infinities: there the high part is the nearest, its low part has either sign
+              const uint32_t hi = T::F8 ? pack2<T::BF16>(x, y) : pack2_down<T::BF16>(x, y);
               const float2 back = unpack2<T::BF16>(hi);
+              const uint32_t lo = pack2<T::BF16>(x - back.x, y - back.y);
               ph[n][e] = transpose8x8(hi);
-              pl[n][e] = transpose8x8(pack2<T::BF16>(x - back.x, y - back.y));
+              pl[n][e] = transpose8x8(T::F8 ? lo : above_zero<T::BF16>(lo));
             }
           }
           if constexpr (T::F8) {
@@ -966,7 +994,7 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
       for (int r = 0; r < kAttnRings; ++r) {
         const float* q = meet + r * (T::MEET / 4) + T::HEADS;
-        const float f = exp2_approx(mw[r] - base);
+        const float f = faded(mw[r] - base);
         const float4 v = *reinterpret_cast<const float4*>(q + T::HEADS + h * T::OPITCH + d);
         sum += f * q[h];
         a.x += f * v.x;
@@ -994,30 +1022,37 @@ paged_attention_kernel(const __grid_constant__ AttnParams p) {
         const int h = x / (D / 4), d = 4 * (x % (D / 4));
         float top = -INFINITY, sum = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int r0 = 0; r0 < size; r0 += 8) {
-          float mr[8], lr[8], most = top;
-          float4 v[8];
+        // N blocks' results with one latency
+        auto take = [&](auto count, int r0) {
+          constexpr int N = decltype(count)::value;
+          float mr[N], lr[N], most = top;
+          float4 v[N];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const int from = (r0 + r) & (size - 1);     // past the cluster's size the same again, at no weight: no branches
-            mr[r] = ld_cluster(mine + 4 * h, from);
-            lr[r] = ld_cluster(mine + 4 * (T::HEADS + h), from);
-            v[r] = ld_cluster4(mine + 4 * (2 * T::HEADS + h * D + d), from);
+          for (int r = 0; r < N; ++r) {
+            mr[r] = ld_cluster(mine + 4 * h, r0 + r);
+            lr[r] = ld_cluster(mine + 4 * (T::HEADS + h), r0 + r);
+            v[r] = ld_cluster4(mine + 4 * (2 * T::HEADS + h * D + d), r0 + r);
             most = fmaxf(most, mr[r]);
           }
-          const float base = most == -INFINITY ? 0.f : most, f0 = exp2_approx(top - base);
+          const float base = most == -INFINITY ? 0.f : most, f0 = faded(top - base);
           top = most;
           sum *= f0, a.x *= f0, a.y *= f0, a.z *= f0, a.w *= f0;
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const float f = r < size ? exp2_approx(mr[r] - base) : 0.f;
+          for (int r = 0; r < N; ++r) {
+            const float f = faded(mr[r] - base);
             sum += f * lr[r];
             a.x += f * v[r].x;
             a.y += f * v[r].y;
             a.z += f * v[r].z;
             a.w += f * v[r].w;
           }
-        }
+        };
+        if (size >= 8)
+          for (int r0 = 0; r0 < size; r0 += 8) take(std::integral_constant<int, 8>{}, r0);
+        else if (size == 4)
+          take(std::integral_constant<int, 4>{}, 0);
+        else
+          take(std::integral_constant<int, 2>{}, 0);
         write_out<T>(p, seg.b, sh0 + h, d, D, a, top, sum, vs);
       }
       cluster_sync();                                 // no block leaves while another reads its result
