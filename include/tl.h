@@ -451,10 +451,11 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
  *   base    [M, N] of y_dtype (TL_BF16, TL_F16 or TL_F32), ldb elements from token to token
  *   y       [M, N] likewise; may be base (in place, ldy = ldb), must not overlap it otherwise
  * The products are exact and summed in fp32; A[a] x[m] is kept in fp32 and enters the second product
- * as the sum of two or three 16-bit numbers, so that it counts with 16 (bf16), 22
- * (fp16) or, for an fp32 y, 24 bits; base + delta is rounded once to y_dtype. For given
+ * as the sum of two 16-bit numbers, or three for bf16 operands and an fp32 y. So it counts with 22 bits for fp16
+ * operands, 16 for bf16 ones, and 24 for those with an fp32 y: bits of the largest of a token's rank elements for fp16,
+ * of each for bf16. base + delta is rounded once to y_dtype. For given
  * M and n_adapters, a token's result does not depend on the other tokens of the batch.
- * rank is a multiple of 8 up to 128; K, N (at most 2^22) and the lds multiples of 8;
+ * rank is a multiple of 8 up to 128; K, N and the lds multiples of 8, N at most 2^22;
  * anything else returns TL_EUNSUPPORTED.
  */
 int tl_lora_plan_size(int M, int n_adapters, size_t* bytes);
