@@ -2,9 +2,10 @@
 //
 // For the operators of a decode step, whose kernels take 2 to 6 us: the same
 // checks in Python and a ctypes call took 7 to 10 us per call, this takes 3 to 4. The module
-// calls nothing of PyTorch but the tensors' accessors and the current stream; all arithmetic is the library's.
+// calls nothing of PyTorch but the tensors' accessors, the current stream and the current device; all arithmetic is the library's.
 #include <Python.h>
 
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -16,6 +17,11 @@
 namespace {
 
 struct Refused {};      // a Python exception is set
+
+// What PagedKVCache hands over the address of: its description, and the number of the GPU that it lies on.
+struct Cache : tl_kv_cache {
+  int device;
+};
 
 [[noreturn]] void refuse(const char* format, ...) {
   va_list args;
@@ -33,6 +39,19 @@ const at::Tensor* tensor(PyObject* o, const char* name, bool optional = false) {
   if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
   return &t;
 }
+
+// All of a call's tensors lie on one GPU, which is where it is launched.
+void on_device(const at::Tensor* t, int device, const char* name) {
+  if (t != nullptr && t->device().index() != device) refuse("%s is on GPU %d, not on GPU %d", name, static_cast<int>(t->device().index()), device);
+}
+
+// Makes it the current device meanwhile, where it is not.
+struct OnDevice {
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit OnDevice(int device) {
+    if (c10::cuda::current_device() != device) guard.set_index(static_cast<c10::DeviceIndex>(device));
+  }
+};
 
 const char* type_name(at::ScalarType t) { return c10::toString(t); }
 
@@ -106,9 +125,13 @@ PyObject* call(const char* name, Py_ssize_t got, Py_ssize_t want, F&& f) {
 // kv_append(cache, k, v, positions, slots, cos_sin, interleaved, q, q_out, stream) -> tl_status
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call("kv_append", n, 10, [&] {
-    const auto* c = reinterpret_cast<const tl_kv_cache*>(static_cast<intptr_t>(integer(a[0])));
+    const auto* c = reinterpret_cast<const Cache*>(static_cast<intptr_t>(integer(a[0])));
     const at::Tensor &k = *tensor(a[1], "k"), &v = *tensor(a[2], "v"), &slots = *tensor(a[4], "slots");
     const at::Tensor *cos_sin = tensor(a[5], "cos_sin", true), *q = tensor(a[7], "q", true);
+    on_device(&k, c->device, "k"), on_device(&v, c->device, "v"), on_device(&slots, c->device, "slots");
+    on_device(cos_sin, c->device, "cos_sin"), on_device(q, c->device, "q");
+    const at::Tensor* const at = cos_sin != nullptr ? tensor(a[3], "positions") : nullptr;
+    on_device(at, c->device, "positions");
     const int code = half_code(k, "k");
     const auto type = k.scalar_type();
     const int64_t ldk = token_rows(k, c->kv_heads, c->head_dim, type, "k"), ldv = token_rows(v, c->kv_heads, c->head_dim, type, "v");
@@ -119,6 +142,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* po = nullptr;
     if (q != nullptr) {
       const at::Tensor& out = *tensor(a[8], "q_out");
+      on_device(&out, c->device, "q_out");
       if (q->dim() != 3) refuse("q must be [tokens, heads, %d]", c->head_dim);
       heads = q->size(1);
       ldq = token_rows(*q, heads, c->head_dim, type, "q");
@@ -136,10 +160,11 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       rows = cos_sin->size(0);
       rot = cos_sin->size(1);
       table = static_cast<const float*>(cos_sin->data_ptr());
-      positions = static_cast<const int32_t*>(vector(*tensor(a[3], "positions"), at::kInt, T, "positions"));
+      positions = static_cast<const int32_t*>(vector(*at, at::kInt, T, "positions"));
     }
     const int interleaved = PyObject_IsTrue(a[6]);
     if (interleaved < 0) throw Refused{};
+    const OnDevice guard(c->device);
     return tl_kv_append(c, pq, k.data_ptr(), v.data_ptr(), code, fits(T, "k"), fits(heads, "q"), ldq, ldk, ldv, po, ldo, table,
                         fits(rows, "cos_sin"), fits(rot, "cos_sin"), interleaved, positions,
                         static_cast<const int64_t*>(vector(slots, at::kLong, T, "slots")), stream_of(a[9], k));
@@ -149,9 +174,11 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // paged_attention(cache, q, pages, lens, scale, window, out, lse, workspace, stream) -> tl_status
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call("paged_attention", n, 10, [&] {
-    const auto* c = reinterpret_cast<const tl_kv_cache*>(static_cast<intptr_t>(integer(a[0])));
+    const auto* c = reinterpret_cast<const Cache*>(static_cast<intptr_t>(integer(a[0])));
     const at::Tensor &q = *tensor(a[1], "q"), &pages = *tensor(a[2], "pages"), &lens = *tensor(a[3], "lens");
     const at::Tensor &out = *tensor(a[6], "out"), *lse = tensor(a[7], "lse", true), &ws = *tensor(a[8], "workspace");
+    on_device(&q, c->device, "q"), on_device(&pages, c->device, "pages"), on_device(&lens, c->device, "lens");
+    on_device(&out, c->device, "out"), on_device(lse, c->device, "lse"), on_device(&ws, c->device, "workspace");
     const int code = half_code(q, "q");
     if (q.dim() != 3) refuse("q must be [requests, heads, %d]", c->head_dim);
     const int64_t B = q.size(0), heads = q.size(1);
@@ -171,6 +198,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const double scale = PyFloat_AsDouble(a[4]);
     if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
     const int64_t window = integer(a[5]);
+    const OnDevice guard(c->device);
     return tl_paged_attention(c, q.data_ptr(), code, fits(B, "q"), fits(heads, "q"), ldq, static_cast<const int32_t*>(pages.data_ptr()),
                               fits(width, "pages"), ldp, static_cast<const int32_t*>(vector(lens, at::kInt, B, "lens")),
                               static_cast<float>(scale), window > INT32_MAX ? 0 : fits(window, "window"), out.data_ptr(), ldo, pl,
@@ -183,6 +211,9 @@ PyObject* lora_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call("lora_apply", n, 9, [&] {
     const at::Tensor &A = *tensor(a[0], "A"), &B = *tensor(a[1], "B"), &scale = *tensor(a[2], "scale"), &plan = *tensor(a[3], "plan");
     const at::Tensor &x = *tensor(a[5], "x"), &base = *tensor(a[6], "base"), &out = *tensor(a[7], "out");
+    const int device = A.device().index();
+    on_device(&B, device, "B"), on_device(&scale, device, "scale"), on_device(&plan, device, "plan");
+    on_device(&x, device, "x"), on_device(&base, device, "base"), on_device(&out, device, "out");
     const int64_t adapters = A.size(0), rank = A.size(1), K = A.size(2), N = B.size(1), M = integer(a[4]);
     const int code = half_code(A, "A");
     want_type(x, A.scalar_type(), "x");
@@ -190,6 +221,7 @@ PyObject* lora_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (base.scalar_type() != at::kFloat) y_code = half_code(base, "base");
     want_type(out, base.scalar_type(), "out");
     const int64_t ldx = matrix(x, M, K, "x"), ldb = matrix(base, M, N, "base"), ldy = matrix(out, M, N, "out");
+    const OnDevice guard(device);
     return tl_lora_apply(x.data_ptr(), ldx, A.data_ptr(), B.data_ptr(), static_cast<const float*>(scale.data_ptr()), code,
                          fits(adapters, "A"), fits(rank, "A"), plan.data_ptr(), fits(M, "x"), fits(N, "B"), fits(K, "A"), base.data_ptr(),
                          ldb, out.data_ptr(), ldy, y_code, stream_of(a[8], x));

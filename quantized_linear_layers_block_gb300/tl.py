@@ -39,6 +39,12 @@ class tl_kv_cache(ctypes.Structure):
                 ("dtype", _I), ("kv_heads", _I), ("head_dim", _I), ("page_size", _I), ("num_pages", _I)]
 
 
+class _Cache(ctypes.Structure):
+    """What _tensors takes the address of: a cache and the number of its GPU."""
+
+    _fields_ = [("cache", tl_kv_cache), ("device", _I)]
+
+
 _PKV = ctypes.POINTER(tl_kv_cache)
 SIGNATURES = {
     "tl_strerror": (ctypes.c_char_p, [_I]),
@@ -388,18 +394,22 @@ class PagedKVCache:
                 _dev_tensor(t, torch.float32, name)
                 if tuple(t.shape) != (kv_heads,):
                     raise ValueError(f"{name} must be [{kv_heads}]")
+        if any(t is not None and t.device != k.device for t in (v, k_scale, v_scale)):
+            raise ValueError("k, v and their scales must be on one GPU")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = shape[0], page_size, kv_heads, head_dim
         self.dtype, self.device = dtype, k.device
         self.scale = head_dim ** -0.5      # of attend(), unless it is given another
-        self.struct = tl_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), k.stride(1), k.stride(2),
-                                  _CACHE_DTYPES[dtype], kv_heads, head_dim, page_size, num_pages)
-        self._address = ctypes.addressof(self.struct)
+        self._bound = _Cache(tl_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), k.stride(1), k.stride(2),
+                                         _CACHE_DTYPES[dtype], kv_heads, head_dim, page_size, num_pages), k.device.index)
+        self.struct = self._bound.cache
+        self._address = ctypes.addressof(self._bound)
         # attend()'s workspace: of the most query heads to a key-value head that take one (17), as its size depends
         # neither on the requests nor on more heads. Zeroed once here; every call leaves its counters zero again.
         self._ws = None
         if head_dim in (64, 128, 256) and kv_heads <= 1024:
-            need = tl_paged_attention_workspace_size(1, kv_heads * min(17, 1024 // kv_heads), kv_heads, head_dim)
+            with torch.cuda.device(k.device):
+                need = tl_paged_attention_workspace_size(1, kv_heads * min(17, 1024 // kv_heads), kv_heads, head_dim)
             self._ws = torch.zeros((need,), dtype=torch.uint8, device=k.device)
 
     def append(self, k, v, positions, slots, cos_sin=None, interleaved: bool = False, q=None, q_out=None, stream=None):
@@ -474,6 +484,11 @@ def tl_lora_plan(ids: torch.Tensor, n_adapters: int, plan: LoraPlan | None = Non
         plan = LoraPlan(M, n_adapters, _allocate(torch.empty, (tl_lora_plan_size(M, n_adapters),), torch.uint8, ids.device, stream))
     elif (plan.M, plan.n_adapters) != (M, n_adapters):
         raise ValueError("the plan is of another number of tokens or adapters")
+    elif plan.data.device != ids.device:
+        raise ValueError("the plan and ids must be on one GPU")
+    if ids.device.index != torch.cuda.current_device():
+        with torch.cuda.device(ids.device):
+            return tl_lora_plan(ids, n_adapters, plan, stream)
     _check(lib().tl_lora_plan(_ptr(ids), M, n_adapters, plan.data.data_ptr(), plan.data.numel(), _stream(stream)), "tl_lora_plan")
     return plan
 
@@ -498,6 +513,8 @@ class LoraBank:
         _dev_tensor(scale, torch.float32, "scale")
         if tuple(scale.shape) != (A.shape[0],):
             raise ValueError(f"scale must be [{A.shape[0]}]")
+        if B.device != A.device or scale.device != A.device:
+            raise ValueError("A, B and scale must be on one GPU")
         self.A, self.B, self.scale = A, B, scale
         self.n_adapters, self.rank, self.K = A.shape
         self.N = B.shape[1]
