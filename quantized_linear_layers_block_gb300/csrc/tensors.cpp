@@ -198,10 +198,11 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const double scale = PyFloat_AsDouble(a[4]);
     if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
     const int64_t window = integer(a[5]);
+    const int tokens = window > INT32_MAX ? 0 : window < 0 ? -1 : static_cast<int>(window);      // wider than any length: all; negative: refused
     const OnDevice guard(c->device);
     return tl_paged_attention(c, q.data_ptr(), code, fits(B, "q"), fits(heads, "q"), ldq, static_cast<const int32_t*>(pages.data_ptr()),
                               fits(width, "pages"), ldp, static_cast<const int32_t*>(vector(lens, at::kInt, B, "lens")),
-                              static_cast<float>(scale), window > INT32_MAX ? 0 : fits(window, "window"), out.data_ptr(), ldo, pl,
+                              static_cast<float>(scale), tokens, out.data_ptr(), ldo, pl,
                               ws.data_ptr(), ws.nbytes(), stream_of(a[9], q));
   });
 }
