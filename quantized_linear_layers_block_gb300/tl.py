@@ -348,10 +348,12 @@ def _raw_stream(stream):
 
 def _allocate(make, shape, dtype, device, stream):
     """A tensor that the kernels of `stream` are the first to use: allocated, and filled, in that stream's order."""
-    if isinstance(stream, torch.cuda.Stream):
-        with torch.cuda.stream(stream):
-            return make(shape, dtype=dtype, device=device)
-    return make(shape, dtype=dtype, device=device)
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):      # a handle: memory that the current stream still uses is not that one's
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
 
 
 class PagedKVCache:
