@@ -356,6 +356,12 @@ def _allocate(make, shape, dtype, device, stream):
         return make(shape, dtype=dtype, device=device)
 
 
+def _filled(device):
+    """Waits for what a constructor has the current stream fill: the object may be used on any stream from now on."""
+    if not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
+
+
 class PagedKVCache:
     """The paged key-value cache of one layer, and the two operators on it.
 
@@ -413,6 +419,7 @@ class PagedKVCache:
             with torch.cuda.device(k.device):
                 need = tl_paged_attention_workspace_size(1, kv_heads * min(17, 1024 // kv_heads), kv_heads, head_dim)
             self._ws = torch.zeros((need,), dtype=torch.uint8, device=k.device)
+        _filled(k.device)
 
     def append(self, k, v, positions, slots, cos_sin=None, interleaved: bool = False, q=None, q_out=None, stream=None):
         """tl_kv_append on this cache; returns the rotated queries (None without q)."""
@@ -512,6 +519,7 @@ class LoraBank:
             raise ValueError("A must be [n_adapters, rank, K] and B [n_adapters, N, rank]")
         if scale is None:
             scale = torch.ones((A.shape[0],), dtype=torch.float32, device=A.device)
+            _filled(A.device)
         _dev_tensor(scale, torch.float32, "scale")
         if tuple(scale.shape) != (A.shape[0],):
             raise ValueError(f"scale must be [{A.shape[0]}]")

@@ -45,3 +45,30 @@ def test_default_stream(handle):
     kv, q, table, k64, v64 = build(22, lens, 4, 2, 64, 16)
     qd, td, ld = q.cuda(), torch.tensor(table).cuda(), torch.tensor(np.asarray(lens, dtype=np.int32)).cuda()
     assert torch.equal(kv.attend(qd, td, ld, stream=handle), check(kv, q, table, k64, v64, lens))
+
+
+def test_objects_made_on_a_stream_that_is_behind():
+    """A cache's workspace (and its own k and v) and a bank's scales are there when the constructor returns, on any stream."""
+    lens = [3000, 20]
+    kv, q, table, k64, v64 = build(21, lens, 8, 2, 128, 16)
+    qd, td, ld = q.cuda(), torch.tensor(table).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    good = check(kv, q, table, k64, v64, lens)
+    x, A, B, scale, base, ids = (t.cuda() if torch.is_tensor(t) else t for t in make(9, 45, 264, 200, 16, 3))
+    ids = torch.tensor(ids).cuda()
+    ones = tl.LoraBank(A, B, torch.ones_like(scale))
+    expected = ones.apply(x, base, ones.plan(ids))
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    dirty = [torch.full_like(kv._ws, 7), torch.full_like(scale, 9.0)]      # where the new ones may lie
+    keep_current_stream_behind()
+    del dirty
+    again = tl.PagedKVCache(kv.num_pages, kv.page_size, kv.kv_heads, kv.head_dim, k=kv.k, v=kv.v)
+    keep_current_stream_behind()
+    empty = tl.PagedKVCache(kv.num_pages, kv.page_size, kv.kv_heads, kv.head_dim)
+    keep_current_stream_behind()
+    bank = tl.LoraBank(A, B)
+    y = again.attend(qd, td, ld, stream=st)
+    z = bank.apply(x, base, bank.plan(ids, stream=st), stream=st)
+    zero = empty.attend(qd, td.clamp(min=0), ld, stream=st)
+    st.synchronize()
+    assert torch.equal(y, good) and torch.equal(z, expected) and not zero.any()
