@@ -415,7 +415,10 @@ int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const v
  *            large enough for. Calls that can overlap on the GPU must not share one.
  * head_dim is 64, 128 or 256; q_heads a multiple of kv_heads, at most 128 query
  * heads for each key-value head; q_heads at most 1024. Sums, maxima and scores
- * are fp32. A length that is negative or above max_pages * page_size, and a page
+ * are fp32; p_j meets V_j with 16 bits for a bf16 cache, 22 for the others. Over an 8-bit cache a bf16 query counts
+ * as fp16 relative to its head's largest element: one below 2^-14 of that loses bits. An infinite value that
+ * a request attends to makes its channel infinite; a NaN, or infinities of both signs, make it NaN; a
+ * score of +inf or NaN makes its head NaN. A length that is negative or above max_pages * page_size, and a page
  * outside [0, num_pages) among those that a request needs, record TL_EDATA; nothing
  * is read out of range and that request's output is unspecified. What lies in the pages past a
  * request's length has no influence, NaN included. The result does not depend on
@@ -446,14 +449,15 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
  *   x       [M, K], dtype TL_BF16 or TL_F16, ldx elements from token to token
  *   A, B    [n_adapters, rank, K] and [n_adapters, N, rank] of the same dtype, dense
  *   scale   fp32 [n_adapters]
- *   plan    of the same M and n_adapters (another one's is refused on the
- *           device: TL_EDATA, and nothing is written)
+ *   plan    of the same M and n_adapters (another one's, of one token or more, is refused on
+ *           the device: TL_EDATA, and nothing is written or read past its end)
  *   base    [M, N] of y_dtype (TL_BF16, TL_F16 or TL_F32), ldb elements from token to token
  *   y       [M, N] likewise; may be base (in place, ldy = ldb), must not overlap it otherwise
  * The products are exact and summed in fp32; A[a] x[m] is kept in fp32 and enters the second product
  * as the sum of two 16-bit numbers, or three for bf16 operands and an fp32 y. So it counts with 22 bits for fp16
  * operands, 16 for bf16 ones, and 24 for those with an fp32 y: bits of the largest of a token's rank elements for fp16,
- * of each for bf16. base + delta is rounded once to y_dtype. For given
+ * of each for bf16. base + delta is rounded once to y_dtype. An infinite element of B may make its column NaN where
+ * the formula gives an infinity. For given
  * M and n_adapters, a token's result does not depend on the other tokens of the batch.
  * rank is a multiple of 8 up to 128; K, N and the lds multiples of 8, N at most 2^22;
  * anything else returns TL_EUNSUPPORTED.

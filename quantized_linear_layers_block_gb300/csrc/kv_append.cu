@@ -190,9 +190,11 @@ cudaError_t launch(const AppendParams& p, int T, bool bf16, bool f8, cudaStream_
 
 cudaError_t launch_kv_append(const AppendParams& p, int T, bool bf16, bool f8, int sms, cudaStream_t st) {
   // One block for each token. Few tokens: all their heads at once, as the latency of one pass is the time (24 tokens of 32
-  // heads of 256: 2.4 us with 512 threads, 3.0 with 128, 4.2 with 64). Many: small blocks, which start and end
-  // out of step and so keep the memory busy (16000 tokens of 56 heads of 128: 141 us with 512, 87 with 256, 75 with 128, 72 with 64,
-  // 0.96 of the copy rate; 512 tokens: 4.9, 3.7, 4.1 and 5.3; 1000 tokens: 5.8 with 256, 5.5 with 64).
+  // heads of 256: 2.4 us with 512 threads, 2.6 with 256, 3.1 with 128, 4.4 with 64). Many: small blocks, which start and end
+  // out of step and so keep the memory busy (40 + 16 heads of 128, us with 256, 128 and 64 threads: bf16, 512 tokens 4.1, 4.1, 5.0;
+  // 1000: 6.9, 6.5, 7.9; 4000: 27.2, 22.1, 22.1; 16000: 97.8, 77.9, 72.0, 0.96 of the copy rate. Into 8 bits, where 64 threads have
+  // 48 registers and spill some: 512: 4.0, 4.3, 6.1; 1000: 6.4, 5.5, 7.6; 4000: 27.8, 24.4, 25.5; 16000: 99.8, 86.3, 77.1, 0.82 of it).
+  // Around 1000 tokens, and for 8 bits up to some thousand, the rule gives away up to a quarter of the time.
   return T <= sms ? launch<512>(p, T, bf16, f8, st) : T < 4 * sms ? launch<256>(p, T, bf16, f8, st) : launch<64>(p, T, bf16, f8, st);
 }
 

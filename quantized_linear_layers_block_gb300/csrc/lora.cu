@@ -20,11 +20,12 @@
 // an item's columns, and each forms h for itself (its A is in L2 by then).
 //
 // Measured on GB300: 4096 tokens, rank 16, K = 5120, N = 34816, bf16: 102 us, 6.05 TB/s, 0.89 of the copy rate (two kernels
-// with h in memory: 169 us). 515 tokens, rank 64, K = 17408, N = 5120, fp32 out: 16 us, of which the first
+// with h in memory: 169 us). 515 tokens, rank 64, K = 17408, N = 5120, fp32 out: 19.7 us, of which the first
 // product takes 6 (96 MB of x and A per item into the SMs, 83 B/ns each), the second 3 and the chain
 // around them (plan, sums, meetings of the cluster, parts) the rest. 48 tokens of 32 adapters, rank 32, K = N = 5120:
-// 7.4 us; one token, rank 16, N = 17408: 5.0 us, all of it that chain. 4096 tokens, rank 128, K = 5120, N = 17408: 148 us,
-// where the bytes take 52 and the MMAs of both parts 69.
+// 7.6 us; one token, rank 16, N = 17408: 5.2 us, all of it that chain. 4096 tokens, rank 128, K = 5120, N = 17408: 148 us,
+// where the bytes take 52 and the MMAs of both parts 69. The plan, once per step: 2.8 us for one token, 3.1 for 48, 5.5 for
+// 515, 24 for 4096 (one block, whose warps take turns: 6 us per 1024 tokens).
 #include "lora.cuh"
 #include "tl_internal.cuh"
 

@@ -25,9 +25,10 @@ struct LoraPlanHeader {
 
 // Tokens of an item. 32 read an adapter's matrices half as often as 16 and fill the matrix instructions' rows as
 // well; 16 leave twice as many items, which blocks share the SMs more evenly with, and a shorter chain. The plan
-// serves adapters of any rank and width, and both sides meet at about the same M for all of them (K = 5120, N = 17408,
-// 4 adapters, 16 against 32 tokens, us: rank 8: 512 tokens 12.8, 16.6; 1024: 24.4, 19.9; 2048: 43, 33;
-// rank 128: 512 tokens 35, 52; 1024: 54, 53; 2048: 96, 83).
+// serves adapters of any rank and width, and both sides meet at about the same M for all of them (bf16, K = 5120, N = 17408,
+// 4 adapters, 16 against 32 tokens, us: rank 8: 256 tokens 8.8, 9.8; 512: 14.9, 14.8; 1024: 22.5, 19.9; 2048: 38.6, 32.7;
+// rank 32: 512 tokens 16.0, 17.4; 1024: 23.9, 23.2; rank 64: 21.0, 23.0; 32.9, 30.0; rank 128: 30.8, 34.1; 53.0, 46.0; 2048:
+// 96.5, 79.0; 515 tokens of 5 adapters, rank 64, K = 17408, N = 5120, fp16 to fp32: 19.8, 28.8).
 inline int lora_tile(int M) { return M >= 1024 ? 32 : 16; }
 
 // most items that M tokens of n_adapters adapters (and none) can need

@@ -38,12 +38,12 @@
 // through their shared memory; many segments of few keys with a ring each: no list, no workspace, no atomics.
 //
 // Measured on GB300 (copy rate 6.79 TB/s): the loop streams at 7.4-7.7 TB/s. 160 requests of 512-16384 tokens, 8 heads of 128
-// channels, 8 bits: 222 us, 6.8 TB/s of 1.51 GB. 24 requests of 40-9000 tokens, 4 heads of 256, bf16: 37 us, 4.7 TB/s;
+// channels, 8 bits: 226 us, 6.7 TB/s of 1.51 GB. 24 requests of 40-9000 tokens, 4 heads of 256, bf16: 37 us, 4.7 TB/s;
 // 23 us of it stream, 3.4 us pass before the first loads are out (lengths, place in the list, page
-// table) and 8 us in meetings and joins. One request of 80001: 61 us, 5.3 TB/s. 577 tokens of
-// one request: 5.6 us. The 16-bit loop takes 1.3 us for a tile of 64 KB per SM whatever is left out of its
-// arithmetic; above 16 query heads to a key-value head it is the arithmetic that bounds (32 heads of 128
-// channels: 103 us where the bytes take 50).
+// table) and 8 us in meetings and joins. One request of 80001: 62 us, 5.3 TB/s. 577 tokens of
+// one request: 5.8 us. 1024 requests of 1-400 tokens, 8 heads of 128: 155 us, 5.6 TB/s. The 16-bit loop takes 1.3 us for a tile of
+// 64 KB per SM whatever is left out of its arithmetic; above 16 query heads to a key-value head it is the arithmetic that
+// bounds (32 heads of 128 channels: 106 us where the bytes take 50).
 #pragma once
 
 #include "attention_join.h"
@@ -1121,7 +1121,9 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
   long long grid = static_cast<long long>(sms) * n;
   if (grid > kAttnMaxGrid) grid = kAttnMaxGrid;
   // Few segments: a cluster each, of 16 to 1 blocks, the most of which all run at once (sixteens on SMs of their own), while a
-  // block has eight tiles at most and a smaller cluster would not have next to none. bf16, 128 channels, list against clusters:
+  // block has eight tiles at most. A cluster of 16 is for more than 8 tiles, of 8 for more than 4, of 4 for more than 2, as blocks
+  // without a tile only lengthen the join; a pair for more than 4, as up to there a single block is as fast (the last figures
+  // here). The last list figure is a loss that the rule accepts. bf16, 128 channels, list against clusters:
   // 4 segments of 4000 keys 14.5, 10.1 (7.5 with sixteens), 5 of 8000 14.5, 11.1; 36 of 2000 12.1, 9.0; 56 of 600 9.9, 7.5; 152 of
   // 600 14.2, 10.2; 300 of 200 8.6, 6.9, of 50 to 400 12.8, 8.7, of 100 to 800 16.8, 15.3, of 187 to 1500 24.7, 27.4. Pairs
   // against single blocks: 152 of 200 6.7, 5.9, of 400 8.3, 9.0. Clusters that do not all run at once lose (256

@@ -373,6 +373,8 @@ class PagedKVCache:
 
     Which pages belong to which request is the caller's: append() takes a slot
     (page * page_size + row) for each token, attend() a table of pages for each request.
+    append() takes any head_dim that is a multiple of 16 up to 512, attend() 64, 128 and 256.
+    All tensors of a call lie on the cache's GPU.
 
     The cache keeps one workspace for attend(), which joins requests that several
     blocks share: attend() calls on one cache that can run at the same time on
