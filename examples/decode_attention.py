@@ -64,6 +64,7 @@ class AttentionHalf:
         order = torch.randperm(pages, generator=gen, device=device, dtype=torch.int32)
         self.pages = order.view(requests, -1).contiguous()
         self.lens = torch.zeros(requests, dtype=torch.int32, device=device)
+        self.max_context, self.tokens = max_context, [0] * requests        # (the lengths once more, on the host)
         self.adapter = torch.randint(-1, adapters, (requests,), generator=gen, device=device, dtype=torch.int32)
         self.plan = self.qkv_bank.plan(self.adapter)
         self.x = torch.empty((requests, hidden), dtype=torch.bfloat16, device=device)
@@ -84,9 +85,18 @@ class AttentionHalf:
         q, k, v = qkv.split([hq * d, hkv * d, hkv * d], dim=1)
         return q.unflatten(1, (hq, d)), k.unflatten(1, (hkv, d)), v.unflatten(1, (hkv, d))
 
+    def _take(self, requests, n):
+        """n more tokens of each of these requests, whose pages have to hold them: their places are looked up unchecked."""
+        full = [r for r in requests if self.tokens[r] + n > self.max_context]
+        if full:
+            raise ValueError(f"requests {full}: {n} more tokens are beyond {self.max_context}")
+        for r in requests:
+            self.tokens[r] += n
+
     def prompt(self, request, x):
         """Appends the keys and values of a prompt's tokens x [T, hidden] to one request."""
-        begin = int(self.lens[request])
+        begin = self.tokens[request]
+        self._take([request], x.shape[0])
         at = torch.arange(begin, begin + x.shape[0], dtype=torch.int32, device=x.device)
         plan = self.qkv_bank.plan(self.adapter[request].expand(x.shape[0]).contiguous())
         _, k, v = self.project(x, plan)
@@ -105,6 +115,7 @@ class AttentionHalf:
 
     def step(self, x):
         """One new token of every request: x [requests, hidden] -> the half's output, in a buffer that the next step reuses."""
+        self._take(range(len(self.tokens)), 1)
         self.x.copy_(x)
         if self.graph is None:                       # warm up and capture on a copy of the scheduler's state
             lens = self.lens.clone()
