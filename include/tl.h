@@ -433,6 +433,118 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
                        float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * tl_kv_append with the norms of queries and keys for each head, in the same pass: every head x of
+ * q (of k) becomes
+ *   y_i = x_i w_i / sqrt(mean_i x_i^2 + eps)
+ * before it is rotated and stored; values pass as they are.
+ *   q_norm, k_norm   fp32 [head_dim], the weights w; NULL: q (k) is not normalised
+ *   eps              positive and finite
+ * Everything else, rounding included, is tl_kv_append's: sums, norms and rotation are fp32, rounded once
+ * to the type that is stored. A head with an infinite or NaN element becomes NaN where the formula does.
+ */
+int tl_kv_append_norm(const tl_kv_cache* cache, const void* q, const void* k, const void* v,
+                      int dtype, int T, int q_heads, int64_t ldq, int64_t ldk, int64_t ldv,
+                      void* q_out, int64_t ldqo, const float* q_norm, const float* k_norm,
+                      float eps, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                      const int32_t* positions, const int64_t* slots, void* stream);
+
+/*
+ * Trees of drafted tokens. The four calls below check several drafted tokens of every request in one pass
+ * of a model. A request's tokens of this pass are the nodes of a tree: node 0 is the last token that is
+ * certain (its key is not cached yet), each other node a guess at what follows its parent. The nodes of all requests
+ * lie behind each other, in rows starts[b] .. starts[b + 1] - 1 of T rows; a request has at most
+ * TL_TREE_NODES of them, or none. Rows from starts[B] on are padding. Node i of a request is cached
+ * at its place lens[b] + i, whatever its depth, lens[b] being the tokens cached before this pass.
+ *
+ *   starts   int32 [B + 1], 0 <= starts[0] <= starts[1] <= ... <= starts[B] <= T
+ *   lens     int32 [B]
+ *   pages    int32 [B, max_pages], ldp entries apart (as for tl_paged_attention); they hold the
+ *            nodes' places too
+ * A request whose starts are out of order, outside [0, T] or further than TL_TREE_NODES apart, or whose
+ * length is negative or does not leave room for its nodes in max_pages * page_size, records
+ * TL_EDATA; nothing is read or written out of range for it, and what the call writes for it, or for a row that two
+ * requests claim, is unspecified.
+ */
+#define TL_TREE_NODES 64
+
+/*
+ * What a pass over trees needs, from the parents; once per pass for all layers.
+ *   parents    int32 [T]: the parent of node i of a request, a node before it, or -1 for a root (node 0);
+ *              another value records TL_EDATA and counts as -1
+ *   masks      out int64 [T]: bit j is set for node j = i and every ancestor j of i; 0 for padding
+ *   positions  out int32 [T]: lens[b] + the node's depth; 0 for padding
+ *   slots      out int64 [T]: where tl_kv_append stores the node; -1 for padding, and with TL_EDATA for a place
+ *              whose page is outside [0, num_pages)
+ */
+int tl_tree_plan(const int32_t* parents, const int32_t* starts, int B, int T, const int32_t* lens,
+                 const int32_t* pages, int max_pages, int64_t ldp, int page_size, int num_pages,
+                 int64_t* masks, int32_t* positions, int64_t* slots, void* stream);
+
+/*
+ * Attention of every node over its request's cached tokens and the nodes of its mask:
+ *   out[t,h] = sum_j p_j V_j / sum_j p_j,  p_j = exp(scale q[t,h] . K_j)
+ * with j over the cached tokens j < lens[b] and the nodes' places lens[b] + i for the bits i of masks[t]
+ * (bits from the request's nodes on are ignored). A row that sees nothing gets out = 0 and lse = -inf.
+ *   q, out     [T, q_heads, head_dim], types, rows and heads as for tl_paged_attention
+ *   masks      int64 [T], of tl_tree_plan or any others (a chain: 2^(i + 1) - 1)
+ *   window     0: all cached tokens. Else at least TL_TREE_NODES: how many keys a node sees besides the sinks,
+ *              its mask's nodes and the last cached tokens, max(0, window - bits of its mask) of them
+ *   sinks      with a window, the first cached tokens that stay visible; 0 without one
+ *   lse        optional fp32 [T, q_heads]: log sum_j p_j
+ *   workspace  ws_bytes >= tl_tree_attention_workspace_size; its contents do not matter. Calls that can overlap on the
+ *              GPU must not share one.
+ * Rows outside every request (padding) of out and lse are left as they were. Sizes and the meaning of the rest
+ * are tl_paged_attention's, as are what it says of infinities, of bad pages and of what lies past a request's end;
+ * a tree of one node is its decode step, with sinks if wanted. q_heads / kv_heads is at most 128.
+ */
+int tl_tree_attention_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim,
+                                     size_t* bytes);
+int tl_tree_attention(const tl_kv_cache* cache, const void* q, int dtype, int B, int T, int q_heads,
+                      int64_t ldq, const int64_t* masks, const int32_t* starts,
+                      const int32_t* pages, int max_pages, int64_t ldp, const int32_t* lens,
+                      float scale, int window, int sinks, void* out, int64_t ldo, float* lse,
+                      void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Verification: which drafted tokens hold against the target's probabilities, and the token after them, so that what a
+ * request emits is distributed as if the target itself had been sampled token by token.
+ *   target   fp32 [T, vocab], ldt elements apart: row of node i: the target's probabilities of what follows it
+ *   draft    fp32 [T, vocab], ldd apart: row of node i: the distribution that the children of i were drawn from,
+ *            independently. NULL: they were not drawn but chosen, each with probability one.
+ *   tokens   int32 [T] of the nodes (node 0's is not read); one outside [0, vocab) records TL_EDATA and is refused
+ *   parents, starts   as for tl_tree_plan
+ *   uniform  fp32 [T] in [0, 1): a node's own number decides about it, node 0's draws the token at the end
+ * The walk starts at node 0 with R = its row of target and S = 1, and tries the children of the node where it stands
+ * in their order. Child c with token x, q = the draft's row there: accepted when u_c q(x) S < R(x), and the walk goes
+ * on at c with R its row and S = 1; else R becomes max(R - S q, 0) and S the sum of R. Where no child is
+ * left, the token after is the smallest x with sum_{y <= x} R(y) > u_0 sum_y R(y), R being the target's row again
+ * where nothing is left of it.
+ *   path     out int32 [T]: a request's accepted nodes in order, node 0 first, then -1 (padding too)
+ *   counts   out int32 [B]: how many they are (0 for a request without nodes)
+ *   next     out int32 [B]: the token after the last of them (-1 for a request without nodes)
+ * Probabilities are taken as multiples of 2^-60 (rounded down), and sums of them are exact, so the result does not
+ * depend on any order. Below 0 and NaN count as 0, above 1 as 1; uniforms outside [0, 1) as the nearest number in it. vocab is at
+ * most 2^24; rows need no alignment beyond their elements'.
+ */
+int tl_verify_tree(const float* target, int64_t ldt, const float* draft, int64_t ldd, int vocab,
+                   const int32_t* tokens, const int32_t* parents, const int32_t* starts, int B,
+                   int T, const float* uniform, int32_t* path, int32_t* counts, int32_t* next,
+                   void* stream);
+
+/*
+ * Moves the keys and values of a request's accepted nodes together, in place: the row at place
+ * lens[b] + path[starts[b] + j] goes to place lens[b] + j for j < counts[b], all as they were before the call. Afterwards
+ * the first lens[b] + counts[b] places are the request's cached tokens; what lies behind them is unspecified.
+ *   path     int32 [T], counts int32 [B]: tl_verify_tree's. A request's entries increase and are among its nodes; a
+ *            request with others, or a count outside [0, its nodes], records TL_EDATA and is left as it was, as is one of
+ *            whose pages one that is needed is outside [0, num_pages).
+ * One layer's cache; requests must not share the pages that hold their nodes' places. head_dim is as for tl_kv_append.
+ */
+int tl_kv_compact(const tl_kv_cache* cache, const int32_t* path, const int32_t* counts,
+                  const int32_t* starts, int B, int T, const int32_t* pages, int max_pages,
+                  int64_t ldp, const int32_t* lens, void* stream);
+
+/*
  * Low-rank adapters of many requests beside a projection (ternary weights cannot
  * absorb an adapter, so each request's runs beside them):
  *   y[m] = base[m] + scale[a] B[a] (A[a] x[m]),   a = ids[m]

@@ -27,7 +27,8 @@ LIB = os.path.join(PKG, "libtl_gb300.so")
 TENSORS = os.path.join(PKG, "_tensors.so")
 SOURCES = ["tl_api.cu", "pack.cu", "rotate_quant.cu", "decode.cu", "decode_fused_m.cu", "prefill.cu", "codec.cu",
            "decode_f32.cu", "decode_tc.cu", "kv_append.cu", "paged_attention_bf16.cu", "paged_attention_f16.cu",
-           "paged_attention_f8.cu", "lora.cu"]
+           "paged_attention_f8.cu", "lora.cu", "tree_plan.cu", "tree_attention_bf16.cu", "tree_attention_f16.cu",
+           "tree_attention_f8.cu", "verify_tree.cu", "kv_compact.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include")]
 

@@ -59,10 +59,18 @@ __device__ __forceinline__ uint2 narrow8_e4m3(const float (&f)[8], float inv) {
   return make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16));
 }
 
-// lanes = head_dim / 16 threads cover a head; `rows` heads are taken at a time
-template <bool BF16, bool F8, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 64 ? 20 : THREADS == 256 ? 4 : 1) kv_append_kernel(const __grid_constant__ AppendParams p) {
-  const int lanes = p.dim >> 4;
+// the least power of two that is at least n <= 32
+__host__ __device__ constexpr int power_of_two(int n) {
+  int p = 1;
+  while (p < n) p *= 2;
+  return p;
+}
+
+// lanes = head_dim / 16 threads cover a head; `rows` heads are taken at a time. With NORM they are a power of two of neighbouring
+// lanes of one warp, the last of them idle for other sizes, and add up the squares of their head by shuffles.
+template <bool BF16, bool F8, int THREADS, bool NORM>
+__global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 12 : 20) : THREADS == 256 ? (NORM ? 2 : 4) : 1) kv_append_kernel(const __grid_constant__ AppendParams p) {
+  const int lanes = NORM ? power_of_two(p.dim >> 4) : p.dim >> 4;
   const int row = threadIdx.x / lanes, j = threadIdx.x - row * lanes;
   const int rows = blockDim.x / lanes;
   const int tok = blockIdx.x;
@@ -74,8 +82,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? 20 : THREADS == 256 ?
   // the thread's two vectors of 8 channels: pairs (a[i], b[i]), or pairs of neighbours in a, then in b
   const int c0 = turn && !p.interleaved ? 8 * j : 16 * j;
   const int c1 = turn && !p.interleaved ? 8 * j + (p.rot >> 1) : 16 * j + 8;
+  const bool idle = NORM && 16 * j >= p.dim;
   // q may be q_out: not the read-only path
   auto load = [&](int h, uint4& v0, uint4& v1) {
+    if (idle) {
+      v0 = v1 = make_uint4(0, 0, 0, 0);
+      return;
+    }
     const bool is_v = h >= p.q_heads + p.kv_heads;
     const uint16_t* src = h < p.q_heads ? p.q + tok * p.ldq + h * p.dim
                           : is_v        ? p.v + tok * p.ldv + (h - p.q_heads - p.kv_heads) * p.dim
@@ -113,16 +126,43 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? 20 : THREADS == 256 ?
     cell = page * p.page_stride + (slot - page * p.page_size) * p.token_stride;
   }
   const int heads = p.q_heads + (keep ? 2 * p.kv_heads : 0);
+  float wt[16];                         // norm weights of the thread's channels, of q's heads, then of k's
+  int wt_of = 0;                        // 1: q's, 2: k's
+  const unsigned head_lanes = NORM ? (lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1) << ((threadIdx.x & 31) / lanes * lanes)) : 0u;
+  const float per_channel = 1.f / static_cast<float>(p.dim);
   auto store = [&](int h, const uint4& v0, const uint4& v1) {
     const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
     const int kh = h - p.q_heads - (is_v ? p.kv_heads : 0);
     uint4 r0 = v0, r1 = v1;
     float a[8], b[8];
     const bool turned = turn && !is_v;
-    if (turned || (F8 && !is_q)) {
+    const float* const weight = !NORM || is_v ? nullptr : is_q ? p.q_norm : p.k_norm;
+    const bool normed = NORM && weight != nullptr;
+    if (turned || normed || (F8 && !is_q)) {
       widen8<BF16>(v0, a);
       widen8<BF16>(v1, b);
     }
+    if (normed) {
+      if (wt_of != 2 - is_q) {
+        wt_of = 2 - is_q;
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 w = idle ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldg(reinterpret_cast<const float4*>(weight + (i < 8 ? c0 + i : c1 + i - 8)));
+          wt[i] = w.x, wt[i + 1] = w.y, wt[i + 2] = w.z, wt[i + 3] = w.w;
+        }
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
+      for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(head_lanes, sum, o);
+      const float inv = __frsqrt_rn(sum * per_channel + p.eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = __fmul_rn(__fmul_rn(a[i], inv), wt[i]);
+        b[i] = __fmul_rn(__fmul_rn(b[i], inv), wt[8 + i]);
+      }
+    }
+    if (idle) return;
     if (turned) {
       if (p.interleaved) {
 #pragma unroll
@@ -142,10 +182,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? 20 : THREADS == 256 ?
           b[i] = __fadd_rn(__fmul_rn(y, cs[i]), __fmul_rn(x, sn[i]));
         }
       }
-      if (!F8 || is_q) {
-        r0 = narrow8<BF16>(a);
-        r1 = narrow8<BF16>(b);
-      }
+    }
+    if ((turned || normed) && (!F8 || is_q)) {
+      r0 = narrow8<BF16>(a);
+      r1 = narrow8<BF16>(b);
     }
     if (is_q) {
       uint16_t* dst = p.q_out + tok * p.ldqo + h * p.dim;
@@ -175,15 +215,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? 20 : THREADS == 256 ?
   }
 }
 
-template <int THREADS>
+template <int THREADS, bool NORM>
 cudaError_t launch(const AppendParams& p, int T, bool bf16, bool f8, cudaStream_t st) {
-  const int lanes = p.dim / 16;
+  const int lanes = NORM ? power_of_two(p.dim / 16) : p.dim / 16;
   const dim3 grid(static_cast<unsigned>(T)), block(static_cast<unsigned>(THREADS / lanes * lanes));
   if (bf16)
-    return f8 ? launch_pdl(kv_append_kernel<true, true, THREADS>, grid, block, 0, st, p)
-              : launch_pdl(kv_append_kernel<true, false, THREADS>, grid, block, 0, st, p);
-  return f8 ? launch_pdl(kv_append_kernel<false, true, THREADS>, grid, block, 0, st, p)
-            : launch_pdl(kv_append_kernel<false, false, THREADS>, grid, block, 0, st, p);
+    return f8 ? launch_pdl(kv_append_kernel<true, true, THREADS, NORM>, grid, block, 0, st, p)
+              : launch_pdl(kv_append_kernel<true, false, THREADS, NORM>, grid, block, 0, st, p);
+  return f8 ? launch_pdl(kv_append_kernel<false, true, THREADS, NORM>, grid, block, 0, st, p)
+            : launch_pdl(kv_append_kernel<false, false, THREADS, NORM>, grid, block, 0, st, p);
 }
 
 }  // namespace
@@ -195,7 +235,9 @@ cudaError_t launch_kv_append(const AppendParams& p, int T, bool bf16, bool f8, i
   // 1000: 6.9, 6.5, 7.9; 4000: 27.2, 22.1, 22.1; 16000: 97.8, 77.9, 72.0, 0.96 of the copy rate. Into 8 bits, where 64 threads have
   // 48 registers and spill some: 512: 4.0, 4.3, 6.1; 1000: 6.4, 5.5, 7.6; 4000: 27.8, 24.4, 25.5; 16000: 99.8, 86.3, 77.1, 0.82 of it).
   // Around 1000 tokens, and for 8 bits up to some thousand, the rule gives away up to a quarter of the time.
-  return T <= sms ? launch<512>(p, T, bf16, f8, st) : T < 4 * sms ? launch<256>(p, T, bf16, f8, st) : launch<64>(p, T, bf16, f8, st);
+  if (p.q_norm != nullptr || p.k_norm != nullptr)
+    return T <= sms ? launch<512, true>(p, T, bf16, f8, st) : T < 4 * sms ? launch<256, true>(p, T, bf16, f8, st) : launch<64, true>(p, T, bf16, f8, st);
+  return T <= sms ? launch<512, false>(p, T, bf16, f8, st) : T < 4 * sms ? launch<256, false>(p, T, bf16, f8, st) : launch<64, false>(p, T, bf16, f8, st);
 }
 
 }  // namespace tl

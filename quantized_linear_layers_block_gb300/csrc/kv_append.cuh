@@ -23,8 +23,12 @@ struct AppendParams {
   const int64_t* slots;
   int* status;
   int q_heads, kv_heads, dim, page_size, rot, max_pos, interleaved;
+  const float* q_norm;       // weights of the heads' norms; NULL: none
+  const float* k_norm;
+  float eps;
 };
 
+// with q_norm or k_norm the kernel that normalises
 cudaError_t launch_kv_append(const AppendParams& p, int T, bool bf16, bool f8, int sms, cudaStream_t st);
 
 }  // namespace tl

@@ -122,54 +122,84 @@ PyObject* call(const char* name, Py_ssize_t got, Py_ssize_t want, F&& f) {
   return nullptr;
 }
 
+// a contiguous vector of n floats, or nothing for None
+const float* weights(PyObject* o, int64_t n, int device, const char* name) {
+  const at::Tensor* const t = tensor(o, name, true);
+  if (t == nullptr) return nullptr;
+  on_device(t, device, name);
+  return static_cast<const float*>(vector(*t, at::kFloat, n, name));
+}
+
+double number(PyObject* o) {
+  const double x = PyFloat_AsDouble(o);
+  if (x == -1.0 && PyErr_Occurred()) throw Refused{};
+  return x;
+}
+
+// The arguments of kv_append but its stream, which `stream` is; `norms` are q_norm, k_norm, eps, or NULL for none.
+int append(PyObject* const* a, PyObject* const* norms, PyObject* stream) {
+  const auto* c = reinterpret_cast<const Cache*>(static_cast<intptr_t>(integer(a[0])));
+  const at::Tensor &k = *tensor(a[1], "k"), &v = *tensor(a[2], "v"), &slots = *tensor(a[4], "slots");
+  const at::Tensor *cos_sin = tensor(a[5], "cos_sin", true), *q = tensor(a[7], "q", true);
+  on_device(&k, c->device, "k"), on_device(&v, c->device, "v"), on_device(&slots, c->device, "slots");
+  on_device(cos_sin, c->device, "cos_sin"), on_device(q, c->device, "q");
+  const at::Tensor* const at = cos_sin != nullptr ? tensor(a[3], "positions") : nullptr;
+  on_device(at, c->device, "positions");
+  const int code = half_code(k, "k");
+  const auto type = k.scalar_type();
+  const int64_t ldk = token_rows(k, c->kv_heads, c->head_dim, type, "k"), ldv = token_rows(v, c->kv_heads, c->head_dim, type, "v");
+  const int64_t T = k.size(0);
+  if (v.size(0) != T) refuse("k and v must have the same number of tokens");
+  int64_t heads = 0, ldq = 0, ldo = 0;
+  const void* pq = nullptr;
+  void* po = nullptr;
+  if (q != nullptr) {
+    const at::Tensor& out = *tensor(a[8], "q_out");
+    on_device(&out, c->device, "q_out");
+    if (q->dim() != 3) refuse("q must be [tokens, heads, %d]", c->head_dim);
+    heads = q->size(1);
+    ldq = token_rows(*q, heads, c->head_dim, type, "q");
+    ldo = token_rows(out, heads, c->head_dim, type, "q_out");
+    if (q->size(0) != T || out.size(0) != T) refuse("q, q_out and k must have the same number of tokens");
+    pq = q->data_ptr();
+    po = out.data_ptr();
+  }
+  const float* table = nullptr;
+  const int32_t* positions = nullptr;
+  int64_t rows = 0, rot = 0;
+  if (cos_sin != nullptr) {
+    want_type(*cos_sin, at::kFloat, "cos_sin");
+    if (cos_sin->dim() != 2 || !cos_sin->is_contiguous()) refuse("cos_sin must be a contiguous matrix [positions, channels]");
+    rows = cos_sin->size(0);
+    rot = cos_sin->size(1);
+    table = static_cast<const float*>(cos_sin->data_ptr());
+    positions = static_cast<const int32_t*>(vector(*at, at::kInt, T, "positions"));
+  }
+  const int interleaved = PyObject_IsTrue(a[6]);
+  if (interleaved < 0) throw Refused{};
+  const float *q_norm = nullptr, *k_norm = nullptr;
+  double eps = 1.0;
+  if (norms != nullptr) {
+    q_norm = weights(norms[0], c->head_dim, c->device, "q_norm");
+    k_norm = weights(norms[1], c->head_dim, c->device, "k_norm");
+    eps = number(norms[2]);
+  }
+  const OnDevice guard(c->device);
+  return tl_kv_append_norm(c, pq, k.data_ptr(), v.data_ptr(), code, fits(T, "k"), fits(heads, "q"), ldq, ldk, ldv, po, ldo, q_norm, k_norm,
+                           static_cast<float>(eps), table, fits(rows, "cos_sin"), fits(rot, "cos_sin"), interleaved, positions,
+                           static_cast<const int64_t*>(vector(slots, at::kLong, T, "slots")), stream_of(stream, k));
+}
+
 // kv_append(cache, k, v, positions, slots, cos_sin, interleaved, q, q_out, stream) -> tl_status
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call("kv_append", n, 10, [&] {
-    const auto* c = reinterpret_cast<const Cache*>(static_cast<intptr_t>(integer(a[0])));
-    const at::Tensor &k = *tensor(a[1], "k"), &v = *tensor(a[2], "v"), &slots = *tensor(a[4], "slots");
-    const at::Tensor *cos_sin = tensor(a[5], "cos_sin", true), *q = tensor(a[7], "q", true);
-    on_device(&k, c->device, "k"), on_device(&v, c->device, "v"), on_device(&slots, c->device, "slots");
-    on_device(cos_sin, c->device, "cos_sin"), on_device(q, c->device, "q");
-    const at::Tensor* const at = cos_sin != nullptr ? tensor(a[3], "positions") : nullptr;
-    on_device(at, c->device, "positions");
-    const int code = half_code(k, "k");
-    const auto type = k.scalar_type();
-    const int64_t ldk = token_rows(k, c->kv_heads, c->head_dim, type, "k"), ldv = token_rows(v, c->kv_heads, c->head_dim, type, "v");
-    const int64_t T = k.size(0);
-    if (v.size(0) != T) refuse("k and v must have the same number of tokens");
-    int64_t heads = 0, ldq = 0, ldo = 0;
-    const void* pq = nullptr;
-    void* po = nullptr;
-    if (q != nullptr) {
-      const at::Tensor& out = *tensor(a[8], "q_out");
-      on_device(&out, c->device, "q_out");
-      if (q->dim() != 3) refuse("q must be [tokens, heads, %d]", c->head_dim);
-      heads = q->size(1);
-      ldq = token_rows(*q, heads, c->head_dim, type, "q");
-      ldo = token_rows(out, heads, c->head_dim, type, "q_out");
-      if (q->size(0) != T || out.size(0) != T) refuse("q, q_out and k must have the same number of tokens");
-      pq = q->data_ptr();
-      po = out.data_ptr();
-    }
-    const float* table = nullptr;
-    const int32_t* positions = nullptr;
-    int64_t rows = 0, rot = 0;
-    if (cos_sin != nullptr) {
-      want_type(*cos_sin, at::kFloat, "cos_sin");
-      if (cos_sin->dim() != 2 || !cos_sin->is_contiguous()) refuse("cos_sin must be a contiguous matrix [positions, channels]");
-      rows = cos_sin->size(0);
-      rot = cos_sin->size(1);
-      table = static_cast<const float*>(cos_sin->data_ptr());
-      positions = static_cast<const int32_t*>(vector(*at, at::kInt, T, "positions"));
-    }
-    const int interleaved = PyObject_IsTrue(a[6]);
-    if (interleaved < 0) throw Refused{};
-    const OnDevice guard(c->device);
-    return tl_kv_append(c, pq, k.data_ptr(), v.data_ptr(), code, fits(T, "k"), fits(heads, "q"), ldq, ldk, ldv, po, ldo, table,
-                        fits(rows, "cos_sin"), fits(rot, "cos_sin"), interleaved, positions,
-                        static_cast<const int64_t*>(vector(slots, at::kLong, T, "slots")), stream_of(a[9], k));
-  });
+  return call("kv_append", n, 10, [&] { return append(a, nullptr, a[9]); });
 }
+
+// kv_append_norm(cache, k, v, positions, slots, cos_sin, interleaved, q, q_out, q_norm, k_norm, eps, stream) -> tl_status
+PyObject* kv_append_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call("kv_append_norm", n, 13, [&] { return append(a, a + 9, a[12]); });
+}
+
 
 // paged_attention(cache, q, pages, lens, scale, window, out, lse, workspace, stream) -> tl_status
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -195,8 +225,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       matrix(*lse, B, heads, "lse");
       pl = static_cast<float*>(lse->data_ptr());
     }
-    const double scale = PyFloat_AsDouble(a[4]);
-    if (scale == -1.0 && PyErr_Occurred()) throw Refused{};
+    const double scale = number(a[4]);
     const int64_t window = integer(a[5]);
     const int tokens = window > INT32_MAX ? 0 : window < 0 ? -1 : static_cast<int>(window);      // wider than any length: all; negative: refused
     const OnDevice guard(c->device);
@@ -204,6 +233,131 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                               fits(width, "pages"), ldp, static_cast<const int32_t*>(vector(lens, at::kInt, B, "lens")),
                               static_cast<float>(scale), tokens, out.data_ptr(), ldo, pl,
                               ws.data_ptr(), ws.nbytes(), stream_of(a[9], q));
+  });
+}
+
+// What the calls on drafted trees share: starts [B + 1], lens [B], pages [B, width], all on one GPU.
+struct Trees {
+  const int32_t *starts, *lens, *pages;
+  int64_t ldp;
+  int B, width;
+  Trees(PyObject* s, PyObject* p, PyObject* l, int device) {
+    const at::Tensor &st = *tensor(s, "starts"), &pg = *tensor(p, "pages"), &ln = *tensor(l, "lens");
+    on_device(&st, device, "starts"), on_device(&pg, device, "pages"), on_device(&ln, device, "lens");
+    B = requests(st);
+    starts = static_cast<const int32_t*>(st.data_ptr());
+    lens = static_cast<const int32_t*>(vector(ln, at::kInt, B, "lens"));
+    want_type(pg, at::kInt, "pages");
+    if (pg.dim() != 2) refuse("pages must be a matrix [requests, max_pages]");
+    width = fits(pg.size(1), "pages");
+    ldp = matrix(pg, B, width, "pages");
+    pages = static_cast<const int32_t*>(pg.data_ptr());
+  }
+  static int requests(const at::Tensor& starts) {
+    if (starts.dim() != 1 || starts.size(0) < 1) refuse("starts must be a vector [requests + 1]");
+    vector(starts, at::kInt, starts.size(0), "starts");
+    return fits(starts.size(0) - 1, "starts");
+  }
+};
+
+// tree_plan(cache, parents, starts, lens, pages, masks, positions, slots, stream) -> tl_status
+PyObject* tree_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call("tree_plan", n, 9, [&] {
+    const auto* c = reinterpret_cast<const Cache*>(static_cast<intptr_t>(integer(a[0])));
+    const at::Tensor &parents = *tensor(a[1], "parents"), &masks = *tensor(a[5], "masks"), &positions = *tensor(a[6], "positions"),
+                     &slots = *tensor(a[7], "slots");
+    on_device(&parents, c->device, "parents"), on_device(&masks, c->device, "masks"), on_device(&positions, c->device, "positions");
+    on_device(&slots, c->device, "slots");
+    const Trees trees(a[2], a[4], a[3], c->device);
+    const int64_t T = parents.dim() == 1 ? parents.size(0) : 0;
+    const void* const up = vector(parents, at::kInt, T, "parents");
+    const OnDevice guard(c->device);
+    return tl_tree_plan(static_cast<const int32_t*>(up), trees.starts, trees.B, fits(T, "parents"), trees.lens, trees.pages, trees.width,
+                        trees.ldp, c->page_size, c->num_pages, static_cast<int64_t*>(const_cast<void*>(vector(masks, at::kLong, T, "masks"))),
+                        static_cast<int32_t*>(const_cast<void*>(vector(positions, at::kInt, T, "positions"))),
+                        static_cast<int64_t*>(const_cast<void*>(vector(slots, at::kLong, T, "slots"))), stream_of(a[8], parents));
+  });
+}
+
+// tree_attention(cache, q, masks, starts, pages, lens, scale, window, sinks, out, lse, workspace, stream) -> tl_status
+PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call("tree_attention", n, 13, [&] {
+    const auto* c = reinterpret_cast<const Cache*>(static_cast<intptr_t>(integer(a[0])));
+    const at::Tensor &q = *tensor(a[1], "q"), &masks = *tensor(a[2], "masks"), &out = *tensor(a[9], "out");
+    const at::Tensor *lse = tensor(a[10], "lse", true), &ws = *tensor(a[11], "workspace");
+    on_device(&q, c->device, "q"), on_device(&masks, c->device, "masks"), on_device(&out, c->device, "out");
+    on_device(lse, c->device, "lse"), on_device(&ws, c->device, "workspace");
+    const Trees trees(a[3], a[4], a[5], c->device);
+    const int code = half_code(q, "q");
+    if (q.dim() != 3) refuse("q must be [tokens, heads, %d]", c->head_dim);
+    const int64_t T = q.size(0), heads = q.size(1);
+    const int64_t ldq = token_rows(q, heads, c->head_dim, q.scalar_type(), "q");
+    const int64_t ldo = token_rows(out, heads, c->head_dim, q.scalar_type(), "out");
+    if (out.size(0) != T) refuse("out and q must have the same number of tokens");
+    float* pl = nullptr;
+    if (lse != nullptr) {
+      want_type(*lse, at::kFloat, "lse");
+      if (!lse->is_contiguous()) refuse("lse must be contiguous");
+      matrix(*lse, T, heads, "lse");
+      pl = static_cast<float*>(lse->data_ptr());
+    }
+    const double scale = number(a[6]);
+    const int64_t window = integer(a[7]), sinks = integer(a[8]);
+    // wider than any length: all (and then no sinks, which lie in it); negative: refused
+    const bool all = window > INT32_MAX;
+    const int tokens = all ? 0 : window < 0 ? -1 : static_cast<int>(window);
+    const int first = sinks < 0 ? -1 : all ? 0 : sinks > INT32_MAX ? INT32_MAX : static_cast<int>(sinks);
+    const OnDevice guard(c->device);
+    return tl_tree_attention(c, q.data_ptr(), code, trees.B, fits(T, "q"), fits(heads, "q"), ldq,
+                             static_cast<const int64_t*>(vector(masks, at::kLong, T, "masks")), trees.starts, trees.pages, trees.width,
+                             trees.ldp, trees.lens, static_cast<float>(scale), tokens, first, out.data_ptr(), ldo, pl, ws.data_ptr(),
+                             ws.nbytes(), stream_of(a[12], q));
+  });
+}
+
+// verify_tree(target, draft, tokens, parents, starts, uniform, path, counts, next, stream) -> tl_status
+PyObject* verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call("verify_tree", n, 10, [&] {
+    const at::Tensor &target = *tensor(a[0], "target"), *draft = tensor(a[1], "draft", true), &tokens = *tensor(a[2], "tokens");
+    const at::Tensor &parents = *tensor(a[3], "parents"), &starts = *tensor(a[4], "starts"), &uniform = *tensor(a[5], "uniform");
+    const at::Tensor &path = *tensor(a[6], "path"), &counts = *tensor(a[7], "counts"), &next = *tensor(a[8], "next");
+    const int device = target.device().index();
+    on_device(draft, device, "draft"), on_device(&tokens, device, "tokens"), on_device(&parents, device, "parents");
+    on_device(&starts, device, "starts"), on_device(&uniform, device, "uniform"), on_device(&path, device, "path");
+    on_device(&counts, device, "counts"), on_device(&next, device, "next");
+    if (target.dim() != 2) refuse("target must be a matrix [tokens, vocabulary]");
+    const int64_t T = target.size(0), vocab = target.size(1);
+    want_type(target, at::kFloat, "target");
+    const int64_t ldt = matrix(target, T, vocab, "target");
+    int64_t ldd = 0;
+    const float* pd = nullptr;
+    if (draft != nullptr) {
+      want_type(*draft, at::kFloat, "draft");
+      ldd = matrix(*draft, T, vocab, "draft");
+      pd = static_cast<const float*>(draft->data_ptr());
+    }
+    const int B = Trees::requests(starts);
+    auto ints = [&](const at::Tensor& t, int64_t size, const char* name) { return static_cast<int32_t*>(const_cast<void*>(vector(t, at::kInt, size, name))); };
+    const OnDevice guard(device);
+    return tl_verify_tree(static_cast<const float*>(target.data_ptr()), ldt, pd, ldd, fits(vocab, "the vocabulary"), ints(tokens, T, "tokens"),
+                          ints(parents, T, "parents"), static_cast<const int32_t*>(starts.data_ptr()), B, fits(T, "target"),
+                          static_cast<const float*>(vector(uniform, at::kFloat, T, "uniform")), ints(path, T, "path"), ints(counts, B, "counts"),
+                          ints(next, B, "next"), stream_of(a[9], target));
+  });
+}
+
+// kv_compact(cache, path, counts, starts, pages, lens, stream) -> tl_status
+PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call("kv_compact", n, 7, [&] {
+    const auto* c = reinterpret_cast<const Cache*>(static_cast<intptr_t>(integer(a[0])));
+    const at::Tensor &path = *tensor(a[1], "path"), &counts = *tensor(a[2], "counts");
+    on_device(&path, c->device, "path"), on_device(&counts, c->device, "counts");
+    const Trees trees(a[3], a[4], a[5], c->device);
+    const int64_t T = path.dim() == 1 ? path.size(0) : 0;
+    const void* const nodes = vector(path, at::kInt, T, "path");
+    const OnDevice guard(c->device);
+    return tl_kv_compact(c, static_cast<const int32_t*>(nodes), static_cast<const int32_t*>(vector(counts, at::kInt, trees.B, "counts")),
+                         trees.starts, trees.B, fits(T, "path"), trees.pages, trees.width, trees.ldp, trees.lens, stream_of(a[6], path));
   });
 }
 
@@ -230,7 +384,9 @@ PyObject* lora_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(kv_append), METHOD(paged_attention), METHOD(lora_apply), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(kv_append),      METHOD(kv_append_norm), METHOD(paged_attention),
+                         METHOD(lora_apply),     METHOD(tree_plan),      METHOD(tree_attention),
+                         METHOD(verify_tree),    METHOD(kv_compact),     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

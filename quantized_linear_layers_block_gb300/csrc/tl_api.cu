@@ -9,6 +9,8 @@
 #include "kv_append.cuh"
 #include "lora.cuh"
 #include "paged_attention.cuh"
+#include "tree.cuh"
+#include "tree_attention.cuh"
 
 namespace {
 
@@ -92,6 +94,24 @@ int check_cache(const tl_kv_cache* c) {
   if (c->page_stride <= 0 || c->head_stride <= 0 || c->token_stride <= 0) return TL_EINVAL;
   if (c->page_stride % step || c->head_stride % step || c->token_stride % step) return TL_EUNSUPPORTED;
   if (c->kv_heads > 1024) return TL_EUNSUPPORTED;
+  return TL_OK;
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// Places of a request's pages; keys and a tile more stay in an int.
+int tree_capacity(int max_pages, int page_size) {
+  const int64_t most = static_cast<int64_t>(max_pages) * page_size, limit = 0x7FFF0000;
+  return static_cast<int>(most < limit ? most : limit);
+}
+
+// What the calls on drafted trees share.
+int check_trees(const int32_t* starts, int B, int T, const int32_t* lens, const int32_t* pages, int max_pages, int64_t ldp) {
+  if (B < 0 || T < 0 || max_pages < 0) return TL_EINVAL;
+  if (B == 0 && T == 0) return TL_OK;
+  if (!starts || !aligned4(starts) || !aligned4(lens) || !aligned4(pages)) return TL_EINVAL;
+  if (B > 0 && (!lens || (max_pages > 0 && !pages))) return TL_EINVAL;
+  if (B > 1 && ldp < max_pages) return TL_EINVAL;
   return TL_OK;
 }
 
@@ -336,11 +356,21 @@ int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const v
                  int T, int q_heads, int64_t ldq, int64_t ldk, int64_t ldv, void* q_out,
                  int64_t ldqo, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
                  const int32_t* positions, const int64_t* slots, void* stream) {
+  return tl_kv_append_norm(cache, q, k, v, dtype, T, q_heads, ldq, ldk, ldv, q_out, ldqo, nullptr, nullptr, 1.f, cos_sin, max_pos,
+                           rot_dim, interleaved, positions, slots, stream);
+}
+
+int tl_kv_append_norm(const tl_kv_cache* cache, const void* q, const void* k, const void* v,
+                      int dtype, int T, int q_heads, int64_t ldq, int64_t ldk, int64_t ldv,
+                      void* q_out, int64_t ldqo, const float* q_norm, const float* k_norm,
+                      float eps, const float* cos_sin, int max_pos, int rot_dim, int interleaved,
+                      const int32_t* positions, const int64_t* slots, void* stream) {
   int r = check_cache(cache);
   if (r != TL_OK) return r;
   if (T < 0 || q_heads < 0 || rot_dim < 0 || max_pos < 0 || (interleaved != 0 && interleaved != 1)) return TL_EINVAL;
   if (dtype != TL_BF16 && dtype != TL_F16) return TL_EINVAL;
   if (cache->dtype != TL_F8E4M3 && cache->dtype != dtype) return TL_EINVAL;
+  if (!(eps > 0.f) || !(eps - eps == 0.f)) return TL_EINVAL;
   const int d = cache->head_dim;
   if (d % 16 != 0 || d > 512 || q_heads > 1024 || rot_dim % 16 != 0 || rot_dim > d) return TL_EUNSUPPORTED;
   if (q == nullptr) q_heads = 0;
@@ -348,7 +378,7 @@ int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const v
   if (!k || !v || !slots || (q_heads > 0 && !q_out)) return TL_EINVAL;
   if (rot_dim > 0 && (!cos_sin || !positions)) return TL_EINVAL;
   if (!aligned16(k) || !aligned16(v) || !aligned16(q) || (q_heads > 0 && !aligned16(q_out)) || !aligned16(cos_sin) ||
-      !aligned4(positions) || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+      !aligned16(q_norm) || !aligned16(k_norm) || !aligned4(positions) || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
     return TL_EINVAL;
   const int64_t wq = static_cast<int64_t>(q_heads) * d, wk = static_cast<int64_t>(cache->kv_heads) * d;
   if ((r = check_rows(ldk, wk, T, 8)) != TL_OK || (r = check_rows(ldv, wk, T, 8)) != TL_OK) return r;
@@ -367,6 +397,7 @@ int tl_kv_append(const tl_kv_cache* cache, const void* q, const void* k, const v
   p.cos_sin = cos_sin, p.positions = positions, p.slots = slots, p.status = status;
   p.q_heads = q_heads, p.kv_heads = cache->kv_heads, p.dim = d, p.page_size = cache->page_size;
   p.rot = rot_dim, p.max_pos = max_pos, p.interleaved = interleaved;
+  p.q_norm = q_heads > 0 ? q_norm : nullptr, p.k_norm = k_norm, p.eps = eps;
   return tl::launch_kv_append(p, T, dtype == TL_BF16, cache->dtype == TL_F8E4M3, sms, as_stream(stream)) == cudaSuccess
              ? TL_OK
              : TL_ECUDA;
@@ -434,6 +465,127 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
                         : cache->dtype == TL_F16 ? tl::launch_attn_f16(p, cache->head_dim, columns, sms, st)
                                                  : tl::launch_attn_f8(p, cache->head_dim, columns, sms, st);
   return e == cudaSuccess ? TL_OK : TL_ECUDA;
+}
+
+int tl_tree_plan(const int32_t* parents, const int32_t* starts, int B, int T, const int32_t* lens,
+                 const int32_t* pages, int max_pages, int64_t ldp, int page_size, int num_pages,
+                 int64_t* masks, int32_t* positions, int64_t* slots, void* stream) {
+  if (B < 0 || T < 0 || page_size <= 0 || num_pages < 0) return TL_EINVAL;
+  int r = check_trees(starts, B, T, lens, pages, max_pages, ldp);
+  if (r != TL_OK || T == 0) return r;
+  if (!parents || !masks || !positions || !slots) return TL_EINVAL;
+  if (!aligned4(parents) || !aligned8(masks) || !aligned4(positions) || !aligned8(slots)) return TL_EINVAL;
+  int* status = nullptr;
+  if ((r = status_ptr(&status)) != TL_OK) return r;
+  const tl::TreePlanParams p{parents, starts, lens, pages, ldp, masks, positions, slots, status, B, T, page_size, num_pages,
+                             tree_capacity(max_pages, page_size)};
+  return tl::launch_tree_plan(p, as_stream(stream)) == cudaSuccess ? TL_OK : TL_ECUDA;
+}
+
+int tl_tree_attention_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim, size_t* bytes) {
+  if (bytes == nullptr || T < 0) return TL_EINVAL;
+  int r = check_attention_shape(B, q_heads, kv_heads, head_dim);
+  if (r != TL_OK) return r;
+  *bytes = 0;
+  if (B == 0 || T == 0) return TL_OK;
+  int sms = 0;
+  if ((r = num_sms(&sms)) != TL_OK) return r;
+  const long long all = static_cast<long long>(sms) * tl::tree_blocks_per_sm(head_dim);
+  const long long grid = all < tl::kTreeMaxGrid ? all : tl::kTreeMaxGrid;
+  *bytes = tl::kTreeMaxGrid * sizeof(tl::TreeCut) + 2 * grid * tl::tree_partial_floats(head_dim) * sizeof(float);
+  return TL_OK;
+}
+
+int tl_tree_attention(const tl_kv_cache* cache, const void* q, int dtype, int B, int T, int q_heads,
+                      int64_t ldq, const int64_t* masks, const int32_t* starts,
+                      const int32_t* pages, int max_pages, int64_t ldp, const int32_t* lens,
+                      float scale, int window, int sinks, void* out, int64_t ldo, float* lse,
+                      void* workspace, size_t ws_bytes, void* stream) {
+  int r = check_cache(cache);
+  if (r != TL_OK) return r;
+  if (T < 0 || window < 0 || sinks < 0 || (window == 0 && sinks != 0) || !(scale - scale == 0.f)) return TL_EINVAL;
+  if (dtype != TL_BF16 && dtype != TL_F16) return TL_EINVAL;
+  if (cache->dtype != TL_F8E4M3 && cache->dtype != dtype) return TL_EINVAL;
+  if ((r = check_attention_shape(B, q_heads, cache->kv_heads, cache->head_dim)) != TL_OK) return r;
+  if (window > 0 && window < TL_TREE_NODES) return TL_EUNSUPPORTED;
+  if ((r = check_trees(starts, B, T, lens, pages, max_pages, ldp)) != TL_OK || T == 0 || B == 0) return r;
+  if (!q || !out || !masks || !workspace) return TL_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned8(masks) || !aligned4(lse)) return TL_EINVAL;
+  const int64_t wq = static_cast<int64_t>(q_heads) * cache->head_dim;
+  if ((r = check_rows(ldq, wq, T, 8)) != TL_OK || (r = check_rows(ldo, wq, T, 8)) != TL_OK) return r;
+  size_t need = 0;
+  if ((r = tl_tree_attention_workspace_size(B, T, q_heads, cache->kv_heads, cache->head_dim, &need)) != TL_OK) return r;
+  if (ws_bytes < need) return TL_ENOSPACE;
+  int sms = 0;
+  int* status = nullptr;
+  if ((r = num_sms(&sms)) != TL_OK || (r = status_ptr(&status)) != TL_OK) return r;
+  const int bytes = cache->dtype == TL_F8E4M3 ? 1 : 2;
+  tl::TreeAttnParams p{};
+  p.k = static_cast<const uint8_t*>(cache->k), p.v = static_cast<const uint8_t*>(cache->v);
+  p.k_scale = cache->k_scale, p.v_scale = cache->v_scale;
+  p.page_stride = cache->page_stride * bytes, p.head_stride = cache->head_stride * bytes, p.token_stride = cache->token_stride * bytes;
+  p.num_pages = cache->num_pages;
+  p.page = tl::FastDiv::make(static_cast<uint32_t>(cache->page_size));
+  p.group = q_heads / cache->kv_heads;
+  p.group_div = tl::FastDiv::make(static_cast<uint32_t>(p.group));
+  p.q = static_cast<const uint16_t*>(q), p.out = static_cast<uint16_t*>(out), p.ldq = ldq, p.ldo = ldo;
+  p.masks = masks, p.starts = starts, p.lens = lens, p.pages = pages, p.ldp = ldp, p.lse = lse;
+  p.scale_log2 = scale * tl::kLog2e;
+  p.B = B, p.T = T, p.q_heads = q_heads, p.kv_heads = cache->kv_heads, p.window = window, p.sinks = sinks;
+  p.q_bf16 = dtype == TL_BF16;
+  p.capacity = tree_capacity(max_pages, cache->page_size);
+  p.cuts = static_cast<tl::TreeCut*>(workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + tl::kTreeMaxGrid * sizeof(tl::TreeCut));
+  p.status = status;
+  const cudaStream_t st = as_stream(stream);
+  const cudaError_t e = cache->dtype == TL_BF16  ? tl::launch_tree_attn_bf16(p, cache->head_dim, sms, st)
+                        : cache->dtype == TL_F16 ? tl::launch_tree_attn_f16(p, cache->head_dim, sms, st)
+                                                 : tl::launch_tree_attn_f8(p, cache->head_dim, sms, st);
+  return e == cudaSuccess ? TL_OK : TL_ECUDA;
+}
+
+int tl_verify_tree(const float* target, int64_t ldt, const float* draft, int64_t ldd, int vocab,
+                   const int32_t* tokens, const int32_t* parents, const int32_t* starts, int B,
+                   int T, const float* uniform, int32_t* path, int32_t* counts, int32_t* next,
+                   void* stream) {
+  if (B < 0 || T < 0 || vocab <= 0) return TL_EINVAL;
+  if (vocab > (1 << 24)) return TL_EUNSUPPORTED;
+  if (B == 0) return TL_OK;
+  if (!starts || !counts || !next || (T > 0 && (!target || !tokens || !parents || !uniform || !path))) return TL_EINVAL;
+  for (const void* x : {static_cast<const void*>(target), static_cast<const void*>(draft), static_cast<const void*>(tokens),
+                        static_cast<const void*>(parents), static_cast<const void*>(starts), static_cast<const void*>(uniform),
+                        static_cast<const void*>(path), static_cast<const void*>(counts), static_cast<const void*>(next)})
+    if (!aligned4(x)) return TL_EINVAL;
+  int r;
+  if ((r = check_rows(ldt, vocab, T, 1)) != TL_OK || (draft != nullptr && (r = check_rows(ldd, vocab, T, 1)) != TL_OK)) return r;
+  int sms = 0;
+  int* status = nullptr;
+  if ((r = num_sms(&sms)) != TL_OK || (r = status_ptr(&status)) != TL_OK) return r;
+  const tl::VerifyParams p{target, draft, ldt, ldd, tokens, parents, starts, uniform, path, counts, next, status, vocab, B, T};
+  return tl::launch_verify_tree(p, sms, as_stream(stream)) == cudaSuccess ? TL_OK : TL_ECUDA;
+}
+
+int tl_kv_compact(const tl_kv_cache* cache, const int32_t* path, const int32_t* counts,
+                  const int32_t* starts, int B, int T, const int32_t* pages, int max_pages,
+                  int64_t ldp, const int32_t* lens, void* stream) {
+  int r = check_cache(cache);
+  if (r != TL_OK) return r;
+  if (T < 0) return TL_EINVAL;
+  const int d = cache->head_dim;
+  if (d % 16 != 0 || d > 512) return TL_EUNSUPPORTED;
+  if ((r = check_trees(starts, B, T, lens, pages, max_pages, ldp)) != TL_OK || B == 0 || T == 0) return r;
+  if (!path || !counts || !aligned4(path) || !aligned4(counts)) return TL_EINVAL;
+  int* status = nullptr;
+  if ((r = status_ptr(&status)) != TL_OK) return r;
+  const int bytes = cache->dtype == TL_F8E4M3 ? 1 : 2;
+  tl::CompactParams p{};
+  p.k = static_cast<uint8_t*>(cache->k), p.v = static_cast<uint8_t*>(cache->v);
+  p.page_stride = cache->page_stride * bytes, p.head_stride = cache->head_stride * bytes, p.token_stride = cache->token_stride * bytes;
+  p.path = path, p.counts = counts, p.starts = starts, p.lens = lens, p.pages = pages, p.ldp = ldp, p.status = status;
+  p.B = B, p.T = T, p.page_size = cache->page_size, p.num_pages = cache->num_pages;
+  p.capacity = tree_capacity(max_pages, cache->page_size);
+  p.kv_heads = cache->kv_heads, p.row = d * bytes / 16;
+  return tl::launch_kv_compact(p, as_stream(stream)) == cudaSuccess ? TL_OK : TL_ECUDA;
 }
 
 int tl_lora_plan_size(int M, int n_adapters, size_t* bytes) {

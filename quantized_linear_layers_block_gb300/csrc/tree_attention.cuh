@@ -1,0 +1,893 @@
+// Attention of the nodes of drafted trees over a paged key-value cache.
+//
+//   out[t,h] = sum_j p_j V_j / sum_j p_j,   p_j = exp(scale q[t,h] . K_j)
+//
+// over a request's cached tokens and the nodes of t's mask. All nodes of a request read the same keys, and G = q_heads /
+// kv_heads query heads share a key-value head: n G rows use each cached byte, 2 n G flops a 16-bit element. At 8 nodes and
+// 6 heads that is 48 rows, which mma.sync could just feed; at 26 nodes it could not, so the products run on tcgen05, with 128 rows
+// (node, head) to a tile: S = Q K^T and O += P V with S, P and O in tensor memory. Up to 128 rows HBM bounds, above it the MMAs.
+//
+// Work. A (request, key-value head, 128 rows) is a segment; its keys are cut into tiles of 64 and the tiles of all segments form
+// one list, cut into equal shares for the blocks of one resident wave, so that ragged lengths need no plan from the host.
+// A segment inside one block's share is finished there; one that is cut leaves partial (m, l, o) in the workspace, and a second small
+// kernel joins them, in block order.
+//
+// Warps. Four (a thread to a row) turn S into P and write results; one issues the MMAs; four load keys and values. Tiles go through a ring
+// of slots in the order in which the MMAs take them: K0, K1, V0, K2, V1, ...
+//
+// Softmax. One pass with a running maximum m, sum l and output o; o is rescaled only where m grows by more than 2^8 (bf16) or
+// 2^3 (f16): p just has to stay in range. Probabilities enter the second product as two 16-bit parts (16 bits for bf16, 22
+// for f16): one part would add an error as large as the output's own rounding. Both parts are at least the least
+// positive number, so that an infinite value makes its channel infinite instead of NaN.
+//
+// Masks. A key that only some rows see meets the others with p = 0, and 0 V is NaN where V is not finite. So in tiles that not
+// every row sees whole (the nodes, the edge of a window) such values are taken out when they are loaded, and added
+// at the end to the rows that see them.
+#pragma once
+
+#include "paged_attention.cuh"
+#include "tree.cuh"
+
+namespace tl {
+
+struct TreeAttnParams {
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t page_stride, head_stride, token_stride;     // bytes
+  int num_pages;
+  FastDiv page, group_div;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t ldq, ldo;
+  const int64_t* masks;
+  const int32_t* starts;
+  const int32_t* lens;
+  const int32_t* pages;
+  int64_t ldp;
+  float* lse;
+  float scale_log2;
+  int B, T, q_heads, kv_heads, group, window, sinks, q_bf16, capacity;
+  int grid;                                           // blocks of the first kernel
+  float* partials;                                    // two per block
+  struct TreeCut* cuts;                               // one per block
+  int* status;
+};
+
+// A segment that is cut, noted by the block in whose share it begins; parts = 0: none.
+struct TreeCut {
+  int parts, row0, kvh, first_row, rows;              // row0: the request's first node; first_row: of its rows (node, head)
+  float v_scale;
+};
+
+constexpr int kTreeRows = 128;
+constexpr int kTreeMaxGrid = 2048;
+
+__host__ __device__ constexpr size_t tree_partial_floats(int dim) { return static_cast<size_t>(kTreeRows) * (dim + 2); }
+
+cudaError_t launch_tree_attn_bf16(TreeAttnParams p, int dim, int sms, cudaStream_t st);
+cudaError_t launch_tree_attn_f16(TreeAttnParams p, int dim, int sms, cudaStream_t st);
+cudaError_t launch_tree_attn_f8(TreeAttnParams p, int dim, int sms, cudaStream_t st);
+
+// Blocks of the first kernel on an SM, by head_dim: tensor memory and shared memory for two up to 128 channels.
+__host__ __device__ constexpr int tree_blocks_per_sm(int dim) { return dim == 256 ? 1 : 2; }
+
+namespace tree {
+
+using attn::above_zero;
+using attn::cp_async16;
+using attn::cp_async_commit;
+using attn::cp_async_wait;
+using attn::exp2_approx;
+using attn::faded;
+using attn::pack2;
+using attn::pack2_down;
+using attn::unpack2;
+using attn::widen_hi;
+using attn::widen_lo;
+
+constexpr int kKeys = 64;                // keys of a tile
+constexpr int kSegmentCost = 2;          // what a segment costs besides its tiles, in tiles
+constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5, kLoadWarps = 4;
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kAhead = 8;                // pieces: more than the loading warps can be ahead of the others, or of each other
+
+template <int CACHE, int D>
+struct Traits {
+  static constexpr bool F8 = CACHE == kCacheF8, BF16 = CACHE == kCacheBf16;
+  static constexpr int ROW = D * (F8 ? 1 : 2);                   // bytes of a cached row
+  static constexpr int BLOCKS = tree_blocks_per_sm(D);
+  static constexpr int Q = kTreeRows * D * 2, SLOT = kKeys * D * 2, STAGE = F8 ? SLOT / 2 : 0;
+  static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 12) : F8 ? 3 : 5;
+  static constexpr int STAGES = F8 ? (D == 64 ? 12 : 4) : 0;     // of 8-bit rows on their way
+  static constexpr int LAG = F8 ? STAGES - 1 : D == 64 ? 8 : 3;  // loads in flight
+  static constexpr int OFF_SLOT = Q, OFF_STAGE = OFF_SLOT + SLOTS * SLOT, OFF_MISC = OFF_STAGE + STAGES * STAGE;
+  static constexpr int SMEM = OFF_MISC + 1024;
+  static constexpr int SBUF = D == 128 ? 2 : 3;                  // buffers of S and P
+  static constexpr int TMEM = D == 256 ? 512 : 256, TMEM_S = D;  // columns; O in the first D
+  static constexpr float POFF = BF16 ? 0.f : 12.f;               // p is kept 2^POFF as large (f16: away from the subnormals)
+  static constexpr float SLACK = BF16 ? 8.f : 3.f;               // by how much m may lag behind the maximum
+};
+static_assert(Traits<kCacheBf16, 256>::SMEM <= 232448 && Traits<kCacheF8, 256>::SMEM <= 232448, "one block");
+static_assert(Traits<kCacheBf16, 128>::SMEM <= 115712 && Traits<kCacheF8, 128>::SMEM <= 115712 && Traits<kCacheBf16, 64>::SMEM <= 115712 &&
+                  Traits<kCacheF8, 64>::SMEM <= 115712, "two blocks");
+// a piece takes two slots at least
+static_assert(Traits<kCacheBf16, 64>::SLOTS / 2 + 1 < kAhead, "ahead");
+static_assert(Traits<kCacheBf16, 128>::TMEM_S + 2 * kKeys <= 256 && Traits<kCacheBf16, 256>::TMEM_S + 3 * kKeys <= 512, "tensor memory");
+
+// The small things behind the slots.
+template <class T>
+struct Misc {
+  uint64_t full[T::SLOTS], empty[T::SLOTS];            // a slot holds its rows; its MMAs are done
+  uint64_t s_full[T::SBUF], p_full[T::SBUF], pv_done[T::SBUF];
+  uint64_t q_full;                                     // a piece's queries are in place
+  uint64_t loaded[kAhead];                             // a piece's last rows are, and flag says what was found in them
+  int flag[kAhead];                                    // piece + 1 where values were taken out
+  uint32_t tmem;
+  int abort;
+};
+
+// ---- PTX
+// D[tmem] (+)= A[smem] B[smem]^T and A[tmem] B[smem]^T, 16 channels or keys
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  mma_f16_ts(d, a, b, idesc, accumulate);
+}
+// A 64-channel column block of 128-byte rows, 128-byte swizzle; the operand's other dimension is along the rows (K-major: next 8
+// rows at 1024 bytes), or the summed one is (MN-major: next 8 rows at 1024 bytes, the next 64 channels at `block` bytes).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t block) {
+  uint64_t d = smem_desc_sw128(saddr);
+  d &= ~(static_cast<uint64_t>(0x3FFF) << 16);
+  return d | static_cast<uint64_t>(block >> 4) << 16;
+}
+template <bool BF16>
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn_major) {
+  return idesc_f16_f32(kTreeRows, n) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u);
+}
+
+// byte offset of 16-byte unit u (of 8) of row r in a 64-channel block
+__device__ __forceinline__ uint32_t swizzled(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
+
+// bits 0 .. n - 1
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// All lanes of a warp wait for a phase, and know alike whether it came.
+__device__ __forceinline__ bool wait_all(uint64_t& bar, uint32_t parity, int* abort, int* status) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity & 1, abort));
+  if (!ok) {
+    set_status(status, TL_ETIMEOUT);
+    *const_cast<volatile int*>(abort) = 1;
+  }
+  return ok;
+}
+
+// 32 columns of this warp's lanes, there when it returns (the registers pass through the wait, so that no use of them comes before it).
+__device__ __forceinline__ void read_tmem(uint32_t addr, uint32_t (&v)[32]) {
+  tmem_ld_32x32b_x32(addr, v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]),
+                 "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
+                 "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
+                 "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+}
+
+// ---- the list of work: every warp goes through its block's share by itself
+struct Request {
+  int n, row0, len, first, sinks, sink_tiles, tiles, row_blocks;
+  __device__ __forceinline__ int places(const TreeAttnParams& p) const { return row_blocks == 0 ? 0 : tiles + kSegmentCost; }
+};
+
+__device__ __forceinline__ Request request(const TreeAttnParams& p, int b, bool& bad) {
+  Request r;
+  const bool ok = tree_rows(p.starts, b, p.T, r.row0, r.n);
+  r.len = __ldg(p.lens + b);
+  if (!ok || r.len < 0 || r.len > p.capacity - r.n) {
+    bad = true;
+    r.n = r.len = 0;
+  }
+  r.first = p.window > 0 ? max(0, r.len - p.window) : 0;      // the first key that any row's window reaches
+  r.sinks = min(p.sinks, r.first);
+  r.sink_tiles = (r.sinks + kKeys - 1) / kKeys;
+  r.tiles = r.sink_tiles + (r.len + r.n - r.first + kKeys - 1) / kKeys;
+  r.row_blocks = (r.n * p.group + kTreeRows - 1) / kTreeRows;
+  return r;
+}
+
+struct Piece {              // tiles begin .. end - 1 of a segment
+  int kvh, row_block, begin, end;
+  bool whole, starts_here;
+  int second, parts;        // which of the block's partials; blocks that share the segment
+};
+
+struct Walk {
+  Request r;
+  int b, seg, segs;         // request, segment of it, its segments
+  long long at, share, t1;  // place where the segment begins; places of a share; where this block's share ends
+  long long t0;
+  bool more;
+
+  // All lanes of a warp together.
+  __device__ __forceinline__ void init(const TreeAttnParams& p, bool report) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0;
+    bool bad = false;
+    for (int base = 0; base < p.B; base += 32) {
+      if (base + lane < p.B) {
+        const Request x = request(p, base + lane, bad);
+        total += static_cast<long long>(p.kv_heads) * x.row_blocks * x.places(p);
+      }
+    }
+    if (report && bad) set_status(p.status, TL_EDATA);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    share = attn::divide(total + p.grid - 1, p.grid);
+    t0 = share * blockIdx.x;
+    t1 = min(t0 + share, total);
+    more = t0 < total;
+    if (!more) return;
+    long long run = 0;
+    for (int base = 0;; base += 32) {
+      long long places = 0;
+      if (base + lane < p.B) {
+        const Request x = request(p, base + lane, bad);
+        places = static_cast<long long>(p.kv_heads) * x.row_blocks * x.places(p);
+      }
+      long long incl = places;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, t0 < run + incl);
+      if (who != 0) {
+        const int l = __ffs(who) - 1;
+        b = base + l;
+        at = run + __shfl_sync(0xffffffffu, incl - places, l);
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    r = request(p, b, bad);
+    segs = p.kv_heads * r.row_blocks;
+    seg = static_cast<int>(attn::divide(t0 - at, r.places(p)));
+    at += static_cast<long long>(seg) * r.places(p);
+  }
+
+  // The next piece with tiles in it; false at the end of the share.
+  __device__ __forceinline__ bool next(const TreeAttnParams& p, Piece& x) {
+    while (more) {
+      if (at >= t1) {
+        more = false;
+        break;
+      }
+      if (seg == segs) {
+        bool bad = false;
+        r = request(p, ++b, bad);
+        seg = 0;
+        segs = p.kv_heads * r.row_blocks;
+        continue;
+      }
+      const long long from = max(t0 - at, 0ll) - kSegmentCost, to = min(t1 - at, static_cast<long long>(r.places(p))) - kSegmentCost;
+      x.begin = static_cast<int>(max(from, 0ll));
+      x.end = static_cast<int>(max(to, 0ll));
+      x.kvh = seg / r.row_blocks;
+      x.row_block = seg - x.kvh * r.row_blocks;
+      x.whole = x.begin == 0 && x.end == r.tiles;
+      x.starts_here = x.begin == 0;
+      x.second = x.starts_here;
+      x.parts = 1;
+      if (!x.whole && x.starts_here)
+        x.parts = static_cast<int>(attn::divide(at + kSegmentCost + r.tiles - 1, share)) - static_cast<int>(blockIdx.x) + 1;
+      ++seg;
+      at += r.places(p);
+      if (x.end > x.begin) return true;
+    }
+    return false;
+  }
+};
+
+// A tile of a request: its first key, one past its last, and whether all rows see all of its 64 keys.
+struct Tile {
+  int k0, end;
+  bool sink, plain;
+};
+
+__device__ __forceinline__ Tile tile(const TreeAttnParams& p, const Request& r, int i) {
+  Tile t;
+  t.sink = i < r.sink_tiles;
+  t.k0 = t.sink ? i * kKeys : r.first + (i - r.sink_tiles) * kKeys;
+  t.end = min(t.k0 + kKeys, t.sink ? r.sinks : r.len + r.n);
+  // a row's window holds up to TL_TREE_NODES nodes of its own and so many cached keys fewer
+  t.plain = t.sink ? t.end - t.k0 == kKeys
+                   : t.k0 + kKeys <= r.len && (p.window == 0 || t.k0 >= r.len - p.window + TL_TREE_NODES);
+  return t;
+}
+
+// Which of a tile's keys the row with this mask sees.
+__device__ __forceinline__ uint64_t visible(const TreeAttnParams& p, const Request& r, const Tile& t, uint64_t mask) {
+  if (t.sink) return low_bits(t.end - t.k0);
+  const int first = p.window > 0 ? max(0, r.len - max(0, p.window - __popcll(mask))) : 0;
+  const int nodes = r.len - t.k0;                     // where the nodes begin
+  const uint64_t cached = low_bits(nodes) & (~low_bits(first - t.k0) | low_bits(p.sinks - t.k0));
+  const uint64_t drafted = nodes >= 64 ? 0 : nodes >= 0 ? mask << nodes : nodes > -64 ? mask >> -nodes : 0;
+  return cached | drafted;
+}
+
+// ---- the loading warps: rows of K and V into the ring's slots
+template <int CACHE, int D>
+struct Loader {
+  using T = Traits<CACHE, D>;
+  static constexpr int CPR = T::ROW / 16;               // 16-byte chunks of a cached row
+  static constexpr int RPI = 32 / CPR;                  // rows that one instruction of a warp copies
+  static constexpr int ROWS = kKeys / kLoadWarps;       // of a warp
+  static constexpr int STEPS = ROWS / RPI;
+
+  const TreeAttnParams& p;
+  uint8_t* smem;
+  Misc<T>* misc;
+  int warp, lane;                                       // of the loading warps
+  uint32_t issued = 0, done = 0;                        // loads
+  uint32_t checks = 0, ends = 0;                        // of the loads in flight, the last in bit 0: look for what is not finite; a piece's last
+  int pieces = 0;                                       // whose loads are done
+  bool ok = true;
+
+  __device__ __forceinline__ uint32_t slot(uint32_t i) const { return smem_u32(smem) + T::OFF_SLOT + i % T::SLOTS * T::SLOT; }
+
+  // Byte offset in the cache of the row of this lane (of the first 16), or -1.
+  __device__ __forceinline__ int page_of(const Walk& w, const Tile& t) const {
+    const int key = t.k0 + warp * ROWS + lane;
+    return lane < ROWS && key < t.end ? __ldg(p.pages + w.b * p.ldp + p.page.div(key)) : -1;
+  }
+  __device__ __forceinline__ int64_t row_of(const Piece& x, const Tile& t, int page) const {
+    const int key = t.k0 + warp * ROWS + lane;
+    if (lane >= ROWS || key >= t.end) return -1;
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
+      set_status(p.status, TL_EDATA);
+      return -1;
+    }
+    return page * p.page_stride + x.kvh * p.head_stride + static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
+  }
+
+  __device__ __forceinline__ void wait_empty(uint32_t i) {
+    if (i >= T::SLOTS) ok = wait_all(misc->empty[i % T::SLOTS], i / T::SLOTS - 1, &misc->abort, p.status);
+  }
+
+  __device__ __forceinline__ void load(const uint8_t* base, int64_t off, bool check, bool last) {
+    if (!T::F8) {
+      wait_empty(issued);
+      if (!ok) return;
+    }
+    const int row = lane / CPR, chunk = lane % CPR;
+    const uint32_t to = T::F8 ? smem_u32(smem) + T::OFF_STAGE + issued % (T::F8 ? T::STAGES : 1) * T::STAGE + (warp * 32 + lane) * 16 : slot(issued);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = i * RPI + row, kk = warp * ROWS + r;
+      const int64_t o = __shfl_sync(0xffffffffu, off, r);
+      const uint32_t dst = T::F8 ? to + i * (kLoadWarps * 32 * 16) : to + chunk / 8 * (kKeys * 128) + swizzled(kk, chunk % 8);
+      cp_async16(dst, base + (o < 0 ? 0 : o) + chunk * 16, o < 0 ? 0u : 16u);
+    }
+    cp_async_commit();
+    ++issued;
+    checks = checks << 1 | check;
+    ends = ends << 1 | last;
+    if (issued - done > T::LAG) {
+      cp_async_wait<T::LAG>();
+      hand_over(T::LAG);
+    }
+  }
+
+  // The oldest load in flight, `age` loads ago, has landed: the rows go to the MMAs.
+  __device__ __forceinline__ void hand_over(int age) {
+    const bool check = checks >> age & 1;
+    bool found = false;
+    const int row = lane / CPR, chunk = lane % CPR;
+    if constexpr (T::F8) {
+      wait_empty(done);
+      if (!ok) return;
+      const uint8_t* from = smem + T::OFF_STAGE + done % T::STAGES * T::STAGE + (warp * 32 + lane) * 16;
+      uint8_t* to = smem + T::OFF_SLOT + done % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const int kk = warp * ROWS + i * RPI + row;
+        uint4 x = *reinterpret_cast<const uint4*>(from + i * (kLoadWarps * 32 * 16));
+        if (check) {                                    // e4m3 has NaN (0x7F, 0xFF), no infinities
+          uint32_t* const w = &x.x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t nan = __vcmpeq4(w[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            found |= nan != 0;
+            w[j] &= ~nan;
+          }
+        }
+        const uint4 a = make_uint4(widen_lo(x.x), widen_hi(x.x), widen_lo(x.y), widen_hi(x.y));
+        const uint4 b = make_uint4(widen_lo(x.z), widen_hi(x.z), widen_lo(x.w), widen_hi(x.w));
+        *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2)) = a;
+        *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2 + 1)) = b;
+      }
+    } else if (check) {
+      constexpr uint32_t E = T::BF16 ? 0x7F80u : 0x7C00u;
+      uint8_t* to = smem + T::OFF_SLOT + done % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        uint4* const at = reinterpret_cast<uint4*>(to + swizzled(warp * ROWS + i * RPI + row, chunk % 8));
+        uint4 x = *at;
+        uint32_t* const w = &x.x;
+        uint32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t odd = __vcmpeq2(w[j] & (E * 0x10001u), E * 0x10001u);
+          any |= odd;
+          w[j] &= ~odd;
+        }
+        if (any != 0) *at = x, found = true;
+      }
+    }
+    if (found) *const_cast<volatile int*>(&misc->flag[pieces % kAhead]) = pieces + 1;
+    fence_proxy_async_smem();
+    mbar_arrive(smem_u32(&misc->full[done % T::SLOTS]));
+    if (ends >> age & 1) {
+      mbar_arrive(smem_u32(&misc->loaded[pieces % kAhead]));
+      ++pieces;
+    }
+    ++done;
+  }
+
+  __device__ __forceinline__ void run() {
+    Walk w;
+    w.init(p, false);
+    Piece x;
+    while (ok && w.next(p, x)) {
+      Tile t = tile(p, w.r, x.begin);
+      int64_t off = row_of(x, t, page_of(w, t));
+      Tile t2 = t;
+      int page2 = -1;
+      if (x.begin + 1 < x.end) {
+        t2 = tile(p, w.r, x.begin + 1);
+        page2 = page_of(w, t2);
+      }
+      load(p.k, off, false, false);
+      for (int i = x.begin; ok && i < x.end; ++i) {
+        int64_t off2 = -1;
+        const Tile now = t2;
+        if (i + 1 < x.end) {
+          off2 = row_of(x, now, page2);
+          if (i + 2 < x.end) {
+            t2 = tile(p, w.r, i + 2);
+            page2 = page_of(w, t2);
+          }
+          load(p.k, off2, false, false);
+          if (!ok) break;
+        }
+        load(p.v, off, !t.plain, i + 1 == x.end);
+        t = now;
+        off = off2;
+      }
+    }
+    cp_async_wait<0>();
+    while (ok && done != issued) hand_over(static_cast<int>(issued - done) - 1);
+  }
+};
+
+// ---- the MMA warp
+template <int CACHE, int D>
+__device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* smem, Misc<Traits<CACHE, D>>* misc) {
+  using T = Traits<CACHE, D>;
+  constexpr uint32_t ID_S = idesc<T::BF16>(kKeys, false), ID_O = idesc<T::BF16>(D, true);
+  Walk w;
+  w.init(p, false);
+  Piece x;
+  const bool elected = (threadIdx.x & 31) == 0;
+  const uint32_t base = smem_u32(smem), tm = misc->tmem;
+  uint32_t loads = 0, tiles = 0, pieces = 0;
+  bool ok = true;
+  auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); };
+  auto scores = [&](uint32_t t) {                       // S of tile t
+    const uint32_t buf = t % T::SBUF, s = loads % T::SLOTS;
+    if (t >= T::SBUF && !wait(misc->pv_done[buf], t / T::SBUF - 1)) return;
+    if (!wait(misc->full[s], loads / T::SLOTS)) return;
+    tc_fence_after();
+    if (elected) {
+      const uint32_t kb = base + T::OFF_SLOT + s * T::SLOT;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t off = (i % 4) * 32;
+        mma_ss(tm + T::TMEM_S + buf * kKeys, smem_desc_sw128(base + i / 4 * (kTreeRows * 128) + off), smem_desc_sw128(kb + i / 4 * (kKeys * 128) + off),
+               ID_S, i > 0);
+      }
+      tc_commit(smem_u32(&misc->empty[s]));
+      tc_commit(smem_u32(&misc->s_full[buf]));
+    }
+    __syncwarp();
+    ++loads;
+  };
+  while (ok && w.next(p, x)) {
+    if (!wait(misc->q_full, pieces)) break;
+    tc_fence_after();
+    scores(tiles);
+    for (int i = x.begin; ok && i < x.end; ++i) {
+      if (i + 1 < x.end) scores(tiles + 1);
+      const uint32_t buf = tiles % T::SBUF, s = loads % T::SLOTS;
+      if (!wait(misc->p_full[buf], tiles / T::SBUF) || !wait(misc->full[s], loads / T::SLOTS)) break;
+      tc_fence_after();
+      if (elected) {
+        const uint32_t vb = base + T::OFF_SLOT + s * T::SLOT, pb = tm + T::TMEM_S + buf * kKeys;
+#pragma unroll
+        for (int j = 0; j < kKeys / 16; ++j) {
+          const uint64_t b = desc_mn(vb + j * 2048, kKeys * 128);
+          mma_ts(tm, pb + 16 * j, b, ID_O, i > x.begin || j > 0);        // high part
+          mma_ts(tm, pb + 16 * j + 8, b, ID_O, 1);                       // low part
+        }
+        tc_commit(smem_u32(&misc->empty[s]));
+        tc_commit(smem_u32(&misc->pv_done[buf]));
+      }
+      __syncwarp();
+      ++loads;
+      ++tiles;
+    }
+    ++pieces;
+  }
+}
+
+// ---- the softmax warps: thread = row
+template <int CACHE, int D>
+struct Softmax {
+  using T = Traits<CACHE, D>;
+  const TreeAttnParams& p;
+  uint8_t* smem;
+  Misc<T>* misc;
+  int warp, lane;
+  bool ok = true;
+
+  __device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); }
+
+  // This row's query into shared memory as the MMA's operand; returns by what its scores are scaled (8-bit caches: its power of two).
+  __device__ __forceinline__ float put_query(const uint16_t* row) {
+    const int r = warp * 32 + lane;
+    float up = 1.f, down = 1.f;
+    const bool turn = T::F8 && p.q_bf16;
+    if (turn) {
+      float top = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row) + i);
+        const uint32_t* const w = &x.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = unpack2<true>(w[j]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      // 2^e <= top < 2^(e + 1); e is kept where both 2^e and 2^-e are normal (an infinite or NaN q stays one)
+      const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
+      up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+      down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+#pragma unroll 8
+    for (int i = 0; i < D / 8; ++i) {
+      uint4 x = __ldg(reinterpret_cast<const uint4*>(row) + i);
+      if (turn) {
+        uint32_t* const w = &x.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = unpack2<true>(w[j]);
+          w[j] = pack2<false>(f.x * down, f.y * down);
+        }
+      }
+      *reinterpret_cast<uint4*>(smem + i / 8 * (kTreeRows * 128) + swizzled(r, i % 8)) = x;
+    }
+    return up;
+  }
+
+  // Adds to 32 channels of the row, from d on, the values that were taken out and that it sees.
+  __device__ __noinline__ void add_odd(float (&o)[32], int d, const Walk& w, const Piece& x, uint64_t mask) const {
+    for (int i = x.begin; i < x.end; ++i) {
+      const Tile t = tile(p, w.r, i);
+      if (t.plain) continue;
+      uint64_t sees = visible(p, w.r, t, mask) & low_bits(t.end - t.k0);
+      while (sees != 0) {
+        const int key = t.k0 + __ffsll(static_cast<long long>(sees)) - 1;
+        sees &= sees - 1;
+        const int at = p.page.div(key), page = __ldg(p.pages + w.b * p.ldp + at);
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;
+        const uint8_t* row = p.v + page * p.page_stride + x.kvh * p.head_stride + static_cast<int64_t>(key - at * p.page.d) * p.token_stride;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float v;
+          if constexpr (T::F8) {
+            v = (row[d + c] & 0x7F) == 0x7F ? NAN : 0.f;
+          } else {
+            const uint32_t bits = reinterpret_cast<const uint16_t*>(row)[d + c];
+            v = unpack2<T::BF16>(bits).x;
+          }
+          if (!(fabsf(v) < INFINITY)) o[c] += v;
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void run() {
+    Walk w;
+    w.init(p, blockIdx.x == 0 && warp == 0);
+    Piece x;
+    uint32_t tiles = 0, pieces = 0;
+    TreeCut cut{};
+    const uint32_t mine = misc->tmem + (static_cast<uint32_t>(warp) << 21);      // this warp's 32 lanes
+    while (ok && w.next(p, x)) {
+      const int first_row = x.row_block * kTreeRows, rows = min(kTreeRows, w.r.n * p.group - first_row);
+      const int mr = warp * 32 + lane;
+      const bool busy = warp * 32 < rows, live = mr < rows;
+      const int gr = first_row + (live ? mr : 0), node = static_cast<int>(p.group_div.div(gr)), head = x.kvh * p.group + gr - node * p.group;
+      const int64_t token = static_cast<int64_t>(w.r.row0) + node;
+      uint64_t mask = 0;
+      float sc = p.scale_log2, vs = 1.f;
+      if constexpr (T::F8) {
+        sc *= __ldg(p.k_scale + x.kvh);
+        vs = __ldg(p.v_scale + x.kvh);
+      }
+      if (live) {
+        mask = static_cast<uint64_t>(__ldg(p.masks + token)) & low_bits(w.r.n);
+        sc *= put_query(p.q + token * p.ldq + static_cast<int64_t>(head) * D);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&misc->q_full));
+      float m = -INFINITY, l = 0.f;
+      for (int i = x.begin; i < x.end; ++i, ++tiles) {
+        const uint32_t buf = tiles % T::SBUF;
+        if (!wait(misc->s_full[buf], tiles / T::SBUF)) break;
+        if (busy) {
+          tc_fence_after();
+          const uint32_t sb = mine + T::TMEM_S + buf * kKeys;
+          const Tile t = tile(p, w.r, i);
+          const uint64_t sees = t.plain ? ~0ull : visible(p, w.r, t, mask);
+          float top = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s[32];
+            read_tmem(sb + 32 * h, s);
+            const uint32_t bits = static_cast<uint32_t>(sees >> (32 * h));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float f = __uint_as_float(s[c]) * sc;
+              top = fmaxf(top, t.plain || (bits >> c & 1) ? f : -INFINITY);
+            }
+          }
+          const bool grown = top > m + T::SLACK || (m == -INFINITY && top > m);
+          if (i == x.begin) {
+            m = top;
+          } else if (__any_sync(0xffffffffu, grown)) {
+            // the MMAs of the tile before add to o until they are done
+            if (!wait(misc->pv_done[(tiles - 1) % T::SBUF], (tiles - 1) / T::SBUF)) break;
+            tc_fence_after();
+            const float f = grown ? faded(m - top) : 1.f;
+            if (grown) m = top;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              read_tmem(mine + c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x32(mine + c, o);
+            }
+            tmem_wait_st();
+          }
+          const float base = (m == -INFINITY ? 0.f : m) - T::POFF;
+          float sum = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t s[32];
+            read_tmem(sb + 32 * h, s);
+            const uint32_t bits = static_cast<uint32_t>(sees >> (32 * h));
+            uint32_t out[32];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              float a = exp2_approx(__uint_as_float(s[c]) * sc - base), b = exp2_approx(__uint_as_float(s[c + 1]) * sc - base);
+              if (!t.plain) {
+                a = bits >> c & 1 ? a : 0.f;
+                b = bits >> (c + 1) & 1 ? b : 0.f;
+              }
+              sum += a + b;
+              const uint32_t hi = t.plain ? pack2_down<T::BF16>(a, b) : pack2<T::BF16>(a, b);
+              const float2 back = unpack2<T::BF16>(hi);
+              const uint32_t lo = pack2<T::BF16>(a - back.x, b - back.y);
+              const int at = c / 16 * 16 + c % 16 / 2;             // keys 16 j ..: 8 columns of high parts, 8 of low ones
+              out[at] = hi;
+              out[at + 8] = t.plain ? above_zero<T::BF16>(lo) : lo;
+            }
+            tmem_st_32x32b_x32(sb + 32 * h, out);
+          }
+          l += sum;
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&misc->p_full[buf]));
+      }
+      if (!ok) break;
+      if (!wait(misc->pv_done[(tiles - 1) % T::SBUF], (tiles - 1) / T::SBUF) || !wait(misc->loaded[pieces % kAhead], pieces / kAhead)) break;
+      const bool odd = *const_cast<volatile int*>(&misc->flag[pieces % kAhead]) == static_cast<int>(pieces) + 1;
+      ++pieces;
+      if (busy) {
+        tc_fence_after();
+        float* const part = p.partials + (static_cast<size_t>(2) * blockIdx.x + x.second) * tree_partial_floats(D);
+        const float inv = l == 0.f ? 0.f : vs / l;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t raw[32];
+          read_tmem(mine + c, raw);
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]);
+          if (live) {
+            if (odd) add_odd(o, c, w, x, mask);
+            if (x.whole) {
+              uint16_t* const to = p.out + token * p.ldo + static_cast<int64_t>(head) * D + c;
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float a = o[e + 2 * k] * inv, b = o[e + 2 * k + 1] * inv;
+                  v[k] = p.q_bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
+                }
+                *reinterpret_cast<uint4*>(to + e) = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            } else {
+              float* const to = part + 2 * kTreeRows + static_cast<size_t>(mr) * D + c;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        if (live) {
+          if (x.whole) {
+            if (p.lse != nullptr) p.lse[token * p.q_heads + head] = l == 0.f ? -INFINITY : (m - T::POFF) * kLn2 + logf(l);
+          } else {
+            part[mr] = m;
+            part[kTreeRows + mr] = l;
+          }
+        }
+      }
+      if (!x.whole && x.starts_here) cut = TreeCut{x.parts, w.r.row0, x.kvh, first_row, rows, vs};
+    }
+    if (warp == 0 && lane == 0) p.cuts[blockIdx.x] = cut;
+  }
+};
+
+template <int CACHE, int D>
+__global__ void __launch_bounds__(kThreads, Traits<CACHE, D>::BLOCKS) tree_attention_kernel(const __grid_constant__ TreeAttnParams p) {
+  using T = Traits<CACHE, D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc<T>* const misc = reinterpret_cast<Misc<T>*>(smem + T::OFF_MISC);
+  static_assert(sizeof(Misc<T>) <= 1024, "misc");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023) != 0) {                  // the swizzle goes by addresses
+    if (threadIdx.x == 0) set_status(p.status, TL_ECUDA);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::SLOTS; ++i) mbar_init(smem_u32(&misc->full[i]), kLoadWarps * 32), mbar_init(smem_u32(&misc->empty[i]), 1);
+    for (int i = 0; i < T::SBUF; ++i) {
+      mbar_init(smem_u32(&misc->s_full[i]), 1);
+      mbar_init(smem_u32(&misc->p_full[i]), kSoftmaxWarps);
+      mbar_init(smem_u32(&misc->pv_done[i]), 1);
+    }
+    mbar_init(smem_u32(&misc->q_full), kSoftmaxWarps);
+    for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&misc->loaded[i]), kLoadWarps * 32), misc->flag[i] = 0;
+    misc->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&misc->tmem), T::TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait_prior();
+  if (warp < kSoftmaxWarps) {
+    Softmax<CACHE, D> s{p, smem, misc, warp, lane};
+    s.run();
+  } else if (warp == kMmaWarp) {
+    issue_mmas<CACHE, D>(p, smem, misc);
+  } else {
+    Loader<CACHE, D> l{p, smem, misc, warp - kLoadWarp, lane};
+    l.run();
+  }
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(misc->tmem, T::TMEM);
+  }
+}
+
+// ---- the second kernel: segments that were cut. Block x joins the one that begins in the share of block x of the first kernel,
+// some of its rows; a thread takes four channels of a row.
+constexpr int kJoinThreads = 256;
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeAttnParams p) {
+  constexpr int PER_ROW = D / 4, ROWS = kJoinThreads / PER_ROW;
+  constexpr float POFF = F16 ? Traits<kCacheF16, D>::POFF : Traits<kCacheBf16, D>::POFF;
+  pdl_wait_prior();
+  pdl_launch_dependents();
+  const TreeCut c = p.cuts[blockIdx.x];
+  const int d = threadIdx.x % PER_ROW;
+  for (int r = blockIdx.y * ROWS + threadIdx.x / PER_ROW; c.parts > 0 && r < c.rows; r += gridDim.y * ROWS) {
+    auto part = [&](int i) { return p.partials + (static_cast<size_t>(2) * (blockIdx.x + i) + (i == 0)) * tree_partial_floats(D); };
+    float top = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < c.parts; ++i) top = fmaxf(top, __ldcg(part(i) + r));
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < c.parts; ++i) {
+      const float* const q = part(i);
+      const float f = faded(__ldcg(q + r) - base);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 2 * kTreeRows + static_cast<size_t>(r) * D) + d);
+      l += f * __ldcg(q + kTreeRows + r);
+      a.x += f * v.x;
+      a.y += f * v.y;
+      a.z += f * v.z;
+      a.w += f * v.w;
+    }
+    const int gr = c.first_row + r, node = static_cast<int>(p.group_div.div(gr)), head = c.kvh * p.group + gr - node * p.group;
+    const int64_t token = static_cast<int64_t>(c.row0) + node;
+    const float inv = l == 0.f ? 0.f : c.v_scale / l;
+    uint2 out;
+    out.x = p.q_bf16 ? pack2<true>(a.x * inv, a.y * inv) : pack2<false>(a.x * inv, a.y * inv);
+    out.y = p.q_bf16 ? pack2<true>(a.z * inv, a.w * inv) : pack2<false>(a.z * inv, a.w * inv);
+    *reinterpret_cast<uint2*>(p.out + token * p.ldo + static_cast<int64_t>(head) * D + 4 * d) = out;
+    if (d == 0 && p.lse != nullptr) p.lse[token * p.q_heads + head] = l == 0.f ? -INFINITY : (top - POFF) * kLn2 + logf(l);
+  }
+}
+
+template <int CACHE, int D>
+cudaError_t launch(TreeAttnParams& p, int sms, cudaStream_t st) {
+  using T = Traits<CACHE, D>;
+  static int ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE) == 0) {
+    e = cudaFuncSetAttribute(tree_attention_kernel<CACHE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    if (e != cudaSuccess) return e;
+    __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
+  }
+  long long grid = static_cast<long long>(sms) * T::BLOCKS;
+  if (grid > kTreeMaxGrid) grid = kTreeMaxGrid;
+  // at most as many blocks as the list can have places
+  const long long nodes = p.T < TL_TREE_NODES ? p.T : TL_TREE_NODES;
+  const long long keys = p.window > 0 && p.window + static_cast<long long>(p.sinks) < p.capacity ? p.window + static_cast<long long>(p.sinks) : p.capacity;
+  const long long most = static_cast<long long>(p.B) * p.kv_heads * ((nodes * p.group + kTreeRows - 1) / kTreeRows) * ((keys + 3 * kKeys) / kKeys + kSegmentCost);
+  if (grid > most) grid = most;
+  p.grid = static_cast<int>(grid);
+  e = launch_pdl(tree_attention_kernel<CACHE, D>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), T::SMEM, st, p);
+  if (e != cudaSuccess || grid == 1) return e;
+  return launch_pdl(tree_join_kernel<D, !T::BF16>, dim3(static_cast<unsigned>(grid), 8), dim3(kJoinThreads), 0, st, p);
+}
+
+template <int CACHE>
+cudaError_t launch_dim(TreeAttnParams& p, int dim, int sms, cudaStream_t st) {
+  switch (dim) {
+    case 64: return launch<CACHE, 64>(p, sms, st);
+    case 128: return launch<CACHE, 128>(p, sms, st);
+    case 256: return launch<CACHE, 256>(p, sms, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace tree
+}  // namespace tl

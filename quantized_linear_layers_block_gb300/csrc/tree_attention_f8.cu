@@ -1,0 +1,10 @@
+// Tree attention over a f8 cache: the instantiations of tree_attention.cuh.
+#include "tree_attention.cuh"
+
+namespace tl {
+
+cudaError_t launch_tree_attn_f8(TreeAttnParams p, int dim, int sms, cudaStream_t st) {
+  return tree::launch_dim<kCacheF8>(p, dim, sms, st);
+}
+
+}  // namespace tl

@@ -65,6 +65,12 @@ SIGNATURES = {
     "tl_kv_append": (_I, [_PKV, _P, _P, _P, _I, _I, _I, _L, _L, _L, _P, _L, _P, _I, _I, _I, _P, _P, _P]),
     "tl_paged_attention_workspace_size": (_I, [_I, _I, _I, _I, _PSZ]),
     "tl_paged_attention": (_I, [_PKV, _P, _I, _I, _I, _L, _P, _I, _L, _P, _F, _I, _P, _L, _P, _P, _SZ, _P]),
+    "tl_kv_append_norm": (_I, [_PKV, _P, _P, _P, _I, _I, _I, _L, _L, _L, _P, _L, _P, _P, _F, _P, _I, _I, _I, _P, _P, _P]),
+    "tl_tree_plan": (_I, [_P, _P, _I, _I, _P, _P, _I, _L, _I, _I, _P, _P, _P, _P]),
+    "tl_tree_attention_workspace_size": (_I, [_I, _I, _I, _I, _I, _PSZ]),
+    "tl_tree_attention": (_I, [_PKV, _P, _I, _I, _I, _I, _L, _P, _P, _P, _I, _L, _P, _F, _I, _I, _P, _L, _P, _P, _SZ, _P]),
+    "tl_verify_tree": (_I, [_P, _L, _P, _L, _I, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P]),
+    "tl_kv_compact": (_I, [_PKV, _P, _P, _P, _I, _I, _P, _I, _L, _P, _P]),
     "tl_lora_plan_size": (_I, [_I, _I, _PSZ]),
     "tl_lora_plan": (_I, [_P, _I, _I, _P, _SZ, _P]),
     "tl_lora_apply": (_I, [_P, _L, _P, _P, _P, _I, _I, _I, _P, _I, _I, _I, _P, _L, _P, _L, _I, _P]),
@@ -421,24 +427,48 @@ class PagedKVCache:
             with torch.cuda.device(k.device):
                 need = tl_paged_attention_workspace_size(1, kv_heads * min(17, 1024 // kv_heads), kv_heads, head_dim)
             self._ws = torch.zeros((need,), dtype=torch.uint8, device=k.device)
+            with torch.cuda.device(k.device):
+                self._tree_bytes = tl_tree_attention_workspace_size(1, 1, kv_heads, kv_heads, head_dim)
         _filled(k.device)
 
-    def append(self, k, v, positions, slots, cos_sin=None, interleaved: bool = False, q=None, q_out=None, stream=None):
-        """tl_kv_append on this cache; returns the rotated queries (None without q)."""
-        return tl_kv_append(self, k, v, positions, slots, cos_sin, interleaved, q, q_out, stream)
+    def append(self, k, v, positions, slots, cos_sin=None, interleaved: bool = False, q=None, q_out=None, stream=None,
+               q_norm=None, k_norm=None, eps: float = 1e-6):
+        """tl_kv_append on this cache, with the heads' norms where q_norm or k_norm is given; returns the rotated queries (None without q)."""
+        return tl_kv_append(self, k, v, positions, slots, cos_sin, interleaved, q, q_out, stream, q_norm, k_norm, eps)
 
     def attend(self, q, pages, lens, scale: float | None = None, window: int = 0, out=None, lse=None, stream=None):
         """tl_paged_attention on this cache with its own workspace; returns out [requests, q_heads, head_dim]."""
         return tl_paged_attention(self, q, pages, lens, scale, window, out, lse, None, stream)
 
+    def plan_tree(self, parents, starts, lens, pages, masks=None, positions=None, slots=None, stream=None):
+        """tl_tree_plan for this cache's pages; returns (masks, positions, slots), for all layers of the pass."""
+        return tl_tree_plan(self, parents, starts, lens, pages, masks, positions, slots, stream)
+
+    def attend_tree(self, q, masks, starts, pages, lens, scale: float | None = None, window: int = 0, sinks: int = 0, out=None, lse=None,
+                    stream=None):
+        """tl_tree_attention on this cache; returns out [tokens, q_heads, head_dim]. Calls on different streams need no order."""
+        return tl_tree_attention(self, q, masks, starts, pages, lens, scale, window, sinks, out, lse, None, stream)
+
+    def compact(self, path, counts, starts, pages, lens, stream=None) -> None:
+        """tl_kv_compact on this cache: the accepted nodes' rows move together behind each request's lens tokens."""
+        tl_kv_compact(self, path, counts, starts, pages, lens, stream)
+
 
 def tl_kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None, slots: torch.Tensor,
                  cos_sin: torch.Tensor | None = None, interleaved: bool = False, q: torch.Tensor | None = None,
-                 q_out: torch.Tensor | None = None, stream=None):
+                 q_out: torch.Tensor | None = None, stream=None, q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None,
+                 eps: float = 1e-6):
     """k, v [T, kv_heads, head_dim] into the cache's slots int64 [T], and q [T, q_heads, head_dim] into q_out, keys and
-    queries rotated by cos_sin fp32 [max_pos, rot_dim] at positions int32 [T]. Returns q_out (None without q)."""
+    queries rotated by cos_sin fp32 [max_pos, rot_dim] at positions int32 [T]. With q_norm (k_norm) fp32 [head_dim] each head of
+    q (k) becomes x / sqrt(mean x^2 + eps) times these weights before that (tl_kv_append_norm). Returns q_out (None without q)."""
     if q is not None and q_out is None:
         q_out = _allocate(torch.empty, q.shape, q.dtype, q.device, stream)
+    if q_norm is not None or k_norm is not None:
+        r = (_ext or _tensors()).kv_append_norm(cache._address, k, v, positions, slots, cos_sin, interleaved, q, q_out, q_norm, k_norm, eps,
+                                                _raw_stream(stream))
+        if r != TL_OK:
+            _check(r, "tl_kv_append_norm")
+        return q_out
     r = (_ext or _tensors()).kv_append(cache._address, k, v, positions, slots, cos_sin, interleaved, q, q_out, _raw_stream(stream))
     if r != TL_OK:
         _check(r, "tl_kv_append")
@@ -468,6 +498,80 @@ def tl_paged_attention(cache: PagedKVCache, q: torch.Tensor, pages: torch.Tensor
     if r != TL_OK:
         _check(r, "tl_paged_attention")
     return out
+
+
+TREE_NODES = 64       # of a request's tree, at most
+
+
+def tl_tree_plan(cache: PagedKVCache, parents: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor, pages: torch.Tensor,
+                 masks: torch.Tensor | None = None, positions: torch.Tensor | None = None, slots: torch.Tensor | None = None, stream=None):
+    """Drafted trees: parents int32 [T] (within the request; -1: root) of the nodes of request b in rows starts[b] .. starts[b + 1] - 1
+    (int32 [requests + 1]), lens int32 tokens cached before them, pages int32 [requests, max_pages] -> (masks int64 [T] of each
+    node and its ancestors, positions int32 [T], slots int64 [T] for append). Rows behind the last request are padding: (0, 0, -1)."""
+    if masks is None:
+        masks = _allocate(torch.empty, parents.shape, torch.int64, parents.device, stream)
+    if positions is None:
+        positions = _allocate(torch.empty, parents.shape, torch.int32, parents.device, stream)
+    if slots is None:
+        slots = _allocate(torch.empty, parents.shape, torch.int64, parents.device, stream)
+    r = (_ext or _tensors()).tree_plan(cache._address, parents, starts, lens, pages, masks, positions, slots, _raw_stream(stream))
+    if r != TL_OK:
+        _check(r, "tl_tree_plan")
+    return masks, positions, slots
+
+
+def tl_tree_attention_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().tl_tree_attention_workspace_size(B, T, q_heads, kv_heads, head_dim, ctypes.byref(b)), "tl_tree_attention_workspace_size")
+    return b.value
+
+
+def tl_tree_attention(cache: PagedKVCache, q: torch.Tensor, masks: torch.Tensor, starts: torch.Tensor, pages: torch.Tensor,
+                      lens: torch.Tensor, scale: float | None = None, window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q [T, q_heads, head_dim] of the nodes over their requests' lens cached tokens and the nodes of their masks int64 [T] -> out of
+    q's shape and dtype; lse fp32 [T, q_heads] when given. With a window (64 or more) a node sees that many keys, its own nodes
+    among them, and the first `sinks` cached tokens. Rows of padding are left as they were (in an `out` that is allocated here: zeros).
+    The workspace is taken from torch's allocator for the call unless it is given (tl_tree_attention_workspace_size bytes)."""
+    if out is None:
+        out = _allocate(torch.zeros, q.shape, q.dtype, q.device, stream)
+    if workspace is None:
+        if cache._ws is None:
+            raise TLError(TL_EUNSUPPORTED, "tl_tree_attention")
+        workspace = _allocate(torch.empty, (cache._tree_bytes,), torch.uint8, cache.device, stream)
+    r = (_ext or _tensors()).tree_attention(cache._address, q, masks, starts, pages, lens, cache.scale if scale is None else scale, window,
+                                            sinks, out, lse, workspace, _raw_stream(stream))
+    if r != TL_OK:
+        _check(r, "tl_tree_attention")
+    return out
+
+
+def tl_verify_tree(target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.Tensor, parents: torch.Tensor, starts: torch.Tensor,
+                   uniform: torch.Tensor, path: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                   next: torch.Tensor | None = None, stream=None):
+    """Which nodes of drafted trees hold: target and draft fp32 [T, vocab] (the row of a node: what follows it; draft None: tokens were
+    chosen, not drawn), tokens int32 [T], parents and starts as for tl_tree_plan, uniform fp32 [T] in [0, 1) ->
+    (path int32 [T]: each request's accepted nodes from its root on, then -1; counts int32 [requests]; next int32 [requests]: the token
+    after the last of them)."""
+    if path is None:
+        path = _allocate(torch.empty, tokens.shape, torch.int32, tokens.device, stream)
+    n = (starts.shape[0] - 1,) if starts.dim() == 1 and starts.shape[0] else (0,)
+    if counts is None:
+        counts = _allocate(torch.empty, n, torch.int32, tokens.device, stream)
+    if next is None:
+        next = _allocate(torch.empty, n, torch.int32, tokens.device, stream)
+    r = (_ext or _tensors()).verify_tree(target, draft, tokens, parents, starts, uniform, path, counts, next, _raw_stream(stream))
+    if r != TL_OK:
+        _check(r, "tl_verify_tree")
+    return path, counts, next
+
+
+def tl_kv_compact(cache: PagedKVCache, path: torch.Tensor, counts: torch.Tensor, starts: torch.Tensor, pages: torch.Tensor,
+                  lens: torch.Tensor, stream=None) -> None:
+    """The rows of the accepted nodes (tl_verify_tree's path and counts) move to places lens .. lens + counts - 1 of their requests."""
+    r = (_ext or _tensors()).kv_compact(cache._address, path, counts, starts, pages, lens, _raw_stream(stream))
+    if r != TL_OK:
+        _check(r, "tl_kv_compact")
 
 
 def tl_lora_plan_size(M: int, n_adapters: int) -> int:
