@@ -17,12 +17,11 @@
 //
 // Softmax. One pass with a running maximum m, sum l and output o; o is rescaled only where m grows by more than 2^8 (bf16) or
 // 2^3 (f16): p just has to stay in range. Probabilities enter the second product as two 16-bit parts (16 bits for bf16, 22
-// for f16): one part would add an error as large as the output's own rounding. Both parts are at least the least
-// positive number, so that an infinite value makes its channel infinite instead of NaN.
+// for f16): one part would add an error as large as the output's own rounding.
 //
 // Masks. A key that only some rows see meets the others with p = 0, and 0 V is NaN where V is not finite. So in tiles that not
 // every row sees whole (the nodes, the edge of a window) such values are taken out when they are loaded, and added
-// at the end to the rows that see them.
+// at the end to the rows that see them. In the others a weight that underflowed makes an infinity NaN: a NaN channel at the end is looked into.
 #pragma once
 
 #include "paged_attention.cuh"
@@ -75,21 +74,19 @@ __host__ __device__ constexpr int tree_blocks_per_sm(int dim) { return dim == 25
 
 namespace tree {
 
-using attn::above_zero;
 using attn::cp_async16;
 using attn::cp_async_commit;
 using attn::cp_async_wait;
 using attn::exp2_approx;
 using attn::faded;
 using attn::pack2;
-using attn::pack2_down;
 using attn::unpack2;
 using attn::widen_hi;
 using attn::widen_lo;
 
 constexpr int kKeys = 64;                // keys of a tile
 constexpr int kSegmentCost = 2;          // what a segment costs besides its tiles, in tiles
-constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5, kLoadWarps = 4;
+constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5, kLoadWarps = 2;      // seven: four to a scheduler for two blocks, 128 registers
 constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
 constexpr int kAhead = 8;                // pieces: more than the loading warps can be ahead of the others, or of each other
 
@@ -101,7 +98,7 @@ struct Traits {
   static constexpr int Q = kTreeRows * D * 2, SLOT = kKeys * D * 2, STAGE = F8 ? SLOT / 2 : 0;
   static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 12) : F8 ? 3 : 5;
   static constexpr int STAGES = F8 ? (D == 64 ? 12 : 4) : 0;     // of 8-bit rows on their way
-  static constexpr int LAG = F8 ? STAGES - 1 : D == 64 ? 8 : 3;  // loads in flight
+  static constexpr int LAG = F8 ? STAGES - 1 : 0;                // of them in flight
   static constexpr int OFF_SLOT = Q, OFF_STAGE = OFF_SLOT + SLOTS * SLOT, OFF_MISC = OFF_STAGE + STAGES * STAGE;
   static constexpr int SMEM = OFF_MISC + 1024;
   static constexpr int SBUF = D == 128 ? 2 : 3;                  // buffers of S and P
@@ -168,14 +165,25 @@ __device__ __forceinline__ bool wait_all(uint64_t& bar, uint32_t parity, int* ab
   return ok;
 }
 
-// 32 columns of this warp's lanes, there when it returns (the registers pass through the wait, so that no use of them comes before it).
-__device__ __forceinline__ void read_tmem(uint32_t addr, uint32_t (&v)[32]) {
-  tmem_ld_32x32b_x32(addr, v);
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Waits for the loads from tensor memory so far (the registers pass through the wait, so that no use of them comes before it).
+__device__ __forceinline__ void arrived(uint32_t (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]),
                  "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
                  "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]),
                  "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+}
+
+// 32 columns of this warp's lanes, there when it returns.
+__device__ __forceinline__ void read_tmem(uint32_t addr, uint32_t (&v)[32]) {
+  tmem_ld_32x32b_x32(addr, v);
+  arrived(v);
 }
 
 // ---- the list of work: every warp goes through its block's share by itself
@@ -326,116 +334,140 @@ struct Loader {
   using T = Traits<CACHE, D>;
   static constexpr int CPR = T::ROW / 16;               // 16-byte chunks of a cached row
   static constexpr int RPI = 32 / CPR;                  // rows that one instruction of a warp copies
-  static constexpr int ROWS = kKeys / kLoadWarps;       // of a warp
+  static constexpr int ROWS = kKeys / kLoadWarps;       // of a warp, one to a lane
   static constexpr int STEPS = ROWS / RPI;
+  static_assert(ROWS == 32, "a lane looks one row up");
 
   const TreeAttnParams& p;
   uint8_t* smem;
   Misc<T>* misc;
   int warp, lane;                                       // of the loading warps
   uint32_t issued = 0, done = 0;                        // loads
-  uint32_t checks = 0, ends = 0;                        // of the loads in flight, the last in bit 0: look for what is not finite; a piece's last
+  uint32_t checks = 0, ends = 0;                        // 8 bits: of the loads in flight, the last in bit 0: look for NaN; a piece's last
   int pieces = 0;                                       // whose loads are done
   bool ok = true;
 
-  __device__ __forceinline__ uint32_t slot(uint32_t i) const { return smem_u32(smem) + T::OFF_SLOT + i % T::SLOTS * T::SLOT; }
-
-  // Byte offset in the cache of the row of this lane (of the first 16), or -1.
   __device__ __forceinline__ int page_of(const Walk& w, const Tile& t) const {
     const int key = t.k0 + warp * ROWS + lane;
-    return lane < ROWS && key < t.end ? __ldg(p.pages + w.b * p.ldp + p.page.div(key)) : -1;
+    return key < t.end ? __ldg(p.pages + w.b * p.ldp + p.page.div(key)) : -1;
   }
+  // Byte offset in the cache of this lane's row, or -1.
   __device__ __forceinline__ int64_t row_of(const Piece& x, const Tile& t, int page) const {
     const int key = t.k0 + warp * ROWS + lane;
-    if (lane >= ROWS || key >= t.end) return -1;
+    if (key >= t.end) return -1;
     if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
       set_status(p.status, TL_EDATA);
       return -1;
     }
     return page * p.page_stride + x.kvh * p.head_stride + static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
   }
+  // Each 16 lanes' rows follow each other at equal distances.
+  __device__ __forceinline__ bool even(int64_t off) const {
+    const int64_t first = __shfl_sync(0xffffffffu, off, lane & 16);
+    return __all_sync(0xffffffffu, first >= 0 && off == first + (lane & 15) * p.token_stride);
+  }
 
   __device__ __forceinline__ void wait_empty(uint32_t i) {
     if (i >= T::SLOTS) ok = wait_all(misc->empty[i % T::SLOTS], i / T::SLOTS - 1, &misc->abort, p.status);
   }
 
-  __device__ __forceinline__ void load(const uint8_t* base, int64_t off, bool check, bool last) {
-    if (!T::F8) {
-      wait_empty(issued);
-      if (!ok) return;
-    }
+  __device__ __forceinline__ void copy(const uint8_t* base, int64_t off, bool runs) {
     const int row = lane / CPR, chunk = lane % CPR;
-    const uint32_t to = T::F8 ? smem_u32(smem) + T::OFF_STAGE + issued % (T::F8 ? T::STAGES : 1) * T::STAGE + (warp * 32 + lane) * 16 : slot(issued);
+    const uint32_t to = T::F8 ? smem_u32(smem) + T::OFF_STAGE + issued % (T::F8 ? T::STAGES : 1) * T::STAGE + (warp * 32 + lane) * 16
+                              : smem_u32(smem) + T::OFF_SLOT + issued % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
+    auto dst = [&](int i) { return T::F8 ? to + i * (kLoadWarps * 32 * 16) : to + swizzled(warp * ROWS + i * RPI + row, chunk % 8); };
+    base += chunk * 16;
+    if (runs) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int r = i * RPI + row, kk = warp * ROWS + r;
-      const int64_t o = __shfl_sync(0xffffffffu, off, r);
-      const uint32_t dst = T::F8 ? to + i * (kLoadWarps * 32 * 16) : to + chunk / 8 * (kKeys * 128) + swizzled(kk, chunk % 8);
-      cp_async16(dst, base + (o < 0 ? 0 : o) + chunk * 16, o < 0 ? 0u : 16u);
+      for (int g = 0; g < 2; ++g) {
+        const uint8_t* from = base + __shfl_sync(0xffffffffu, off, 16 * g) + row * p.token_stride;
+#pragma unroll
+        for (int i = 0; i < STEPS / 2; ++i, from += RPI * p.token_stride) cp_async16(dst(g * (STEPS / 2) + i), from);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < STEPS; ++i) {
+        const int64_t o = __shfl_sync(0xffffffffu, off, i * RPI + row);
+        cp_async16(dst(i), base + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
+      }
     }
+  }
+
+  __device__ __forceinline__ void note_odd() { *const_cast<volatile int*>(&misc->flag[pieces % kAhead]) = pieces + 1; }
+  __device__ __forceinline__ void end_piece() {
+    mbar_arrive(smem_u32(&misc->loaded[pieces % kAhead]));
+    ++pieces;
+  }
+
+  // 16 bits: straight into the slot; the copies themselves arrive when they have landed.
+  __device__ __forceinline__ void load16(const uint8_t* base, int64_t off, bool runs, bool check, bool last) {
+    wait_empty(issued);
+    if (!ok) return;
+    copy(base, off, runs);
+    const uint32_t full = smem_u32(&misc->full[issued % T::SLOTS]);
+    if (!check) {
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+    } else {
+      cp_async_commit();
+      cp_async_wait<0>();
+      constexpr uint32_t E = T::BF16 ? 0x7F807F80u : 0x7C007C00u;
+      const int row = lane / CPR, chunk = lane % CPR;
+      uint8_t* const to = smem + T::OFF_SLOT + issued % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
+      bool found = false;
+#pragma unroll 2
+      for (int i = 0; i < STEPS; ++i) {
+        uint4* const at = reinterpret_cast<uint4*>(to + swizzled(warp * ROWS + i * RPI + row, chunk % 8));
+        uint4 x = *at;
+        const uint32_t a = __vcmpeq2(x.x & E, E), b = __vcmpeq2(x.y & E, E), c = __vcmpeq2(x.z & E, E), d = __vcmpeq2(x.w & E, E);
+        if ((a | b | c | d) != 0) *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d), found = true;
+      }
+      if (found) note_odd();
+      fence_proxy_async_smem();
+      mbar_arrive(full);
+    }
+    ++issued;
+    if (last) end_piece();
+  }
+
+  // 8 bits: into this thread's part of a stage, some loads ahead.
+  __device__ __forceinline__ void load8(const uint8_t* base, int64_t off, bool runs, bool check, bool last) {
+    copy(base, off, runs);
     cp_async_commit();
     ++issued;
     checks = checks << 1 | check;
     ends = ends << 1 | last;
     if (issued - done > T::LAG) {
       cp_async_wait<T::LAG>();
-      hand_over(T::LAG);
+      widen(T::LAG);
     }
   }
 
-  // The oldest load in flight, `age` loads ago, has landed: the rows go to the MMAs.
-  __device__ __forceinline__ void hand_over(int age) {
+  // The oldest load in flight, `age` loads ago, has landed: this thread's part of it goes to a slot as f16.
+  __device__ __forceinline__ void widen(int age) {
+    wait_empty(done);
+    if (!ok) return;
     const bool check = checks >> age & 1;
     bool found = false;
     const int row = lane / CPR, chunk = lane % CPR;
-    if constexpr (T::F8) {
-      wait_empty(done);
-      if (!ok) return;
-      const uint8_t* from = smem + T::OFF_STAGE + done % T::STAGES * T::STAGE + (warp * 32 + lane) * 16;
-      uint8_t* to = smem + T::OFF_SLOT + done % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128);
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const int kk = warp * ROWS + i * RPI + row;
-        uint4 x = *reinterpret_cast<const uint4*>(from + i * (kLoadWarps * 32 * 16));
-        if (check) {                                    // e4m3 has NaN (0x7F, 0xFF), no infinities
-          uint32_t* const w = &x.x;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t nan = __vcmpeq4(w[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            found |= nan != 0;
-            w[j] &= ~nan;
-          }
-        }
-        const uint4 a = make_uint4(widen_lo(x.x), widen_hi(x.x), widen_lo(x.y), widen_hi(x.y));
-        const uint4 b = make_uint4(widen_lo(x.z), widen_hi(x.z), widen_lo(x.w), widen_hi(x.w));
-        *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2)) = a;
-        *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2 + 1)) = b;
+    const uint8_t* from = smem + T::OFF_STAGE + done % (T::F8 ? T::STAGES : 1) * T::STAGE + (warp * 32 + lane) * 16;
+    uint8_t* to = smem + T::OFF_SLOT + done % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128);
+#pragma unroll 4
+    for (int i = 0; i < STEPS; ++i) {
+      const int kk = warp * ROWS + i * RPI + row;
+      uint4 x = *reinterpret_cast<const uint4*>(from + i * (kLoadWarps * 32 * 16));
+      if (check) {                                      // e4m3 has NaN (0x7F, 0xFF), no infinities
+        constexpr uint32_t N = 0x7F7F7F7Fu;
+        const uint32_t a = __vcmpeq4(x.x & N, N), b = __vcmpeq4(x.y & N, N), c = __vcmpeq4(x.z & N, N), d = __vcmpeq4(x.w & N, N);
+        found |= (a | b | c | d) != 0;
+        x = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d);
       }
-    } else if (check) {
-      constexpr uint32_t E = T::BF16 ? 0x7F80u : 0x7C00u;
-      uint8_t* to = smem + T::OFF_SLOT + done % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        uint4* const at = reinterpret_cast<uint4*>(to + swizzled(warp * ROWS + i * RPI + row, chunk % 8));
-        uint4 x = *at;
-        uint32_t* const w = &x.x;
-        uint32_t any = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t odd = __vcmpeq2(w[j] & (E * 0x10001u), E * 0x10001u);
-          any |= odd;
-          w[j] &= ~odd;
-        }
-        if (any != 0) *at = x, found = true;
-      }
+      *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2)) = make_uint4(widen_lo(x.x), widen_hi(x.x), widen_lo(x.y), widen_hi(x.y));
+      *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2 + 1)) = make_uint4(widen_lo(x.z), widen_hi(x.z), widen_lo(x.w), widen_hi(x.w));
     }
-    if (found) *const_cast<volatile int*>(&misc->flag[pieces % kAhead]) = pieces + 1;
+    if (found) note_odd();
     fence_proxy_async_smem();
     mbar_arrive(smem_u32(&misc->full[done % T::SLOTS]));
-    if (ends >> age & 1) {
-      mbar_arrive(smem_u32(&misc->loaded[pieces % kAhead]));
-      ++pieces;
-    }
+    if (ends >> age & 1) end_piece();
     ++done;
   }
 
@@ -444,34 +476,41 @@ struct Loader {
     w.init(p, false);
     Piece x;
     while (ok && w.next(p, x)) {
+      // loads K0, K1, V0, K2, V1, ...: `now` is the tile of the next K, `before` the one whose V is due
+      const int n = x.end - x.begin;
       Tile t = tile(p, w.r, x.begin);
-      int64_t off = row_of(x, t, page_of(w, t));
-      Tile t2 = t;
-      int page2 = -1;
-      if (x.begin + 1 < x.end) {
-        t2 = tile(p, w.r, x.begin + 1);
-        page2 = page_of(w, t2);
-      }
-      load(p.k, off, false, false);
-      for (int i = x.begin; ok && i < x.end; ++i) {
-        int64_t off2 = -1;
-        const Tile now = t2;
-        if (i + 1 < x.end) {
-          off2 = row_of(x, now, page2);
-          if (i + 2 < x.end) {
-            t2 = tile(p, w.r, i + 2);
-            page2 = page_of(w, t2);
+      int page = page_of(w, t);
+      int64_t before = -1;
+      bool before_runs = false, before_plain = true;
+      for (int i = 0; ok && i <= n; ++i) {
+        const Tile now = t;
+        int64_t off = -1;
+        bool runs = false;
+        if (i < n) {
+          off = row_of(x, now, page);
+          runs = even(off);
+          if (i + 1 < n) {
+            t = tile(p, w.r, x.begin + i + 1);
+            page = page_of(w, t);
           }
-          load(p.k, off2, false, false);
-          if (!ok) break;
         }
-        load(p.v, off, !t.plain, i + 1 == x.end);
-        t = now;
-        off = off2;
+#pragma unroll 1
+        for (int v = 0; ok && v < 2; ++v) {
+          if (v ? i == 0 : i == n) continue;
+          const uint8_t* const base = v ? p.v : p.k;
+          const int64_t o = v ? before : off;
+          const bool r = v ? before_runs : runs, check = v && !before_plain, last = v && i == n;
+          if constexpr (T::F8)
+            load8(base, o, r, check, last);
+          else
+            load16(base, o, r, check, last);
+        }
+        before = off, before_runs = runs, before_plain = now.plain;
       }
     }
     cp_async_wait<0>();
-    while (ok && done != issued) hand_over(static_cast<int>(issued - done) - 1);
+    if constexpr (T::F8)
+      while (ok && done != issued) widen(static_cast<int>(issued - done) - 1);
   }
 };
 
@@ -492,6 +531,7 @@ __device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* sme
     const uint32_t buf = t % T::SBUF, s = loads % T::SLOTS;
     if (t >= T::SBUF && !wait(misc->pv_done[buf], t / T::SBUF - 1)) return;
     if (!wait(misc->full[s], loads / T::SLOTS)) return;
+    fence_proxy_async_smem();                           // (rows that ordinary copies wrote, to the MMAs)
     tc_fence_after();
     if (elected) {
       const uint32_t kb = base + T::OFF_SLOT + s * T::SLOT;
@@ -515,6 +555,7 @@ __device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* sme
       if (i + 1 < x.end) scores(tiles + 1);
       const uint32_t buf = tiles % T::SBUF, s = loads % T::SLOTS;
       if (!wait(misc->p_full[buf], tiles / T::SBUF) || !wait(misc->full[s], loads / T::SLOTS)) break;
+      fence_proxy_async_smem();
       tc_fence_after();
       if (elected) {
         const uint32_t vb = base + T::OFF_SLOT + s * T::SLOT, pb = tm + T::TMEM_S + buf * kKeys;
@@ -547,12 +588,13 @@ struct Softmax {
 
   __device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); }
 
-  // This row's query into shared memory as the MMA's operand; returns by what its scores are scaled (8-bit caches: its power of two).
+  // This row's query into shared memory as the MMA's operand, times the sign of the scale; returns by what its scores are scaled
+  // besides (8-bit caches: its power of two).
   __device__ __forceinline__ float put_query(const uint16_t* row) {
     const int r = warp * 32 + lane;
-    float up = 1.f, down = 1.f;
-    const bool turn = T::F8 && p.q_bf16;
-    if (turn) {
+    float up = 1.f, by = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
+    const bool narrow = T::F8 && p.q_bf16;
+    if (narrow) {
       float top = 0.f;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
@@ -567,17 +609,17 @@ struct Softmax {
       // 2^e <= top < 2^(e + 1); e is kept where both 2^e and 2^-e are normal (an infinite or NaN q stays one)
       const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
       up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      by *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
 #pragma unroll 8
     for (int i = 0; i < D / 8; ++i) {
       uint4 x = __ldg(reinterpret_cast<const uint4*>(row) + i);
-      if (turn) {
+      if (by != 1.f || narrow) {
         uint32_t* const w = &x.x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack2<true>(w[j]);
-          w[j] = pack2<false>(f.x * down, f.y * down);
+          const float2 f = T::BF16 || p.q_bf16 ? unpack2<true>(w[j]) : unpack2<false>(w[j]);
+          w[j] = pack2<T::BF16>(f.x * by, f.y * by);
         }
       }
       *reinterpret_cast<uint4*>(smem + i / 8 * (kTreeRows * 128) + swizzled(r, i % 8)) = x;
@@ -585,11 +627,57 @@ struct Softmax {
     return up;
   }
 
-  // Adds to 32 channels of the row, from d on, the values that were taken out and that it sees.
-  __device__ __noinline__ void add_odd(float (&o)[32], int d, const Walk& w, const Piece& x, uint64_t mask) const {
+  // S of a tile, what the row does not see as -inf; returns its maximum.
+  __device__ __forceinline__ float scores(uint32_t (&s)[2][32], uint32_t at, uint64_t sees) {
+    tmem_ld_32x32b_x32(at, s[0]);
+    read_tmem(at + 32, s[1]);
+    arrived(s[0]);
+    if (sees != ~0ull) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (!(sees >> (32 * h + c) & 1)) s[h][c] = 0xFF800000u;
+    }
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(s[h][c]), __uint_as_float(s[h][c + 1]));
+    return max3(fmaxf(top[0], top[1]), top[2], top[3]);
+  }
+
+  // P of 32 keys in place of S, as (key, key + 1) pairs: for each 16 keys 8 columns of high parts, 8 of low ones. Adds to sum.
+  __device__ __forceinline__ void weights(uint32_t (&s)[32], uint32_t at, float2 sc, float2 base, float2& sum) {
+    uint32_t out[32];
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, base);
+      const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+      sum = __fadd2_rn(sum, e);
+      uint32_t hi;
+      float2 back;
+      if constexpr (T::BF16) {                          // towards zero: the upper halves
+        hi = __byte_perm(__float_as_uint(e.x), __float_as_uint(e.y), 0x7632);
+        back = make_float2(__uint_as_float(__float_as_uint(e.x) & 0xFFFF0000u), __uint_as_float(__float_as_uint(e.y) & 0xFFFF0000u));
+      } else {
+        hi = pack2<false>(e.x, e.y);
+        back = unpack2<false>(hi);
+      }
+      out[c / 16 * 16 + c % 16 / 2] = hi;
+      out[c / 16 * 16 + c % 16 / 2 + 8] = pack2<T::BF16>(e.x - back.x, e.y - back.y);
+    }
+    tmem_st_32x32b_x32(at, out);
+  }
+
+  // Infinite and NaN values that the row sees, in 32 of its channels from d on: those that were taken out of tiles that not all rows see
+  // whole; and, as a weight that underflowed to 0 makes an infinity NaN, all of them where a channel is NaN.
+  __device__ __noinline__ void add_odd(float* o, int d, const Walk& w, const Piece& x, uint64_t mask, bool all) const {
+    for (int c = 0; c < 32; ++c)
+      if (o[c] != o[c]) o[c] = 0.f;
     for (int i = x.begin; i < x.end; ++i) {
       const Tile t = tile(p, w.r, i);
-      if (t.plain) continue;
+      if (t.plain && !all) continue;
       uint64_t sees = visible(p, w.r, t, mask) & low_bits(t.end - t.k0);
       while (sees != 0) {
         const int key = t.k0 + __ffsll(static_cast<long long>(sees)) - 1;
@@ -597,7 +685,6 @@ struct Softmax {
         const int at = p.page.div(key), page = __ldg(p.pages + w.b * p.ldp + at);
         if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) continue;
         const uint8_t* row = p.v + page * p.page_stride + x.kvh * p.head_stride + static_cast<int64_t>(key - at * p.page.d) * p.token_stride;
-#pragma unroll
         for (int c = 0; c < 32; ++c) {
           float v;
           if constexpr (T::F8) {
@@ -626,7 +713,7 @@ struct Softmax {
       const int gr = first_row + (live ? mr : 0), node = static_cast<int>(p.group_div.div(gr)), head = x.kvh * p.group + gr - node * p.group;
       const int64_t token = static_cast<int64_t>(w.r.row0) + node;
       uint64_t mask = 0;
-      float sc = p.scale_log2, vs = 1.f;
+      float sc = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2), vs = 1.f;       // (its sign, or zero, is in the queries)
       if constexpr (T::F8) {
         sc *= __ldg(p.k_scale + x.kvh);
         vs = __ldg(p.v_scale + x.kvh);
@@ -638,7 +725,9 @@ struct Softmax {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&misc->q_full));
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY;
+      float2 l = make_float2(0.f, 0.f);
+#pragma unroll 1
       for (int i = x.begin; i < x.end; ++i, ++tiles) {
         const uint32_t buf = tiles % T::SBUF;
         if (!wait(misc->s_full[buf], tiles / T::SBUF)) break;
@@ -647,28 +736,19 @@ struct Softmax {
           const uint32_t sb = mine + T::TMEM_S + buf * kKeys;
           const Tile t = tile(p, w.r, i);
           const uint64_t sees = t.plain ? ~0ull : visible(p, w.r, t, mask);
-          float top = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t s[32];
-            read_tmem(sb + 32 * h, s);
-            const uint32_t bits = static_cast<uint32_t>(sees >> (32 * h));
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float f = __uint_as_float(s[c]) * sc;
-              top = fmaxf(top, t.plain || (bits >> c & 1) ? f : -INFINITY);
-            }
-          }
-          const bool grown = top > m + T::SLACK || (m == -INFINITY && top > m);
-          if (i == x.begin) {
-            m = top;
-          } else if (__any_sync(0xffffffffu, grown)) {
-            // the MMAs of the tile before add to o until they are done
+          uint32_t s[2][32];
+          bool settled = false;
+          for (;;) {
+            const float top = scores(s, sb, sees) * sc;
+            const bool grown = top > m + T::SLACK || (m == -INFINITY && top > m);
+            if (i == x.begin) m = top;
+            if (settled || i == x.begin || !__any_sync(0xffffffffu, grown)) break;
+            // o and l are scaled down to the new maximum; the MMAs of the tile before add to o until they are done
             if (!wait(misc->pv_done[(tiles - 1) % T::SBUF], (tiles - 1) / T::SBUF)) break;
             tc_fence_after();
             const float f = grown ? faded(m - top) : 1.f;
             if (grown) m = top;
-            l *= f;
+            l.x *= f, l.y *= f;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -677,34 +757,12 @@ struct Softmax {
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
               tmem_st_32x32b_x32(mine + c, o);
             }
-            tmem_wait_st();
+            settled = true;                             // the scores once more: they need not be kept meanwhile
           }
-          const float base = (m == -INFINITY ? 0.f : m) - T::POFF;
-          float sum = 0.f;
+          if (!ok) break;
+          const float base = T::POFF - (m == -INFINITY ? 0.f : m);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t s[32];
-            read_tmem(sb + 32 * h, s);
-            const uint32_t bits = static_cast<uint32_t>(sees >> (32 * h));
-            uint32_t out[32];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              float a = exp2_approx(__uint_as_float(s[c]) * sc - base), b = exp2_approx(__uint_as_float(s[c + 1]) * sc - base);
-              if (!t.plain) {
-                a = bits >> c & 1 ? a : 0.f;
-                b = bits >> (c + 1) & 1 ? b : 0.f;
-              }
-              sum += a + b;
-              const uint32_t hi = t.plain ? pack2_down<T::BF16>(a, b) : pack2<T::BF16>(a, b);
-              const float2 back = unpack2<T::BF16>(hi);
-              const uint32_t lo = pack2<T::BF16>(a - back.x, b - back.y);
-              const int at = c / 16 * 16 + c % 16 / 2;             // keys 16 j ..: 8 columns of high parts, 8 of low ones
-              out[at] = hi;
-              out[at + 8] = t.plain ? above_zero<T::BF16>(lo) : lo;
-            }
-            tmem_st_32x32b_x32(sb + 32 * h, out);
-          }
-          l += sum;
+          for (int h = 0; h < 2; ++h) weights(s[h], sb + 32 * h, make_float2(sc, sc), make_float2(base, base), l);
           tmem_wait_st();
           tc_fence_before();
         }
@@ -718,16 +776,23 @@ struct Softmax {
       if (busy) {
         tc_fence_after();
         float* const part = p.partials + (static_cast<size_t>(2) * blockIdx.x + x.second) * tree_partial_floats(D);
-        const float inv = l == 0.f ? 0.f : vs / l;
+        const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : vs / sum;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t raw[32];
           read_tmem(mine + c, raw);
-          float o[32];
+          bool nan = false;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]);
+          for (int e = 0; e < 32; ++e) nan |= __uint_as_float(raw[e]) != __uint_as_float(raw[e]);
           if (live) {
-            if (odd) add_odd(o, c, w, x, mask);
+            if ((odd || nan) && sum == sum) {
+              float o[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]);
+              add_odd(o, c, w, x, mask, nan);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(o[e]);
+            }
             if (x.whole) {
               uint16_t* const to = p.out + token * p.ldo + static_cast<int64_t>(head) * D + c;
 #pragma unroll
@@ -735,7 +800,7 @@ struct Softmax {
                 uint32_t v[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const float a = o[e + 2 * k] * inv, b = o[e + 2 * k + 1] * inv;
+                  const float a = __uint_as_float(raw[e + 2 * k]) * inv, b = __uint_as_float(raw[e + 2 * k + 1]) * inv;
                   v[k] = p.q_bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
                 }
                 *reinterpret_cast<uint4*>(to + e) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -743,17 +808,17 @@ struct Softmax {
             } else {
               float* const to = part + 2 * kTreeRows + static_cast<size_t>(mr) * D + c;
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(to + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
             }
           }
         }
         tc_fence_before();
         if (live) {
           if (x.whole) {
-            if (p.lse != nullptr) p.lse[token * p.q_heads + head] = l == 0.f ? -INFINITY : (m - T::POFF) * kLn2 + logf(l);
+            if (p.lse != nullptr) p.lse[token * p.q_heads + head] = sum == 0.f ? -INFINITY : (m - T::POFF) * kLn2 + logf(sum);
           } else {
             part[mr] = m;
-            part[kTreeRows + mr] = l;
+            part[kTreeRows + mr] = sum;
           }
         }
       }
