@@ -86,32 +86,32 @@ using attn::widen_lo;
 
 constexpr int kKeys = 64;                // keys of a tile
 constexpr int kSegmentCost = 2;          // what a segment costs besides its tiles, in tiles
-constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5, kLoadWarps = 2;      // seven: four to a scheduler for two blocks, 128 registers
-constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
-constexpr int kAhead = 8;                // pieces: more than the loading warps can be ahead of the others, or of each other
+constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kAhead = 16;               // pieces: more than the loading warps can be ahead of the others, or of each other
 
 template <int CACHE, int D>
 struct Traits {
   static constexpr bool F8 = CACHE == kCacheF8, BF16 = CACHE == kCacheBf16;
   static constexpr int ROW = D * (F8 ? 1 : 2);                   // bytes of a cached row
   static constexpr int BLOCKS = tree_blocks_per_sm(D);
-  static constexpr int Q = kTreeRows * D * 2, SLOT = kKeys * D * 2, STAGE = F8 ? SLOT / 2 : 0;
-  static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 12) : F8 ? 3 : 5;
-  static constexpr int STAGES = F8 ? (D == 64 ? 12 : 4) : 0;     // of 8-bit rows on their way
+  // up to eight warps: four to a scheduler for two blocks, so 128 registers. 8 bits are widened by the loading warps
+  static constexpr int LOADERS = F8 ? 3 : 2, THREADS = 32 * (kLoadWarp + LOADERS);
+  // queries as the MMA's operand in tensor memory, or, where that has no room for two buffers of S beside them, in shared memory
+  static constexpr bool QT = D != 128;
+  static constexpr int Q = QT ? kSoftmaxWarps * 4096 : kTreeRows * D * 2;        // the results pass through it, 4 KB a warp
+  static constexpr int SLOT = kKeys * D * 2, STAGE = F8 ? SLOT / 2 : 0;
+  static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 12) : D == 128 ? (F8 ? 3 : 5) : F8 ? 4 : 6;
+  static constexpr int STAGES = F8 ? (D == 64 ? 12 : D == 128 ? 4 : 5) : 0;      // of 8-bit rows on their way
   static constexpr int LAG = F8 ? STAGES - 1 : 0;                // of them in flight
   static constexpr int OFF_SLOT = Q, OFF_STAGE = OFF_SLOT + SLOTS * SLOT, OFF_MISC = OFF_STAGE + STAGES * STAGE;
   static constexpr int SMEM = OFF_MISC + 1024;
-  static constexpr int SBUF = D == 128 ? 2 : 3;                  // buffers of S and P
-  static constexpr int TMEM = D == 256 ? 512 : 256, TMEM_S = D;  // columns; O in the first D
+  static constexpr int SBUF = 2;                                 // buffers of S and P
+  static constexpr int TMEM = D == 256 ? 512 : 256, TMEM_S = D, TMEM_Q = TMEM_S + SBUF * kKeys;      // columns; O in the first D
   static constexpr float POFF = BF16 ? 0.f : 12.f;               // p is kept 2^POFF as large (f16: away from the subnormals)
   static constexpr float SLACK = BF16 ? 8.f : 3.f;               // by how much m may lag behind the maximum
+  static_assert(SMEM <= (BLOCKS == 1 ? 232448 : 115712) && TMEM_Q + (QT ? D / 2 : 0) <= TMEM, "room");
+  static_assert(SLOTS / 2 + 1 < kAhead, "a piece takes two slots at least");
 };
-static_assert(Traits<kCacheBf16, 256>::SMEM <= 232448 && Traits<kCacheF8, 256>::SMEM <= 232448, "one block");
-static_assert(Traits<kCacheBf16, 128>::SMEM <= 115712 && Traits<kCacheF8, 128>::SMEM <= 115712 && Traits<kCacheBf16, 64>::SMEM <= 115712 &&
-                  Traits<kCacheF8, 64>::SMEM <= 115712, "two blocks");
-// a piece takes two slots at least
-static_assert(Traits<kCacheBf16, 64>::SLOTS / 2 + 1 < kAhead, "ahead");
-static_assert(Traits<kCacheBf16, 128>::TMEM_S + 2 * kKeys <= 256 && Traits<kCacheBf16, 256>::TMEM_S + 3 * kKeys <= 512, "tensor memory");
 
 // The small things behind the slots.
 template <class T>
@@ -334,9 +334,7 @@ struct Loader {
   using T = Traits<CACHE, D>;
   static constexpr int CPR = T::ROW / 16;               // 16-byte chunks of a cached row
   static constexpr int RPI = 32 / CPR;                  // rows that one instruction of a warp copies
-  static constexpr int ROWS = kKeys / kLoadWarps;       // of a warp, one to a lane
-  static constexpr int STEPS = ROWS / RPI;
-  static_assert(ROWS == 32, "a lane looks one row up");
+  static constexpr int ALL = kKeys / RPI, STEPS = (ALL + T::LOADERS - 1) / T::LOADERS;
 
   const TreeAttnParams& p;
   uint8_t* smem;
@@ -347,49 +345,49 @@ struct Loader {
   int pieces = 0;                                       // whose loads are done
   bool ok = true;
 
-  __device__ __forceinline__ int page_of(const Walk& w, const Tile& t) const {
-    const int key = t.k0 + warp * ROWS + lane;
-    return key < t.end ? __ldg(p.pages + w.b * p.ldp + p.page.div(key)) : -1;
-  }
-  // Byte offset in the cache of this lane's row, or -1.
-  __device__ __forceinline__ int64_t row_of(const Piece& x, const Tile& t, int page) const {
-    const int key = t.k0 + warp * ROWS + lane;
-    if (key >= t.end) return -1;
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-      set_status(p.status, TL_EDATA);
-      return -1;
+  // Each warp knows all rows of a tile: a lane the rows of keys lane and lane + 32.
+  struct Rows {
+    int64_t off[2];                                     // byte offset in the cache, or -1
+  };
+  __device__ __forceinline__ void pages_of(const Walk& w, const Tile& t, int (&page)[2]) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = t.k0 + 32 * h + lane;
+      page[h] = key < t.end ? __ldg(p.pages + w.b * p.ldp + p.page.div(key)) : -1;
     }
-    return page * p.page_stride + x.kvh * p.head_stride + static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
   }
-  // Each 16 lanes' rows follow each other at equal distances.
-  __device__ __forceinline__ bool even(int64_t off) const {
-    const int64_t first = __shfl_sync(0xffffffffu, off, lane & 16);
-    return __all_sync(0xffffffffu, first >= 0 && off == first + (lane & 15) * p.token_stride);
+  __device__ __forceinline__ void rows_of(const Piece& x, const Tile& t, const int (&page)[2], Rows& r) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = t.k0 + 32 * h + lane;
+      r.off[h] = -1;
+      if (key >= t.end) continue;
+      if (static_cast<unsigned>(page[h]) < static_cast<unsigned>(p.num_pages))
+        r.off[h] = page[h] * p.page_stride + x.kvh * p.head_stride + static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
+      else
+        set_status(p.status, TL_EDATA);
+    }
   }
+  // Instruction i of this warp: its first row, or none; a lane copies chunk lane % CPR of row (that) + lane / CPR.
+  __device__ __forceinline__ int first_row(int i) const { return (i * T::LOADERS + warp) * RPI; }
+  __device__ __forceinline__ bool there(int i) const { return ALL % T::LOADERS == 0 || i * T::LOADERS + warp < ALL; }
 
   __device__ __forceinline__ void wait_empty(uint32_t i) {
     if (i >= T::SLOTS) ok = wait_all(misc->empty[i % T::SLOTS], i / T::SLOTS - 1, &misc->abort, p.status);
   }
 
-  __device__ __forceinline__ void copy(const uint8_t* base, int64_t off, bool runs) {
+  __device__ __forceinline__ void copy(const uint8_t* base, const Rows& rows) {
     const int row = lane / CPR, chunk = lane % CPR;
-    const uint32_t to = T::F8 ? smem_u32(smem) + T::OFF_STAGE + issued % (T::F8 ? T::STAGES : 1) * T::STAGE + (warp * 32 + lane) * 16
+    const uint32_t to = T::F8 ? smem_u32(smem) + T::OFF_STAGE + issued % (T::F8 ? T::STAGES : 1) * T::STAGE
                               : smem_u32(smem) + T::OFF_SLOT + issued % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
-    auto dst = [&](int i) { return T::F8 ? to + i * (kLoadWarps * 32 * 16) : to + swizzled(warp * ROWS + i * RPI + row, chunk % 8); };
     base += chunk * 16;
-    if (runs) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint8_t* from = base + __shfl_sync(0xffffffffu, off, 16 * g) + row * p.token_stride;
-#pragma unroll
-        for (int i = 0; i < STEPS / 2; ++i, from += RPI * p.token_stride) cp_async16(dst(g * (STEPS / 2) + i), from);
-      }
-    } else {
-#pragma unroll 4
-      for (int i = 0; i < STEPS; ++i) {
-        const int64_t o = __shfl_sync(0xffffffffu, off, i * RPI + row);
-        cp_async16(dst(i), base + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
-      }
+#pragma unroll 8
+    for (int i = 0; i < STEPS; ++i) {
+      if (!there(i)) continue;
+      const int r = first_row(i);
+      const int64_t o = __shfl_sync(0xffffffffu, r < 32 ? rows.off[0] : rows.off[1], (r + row) & 31);
+      const uint32_t dst = T::F8 ? to + (r + row) * T::ROW + chunk * 16 : to + swizzled(r + row, chunk % 8);
+      cp_async16(dst, base + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
     }
   }
 
@@ -400,10 +398,10 @@ struct Loader {
   }
 
   // 16 bits: straight into the slot; the copies themselves arrive when they have landed.
-  __device__ __forceinline__ void load16(const uint8_t* base, int64_t off, bool runs, bool check, bool last) {
+  __device__ __forceinline__ void load16(const uint8_t* base, const Rows& rows, bool check, bool last) {
     wait_empty(issued);
     if (!ok) return;
-    copy(base, off, runs);
+    copy(base, rows);
     const uint32_t full = smem_u32(&misc->full[issued % T::SLOTS]);
     if (!check) {
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
@@ -416,7 +414,8 @@ struct Loader {
       bool found = false;
 #pragma unroll 2
       for (int i = 0; i < STEPS; ++i) {
-        uint4* const at = reinterpret_cast<uint4*>(to + swizzled(warp * ROWS + i * RPI + row, chunk % 8));
+        if (!there(i)) continue;
+        uint4* const at = reinterpret_cast<uint4*>(to + swizzled(first_row(i) + row, chunk % 8));
         uint4 x = *at;
         const uint32_t a = __vcmpeq2(x.x & E, E), b = __vcmpeq2(x.y & E, E), c = __vcmpeq2(x.z & E, E), d = __vcmpeq2(x.w & E, E);
         if ((a | b | c | d) != 0) *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d), found = true;
@@ -430,8 +429,8 @@ struct Loader {
   }
 
   // 8 bits: into this thread's part of a stage, some loads ahead.
-  __device__ __forceinline__ void load8(const uint8_t* base, int64_t off, bool runs, bool check, bool last) {
-    copy(base, off, runs);
+  __device__ __forceinline__ void load8(const uint8_t* base, const Rows& rows, bool check, bool last) {
+    copy(base, rows);
     cp_async_commit();
     ++issued;
     checks = checks << 1 | check;
@@ -449,12 +448,13 @@ struct Loader {
     const bool check = checks >> age & 1;
     bool found = false;
     const int row = lane / CPR, chunk = lane % CPR;
-    const uint8_t* from = smem + T::OFF_STAGE + done % (T::F8 ? T::STAGES : 1) * T::STAGE + (warp * 32 + lane) * 16;
+    const uint8_t* from = smem + T::OFF_STAGE + done % (T::F8 ? T::STAGES : 1) * T::STAGE + chunk * 16;
     uint8_t* to = smem + T::OFF_SLOT + done % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128);
 #pragma unroll 4
     for (int i = 0; i < STEPS; ++i) {
-      const int kk = warp * ROWS + i * RPI + row;
-      uint4 x = *reinterpret_cast<const uint4*>(from + i * (kLoadWarps * 32 * 16));
+      if (!there(i)) continue;
+      const int kk = first_row(i) + row;
+      uint4 x = *reinterpret_cast<const uint4*>(from + kk * T::ROW);
       if (check) {                                      // e4m3 has NaN (0x7F, 0xFF), no infinities
         constexpr uint32_t N = 0x7F7F7F7Fu;
         const uint32_t a = __vcmpeq4(x.x & N, N), b = __vcmpeq4(x.y & N, N), c = __vcmpeq4(x.z & N, N), d = __vcmpeq4(x.w & N, N);
@@ -479,33 +479,31 @@ struct Loader {
       // loads K0, K1, V0, K2, V1, ...: `now` is the tile of the next K, `before` the one whose V is due
       const int n = x.end - x.begin;
       Tile t = tile(p, w.r, x.begin);
-      int page = page_of(w, t);
-      int64_t before = -1;
-      bool before_runs = false, before_plain = true;
+      int page[2];
+      pages_of(w, t, page);
+      Rows before = {{-1, -1}};
+      bool before_plain = true;
       for (int i = 0; ok && i <= n; ++i) {
         const Tile now = t;
-        int64_t off = -1;
-        bool runs = false;
+        Rows rows = {{-1, -1}};
         if (i < n) {
-          off = row_of(x, now, page);
-          runs = even(off);
+          rows_of(x, now, page, rows);
           if (i + 1 < n) {
             t = tile(p, w.r, x.begin + i + 1);
-            page = page_of(w, t);
+            pages_of(w, t, page);
           }
         }
 #pragma unroll 1
         for (int v = 0; ok && v < 2; ++v) {
           if (v ? i == 0 : i == n) continue;
-          const uint8_t* const base = v ? p.v : p.k;
-          const int64_t o = v ? before : off;
-          const bool r = v ? before_runs : runs, check = v && !before_plain, last = v && i == n;
+          const Rows& r = v ? before : rows;
+          const bool check = v && !before_plain, last = v && i == n;
           if constexpr (T::F8)
-            load8(base, o, r, check, last);
+            load8(v ? p.v : p.k, r, check, last);
           else
-            load16(base, o, r, check, last);
+            load16(v ? p.v : p.k, r, check, last);
         }
-        before = off, before_runs = runs, before_plain = now.plain;
+        before = rows, before_plain = now.plain;
       }
     }
     cp_async_wait<0>();
@@ -529,7 +527,7 @@ __device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* sme
   auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); };
   auto scores = [&](uint32_t t) {                       // S of tile t
     const uint32_t buf = t % T::SBUF, s = loads % T::SLOTS;
-    if (t >= T::SBUF && !wait(misc->pv_done[buf], t / T::SBUF - 1)) return;
+    // (S's buffer was P's of two tiles ago: the MMAs that read it were issued before, and one thread's MMAs run in order)
     if (!wait(misc->full[s], loads / T::SLOTS)) return;
     fence_proxy_async_smem();                           // (rows that ordinary copies wrote, to the MMAs)
     tc_fence_after();
@@ -538,8 +536,11 @@ __device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* sme
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint32_t off = (i % 4) * 32;
-        mma_ss(tm + T::TMEM_S + buf * kKeys, smem_desc_sw128(base + i / 4 * (kTreeRows * 128) + off), smem_desc_sw128(kb + i / 4 * (kKeys * 128) + off),
-               ID_S, i > 0);
+        const uint64_t k = smem_desc_sw128(kb + i / 4 * (kKeys * 128) + off);
+        if constexpr (T::QT)
+          mma_ts(tm + T::TMEM_S + buf * kKeys, tm + T::TMEM_Q + 8 * i, k, ID_S, i > 0);
+        else
+          mma_ss(tm + T::TMEM_S + buf * kKeys, smem_desc_sw128(base + i / 4 * (kTreeRows * 128) + off), k, ID_S, i > 0);
       }
       tc_commit(smem_u32(&misc->empty[s]));
       tc_commit(smem_u32(&misc->s_full[buf]));
@@ -588,9 +589,9 @@ struct Softmax {
 
   __device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); }
 
-  // This row's query into shared memory as the MMA's operand, times the sign of the scale; returns by what its scores are scaled
-  // besides (8-bit caches: its power of two).
-  __device__ __forceinline__ float put_query(const uint16_t* row) {
+  // This row's query to where the MMAs take it, times the sign of the scale; returns by what its scores are scaled
+  // besides (8-bit caches: its power of two). The whole warp together; rows that are not live become zero.
+  __device__ __forceinline__ float put_query(const uint16_t* row, uint32_t mine, bool live) {
     const int r = warp * 32 + lane;
     float up = 1.f, by = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
     const bool narrow = T::F8 && p.q_bf16;
@@ -598,7 +599,7 @@ struct Softmax {
       float top = 0.f;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row) + i);
+        const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(row) + i) : make_uint4(0, 0, 0, 0);
         const uint32_t* const w = &x.x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -611,18 +612,34 @@ struct Softmax {
       up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
       by *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
-#pragma unroll 8
-    for (int i = 0; i < D / 8; ++i) {
-      uint4 x = __ldg(reinterpret_cast<const uint4*>(row) + i);
-      if (by != 1.f || narrow) {
-        uint32_t* const w = &x.x;
+#pragma unroll (D == 256 ? 2 : 1)
+    for (int c = 0; c < D / 64; ++c) {                  // 128 bytes of the row at a time
+      uint32_t w[32];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(row) + 8 * c + i) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+      if (by != 1.f || narrow) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
           const float2 f = T::BF16 || p.q_bf16 ? unpack2<true>(w[j]) : unpack2<false>(w[j]);
           w[j] = pack2<T::BF16>(f.x * by, f.y * by);
         }
       }
-      *reinterpret_cast<uint4*>(smem + i / 8 * (kTreeRows * 128) + swizzled(r, i % 8)) = x;
+      if constexpr (T::QT) {
+        tmem_st_32x32b_x32(mine + T::TMEM_Q + 32 * c, w);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(smem + c * (kTreeRows * 128) + swizzled(r, i)) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
+    }
+    if constexpr (T::QT) {
+      tmem_wait_st();
+      tc_fence_before();
+    } else {
+      fence_proxy_async_smem();
     }
     return up;
   }
@@ -718,11 +735,8 @@ struct Softmax {
         sc *= __ldg(p.k_scale + x.kvh);
         vs = __ldg(p.v_scale + x.kvh);
       }
-      if (live) {
-        mask = static_cast<uint64_t>(__ldg(p.masks + token)) & low_bits(w.r.n);
-        sc *= put_query(p.q + token * p.ldq + static_cast<int64_t>(head) * D);
-      }
-      fence_proxy_async_smem();
+      if (live) mask = static_cast<uint64_t>(__ldg(p.masks + token)) & low_bits(w.r.n);
+      if (busy) sc *= put_query(p.q + token * p.ldq + static_cast<int64_t>(head) * D, mine, live);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&misc->q_full));
       float m = -INFINITY;
@@ -777,40 +791,52 @@ struct Softmax {
         tc_fence_after();
         float* const part = p.partials + (static_cast<size_t>(2) * blockIdx.x + x.second) * tree_partial_floats(D);
         const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : vs / sum;
+        uint8_t* const stage = smem + warp * 4096;      // 128 bytes of 32 rows
+        uint16_t* const to = p.out + token * p.ldo + static_cast<int64_t>(head) * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
-          uint32_t raw[32];
-          read_tmem(mine + c, raw);
+          uint32_t o[32];
+          read_tmem(mine + c, o);
           bool nan = false;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) nan |= __uint_as_float(raw[e]) != __uint_as_float(raw[e]);
-          if (live) {
-            if ((odd || nan) && sum == sum) {
-              float o[32];
+          for (int e = 0; e < 32; ++e) nan |= __uint_as_float(o[e]) != __uint_as_float(o[e]);
+          if (live && (odd || nan) && sum == sum) {
+            float f[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]);
-              add_odd(o, c, w, x, mask, nan);
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]);
+            add_odd(f, c, w, x, mask, nan);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(o[e]);
-            }
-            if (x.whole) {
-              uint16_t* const to = p.out + token * p.ldo + static_cast<int64_t>(head) * D + c;
-#pragma unroll
-              for (int e = 0; e < 32; e += 8) {
-                uint32_t v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float a = __uint_as_float(raw[e + 2 * k]) * inv, b = __uint_as_float(raw[e + 2 * k + 1]) * inv;
-                  v[k] = p.q_bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
-                }
-                *reinterpret_cast<uint4*>(to + e) = make_uint4(v[0], v[1], v[2], v[3]);
-              }
-            } else {
-              float* const to = part + 2 * kTreeRows + static_cast<size_t>(mr) * D + c;
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(to + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f[e]);
           }
+          if (!x.whole) {                               // [4 channels][row]: neighbouring rows side by side
+            float4* const q = reinterpret_cast<float4*>(part + 2 * kTreeRows) + (c / 4) * kTreeRows + mr;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              if (live)
+                q[e / 4 * kTreeRows] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            continue;
+          }
+          // 64 channels of 32 rows pass through shared memory, so that eight lanes write 128 bytes of a row
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = __uint_as_float(o[e + 2 * k]) * inv, b = __uint_as_float(o[e + 2 * k + 1]) * inv;
+              v[k] = p.q_bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
+            }
+            *reinterpret_cast<uint4*>(stage + swizzled(lane, c % 64 / 8 + e / 8)) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+          if (c % 64 == 0) continue;
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + lane / 8, u = lane % 8;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + swizzled(r, u));
+            uint16_t* const at = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
+            if (warp * 32 + r < rows) *reinterpret_cast<uint4*>(at + c - 32 + 8 * u) = v;
+          }
+          __syncwarp();
         }
         tc_fence_before();
         if (live) {
@@ -829,7 +855,7 @@ struct Softmax {
 };
 
 template <int CACHE, int D>
-__global__ void __launch_bounds__(kThreads, Traits<CACHE, D>::BLOCKS) tree_attention_kernel(const __grid_constant__ TreeAttnParams p) {
+__global__ void __launch_bounds__(Traits<CACHE, D>::THREADS, Traits<CACHE, D>::BLOCKS) tree_attention_kernel(const __grid_constant__ TreeAttnParams p) {
   using T = Traits<CACHE, D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc<T>* const misc = reinterpret_cast<Misc<T>*>(smem + T::OFF_MISC);
@@ -840,14 +866,14 @@ __global__ void __launch_bounds__(kThreads, Traits<CACHE, D>::BLOCKS) tree_atten
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < T::SLOTS; ++i) mbar_init(smem_u32(&misc->full[i]), kLoadWarps * 32), mbar_init(smem_u32(&misc->empty[i]), 1);
+    for (int i = 0; i < T::SLOTS; ++i) mbar_init(smem_u32(&misc->full[i]), T::LOADERS * 32), mbar_init(smem_u32(&misc->empty[i]), 1);
     for (int i = 0; i < T::SBUF; ++i) {
       mbar_init(smem_u32(&misc->s_full[i]), 1);
       mbar_init(smem_u32(&misc->p_full[i]), kSoftmaxWarps);
       mbar_init(smem_u32(&misc->pv_done[i]), 1);
     }
     mbar_init(smem_u32(&misc->q_full), kSoftmaxWarps);
-    for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&misc->loaded[i]), kLoadWarps * 32), misc->flag[i] = 0;
+    for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&misc->loaded[i]), T::LOADERS * 32), misc->flag[i] = 0;
     misc->abort = 0;
     fence_barrier_init();
   }
@@ -878,45 +904,78 @@ __global__ void __launch_bounds__(kThreads, Traits<CACHE, D>::BLOCKS) tree_atten
 }
 
 // ---- the second kernel: segments that were cut. Block x joins the one that begins in the share of block x of the first kernel,
-// some of its rows; a thread takes four channels of a row.
-constexpr int kJoinThreads = 256;
+// 32 channels of it; a thread takes them of a row, and where the rows need fewer warps than there are, those share the partials out.
+constexpr int kJoinWarps = 8;
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeAttnParams p) {
-  constexpr int PER_ROW = D / 4, ROWS = kJoinThreads / PER_ROW;
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeAttnParams p) {
   constexpr float POFF = F16 ? Traits<kCacheF16, D>::POFF : Traits<kCacheBf16, D>::POFF;
+  __shared__ float s_o[kJoinWarps][33][32];
+  __shared__ float s_m[kJoinWarps][32];
   pdl_wait_prior();
   pdl_launch_dependents();
   const TreeCut c = p.cuts[blockIdx.x];
-  const int d = threadIdx.x % PER_ROW;
-  for (int r = blockIdx.y * ROWS + threadIdx.x / PER_ROW; c.parts > 0 && r < c.rows; r += gridDim.y * ROWS) {
-    auto part = [&](int i) { return p.partials + (static_cast<size_t>(2) * (blockIdx.x + i) + (i == 0)) * tree_partial_floats(D); };
-    float top = -INFINITY;
+  if (c.parts == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row_warps = c.rows <= 32 ? 1 : c.rows <= 64 ? 2 : 4, share = kJoinWarps / row_warps;     // warps to 32 rows
+  const int r = warp % row_warps * 32 + lane, turn = warp / row_warps, d4 = blockIdx.y * 8;
+  auto part = [&](int i) { return p.partials + (static_cast<size_t>(2) * (blockIdx.x + i) + (i == 0)) * tree_partial_floats(D); };
+  float top = -INFINITY, l = 0.f, a[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) a[e] = 0.f;
+  if (r < c.rows) {
 #pragma unroll 8
-    for (int i = 0; i < c.parts; ++i) top = fmaxf(top, __ldcg(part(i) + r));
+    for (int i = turn; i < c.parts; i += share) top = fmaxf(top, __ldcg(part(i) + r));
     const float base = top == -INFINITY ? 0.f : top;
-    float l = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < c.parts; ++i) {
+#pragma unroll 2
+    for (int i = turn; i < c.parts; i += share) {
       const float* const q = part(i);
       const float f = faded(__ldcg(q + r) - base);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 2 * kTreeRows + static_cast<size_t>(r) * D) + d);
       l += f * __ldcg(q + kTreeRows + r);
-      a.x += f * v.x;
-      a.y += f * v.y;
-      a.z += f * v.z;
-      a.w += f * v.w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 2 * kTreeRows) + (d4 + e) * kTreeRows + r);
+        a[4 * e] += f * v.x;
+        a[4 * e + 1] += f * v.y;
+        a[4 * e + 2] += f * v.z;
+        a[4 * e + 3] += f * v.w;
+      }
     }
-    const int gr = c.first_row + r, node = static_cast<int>(p.group_div.div(gr)), head = c.kvh * p.group + gr - node * p.group;
-    const int64_t token = static_cast<int64_t>(c.row0) + node;
-    const float inv = l == 0.f ? 0.f : c.v_scale / l;
-    uint2 out;
-    out.x = p.q_bf16 ? pack2<true>(a.x * inv, a.y * inv) : pack2<false>(a.x * inv, a.y * inv);
-    out.y = p.q_bf16 ? pack2<true>(a.z * inv, a.w * inv) : pack2<false>(a.z * inv, a.w * inv);
-    *reinterpret_cast<uint2*>(p.out + token * p.ldo + static_cast<int64_t>(head) * D + 4 * d) = out;
-    if (d == 0 && p.lse != nullptr) p.lse[token * p.q_heads + head] = l == 0.f ? -INFINITY : (top - POFF) * kLn2 + logf(l);
   }
+  // the warps of the same rows: halves add to halves, in a fixed order
+  for (int n = share / 2; n > 0; n /= 2) {
+    if (turn >= n && turn < 2 * n) {
+      s_m[warp][lane] = top;
+      s_o[warp][32][lane] = l;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) s_o[warp][e][lane] = a[e];
+    }
+    __syncthreads();
+    if (turn < n) {
+      const int other = warp + n * row_warps;
+      const float m2 = s_m[other][lane], most = fmaxf(top, m2), base = most == -INFINITY ? 0.f : most;
+      const float f1 = faded(top - base), f2 = faded(m2 - base);
+      top = most;
+      l = l * f1 + s_o[other][32][lane] * f2;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) a[e] = a[e] * f1 + s_o[other][e][lane] * f2;
+    }
+    __syncthreads();
+  }
+  if (turn != 0 || r >= c.rows) return;
+  const int gr = c.first_row + r, node = static_cast<int>(p.group_div.div(gr)), head = c.kvh * p.group + gr - node * p.group;
+  const int64_t token = static_cast<int64_t>(c.row0) + node;
+  const float inv = l == 0.f ? 0.f : c.v_scale / l;
+  uint16_t* const to = p.out + token * p.ldo + static_cast<int64_t>(head) * D + 4 * d4;
+#pragma unroll
+  for (int e = 0; e < 32; e += 8) {
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = p.q_bf16 ? pack2<true>(a[e + 2 * k] * inv, a[e + 2 * k + 1] * inv) : pack2<false>(a[e + 2 * k] * inv, a[e + 2 * k + 1] * inv);
+    *reinterpret_cast<uint4*>(to + e) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  if (blockIdx.y == 0 && p.lse != nullptr) p.lse[token * p.q_heads + head] = l == 0.f ? -INFINITY : (top - POFF) * kLn2 + logf(l);
 }
 
 template <int CACHE, int D>
@@ -939,9 +998,9 @@ cudaError_t launch(TreeAttnParams& p, int sms, cudaStream_t st) {
   const long long most = static_cast<long long>(p.B) * p.kv_heads * ((nodes * p.group + kTreeRows - 1) / kTreeRows) * ((keys + 3 * kKeys) / kKeys + kSegmentCost);
   if (grid > most) grid = most;
   p.grid = static_cast<int>(grid);
-  e = launch_pdl(tree_attention_kernel<CACHE, D>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), T::SMEM, st, p);
+  e = launch_pdl(tree_attention_kernel<CACHE, D>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
   if (e != cudaSuccess || grid == 1) return e;
-  return launch_pdl(tree_join_kernel<D, !T::BF16>, dim3(static_cast<unsigned>(grid), 8), dim3(kJoinThreads), 0, st, p);
+  return launch_pdl(tree_join_kernel<D, !T::BF16>, dim3(static_cast<unsigned>(grid), D / 32), dim3(kJoinWarps * 32), 0, st, p);
 }
 
 template <int CACHE>
