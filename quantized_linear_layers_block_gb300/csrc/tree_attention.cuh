@@ -94,8 +94,10 @@ struct Traits {
   static constexpr bool F8 = CACHE == kCacheF8, BF16 = CACHE == kCacheBf16;
   static constexpr int ROW = D * (F8 ? 1 : 2);                   // bytes of a cached row
   static constexpr int BLOCKS = tree_blocks_per_sm(D);
-  // up to eight warps: four to a scheduler for two blocks, so 128 registers. 8 bits are widened by the loading warps
-  static constexpr int LOADERS = F8 ? 3 : 2, THREADS = 32 * (kLoadWarp + LOADERS);
+  // Up to eight warps are four to a scheduler for two blocks, and have 128 registers. 8 bits are widened by the loading warps, which
+  // takes one on each scheduler; the nine warps have 96 registers then, so S is read from tensor memory twice.
+  static constexpr int LOADERS = F8 ? 4 : 2, THREADS = 32 * (kLoadWarp + LOADERS);
+  static constexpr bool TWICE = F8 && BLOCKS == 2;
   // queries as the MMA's operand in tensor memory, or, where that has no room for two buffers of S beside them, in shared memory
   static constexpr bool QT = D != 128;
   static constexpr int Q = QT ? kSoftmaxWarps * 4096 : kTreeRows * D * 2;        // the results pass through it, 4 KB a warp
@@ -126,16 +128,58 @@ struct Misc {
 };
 
 // ---- PTX
-// D[tmem] (+)= A[smem] B[smem]^T and A[tmem] B[smem]^T, 16 channels or keys
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// MMAs in straight-line blocks, with 32-bit arithmetic on the descriptors (all of which have the same upper half): a thread that builds
+// every descriptor anew issues an MMA in 82 cycles, which is longer than one of 64 columns takes.
+// S (+)= Q K^T for 64 channels, Q in tensor memory (8 columns for 16 channels)
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t bhi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p0, p1;\n .reg .b64 bd;\n .reg .b32 t;\n"
+      "setp.ne.b32 p0, %5, 0;\n setp.eq.b32 p1, %2, %2;\n"
+      "mov.b64 bd, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p0;\n"
+      "add.u32 t, %2, 2;\n mov.b64 bd, {t, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+8], bd, %4, p1;\n"
+      "add.u32 t, %2, 4;\n mov.b64 bd, {t, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+16], bd, %4, p1;\n"
+      "add.u32 t, %2, 6;\n mov.b64 bd, {t, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+24], bd, %4, p1;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(bhi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  mma_f16_ts(d, a, b, idesc, accumulate);
+// the same with Q in shared memory
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p0, p1;\n .reg .b64 ad, bd;\n .reg .b32 t;\n"
+      "setp.ne.b32 p0, %5, 0;\n setp.eq.b32 p1, %2, %2;\n"
+      "mov.b64 ad, {%1, %3};\n mov.b64 bd, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p0;\n"
+      "add.u32 t, %1, 2;\n mov.b64 ad, {t, %3};\n add.u32 t, %2, 2;\n mov.b64 bd, {t, %3};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p1;\n"
+      "add.u32 t, %1, 4;\n mov.b64 ad, {t, %3};\n add.u32 t, %2, 4;\n mov.b64 bd, {t, %3};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p1;\n"
+      "add.u32 t, %1, 6;\n mov.b64 ad, {t, %3};\n add.u32 t, %2, 6;\n mov.b64 bd, {t, %3};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %4, p1;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// O (+)= P V for 64 keys: for each 16 of them 8 columns of high parts, 8 of low ones, and 2048 bytes of V
+__device__ __forceinline__ void mma8_pv(uint32_t d, uint32_t a, uint32_t b, uint32_t bhi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p0, p1;\n .reg .b64 bd;\n .reg .b32 t;\n"
+      "setp.ne.b32 p0, %5, 0;\n setp.eq.b32 p1, %2, %2;\n"
+      "mov.b64 bd, {%2, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+8], bd, %4, p1;\n"
+      "add.u32 t, %2, 128;\n mov.b64 bd, {t, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+16], bd, %4, p1;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+24], bd, %4, p1;\n"
+      "add.u32 t, %2, 256;\n mov.b64 bd, {t, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+32], bd, %4, p1;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+40], bd, %4, p1;\n"
+      "add.u32 t, %2, 384;\n mov.b64 bd, {t, %3};\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+48], bd, %4, p1;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1+56], bd, %4, p1;\n"
+      "}" ::"r"(d), "r"(a), "r"(b), "r"(bhi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Both barriers see one arrival when the MMAs issued so far are done.
+__device__ __forceinline__ void commit2(uint32_t bar1, uint32_t bar2) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];" ::"r"(bar1),
+      "r"(bar2)
+      : "memory");
 }
 // A 64-channel column block of 128-byte rows, 128-byte swizzle; the operand's other dimension is along the rows (K-major: next 8
 // rows at 1024 bytes), or the summed one is (MN-major: next 8 rows at 1024 bytes, the next 64 channels at `block` bytes).
@@ -334,7 +378,7 @@ struct Loader {
   using T = Traits<CACHE, D>;
   static constexpr int CPR = T::ROW / 16;               // 16-byte chunks of a cached row
   static constexpr int RPI = 32 / CPR;                  // rows that one instruction of a warp copies
-  static constexpr int ALL = kKeys / RPI, STEPS = (ALL + T::LOADERS - 1) / T::LOADERS;
+  static constexpr int PER = T::LOADERS * RPI, STEPS = kKeys / PER;      // rows of an instruction of all warps
 
   const TreeAttnParams& p;
   uint8_t* smem;
@@ -348,6 +392,7 @@ struct Loader {
   // Each warp knows all rows of a tile: a lane the rows of keys lane and lane + 32.
   struct Rows {
     int64_t off[2];                                     // byte offset in the cache, or -1
+    bool runs;
   };
   __device__ __forceinline__ void pages_of(const Walk& w, const Tile& t, int (&page)[2]) const {
 #pragma unroll
@@ -368,9 +413,18 @@ struct Loader {
         set_status(p.status, TL_EDATA);
     }
   }
-  // Instruction i of this warp: its first row, or none; a lane copies chunk lane % CPR of row (that) + lane / CPR.
-  __device__ __forceinline__ int first_row(int i) const { return (i * T::LOADERS + warp) * RPI; }
-  __device__ __forceinline__ bool there(int i) const { return ALL % T::LOADERS == 0 || i * T::LOADERS + warp < ALL; }
+  // Instruction i of this warp: its first row; a lane copies chunk lane % CPR of row (that) + lane / CPR.
+  __device__ __forceinline__ int first_row(int i) const { return i * PER + warp * RPI; }
+  // Each 16 rows follow each other at equal distances.
+  __device__ __forceinline__ bool even(const Rows& r) const {
+    bool good = true;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t first = __shfl_sync(0xffffffffu, r.off[h], lane & 16);
+      good &= first >= 0 && r.off[h] == first + (lane & 15) * p.token_stride;
+    }
+    return __all_sync(0xffffffffu, good);
+  }
 
   __device__ __forceinline__ void wait_empty(uint32_t i) {
     if (i >= T::SLOTS) ok = wait_all(misc->empty[i % T::SLOTS], i / T::SLOTS - 1, &misc->abort, p.status);
@@ -381,13 +435,26 @@ struct Loader {
     const uint32_t to = T::F8 ? smem_u32(smem) + T::OFF_STAGE + issued % (T::F8 ? T::STAGES : 1) * T::STAGE
                               : smem_u32(smem) + T::OFF_SLOT + issued % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
     base += chunk * 16;
-#pragma unroll 8
-    for (int i = 0; i < STEPS; ++i) {
-      if (!there(i)) continue;
-      const int r = first_row(i);
-      const int64_t o = __shfl_sync(0xffffffffu, r < 32 ? rows.off[0] : rows.off[1], (r + row) & 31);
-      const uint32_t dst = T::F8 ? to + (r + row) * T::ROW + chunk * 16 : to + swizzled(r + row, chunk % 8);
-      cp_async16(dst, base + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
+    auto dst = [&](int i) {
+      const int r = first_row(i) + row;
+      return T::F8 ? to + r * T::ROW + chunk * 16 : to + swizzled(r, chunk % 8);
+    };
+    if (rows.runs) {                                    // one address for 16 rows
+      constexpr int G = PER < 16 ? 16 / PER : 1;
+      const uint8_t* const mine = base + ((warp * RPI + row) & 15) * p.token_stride;
+#pragma unroll
+      for (int i = 0; i < STEPS; i += G) {
+        const uint8_t* from = mine + __shfl_sync(0xffffffffu, rows.off[i * PER / 32], PER < 16 ? i * PER & 16 : first_row(i) & 16);
+#pragma unroll
+        for (int j = 0; j < G; ++j, from += PER * p.token_stride) cp_async16(dst(i + j), from);
+      }
+    } else {
+#pragma unroll 2
+      for (int i = 0; i < STEPS; ++i) {
+        const int r = first_row(i);
+        const int64_t o = __shfl_sync(0xffffffffu, r < 32 ? rows.off[0] : rows.off[1], (r + row) & 31);
+        cp_async16(dst(i), base + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
+      }
     }
   }
 
@@ -414,7 +481,6 @@ struct Loader {
       bool found = false;
 #pragma unroll 2
       for (int i = 0; i < STEPS; ++i) {
-        if (!there(i)) continue;
         uint4* const at = reinterpret_cast<uint4*>(to + swizzled(first_row(i) + row, chunk % 8));
         uint4 x = *at;
         const uint32_t a = __vcmpeq2(x.x & E, E), b = __vcmpeq2(x.y & E, E), c = __vcmpeq2(x.z & E, E), d = __vcmpeq2(x.w & E, E);
@@ -452,7 +518,6 @@ struct Loader {
     uint8_t* to = smem + T::OFF_SLOT + done % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128);
 #pragma unroll 4
     for (int i = 0; i < STEPS; ++i) {
-      if (!there(i)) continue;
       const int kk = first_row(i) + row;
       uint4 x = *reinterpret_cast<const uint4*>(from + kk * T::ROW);
       if (check) {                                      // e4m3 has NaN (0x7F, 0xFF), no infinities
@@ -461,8 +526,11 @@ struct Loader {
         found |= (a | b | c | d) != 0;
         x = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d);
       }
-      *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2)) = make_uint4(widen_lo(x.x), widen_hi(x.x), widen_lo(x.y), widen_hi(x.y));
-      *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2 + 1)) = make_uint4(widen_lo(x.z), widen_hi(x.z), widen_lo(x.w), widen_hi(x.w));
+      // (lanes of the two 64-channel blocks write their halves in different order: different banks)
+      const bool turn = chunk & 4;
+      if (turn) x = make_uint4(x.z, x.w, x.x, x.y);
+      *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2 + turn)) = make_uint4(widen_lo(x.x), widen_hi(x.x), widen_lo(x.y), widen_hi(x.y));
+      *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2 + !turn)) = make_uint4(widen_lo(x.z), widen_hi(x.z), widen_lo(x.w), widen_hi(x.w));
     }
     if (found) note_odd();
     fence_proxy_async_smem();
@@ -481,13 +549,14 @@ struct Loader {
       Tile t = tile(p, w.r, x.begin);
       int page[2];
       pages_of(w, t, page);
-      Rows before = {{-1, -1}};
+      Rows before = {{-1, -1}, false};
       bool before_plain = true;
       for (int i = 0; ok && i <= n; ++i) {
         const Tile now = t;
-        Rows rows = {{-1, -1}};
+        Rows rows = {{-1, -1}, false};
         if (i < n) {
           rows_of(x, now, page, rows);
+          rows.runs = even(rows);
           if (i + 1 < n) {
             t = tile(p, w.r, x.begin + i + 1);
             pages_of(w, t, page);
@@ -520,8 +589,11 @@ __device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* sme
   Walk w;
   w.init(p, false);
   Piece x;
-  const bool elected = (threadIdx.x & 31) == 0;
-  const uint32_t base = smem_u32(smem), tm = misc->tmem;
+  uint32_t elected;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(elected));
+  const uint32_t tm = misc->tmem;
+  const uint64_t kd = smem_desc_sw128(smem_u32(smem)), vd = desc_mn(smem_u32(smem), kKeys * 128);      // of the first byte of shared memory
+  const uint32_t lo = static_cast<uint32_t>(kd), khi = static_cast<uint32_t>(kd >> 32), vlo = static_cast<uint32_t>(vd), vhi = static_cast<uint32_t>(vd >> 32);
   uint32_t loads = 0, tiles = 0, pieces = 0;
   bool ok = true;
   auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); };
@@ -532,18 +604,15 @@ __device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* sme
     fence_proxy_async_smem();                           // (rows that ordinary copies wrote, to the MMAs)
     tc_fence_after();
     if (elected) {
-      const uint32_t kb = base + T::OFF_SLOT + s * T::SLOT;
+      const uint32_t k = lo + (T::OFF_SLOT + s * T::SLOT) / 16;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t off = (i % 4) * 32;
-        const uint64_t k = smem_desc_sw128(kb + i / 4 * (kKeys * 128) + off);
+      for (int c = 0; c < D / 64; ++c) {
         if constexpr (T::QT)
-          mma_ts(tm + T::TMEM_S + buf * kKeys, tm + T::TMEM_Q + 8 * i, k, ID_S, i > 0);
+          mma4_ts(tm + T::TMEM_S + buf * kKeys, tm + T::TMEM_Q + 32 * c, k + c * (kKeys * 128 / 16), khi, ID_S, c > 0);
         else
-          mma_ss(tm + T::TMEM_S + buf * kKeys, smem_desc_sw128(base + i / 4 * (kTreeRows * 128) + off), k, ID_S, i > 0);
+          mma4_ss(tm + T::TMEM_S + buf * kKeys, lo + c * (kTreeRows * 128 / 16), k + c * (kKeys * 128 / 16), khi, ID_S, c > 0);
       }
-      tc_commit(smem_u32(&misc->empty[s]));
-      tc_commit(smem_u32(&misc->s_full[buf]));
+      commit2(smem_u32(&misc->empty[s]), smem_u32(&misc->s_full[buf]));
     }
     __syncwarp();
     ++loads;
@@ -559,15 +628,8 @@ __device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* sme
       fence_proxy_async_smem();
       tc_fence_after();
       if (elected) {
-        const uint32_t vb = base + T::OFF_SLOT + s * T::SLOT, pb = tm + T::TMEM_S + buf * kKeys;
-#pragma unroll
-        for (int j = 0; j < kKeys / 16; ++j) {
-          const uint64_t b = desc_mn(vb + j * 2048, kKeys * 128);
-          mma_ts(tm, pb + 16 * j, b, ID_O, i > x.begin || j > 0);        // high part
-          mma_ts(tm, pb + 16 * j + 8, b, ID_O, 1);                       // low part
-        }
-        tc_commit(smem_u32(&misc->empty[s]));
-        tc_commit(smem_u32(&misc->pv_done[buf]));
+        mma8_pv(tm, tm + T::TMEM_S + buf * kKeys, vlo + (T::OFF_SLOT + s * T::SLOT) / 16, vhi, ID_O, i > x.begin);
+        commit2(smem_u32(&misc->empty[s]), smem_u32(&misc->pv_done[buf]));
       }
       __syncwarp();
       ++loads;
@@ -644,24 +706,39 @@ struct Softmax {
     return up;
   }
 
-  // S of a tile, what the row does not see as -inf; returns its maximum.
-  __device__ __forceinline__ float scores(uint32_t (&s)[2][32], uint32_t at, uint64_t sees) {
-    tmem_ld_32x32b_x32(at, s[0]);
-    read_tmem(at + 32, s[1]);
-    arrived(s[0]);
-    if (sees != ~0ull) {
+  // S of 32 keys, what the row does not see as -inf.
+  __device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t sees) {
+    if (sees != ~0u) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (!(sees >> (32 * h + c) & 1)) s[h][c] = 0xFF800000u;
+      for (int c = 0; c < 32; ++c)
+        if (!(sees >> c & 1)) s[c] = 0xFF800000u;
     }
+  }
+  __device__ __forceinline__ float highest(const uint32_t (&s)[32]) {
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < 32; c += 2) top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(s[h][c]), __uint_as_float(s[h][c + 1]));
+    for (int c = 0; c < 32; c += 2) top[c / 2 % 4] = max3(top[c / 2 % 4], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
     return max3(fmaxf(top[0], top[1]), top[2], top[3]);
+  }
+  // Of a tile; returns the maximum.
+  __device__ __forceinline__ float scores(uint32_t (&s)[T::TWICE ? 1 : 2][32], uint32_t at, uint64_t sees) {
+    if constexpr (T::TWICE) {
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        read_tmem(at + 32 * h, s[0]);
+        hide(s[0], static_cast<uint32_t>(sees >> (32 * h)));
+        top = fmaxf(top, highest(s[0]));
+      }
+      return top;
+    } else {
+      tmem_ld_32x32b_x32(at, s[0]);
+      read_tmem(at + 32, s[1]);
+      arrived(s[0]);
+      hide(s[0], static_cast<uint32_t>(sees));
+      hide(s[1], static_cast<uint32_t>(sees >> 32));
+      return fmaxf(highest(s[0]), highest(s[1]));
+    }
   }
 
   // P of 32 keys in place of S, as (key, key + 1) pairs: for each 16 keys 8 columns of high parts, 8 of low ones. Adds to sum.
@@ -750,7 +827,7 @@ struct Softmax {
           const uint32_t sb = mine + T::TMEM_S + buf * kKeys;
           const Tile t = tile(p, w.r, i);
           const uint64_t sees = t.plain ? ~0ull : visible(p, w.r, t, mask);
-          uint32_t s[2][32];
+          uint32_t s[T::TWICE ? 1 : 2][32];
           bool settled = false;
           for (;;) {
             const float top = scores(s, sb, sees) * sc;
@@ -775,8 +852,17 @@ struct Softmax {
           }
           if (!ok) break;
           const float base = T::POFF - (m == -INFINITY ? 0.f : m);
+          if constexpr (T::TWICE) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              read_tmem(sb + 32 * h, s[0]);
+              hide(s[0], static_cast<uint32_t>(sees >> (32 * h)));
+              weights(s[0], sb + 32 * h, make_float2(sc, sc), make_float2(base, base), l);
+            }
+          } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) weights(s[h], sb + 32 * h, make_float2(sc, sc), make_float2(base, base), l);
+            for (int h = 0; h < 2; ++h) weights(s[h], sb + 32 * h, make_float2(sc, sc), make_float2(base, base), l);
+          }
           tmem_wait_st();
           tc_fence_before();
         }
