@@ -522,8 +522,9 @@ int tl_tree_attention(const tl_kv_cache* cache, const void* q, int dtype, int B,
  *   path     out int32 [T]: a request's accepted nodes in order, node 0 first, then -1 (padding too)
  *   counts   out int32 [B]: how many they are (0 for a request without nodes)
  *   next     out int32 [B]: the token after the last of them (-1 for a request without nodes)
- * Probabilities are taken as multiples of 2^-60 (rounded down), and sums of them are exact, so the result does not
- * depend on any order. Below 0 and NaN count as 0, above 1 as 1; uniforms outside [0, 1) as the nearest number in it. vocab is at
+ * Sums and differences of probabilities have 44 bits or more. Below 0 and NaN count as 0, above 1 as 1; for rows of target that sum
+ * to more than 1 + 2^-8 the path and the
+ * token are unspecified, within the tree and the vocabulary. Uniforms outside [0, 1) count as the nearest number in it. vocab is at
  * most 2^24; rows need no alignment beyond their elements'.
  */
 int tl_verify_tree(const float* target, int64_t ldt, const float* draft, int64_t ldd, int vocab,
