@@ -533,6 +533,7 @@ int tl_tree_attention(const tl_kv_cache* cache, const void* q, int dtype, int B,
   p.scale_log2 = scale * tl::kLog2e;
   p.B = B, p.T = T, p.q_heads = q_heads, p.kv_heads = cache->kv_heads, p.window = window, p.sinks = sinks;
   p.q_bf16 = dtype == TL_BF16;
+  p.runs16 = cache->page_size % 16 == 0;
   p.capacity = tree_capacity(max_pages, cache->page_size);
   p.cuts = static_cast<tl::TreeCut*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + tl::kTreeMaxGrid * sizeof(tl::TreeCut));

@@ -48,6 +48,7 @@ struct TreeAttnParams {
   float* lse;
   float scale_log2;
   int B, T, q_heads, kv_heads, group, window, sinks, q_bf16, capacity;
+  int runs16;                                         // page_size is a multiple of 16: 16 keys from a multiple of 16 lie at equal distances
   int grid;                                           // blocks of the first kernel
   float* partials;                                    // two per block
   struct TreeCut* cuts;                               // one per block
@@ -85,7 +86,7 @@ using attn::widen_hi;
 using attn::widen_lo;
 
 constexpr int kKeys = 64;                // keys of a tile
-constexpr int kSegmentCost = 2;          // what a segment costs besides its tiles, in tiles
+constexpr int kSegmentCost = 4;          // what a segment costs besides its tiles, in tiles
 constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
 constexpr int kAhead = 16;               // pieces: more than the loading warps can be ahead of the others, or of each other
 
@@ -94,17 +95,14 @@ struct Traits {
   static constexpr bool F8 = CACHE == kCacheF8, BF16 = CACHE == kCacheBf16;
   static constexpr int ROW = D * (F8 ? 1 : 2);                   // bytes of a cached row
   static constexpr int BLOCKS = tree_blocks_per_sm(D);
-  // Up to eight warps are four to a scheduler for two blocks, and have 128 registers. 8 bits are widened by the loading warps, which
-  // takes one on each scheduler; the nine warps have 96 registers then, so S is read from tensor memory twice.
-  static constexpr int LOADERS = F8 ? 4 : 2, THREADS = 32 * (kLoadWarp + LOADERS);
-  static constexpr bool TWICE = F8 && BLOCKS == 2;
+  // Up to eight warps are four to a scheduler for two blocks, and have 128 registers.
+  static constexpr int LOADERS = BLOCKS == 1 ? 4 : 3, THREADS = 32 * (kLoadWarp + LOADERS);
   // queries as the MMA's operand in tensor memory, or, where that has no room for two buffers of S beside them, in shared memory
   static constexpr bool QT = D != 128;
   static constexpr int Q = QT ? kSoftmaxWarps * 4096 : kTreeRows * D * 2;        // the results pass through it, 4 KB a warp
   static constexpr int SLOT = kKeys * D * 2, STAGE = F8 ? SLOT / 2 : 0;
   static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 12) : D == 128 ? (F8 ? 3 : 5) : F8 ? 4 : 6;
-  static constexpr int STAGES = F8 ? (D == 64 ? 12 : D == 128 ? 4 : 5) : 0;      // of 8-bit rows on their way
-  static constexpr int LAG = F8 ? STAGES - 1 : 0;                // of them in flight
+  static constexpr int STAGES = F8 ? (D == 64 ? 12 : D == 128 ? 3 : 4) : 0;     // of 8-bit rows on their way, shared out to the loading warps
   static constexpr int OFF_SLOT = Q, OFF_STAGE = OFF_SLOT + SLOTS * SLOT, OFF_MISC = OFF_STAGE + STAGES * STAGE;
   static constexpr int SMEM = OFF_MISC + 1024;
   static constexpr int SBUF = 2;                                 // buffers of S and P
@@ -112,7 +110,8 @@ struct Traits {
   static constexpr float POFF = BF16 ? 0.f : 12.f;               // p is kept 2^POFF as large (f16: away from the subnormals)
   static constexpr float SLACK = BF16 ? 8.f : 3.f;               // by how much m may lag behind the maximum
   static_assert(SMEM <= (BLOCKS == 1 ? 232448 : 115712) && TMEM_Q + (QT ? D / 2 : 0) <= TMEM, "room");
-  static_assert(SLOTS / 2 + 1 < kAhead, "a piece takes two slots at least");
+  // a piece takes two slots at least, and a loading warp has one load of any LOADERS
+  static_assert(SLOTS / 2 + 3 < kAhead && LOADERS <= 4 && (!F8 || STAGES >= LOADERS), "ahead");
 };
 
 // The small things behind the slots.
@@ -232,7 +231,7 @@ __device__ __forceinline__ void read_tmem(uint32_t addr, uint32_t (&v)[32]) {
 
 // ---- the list of work: every warp goes through its block's share by itself
 struct Request {
-  int n, row0, len, first, sinks, sink_tiles, tiles, row_blocks;
+  int n, row0, len, first, begin, sinks, sink_tiles, tiles, row_blocks;
   __device__ __forceinline__ int places(const TreeAttnParams& p) const { return row_blocks == 0 ? 0 : tiles + kSegmentCost; }
 };
 
@@ -245,9 +244,10 @@ __device__ __forceinline__ Request request(const TreeAttnParams& p, int b, bool&
     r.n = r.len = 0;
   }
   r.first = p.window > 0 ? max(0, r.len - p.window) : 0;      // the first key that any row's window reaches
+  r.begin = p.runs16 ? r.first & ~15 : r.first;               // its tiles begin with that key's run
   r.sinks = min(p.sinks, r.first);
   r.sink_tiles = (r.sinks + kKeys - 1) / kKeys;
-  r.tiles = r.sink_tiles + (r.len + r.n - r.first + kKeys - 1) / kKeys;
+  r.tiles = r.sink_tiles + (r.len + r.n - r.begin + kKeys - 1) / kKeys;
   r.row_blocks = (r.n * p.group + kTreeRows - 1) / kTreeRows;
   return r;
 }
@@ -261,37 +261,54 @@ struct Piece {              // tiles begin .. end - 1 of a segment
 struct Walk {
   Request r;
   int b, seg, segs;         // request, segment of it, its segments
+  int places;               // of a segment of this request
   long long at, share, t1;  // place where the segment begins; places of a share; where this block's share ends
   long long t0;
   bool more;
 
+  // Where several row blocks share the keys, each one's places are a whole number of shares: then the blocks that read the same
+  // keys do so at the same time, and all but the first find them in L2.
+  __device__ __forceinline__ int places_of(const TreeAttnParams& p, const Request& x) const {
+    const int n = x.places(p);
+    return x.row_blocks > 1 && n > share && share > 0 ? static_cast<int>((n + share - 1) / share * share) : n;
+  }
+  __device__ __forceinline__ long long all_of(const TreeAttnParams& p, const Request& x) const {
+    return static_cast<long long>(p.kv_heads) * x.row_blocks * places_of(p, x);
+  }
+
   // All lanes of a warp together.
   __device__ __forceinline__ void init(const TreeAttnParams& p, bool report) {
     const int lane = threadIdx.x & 31;
-    long long total = 0;
     bool bad = false;
-    for (int base = 0; base < p.B; base += 32) {
-      if (base + lane < p.B) {
-        const Request x = request(p, base + lane, bad);
-        total += static_cast<long long>(p.kv_heads) * x.row_blocks * x.places(p);
+    long long total;
+    share = 0;
+    for (;;) {              // the least share with which the places fit the blocks, within 3 %
+      total = 0;
+      bool wide = false;
+      for (int base = 0; base < p.B; base += 32) {
+        if (base + lane < p.B) {
+          const Request x = request(p, base + lane, bad);
+          total += all_of(p, x);
+          wide |= x.row_blocks > 1;
+        }
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      const long long least = attn::divide(total + p.grid - 1, p.grid);
+      if (least <= share) break;
+      share = share == 0 ? least : max(least, share + share / 32);
+      if (!__any_sync(0xffffffffu, wide)) break;
     }
     if (report && bad) set_status(p.status, TL_EDATA);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    share = attn::divide(total + p.grid - 1, p.grid);
     t0 = share * blockIdx.x;
     t1 = min(t0 + share, total);
     more = t0 < total;
     if (!more) return;
     long long run = 0;
     for (int base = 0;; base += 32) {
-      long long places = 0;
-      if (base + lane < p.B) {
-        const Request x = request(p, base + lane, bad);
-        places = static_cast<long long>(p.kv_heads) * x.row_blocks * x.places(p);
-      }
-      long long incl = places;
+      long long mine = 0;
+      if (base + lane < p.B) mine = all_of(p, request(p, base + lane, bad));
+      long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -301,15 +318,16 @@ struct Walk {
       if (who != 0) {
         const int l = __ffs(who) - 1;
         b = base + l;
-        at = run + __shfl_sync(0xffffffffu, incl - places, l);
+        at = run + __shfl_sync(0xffffffffu, incl - mine, l);
         break;
       }
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
     r = request(p, b, bad);
+    places = places_of(p, r);
     segs = p.kv_heads * r.row_blocks;
-    seg = static_cast<int>(attn::divide(t0 - at, r.places(p)));
-    at += static_cast<long long>(seg) * r.places(p);
+    seg = static_cast<int>(attn::divide(t0 - at, places));
+    at += static_cast<long long>(seg) * places;
   }
 
   // The next piece with tiles in it; false at the end of the share.
@@ -322,11 +340,12 @@ struct Walk {
       if (seg == segs) {
         bool bad = false;
         r = request(p, ++b, bad);
+        places = places_of(p, r);
         seg = 0;
         segs = p.kv_heads * r.row_blocks;
         continue;
       }
-      const long long from = max(t0 - at, 0ll) - kSegmentCost, to = min(t1 - at, static_cast<long long>(r.places(p))) - kSegmentCost;
+      const long long from = max(t0 - at, 0ll) - kSegmentCost, to = min(t1 - at, static_cast<long long>(r.places(p))) - kSegmentCost;      // (what is left of a whole number of shares stays empty)
       x.begin = static_cast<int>(max(from, 0ll));
       x.end = static_cast<int>(max(to, 0ll));
       x.kvh = seg / r.row_blocks;
@@ -338,7 +357,7 @@ struct Walk {
       if (!x.whole && x.starts_here)
         x.parts = static_cast<int>(attn::divide(at + kSegmentCost + r.tiles - 1, share)) - static_cast<int>(blockIdx.x) + 1;
       ++seg;
-      at += r.places(p);
+      at += places;
       if (x.end > x.begin) return true;
     }
     return false;
@@ -354,7 +373,7 @@ struct Tile {
 __device__ __forceinline__ Tile tile(const TreeAttnParams& p, const Request& r, int i) {
   Tile t;
   t.sink = i < r.sink_tiles;
-  t.k0 = t.sink ? i * kKeys : r.first + (i - r.sink_tiles) * kKeys;
+  t.k0 = t.sink ? i * kKeys : r.begin + (i - r.sink_tiles) * kKeys;
   t.end = min(t.k0 + kKeys, t.sink ? r.sinks : r.len + r.n);
   // a row's window holds up to TL_TREE_NODES nodes of its own and so many cached keys fewer
   t.plain = t.sink ? t.end - t.k0 == kKeys
@@ -367,159 +386,127 @@ __device__ __forceinline__ uint64_t visible(const TreeAttnParams& p, const Reque
   if (t.sink) return low_bits(t.end - t.k0);
   const int first = p.window > 0 ? max(0, r.len - max(0, p.window - __popcll(mask))) : 0;
   const int nodes = r.len - t.k0;                     // where the nodes begin
-  const uint64_t cached = low_bits(nodes) & (~low_bits(first - t.k0) | low_bits(p.sinks - t.k0));
+  const uint64_t cached = low_bits(nodes) & ~low_bits(r.first - t.k0) & (~low_bits(first - t.k0) | low_bits(p.sinks - t.k0));
   const uint64_t drafted = nodes >= 64 ? 0 : nodes >= 0 ? mask << nodes : nodes > -64 ? mask >> -nodes : 0;
   return cached | drafted;
 }
 
-// ---- the loading warps: rows of K and V into the ring's slots
+// ---- the loading warps: rows of K and V into the ring's slots. They take the loads in turn, each a whole one: looking the rows' addresses up
+// takes as long as copying them, and all warps together at every load took 3000 cycles for a tile of 256 channels.
 template <int CACHE, int D>
 struct Loader {
   using T = Traits<CACHE, D>;
   static constexpr int CPR = T::ROW / 16;               // 16-byte chunks of a cached row
-  static constexpr int RPI = 32 / CPR;                  // rows that one instruction of a warp copies
-  static constexpr int PER = T::LOADERS * RPI, STEPS = kKeys / PER;      // rows of an instruction of all warps
+  static constexpr int RPI = 32 / CPR;                  // rows that one instruction copies
+  static constexpr int STEPS = kKeys / RPI;
 
   const TreeAttnParams& p;
   uint8_t* smem;
   Misc<T>* misc;
   int warp, lane;                                       // of the loading warps
-  uint32_t issued = 0, done = 0;                        // loads
-  uint32_t checks = 0, ends = 0;                        // 8 bits: of the loads in flight, the last in bit 0: look for NaN; a piece's last
   int pieces = 0;                                       // whose loads are done
   bool ok = true;
 
-  // Each warp knows all rows of a tile: a lane the rows of keys lane and lane + 32.
+  // Where a tile's rows lie. With runs of 16, lanes 0 to 3 know the first row of theirs; otherwise a lane the rows of keys lane and lane + 32.
   struct Rows {
     int64_t off[2];                                     // byte offset in the cache, or -1
-    bool runs;
   };
-  __device__ __forceinline__ void pages_of(const Walk& w, const Tile& t, int (&page)[2]) const {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int key = t.k0 + 32 * h + lane;
-      page[h] = key < t.end ? __ldg(p.pages + w.b * p.ldp + p.page.div(key)) : -1;
-    }
+  __device__ __forceinline__ void pages_of(const int32_t* pages, const Tile& t, int (&page)[2]) const {
+    const int key = t.k0 + (p.runs16 ? 16 * (lane & 3) : lane);
+    page[0] = key < t.end ? __ldg(pages + p.page.div(key)) : -1;
+    page[1] = !p.runs16 && key + 32 < t.end ? __ldg(pages + p.page.div(key + 32)) : -1;
   }
-  __device__ __forceinline__ void rows_of(const Piece& x, const Tile& t, const int (&page)[2], Rows& r) const {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int key = t.k0 + 32 * h + lane;
-      r.off[h] = -1;
-      if (key >= t.end) continue;
-      if (static_cast<unsigned>(page[h]) < static_cast<unsigned>(p.num_pages))
-        r.off[h] = page[h] * p.page_stride + x.kvh * p.head_stride + static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
-      else
-        set_status(p.status, TL_EDATA);
+  __device__ __forceinline__ int64_t row_of(int key, int page, const Tile& t, int64_t head) const {
+    if (key >= t.end) return -1;
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
+      set_status(p.status, TL_EDATA);
+      return -1;
     }
+    return page * p.page_stride + head + static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
   }
-  // Instruction i of this warp: its first row; a lane copies chunk lane % CPR of row (that) + lane / CPR.
-  __device__ __forceinline__ int first_row(int i) const { return i * PER + warp * RPI; }
-  // Each 16 rows follow each other at equal distances.
-  __device__ __forceinline__ bool even(const Rows& r) const {
-    bool good = true;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t first = __shfl_sync(0xffffffffu, r.off[h], lane & 16);
-      good &= first >= 0 && r.off[h] == first + (lane & 15) * p.token_stride;
-    }
-    return __all_sync(0xffffffffu, good);
+  __device__ __forceinline__ void rows_of(const Tile& t, const int (&page)[2], int64_t head, Rows& r) const {
+    const int key = t.k0 + (p.runs16 ? 16 * (lane & 3) : lane);
+    r.off[0] = row_of(key, page[0], t, head);
+    r.off[1] = p.runs16 ? -1 : row_of(key + 32, page[1], t, head);
   }
 
-  __device__ __forceinline__ void wait_empty(uint32_t i) {
-    if (i >= T::SLOTS) ok = wait_all(misc->empty[i % T::SLOTS], i / T::SLOTS - 1, &misc->abort, p.status);
-  }
-
-  __device__ __forceinline__ void copy(const uint8_t* base, const Rows& rows) {
-    const int row = lane / CPR, chunk = lane % CPR;
-    const uint32_t to = T::F8 ? smem_u32(smem) + T::OFF_STAGE + issued % (T::F8 ? T::STAGES : 1) * T::STAGE
-                              : smem_u32(smem) + T::OFF_SLOT + issued % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
-    base += chunk * 16;
-    auto dst = [&](int i) {
-      const int r = first_row(i) + row;
-      return T::F8 ? to + r * T::ROW + chunk * 16 : to + swizzled(r, chunk % 8);
-    };
-    if (rows.runs) {                                    // one address for 16 rows
-      constexpr int G = PER < 16 ? 16 / PER : 1;
-      const uint8_t* const mine = base + ((warp * RPI + row) & 15) * p.token_stride;
+  // A lane copies chunk lane % CPR of rows lane / CPR, + RPI, ...; dst(i): where that of instruction i goes. Rows that are not there become zeros.
+  template <typename F>
+  __device__ __forceinline__ void copy(const uint8_t* base, const Rows& rows, const Tile& t, F&& dst) const {
+    const int row = lane / CPR;
+    base += lane % CPR * 16;
+    if (p.runs16) {
+      constexpr int G = 16 / RPI;
 #pragma unroll
-      for (int i = 0; i < STEPS; i += G) {
-        const uint8_t* from = mine + __shfl_sync(0xffffffffu, rows.off[i * PER / 32], PER < 16 ? i * PER & 16 : first_row(i) & 16);
+      for (int g = 0; g < 4; ++g) {
+        const int64_t o = __shfl_sync(0xffffffffu, rows.off[0], g);
+        const int left = o < 0 ? 0 : t.end - t.k0 - 16 * g - row;      // rows of this lane on
+        const uint8_t* from = base + (o < 0 ? 0 : o) + row * p.token_stride;
 #pragma unroll
-        for (int j = 0; j < G; ++j, from += PER * p.token_stride) cp_async16(dst(i + j), from);
+        for (int i = 0; i < G; ++i) {
+          cp_async16(dst(g * G + i), left > i * RPI ? from : base, left > i * RPI ? 16u : 0u);
+          from += RPI * p.token_stride;
+        }
       }
     } else {
 #pragma unroll 2
       for (int i = 0; i < STEPS; ++i) {
-        const int r = first_row(i);
-        const int64_t o = __shfl_sync(0xffffffffu, r < 32 ? rows.off[0] : rows.off[1], (r + row) & 31);
+        const int64_t o = __shfl_sync(0xffffffffu, i * RPI < 32 ? rows.off[0] : rows.off[1], (i * RPI + row) & 31);
         cp_async16(dst(i), base + (o < 0 ? 0 : o), o < 0 ? 0u : 16u);
       }
     }
   }
 
-  __device__ __forceinline__ void note_odd() { *const_cast<volatile int*>(&misc->flag[pieces % kAhead]) = pieces + 1; }
-  __device__ __forceinline__ void end_piece() {
-    mbar_arrive(smem_u32(&misc->loaded[pieces % kAhead]));
-    ++pieces;
+  // For load i: load i - SLOTS has been taken. A wait tells a phase from its neighbours only where the one before is known to be
+  // over: this warp's last wait said so of all loads up to i - LOADERS - SLOTS, and load i - 2 SLOTS has to be among them.
+  __device__ __forceinline__ void wait_empty(uint32_t i) {
+    static_assert(T::LOADERS <= T::SLOTS, "phases");
+    if (i >= T::SLOTS) ok = wait_all(misc->empty[i % T::SLOTS], i / T::SLOTS - 1, &misc->abort, p.status);
   }
+  __device__ __forceinline__ void note_odd() const { *const_cast<volatile int*>(&misc->flag[pieces % kAhead]) = pieces + 1; }
 
-  // 16 bits: straight into the slot; the copies themselves arrive when they have landed.
-  __device__ __forceinline__ void load16(const uint8_t* base, const Rows& rows, bool check, bool last) {
-    wait_empty(issued);
+  // 16 bits: straight into slot n % SLOTS; the copies themselves arrive when they have landed.
+  __device__ __forceinline__ void load16(uint32_t n, const uint8_t* base, const Rows& rows, const Tile& t, bool check) {
+    wait_empty(n);
     if (!ok) return;
-    copy(base, rows);
-    const uint32_t full = smem_u32(&misc->full[issued % T::SLOTS]);
+    const int row = lane / CPR, chunk = lane % CPR, off = T::OFF_SLOT + n % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
+    copy(base, rows, t, [&](int i) { return smem_u32(smem) + off + swizzled(i * RPI + row, chunk % 8); });
+    const uint32_t full = smem_u32(&misc->full[n % T::SLOTS]);
     if (!check) {
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
-    } else {
-      cp_async_commit();
-      cp_async_wait<0>();
-      constexpr uint32_t E = T::BF16 ? 0x7F807F80u : 0x7C007C00u;
-      const int row = lane / CPR, chunk = lane % CPR;
-      uint8_t* const to = smem + T::OFF_SLOT + issued % T::SLOTS * T::SLOT + chunk / 8 * (kKeys * 128);
-      bool found = false;
-#pragma unroll 2
-      for (int i = 0; i < STEPS; ++i) {
-        uint4* const at = reinterpret_cast<uint4*>(to + swizzled(first_row(i) + row, chunk % 8));
-        uint4 x = *at;
-        const uint32_t a = __vcmpeq2(x.x & E, E), b = __vcmpeq2(x.y & E, E), c = __vcmpeq2(x.z & E, E), d = __vcmpeq2(x.w & E, E);
-        if ((a | b | c | d) != 0) *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d), found = true;
-      }
-      if (found) note_odd();
-      fence_proxy_async_smem();
-      mbar_arrive(full);
+      return;
     }
-    ++issued;
-    if (last) end_piece();
-  }
-
-  // 8 bits: into this thread's part of a stage, some loads ahead.
-  __device__ __forceinline__ void load8(const uint8_t* base, const Rows& rows, bool check, bool last) {
-    copy(base, rows);
     cp_async_commit();
-    ++issued;
-    checks = checks << 1 | check;
-    ends = ends << 1 | last;
-    if (issued - done > T::LAG) {
-      cp_async_wait<T::LAG>();
-      widen(T::LAG);
+    cp_async_wait<0>();
+    constexpr uint32_t E = T::BF16 ? 0x7F807F80u : 0x7C007C00u;
+    bool found = false;
+#pragma unroll 2
+    for (int i = 0; i < STEPS; ++i) {
+      uint4* const at = reinterpret_cast<uint4*>(smem + off + swizzled(i * RPI + row, chunk % 8));
+      uint4 x = *at;
+      const uint32_t a = __vcmpeq2(x.x & E, E), b = __vcmpeq2(x.y & E, E), c = __vcmpeq2(x.z & E, E), d = __vcmpeq2(x.w & E, E);
+      if ((a | b | c | d) != 0) *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d), found = true;
     }
+    if (found) note_odd();
+    fence_proxy_async_smem();
+    mbar_arrive(full);
   }
 
-  // The oldest load in flight, `age` loads ago, has landed: this thread's part of it goes to a slot as f16.
-  __device__ __forceinline__ void widen(int age) {
-    wait_empty(done);
-    if (!ok) return;
-    const bool check = checks >> age & 1;
-    bool found = false;
+  // 8 bits: into this warp's stage, and from there to the slot as f16. (While one warp widens, the others' rows are on their way.)
+  __device__ __forceinline__ void load8(uint32_t n, const uint8_t* base, const Rows& rows, const Tile& t, bool check) {
     const int row = lane / CPR, chunk = lane % CPR;
-    const uint8_t* from = smem + T::OFF_STAGE + done % (T::F8 ? T::STAGES : 1) * T::STAGE + chunk * 16;
-    uint8_t* to = smem + T::OFF_SLOT + done % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128);
+    uint8_t* const stage = smem + T::OFF_STAGE + warp * T::STAGE + chunk * 16;
+    copy(base, rows, t, [&](int i) { return smem_u32(stage) + (i * RPI + row) * T::ROW; });
+    cp_async_commit();
+    cp_async_wait<0>();
+    wait_empty(n);
+    if (!ok) return;
+    bool found = false;
+    uint8_t* const to = smem + T::OFF_SLOT + n % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128);
 #pragma unroll 4
     for (int i = 0; i < STEPS; ++i) {
-      const int kk = first_row(i) + row;
-      uint4 x = *reinterpret_cast<const uint4*>(from + kk * T::ROW);
+      const int kk = i * RPI + row;
+      uint4 x = *reinterpret_cast<const uint4*>(stage + kk * T::ROW);
       if (check) {                                      // e4m3 has NaN (0x7F, 0xFF), no infinities
         constexpr uint32_t N = 0x7F7F7F7Fu;
         const uint32_t a = __vcmpeq4(x.x & N, N), b = __vcmpeq4(x.y & N, N), c = __vcmpeq4(x.z & N, N), d = __vcmpeq4(x.w & N, N);
@@ -534,50 +521,48 @@ struct Loader {
     }
     if (found) note_odd();
     fence_proxy_async_smem();
-    mbar_arrive(smem_u32(&misc->full[done % T::SLOTS]));
-    if (ends >> age & 1) end_piece();
-    ++done;
+    mbar_arrive(smem_u32(&misc->full[n % T::SLOTS]));
   }
 
   __device__ __forceinline__ void run() {
     Walk w;
     w.init(p, false);
     Piece x;
+    uint32_t before = 0;                                // loads of the pieces before
     while (ok && w.next(p, x)) {
-      // loads K0, K1, V0, K2, V1, ...: `now` is the tile of the next K, `before` the one whose V is due
+      // loads K0, K1, V0, K2, V1, ... of n tiles
       const int n = x.end - x.begin;
-      Tile t = tile(p, w.r, x.begin);
-      int page[2];
-      pages_of(w, t, page);
-      Rows before = {{-1, -1}, false};
-      bool before_plain = true;
-      for (int i = 0; ok && i <= n; ++i) {
-        const Tile now = t;
-        Rows rows = {{-1, -1}, false};
-        if (i < n) {
-          rows_of(x, now, page, rows);
-          rows.runs = even(rows);
-          if (i + 1 < n) {
-            t = tile(p, w.r, x.begin + i + 1);
-            pages_of(w, t, page);
-          }
-        }
-#pragma unroll 1
-        for (int v = 0; ok && v < 2; ++v) {
-          if (v ? i == 0 : i == n) continue;
-          const Rows& r = v ? before : rows;
-          const bool check = v && !before_plain, last = v && i == n;
-          if constexpr (T::F8)
-            load8(v ? p.v : p.k, r, check, last);
-          else
-            load16(v ? p.v : p.k, r, check, last);
-        }
-        before = rows, before_plain = now.plain;
+      auto tile_of = [&](int j) { return tile(p, w.r, x.begin + (j == 2 * n - 1 ? n - 1 : j & 1 ? (j + 1) / 2 : j == 0 ? 0 : j / 2 - 1)); };
+      int j = (warp + T::LOADERS - static_cast<int>(before % T::LOADERS)) % T::LOADERS;
+      const int32_t* const pages = p.pages + w.b * p.ldp;
+      const int64_t head = x.kvh * p.head_stride;
+      int page[2] = {-1, -1};
+      Tile t{};
+      if (j < 2 * n) {
+        t = tile_of(j);
+        pages_of(pages, t, page);
       }
+      for (; ok && j < 2 * n; j += T::LOADERS) {
+        const Tile now = t;
+        Rows rows;
+        rows_of(now, page, head, rows);
+        if (j + T::LOADERS < 2 * n) {
+          t = tile_of(j + T::LOADERS);
+          pages_of(pages, t, page);
+        }
+        const bool v = j == 2 * n - 1 || (j != 0 && !(j & 1));
+        if constexpr (T::F8)
+          load8(before + j, v ? p.v : p.k, rows, now, v && !now.plain);
+        else
+          load16(before + j, v ? p.v : p.k, rows, now, v && !now.plain);
+      }
+      before += 2 * n;
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&misc->loaded[pieces % kAhead]));      // this warp's part of the piece
+      ++pieces;
     }
     cp_async_wait<0>();
-    if constexpr (T::F8)
-      while (ok && done != issued) widen(static_cast<int>(issued - done) - 1);
   }
 };
 
@@ -721,24 +706,13 @@ struct Softmax {
     return max3(fmaxf(top[0], top[1]), top[2], top[3]);
   }
   // Of a tile; returns the maximum.
-  __device__ __forceinline__ float scores(uint32_t (&s)[T::TWICE ? 1 : 2][32], uint32_t at, uint64_t sees) {
-    if constexpr (T::TWICE) {
-      float top = -INFINITY;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        read_tmem(at + 32 * h, s[0]);
-        hide(s[0], static_cast<uint32_t>(sees >> (32 * h)));
-        top = fmaxf(top, highest(s[0]));
-      }
-      return top;
-    } else {
-      tmem_ld_32x32b_x32(at, s[0]);
-      read_tmem(at + 32, s[1]);
-      arrived(s[0]);
-      hide(s[0], static_cast<uint32_t>(sees));
-      hide(s[1], static_cast<uint32_t>(sees >> 32));
-      return fmaxf(highest(s[0]), highest(s[1]));
-    }
+  __device__ __forceinline__ float scores(uint32_t (&s)[2][32], uint32_t at, uint64_t sees) {
+    tmem_ld_32x32b_x32(at, s[0]);
+    read_tmem(at + 32, s[1]);
+    arrived(s[0]);
+    hide(s[0], static_cast<uint32_t>(sees));
+    hide(s[1], static_cast<uint32_t>(sees >> 32));
+    return fmaxf(highest(s[0]), highest(s[1]));
   }
 
   // P of 32 keys in place of S, as (key, key + 1) pairs: for each 16 keys 8 columns of high parts, 8 of low ones. Adds to sum.
@@ -827,7 +801,7 @@ struct Softmax {
           const uint32_t sb = mine + T::TMEM_S + buf * kKeys;
           const Tile t = tile(p, w.r, i);
           const uint64_t sees = t.plain ? ~0ull : visible(p, w.r, t, mask);
-          uint32_t s[T::TWICE ? 1 : 2][32];
+          uint32_t s[2][32];
           bool settled = false;
           for (;;) {
             const float top = scores(s, sb, sees) * sc;
@@ -852,17 +826,8 @@ struct Softmax {
           }
           if (!ok) break;
           const float base = T::POFF - (m == -INFINITY ? 0.f : m);
-          if constexpr (T::TWICE) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              read_tmem(sb + 32 * h, s[0]);
-              hide(s[0], static_cast<uint32_t>(sees >> (32 * h)));
-              weights(s[0], sb + 32 * h, make_float2(sc, sc), make_float2(base, base), l);
-            }
-          } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) weights(s[h], sb + 32 * h, make_float2(sc, sc), make_float2(base, base), l);
-          }
+          for (int h = 0; h < 2; ++h) weights(s[h], sb + 32 * h, make_float2(sc, sc), make_float2(base, base), l);
           tmem_wait_st();
           tc_fence_before();
         }
@@ -952,14 +917,14 @@ __global__ void __launch_bounds__(Traits<CACHE, D>::THREADS, Traits<CACHE, D>::B
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < T::SLOTS; ++i) mbar_init(smem_u32(&misc->full[i]), T::LOADERS * 32), mbar_init(smem_u32(&misc->empty[i]), 1);
+    for (int i = 0; i < T::SLOTS; ++i) mbar_init(smem_u32(&misc->full[i]), 32), mbar_init(smem_u32(&misc->empty[i]), 1);
     for (int i = 0; i < T::SBUF; ++i) {
       mbar_init(smem_u32(&misc->s_full[i]), 1);
       mbar_init(smem_u32(&misc->p_full[i]), kSoftmaxWarps);
       mbar_init(smem_u32(&misc->pv_done[i]), 1);
     }
     mbar_init(smem_u32(&misc->q_full), kSoftmaxWarps);
-    for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&misc->loaded[i]), T::LOADERS * 32), misc->flag[i] = 0;
+    for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&misc->loaded[i]), T::LOADERS), misc->flag[i] = 0;
     misc->abort = 0;
     fence_barrier_init();
   }
