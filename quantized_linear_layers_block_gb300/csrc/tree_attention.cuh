@@ -49,7 +49,8 @@ struct TreeAttnParams {
   float scale_log2;
   int B, T, q_heads, kv_heads, group, window, sinks, q_bf16, capacity;
   int runs16;                                         // page_size is a multiple of 16: 16 keys from a multiple of 16 lie at equal distances
-  int grid;                                           // blocks of the first kernel
+  int cluster_log, row_blocks;                        // kCluster: 2^cluster_log blocks to a segment; row blocks that a request may have
+  int grid;                                           // kList: blocks of the first kernel
   float* partials;                                    // two per block
   struct TreeCut* cuts;                               // one per block
   int* status;
@@ -88,6 +89,13 @@ using attn::widen_lo;
 constexpr int kKeys = 64;                // keys of a tile
 constexpr int kSegmentCost = 4;          // what a segment costs besides its tiles, in tiles
 constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kMaxClusterLog = 4;
+constexpr long long kReread = 64 << 20;  // bytes of K and V that several row blocks read, from which on they do so together
+
+enum Mode {
+  kList,      // the list of tiles, in equal shares, and a second kernel for the segments that are cut
+  kCluster    // a cluster of blocks takes a segment, and joins it through its shared memory
+};
 constexpr int kAhead = 16;               // pieces: more than the loading warps can be ahead of the others, or of each other
 
 template <int CACHE, int D>
@@ -96,7 +104,8 @@ struct Traits {
   static constexpr int ROW = D * (F8 ? 1 : 2);                   // bytes of a cached row
   static constexpr int BLOCKS = tree_blocks_per_sm(D);
   // Up to eight warps are four to a scheduler for two blocks, and have 128 registers.
-  static constexpr int LOADERS = BLOCKS == 1 ? 4 : 3, THREADS = 32 * (kLoadWarp + LOADERS);
+  static constexpr int LOADERS = BLOCKS == 1 ? 4 : 3;
+  static constexpr int THREADS = 32 * (kLoadWarp + LOADERS);
   // queries as the MMA's operand in tensor memory, or, where that has no room for two buffers of S beside them, in shared memory
   static constexpr bool QT = D != 128;
   static constexpr int Q = QT ? kSoftmaxWarps * 4096 : kTreeRows * D * 2;        // the results pass through it, 4 KB a warp
@@ -258,6 +267,7 @@ struct Piece {              // tiles begin .. end - 1 of a segment
   int second, parts;        // which of the block's partials; blocks that share the segment
 };
 
+template <Mode MODE>
 struct Walk {
   Request r;
   int b, seg, segs;         // request, segment of it, its segments
@@ -266,38 +276,59 @@ struct Walk {
   long long t0;
   bool more;
 
-  // Where several row blocks share the keys, each one's places are a whole number of shares: then the blocks that read the same
+  // Where several row blocks share many keys, each one's places are a whole number of shares: then the blocks that read the same
   // keys do so at the same time, and all but the first find them in L2.
-  __device__ __forceinline__ int places_of(const TreeAttnParams& p, const Request& x) const {
-    const int n = x.places(p);
-    return x.row_blocks > 1 && n > share && share > 0 ? static_cast<int>((n + share - 1) / share * share) : n;
-  }
-  __device__ __forceinline__ long long all_of(const TreeAttnParams& p, const Request& x) const {
-    return static_cast<long long>(p.kv_heads) * x.row_blocks * places_of(p, x);
+  __device__ __forceinline__ int padded(int n, int row_blocks, bool together) const {
+    if (!together || row_blocks < 2 || n <= share) return n;
+    const int s = static_cast<int>(share);
+    return (n + s - 1) / s * s;
   }
 
-  // All lanes of a warp together.
-  __device__ __forceinline__ void init(const TreeAttnParams& p, bool report) {
+  // All lanes of a warp together. `tile_bytes`: of K and V of a tile.
+  __device__ __forceinline__ void init(const TreeAttnParams& p, int tile_bytes, bool report) {
     const int lane = threadIdx.x & 31;
     bool bad = false;
-    long long total;
+    if constexpr (MODE == kCluster) {
+      b = static_cast<int>((blockIdx.x >> p.cluster_log) / static_cast<unsigned>(p.kv_heads * p.row_blocks));
+      seg = static_cast<int>(blockIdx.x >> p.cluster_log) - b * p.kv_heads * p.row_blocks;
+      r = request(p, b, bad);
+      if (report && bad && lane == 0) set_status(p.status, TL_EDATA);
+      more = seg % p.row_blocks < r.row_blocks;
+      return;
+    }
+    // what a lane knows of its request, of up to 32 for good
+    int n = 0, row_blocks = 0;
+    auto look = [&](int base) {
+      n = row_blocks = 0;
+      if (base + lane >= p.B) return;
+      const Request x = request(p, base + lane, bad);
+      n = x.places(p), row_blocks = x.row_blocks;
+    };
+    look(0);
     share = 0;
+    bool together = false;
+    long long total, again = 0;
     for (;;) {              // the least share with which the places fit the blocks, within 3 %
       total = 0;
-      bool wide = false;
       for (int base = 0; base < p.B; base += 32) {
-        if (base + lane < p.B) {
-          const Request x = request(p, base + lane, bad);
-          total += all_of(p, x);
-          wide |= x.row_blocks > 1;
-        }
+        if (p.B > 32) look(base);
+        total += static_cast<long long>(p.kv_heads) * row_blocks * padded(n, row_blocks, together);
+        if (share == 0 && row_blocks > 1) again += static_cast<long long>(p.kv_heads) * n * tile_bytes;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
       const long long least = attn::divide(total + p.grid - 1, p.grid);
       if (least <= share) break;
-      share = share == 0 ? least : max(least, share + share / 32);
-      if (!__any_sync(0xffffffffu, wide)) break;
+      if (share == 0) {
+        share = least;
+        if (!__any_sync(0xffffffffu, row_blocks > 1 || again > 0)) break;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) again += __shfl_xor_sync(0xffffffffu, again, o);
+        together = again > kReread && share < (1 << 30);
+        if (!together) break;
+      } else {
+        share = max(least, share + share / 32);
+      }
     }
     if (report && bad) set_status(p.status, TL_EDATA);
     t0 = share * blockIdx.x;
@@ -306,8 +337,8 @@ struct Walk {
     if (!more) return;
     long long run = 0;
     for (int base = 0;; base += 32) {
-      long long mine = 0;
-      if (base + lane < p.B) mine = all_of(p, request(p, base + lane, bad));
+      if (p.B > 32) look(base);
+      const long long mine = static_cast<long long>(p.kv_heads) * row_blocks * padded(n, row_blocks, together);
       long long incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -323,15 +354,34 @@ struct Walk {
       }
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
+    join = together;
     r = request(p, b, bad);
-    places = places_of(p, r);
-    segs = p.kv_heads * r.row_blocks;
+    enter(p);
     seg = static_cast<int>(attn::divide(t0 - at, places));
     at += static_cast<long long>(seg) * places;
+  }
+  bool join;                // (of `padded`)
+
+  __device__ __forceinline__ void enter(const TreeAttnParams& p) {
+    places = padded(r.places(p), r.row_blocks, join);
+    segs = p.kv_heads * r.row_blocks;
+    seg = 0;
   }
 
   // The next piece with tiles in it; false at the end of the share.
   __device__ __forceinline__ bool next(const TreeAttnParams& p, Piece& x) {
+    if constexpr (MODE == kCluster) {
+      if (!more) return false;
+      more = false;
+      const int rank = blockIdx.x & ((1 << p.cluster_log) - 1);
+      x.kvh = seg / p.row_blocks;
+      x.row_block = seg - x.kvh * p.row_blocks;
+      x.begin = static_cast<int>(static_cast<long long>(r.tiles) * rank >> p.cluster_log);
+      x.end = static_cast<int>(static_cast<long long>(r.tiles) * (rank + 1) >> p.cluster_log);
+      x.whole = p.cluster_log == 0;
+      x.starts_here = false, x.second = 0, x.parts = 0;
+      return x.end > x.begin;
+    }
     while (more) {
       if (at >= t1) {
         more = false;
@@ -340,12 +390,11 @@ struct Walk {
       if (seg == segs) {
         bool bad = false;
         r = request(p, ++b, bad);
-        places = places_of(p, r);
-        seg = 0;
-        segs = p.kv_heads * r.row_blocks;
+        enter(p);
         continue;
       }
-      const long long from = max(t0 - at, 0ll) - kSegmentCost, to = min(t1 - at, static_cast<long long>(r.places(p))) - kSegmentCost;      // (what is left of a whole number of shares stays empty)
+      // (what is left of a whole number of shares stays empty)
+      const long long from = max(t0 - at, 0ll) - kSegmentCost, to = min(t1 - at, static_cast<long long>(r.places(p))) - kSegmentCost;
       x.begin = static_cast<int>(max(from, 0ll));
       x.end = static_cast<int>(max(to, 0ll));
       x.kvh = seg / r.row_blocks;
@@ -393,7 +442,7 @@ __device__ __forceinline__ uint64_t visible(const TreeAttnParams& p, const Reque
 
 // ---- the loading warps: rows of K and V into the ring's slots. They take the loads in turn, each a whole one: looking the rows' addresses up
 // takes as long as copying them, and all warps together at every load took 3000 cycles for a tile of 256 channels.
-template <int CACHE, int D>
+template <int CACHE, int D, Mode MODE>
 struct Loader {
   using T = Traits<CACHE, D>;
   static constexpr int CPR = T::ROW / 16;               // 16-byte chunks of a cached row
@@ -525,8 +574,8 @@ struct Loader {
   }
 
   __device__ __forceinline__ void run() {
-    Walk w;
-    w.init(p, false);
+    Walk<MODE> w;
+    w.init(p, 2 * kKeys * T::ROW, false);
     Piece x;
     uint32_t before = 0;                                // loads of the pieces before
     while (ok && w.next(p, x)) {
@@ -566,28 +615,31 @@ struct Loader {
   }
 };
 
-// ---- the MMA warp
-template <int CACHE, int D>
-__device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* smem, Misc<Traits<CACHE, D>>* misc) {
+// ---- the MMA warps. Loads come as K0, K1, V0, K2, V1, ... of a piece of n tiles: K_i is load max(2 i - 1, 0), V_i load min(2 i + 2, 2 n - 1).
+template <int CACHE, int D, Mode MODE>
+struct Mma {
   using T = Traits<CACHE, D>;
-  constexpr uint32_t ID_S = idesc<T::BF16>(kKeys, false), ID_O = idesc<T::BF16>(D, true);
-  Walk w;
-  w.init(p, false);
-  Piece x;
-  uint32_t elected;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(elected));
-  const uint32_t tm = misc->tmem;
-  const uint64_t kd = smem_desc_sw128(smem_u32(smem)), vd = desc_mn(smem_u32(smem), kKeys * 128);      // of the first byte of shared memory
-  const uint32_t lo = static_cast<uint32_t>(kd), khi = static_cast<uint32_t>(kd >> 32), vlo = static_cast<uint32_t>(vd), vhi = static_cast<uint32_t>(vd >> 32);
-  uint32_t loads = 0, tiles = 0, pieces = 0;
+  static constexpr uint32_t ID_S = idesc<T::BF16>(kKeys, false), ID_O = idesc<T::BF16>(D, true);
+  const TreeAttnParams& p;
+  uint8_t* smem;
+  Misc<T>* misc;
+  uint32_t elected = 0, tm = 0, lo = 0, khi = 0, vlo = 0, vhi = 0;
   bool ok = true;
-  auto wait = [&](uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); };
-  auto scores = [&](uint32_t t) {                       // S of tile t
-    const uint32_t buf = t % T::SBUF, s = loads % T::SLOTS;
-    // (S's buffer was P's of two tiles ago: the MMAs that read it were issued before, and one thread's MMAs run in order)
-    if (!wait(misc->full[s], loads / T::SLOTS)) return;
-    fence_proxy_async_smem();                           // (rows that ordinary copies wrote, to the MMAs)
-    tc_fence_after();
+
+  __device__ __forceinline__ void init() {
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(elected));
+    tm = misc->tmem;
+    const uint64_t kd = smem_desc_sw128(smem_u32(smem)), vd = desc_mn(smem_u32(smem), kKeys * 128);      // of the first byte of shared memory
+    lo = static_cast<uint32_t>(kd), khi = static_cast<uint32_t>(kd >> 32), vlo = static_cast<uint32_t>(vd), vhi = static_cast<uint32_t>(vd >> 32);
+  }
+  __device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); }
+
+  __device__ __forceinline__ bool ready(uint64_t& bar, uint32_t parity) const { return mbar_try_wait(smem_u32(&bar), parity & 1); }
+
+  // S of tile t, K being load n, which is there. S's buffer was P's of two tiles ago: the MMAs that read it were issued before, and
+  // one thread's MMAs run in order.
+  __device__ __forceinline__ void scores(uint32_t t, uint32_t n) {
+    const uint32_t buf = t % T::SBUF, s = n % T::SLOTS;
     if (elected) {
       const uint32_t k = lo + (T::OFF_SLOT + s * T::SLOT) / 16;
 #pragma unroll
@@ -600,32 +652,64 @@ __device__ __forceinline__ void issue_mmas(const TreeAttnParams& p, uint8_t* sme
       commit2(smem_u32(&misc->empty[s]), smem_u32(&misc->s_full[buf]));
     }
     __syncwarp();
-    ++loads;
-  };
-  while (ok && w.next(p, x)) {
-    if (!wait(misc->q_full, pieces)) break;
-    tc_fence_after();
-    scores(tiles);
-    for (int i = x.begin; ok && i < x.end; ++i) {
-      if (i + 1 < x.end) scores(tiles + 1);
-      const uint32_t buf = tiles % T::SBUF, s = loads % T::SLOTS;
-      if (!wait(misc->p_full[buf], tiles / T::SBUF) || !wait(misc->full[s], loads / T::SLOTS)) break;
-      fence_proxy_async_smem();
-      tc_fence_after();
-      if (elected) {
-        mma8_pv(tm, tm + T::TMEM_S + buf * kKeys, vlo + (T::OFF_SLOT + s * T::SLOT) / 16, vhi, ID_O, i > x.begin);
-        commit2(smem_u32(&misc->empty[s]), smem_u32(&misc->pv_done[buf]));
-      }
-      __syncwarp();
-      ++loads;
-      ++tiles;
-    }
-    ++pieces;
   }
-}
+  // O (+)= P V of tile t, V being load n.
+  __device__ __forceinline__ void output(uint32_t t, uint32_t n, bool first) {
+    const uint32_t buf = t % T::SBUF, s = n % T::SLOTS;
+    if (elected) {
+      mma8_pv(tm, tm + T::TMEM_S + buf * kKeys, vlo + (T::OFF_SLOT + s * T::SLOT) / 16, vhi, ID_O, !first);
+      commit2(smem_u32(&misc->empty[s]), smem_u32(&misc->pv_done[buf]));
+    }
+    __syncwarp();
+  }
+  // Load n is there, for the MMAs to read what ordinary copies wrote.
+  __device__ __forceinline__ bool take(uint32_t n) {
+    if (!wait(misc->full[n % T::SLOTS], n / T::SLOTS)) return false;
+    fence_proxy_async_smem();
+    tc_fence_after();
+    return true;
+  }
+
+  // S_0, S_1, O_0, S_2, O_1, ... A wait takes 200 cycles even where nothing is to be waited for, and four of them a tile left the tensor cores
+  // idle for a third of the time: so the three barriers of a step are asked together.
+  __device__ __forceinline__ void run() {
+    init();
+    Walk<MODE> w;
+    w.init(p, 2 * kKeys * T::ROW, false);
+    Piece x;
+    uint32_t before = 0, tiles = 0, pieces = 0;
+    while (ok && w.next(p, x)) {
+      const uint32_t n = x.end - x.begin;
+      if (!wait(misc->q_full, pieces) || !take(before)) break;
+      scores(tiles, before);
+      if (n > 1) {
+        if (!take(before + 1)) break;
+        scores(tiles + 1, before + 1);
+      }
+#pragma unroll 1
+      for (uint32_t i = 0; ok && i < n; ++i, ++tiles) {
+        const uint32_t buf = tiles % T::SBUF, v = before + min(2 * i + 2, 2 * n - 1), k = before + 2 * i + 3;
+        const bool more = i + 2 < n;
+        const bool p_there = ready(misc->p_full[buf], tiles / T::SBUF), v_there = ready(misc->full[v % T::SLOTS], v / T::SLOTS);
+        const bool k_there = more && ready(misc->full[k % T::SLOTS], k / T::SLOTS);
+        const unsigned there = __reduce_and_sync(0xffffffffu, (p_there && v_there ? 1u : 0u) | (k_there ? 2u : 0u));
+        if (!(there & 1u) && (!wait(misc->p_full[buf], tiles / T::SBUF) || !wait(misc->full[v % T::SLOTS], v / T::SLOTS))) break;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        output(tiles, v, i == 0);
+        if (more) {
+          if (!(there & 2u) && !take(k)) break;
+          scores(tiles + 2, k);
+        }
+      }
+      before += 2 * n;
+      ++pieces;
+    }
+  }
+};
 
 // ---- the softmax warps: thread = row
-template <int CACHE, int D>
+template <int CACHE, int D, Mode MODE>
 struct Softmax {
   using T = Traits<CACHE, D>;
   const TreeAttnParams& p;
@@ -740,7 +824,7 @@ struct Softmax {
 
   // Infinite and NaN values that the row sees, in 32 of its channels from d on: those that were taken out of tiles that not all rows see
   // whole; and, as a weight that underflowed to 0 makes an infinity NaN, all of them where a channel is NaN.
-  __device__ __noinline__ void add_odd(float* o, int d, const Walk& w, const Piece& x, uint64_t mask, bool all) const {
+  __device__ __noinline__ void add_odd(float* o, int d, const Walk<MODE>& w, const Piece& x, uint64_t mask, bool all) const {
     for (int c = 0; c < 32; ++c)
       if (o[c] != o[c]) o[c] = 0.f;
     for (int i = x.begin; i < x.end; ++i) {
@@ -768,8 +852,8 @@ struct Softmax {
   }
 
   __device__ __forceinline__ void run() {
-    Walk w;
-    w.init(p, blockIdx.x == 0 && warp == 0);
+    Walk<MODE> w;
+    w.init(p, 2 * kKeys * T::ROW, MODE == kCluster ? warp == 0 : blockIdx.x == 0 && warp == 0);
     Piece x;
     uint32_t tiles = 0, pieces = 0;
     TreeCut cut{};
@@ -840,7 +924,9 @@ struct Softmax {
       ++pieces;
       if (busy) {
         tc_fence_after();
-        float* const part = p.partials + (static_cast<size_t>(2) * blockIdx.x + x.second) * tree_partial_floats(D);
+        // a cluster's parts stay in the ring, which is at rest
+        float* const part = MODE == kCluster ? reinterpret_cast<float*>(smem + T::OFF_SLOT)
+                                             : p.partials + (static_cast<size_t>(2) * blockIdx.x + x.second) * tree_partial_floats(D);
         const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : vs / sum;
         uint8_t* const stage = smem + warp * 4096;      // 128 bytes of 32 rows
         uint16_t* const to = p.out + token * p.ldo + static_cast<int64_t>(head) * D;
@@ -848,9 +934,11 @@ struct Softmax {
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           read_tmem(mine + c, o);
-          bool nan = false;
+          float2 all[2] = {{0.f, 0.f}, {0.f, 0.f}};     // NaN where one of them is, or where infinities meet
 #pragma unroll
-          for (int e = 0; e < 32; ++e) nan |= __uint_as_float(o[e]) != __uint_as_float(o[e]);
+          for (int e = 0; e < 32; e += 2) all[e / 2 % 2] = __fadd2_rn(all[e / 2 % 2], make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])));
+          all[0] = __fadd2_rn(all[0], all[1]);
+          const bool nan = !(all[0].x + all[0].y == all[0].x + all[0].y);
           if (live && (odd || nan) && sum == sum) {
             float f[32];
 #pragma unroll
@@ -901,16 +989,75 @@ struct Softmax {
       }
       if (!x.whole && x.starts_here) cut = TreeCut{x.parts, w.r.row0, x.kvh, first_row, rows, vs};
     }
-    if (warp == 0 && lane == 0) p.cuts[blockIdx.x] = cut;
+    if (MODE == kList && warp == 0 && lane == 0) p.cuts[blockIdx.x] = cut;
   }
 };
 
+// The blocks of a cluster join their parts, each some (row, four channels); all threads of all of them.
 template <int CACHE, int D>
+__device__ __forceinline__ void join_cluster(const TreeAttnParams& p, uint8_t* smem, const Walk<kCluster>& w) {
+  using T = Traits<CACHE, D>;
+  const int size = 1 << p.cluster_log, rank = blockIdx.x & (size - 1);
+  const int kvh = w.seg / p.row_blocks, first_row = (w.seg - kvh * p.row_blocks) * kTreeRows;
+  const int rows = min(kTreeRows, w.r.n * p.group - first_row), padded = (rows + 31) & ~31;
+  const uint32_t part = smem_u32(smem) + T::OFF_SLOT;
+  float vs = 1.f;
+  if constexpr (T::F8) vs = __ldg(p.v_scale + kvh);
+  for (int i = rank * T::THREADS + static_cast<int>(threadIdx.x); i < padded * (D / 4); i += size * T::THREADS) {
+    const int d4 = i / padded, r = i - d4 * padded;
+    if (r >= rows) continue;
+    float top = -INFINITY, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    // N blocks' parts with one latency
+    auto take = [&](auto count, int from) {
+      constexpr int N = decltype(count)::value;
+      float m[N], s[N], most = top;
+      float4 v[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        m[k] = attn::ld_cluster(part + 4 * r, from + k);
+        s[k] = attn::ld_cluster(part + 4 * (kTreeRows + r), from + k);
+        v[k] = attn::ld_cluster4(part + 4 * (2 * kTreeRows) + 16 * (d4 * kTreeRows + r), from + k);
+        most = fmaxf(most, m[k]);
+      }
+      const float base = most == -INFINITY ? 0.f : most, f0 = faded(top - base);
+      top = most;
+      l *= f0, a.x *= f0, a.y *= f0, a.z *= f0, a.w *= f0;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (s[k] == 0.f) continue;                      // nothing was seen, or there was no tile: o is not what it should be
+        const float f = faded(m[k] - base);
+        l += f * s[k];
+        a.x += f * v[k].x;
+        a.y += f * v[k].y;
+        a.z += f * v[k].z;
+        a.w += f * v[k].w;
+      }
+    };
+    if (size >= 8)
+      for (int k = 0; k < size; k += 8) take(std::integral_constant<int, 8>{}, k);
+    else if (size == 4)
+      take(std::integral_constant<int, 4>{}, 0);
+    else
+      take(std::integral_constant<int, 2>{}, 0);
+    const int gr = first_row + r, node = static_cast<int>(p.group_div.div(gr)), head = kvh * p.group + gr - node * p.group;
+    const int64_t token = static_cast<int64_t>(w.r.row0) + node;
+    const float inv = l == 0.f ? 0.f : vs / l;
+    uint2 out;
+    out.x = p.q_bf16 ? pack2<true>(a.x * inv, a.y * inv) : pack2<false>(a.x * inv, a.y * inv);
+    out.y = p.q_bf16 ? pack2<true>(a.z * inv, a.w * inv) : pack2<false>(a.z * inv, a.w * inv);
+    *reinterpret_cast<uint2*>(p.out + token * p.ldo + static_cast<int64_t>(head) * D + 4 * d4) = out;
+    if (d4 == 0 && p.lse != nullptr) p.lse[token * p.q_heads + head] = l == 0.f ? -INFINITY : (top - T::POFF) * kLn2 + logf(l);
+  }
+}
+
+template <int CACHE, int D, Mode MODE>
 __global__ void __launch_bounds__(Traits<CACHE, D>::THREADS, Traits<CACHE, D>::BLOCKS) tree_attention_kernel(const __grid_constant__ TreeAttnParams p) {
   using T = Traits<CACHE, D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc<T>* const misc = reinterpret_cast<Misc<T>*>(smem + T::OFF_MISC);
   static_assert(sizeof(Misc<T>) <= 1024, "misc");
+  static_assert(tree_partial_floats(D) * 4 <= T::OFF_MISC - T::OFF_SLOT, "a part fits the ring");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023) != 0) {                  // the swizzle goes by addresses
     if (threadIdx.x == 0) set_status(p.status, TL_ECUDA);
@@ -937,15 +1084,35 @@ __global__ void __launch_bounds__(Traits<CACHE, D>::THREADS, Traits<CACHE, D>::B
   tc_fence_after();
   pdl_wait_prior();
   if (warp < kSoftmaxWarps) {
-    Softmax<CACHE, D> s{p, smem, misc, warp, lane};
+    Softmax<CACHE, D, MODE> s{p, smem, misc, warp, lane};
     s.run();
   } else if (warp == kMmaWarp) {
-    issue_mmas<CACHE, D>(p, smem, misc);
+    Mma<CACHE, D, MODE> m{p, smem, misc};
+    m.run();
   } else {
-    Loader<CACHE, D> l{p, smem, misc, warp - kLoadWarp, lane};
+    Loader<CACHE, D, MODE> l{p, smem, misc, warp - kLoadWarp, lane};
     l.run();
   }
   pdl_launch_dependents();
+  if (MODE == kCluster && p.cluster_log > 0) {
+    Walk<kCluster> w;
+    w.init(p, 0, false);
+    if (w.more) {                                       // the same for all blocks of the cluster
+      if (warp < kSoftmaxWarps && (w.r.tiles >> p.cluster_log) == 0) {
+        // a block without tiles says so
+        Piece x;
+        if (!w.next(p, x)) {
+          float* const part = reinterpret_cast<float*>(smem + T::OFF_SLOT);
+          part[threadIdx.x] = -INFINITY;
+          part[kTreeRows + threadIdx.x] = 0.f;
+        }
+      }
+      __syncwarp();
+      cluster_sync();
+      join_cluster<CACHE, D>(p, smem, w);
+      cluster_sync();                                   // no block leaves while another reads its part
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -1032,24 +1199,53 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
 template <int CACHE, int D>
 cudaError_t launch(TreeAttnParams& p, int sms, cudaStream_t st) {
   using T = Traits<CACHE, D>;
-  static int ready[64];
+  static int ready[64], at_once[64][kMaxClusterLog + 1];         // by device: how many clusters of 2^i blocks run at once
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto* const clusters = tree_attention_kernel<CACHE, D, kCluster>;
   if (__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE) == 0) {
-    e = cudaFuncSetAttribute(tree_attention_kernel<CACHE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    for (auto* kernel : {tree_attention_kernel<CACHE, D, kList>, clusters}) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+      if (e != cudaSuccess) return e;
+    }
+    e = cudaFuncSetAttribute(clusters, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    __atomic_store_n(&at_once[dev][0], sms * T::BLOCKS, __ATOMIC_RELAXED);
+    for (int log = 1; log <= kMaxClusterLog; ++log) {
+      cudaLaunchAttribute size;
+      size.id = cudaLaunchAttributeClusterDimension;
+      size.val.clusterDim.x = 1 << log, size.val.clusterDim.y = size.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1 << log), cfg.blockDim = dim3(T::THREADS), cfg.dynamicSmemBytes = T::SMEM;
+      cfg.attrs = &size, cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, clusters, &cfg);
+      if (e != cudaSuccess) return e;
+      __atomic_store_n(&at_once[dev][log], n, __ATOMIC_RELAXED);
+    }
     __atomic_store_n(&ready[dev], 1, __ATOMIC_RELEASE);
+  }
+  const long long nodes = p.T < TL_TREE_NODES ? p.T : TL_TREE_NODES;
+  const long long seen = p.window > 0 ? p.window + 15ll + p.sinks : p.capacity, keys = (seen < p.capacity ? seen : p.capacity) + nodes;
+  const long long tiles = (keys + kKeys - 1) / kKeys + (p.sinks > 0);
+  p.row_blocks = static_cast<int>((nodes * p.group + kTreeRows - 1) / kTreeRows);
+  const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.row_blocks;
+  // Few segments of few tiles: a cluster each, of the most blocks that all run at once, while a block has eight tiles at most and
+  // none is without.
+  for (int log = kMaxClusterLog; log >= 0; --log) {
+    const int c = 1 << log;
+    if (segments > __atomic_load_n(&at_once[dev][log], __ATOMIC_RELAXED) || (log > 0 && tiles <= c / 2)) continue;
+    if (tiles > 8 * c) break;
+    p.cluster_log = log;
+    return launch_pdl_cluster(clusters, dim3(static_cast<unsigned>(segments * c)), dim3(T::THREADS), T::SMEM, st, c, p);
   }
   long long grid = static_cast<long long>(sms) * T::BLOCKS;
   if (grid > kTreeMaxGrid) grid = kTreeMaxGrid;
-  // at most as many blocks as the list can have places
-  const long long nodes = p.T < TL_TREE_NODES ? p.T : TL_TREE_NODES;
-  const long long keys = p.window > 0 && p.window + static_cast<long long>(p.sinks) < p.capacity ? p.window + static_cast<long long>(p.sinks) : p.capacity;
-  const long long most = static_cast<long long>(p.B) * p.kv_heads * ((nodes * p.group + kTreeRows - 1) / kTreeRows) * ((keys + 3 * kKeys) / kKeys + kSegmentCost);
+  const long long most = segments * (tiles + kSegmentCost);      // places that the list can have
   if (grid > most) grid = most;
   p.grid = static_cast<int>(grid);
-  e = launch_pdl(tree_attention_kernel<CACHE, D>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
+  e = launch_pdl(tree_attention_kernel<CACHE, D, kList>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
   if (e != cudaSuccess || grid == 1) return e;
   return launch_pdl(tree_join_kernel<D, !T::BF16>, dim3(static_cast<unsigned>(grid), D / 32), dim3(kJoinWarps * 32), 0, st, p);
 }
