@@ -87,7 +87,7 @@ using attn::widen_hi;
 using attn::widen_lo;
 
 constexpr int kKeys = 64;                // keys of a tile
-constexpr int kSegmentCost = 4;          // what a segment costs besides its tiles, in tiles
+constexpr int kSegmentCost = 5;          // what a segment costs besides its tiles, in tiles
 constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
 constexpr int kMaxClusterLog = 4;
 constexpr long long kReread = 64 << 20;  // bytes of K and V that several row blocks read, from which on they do so together
@@ -110,9 +110,11 @@ struct Traits {
   static constexpr bool QT = D != 128;
   static constexpr int Q = QT ? kSoftmaxWarps * 4096 : kTreeRows * D * 2;        // the results pass through it, 4 KB a warp
   static constexpr int SLOT = kKeys * D * 2, STAGE = F8 ? SLOT / 2 : 0;
-  static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 12) : D == 128 ? (F8 ? 3 : 5) : F8 ? 4 : 6;
+  static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 8) : D == 128 ? (F8 ? 3 : 4) : F8 ? 4 : 6;
   static constexpr int STAGES = F8 ? (D == 64 ? 12 : D == 128 ? 3 : 4) : 0;     // of 8-bit rows on their way, shared out to the loading warps
-  static constexpr int OFF_SLOT = Q, OFF_STAGE = OFF_SLOT + SLOTS * SLOT, OFF_MISC = OFF_STAGE + STAGES * STAGE;
+  static constexpr int PART = kTreeRows * (D + 2) * 4;           // of a cluster's block, in the ring's place
+  static constexpr int OFF_SLOT = Q, OFF_STAGE = OFF_SLOT + SLOTS * SLOT, END = OFF_STAGE + STAGES * STAGE;
+  static constexpr int OFF_MISC = END > OFF_SLOT + PART ? END : OFF_SLOT + PART;
   static constexpr int SMEM = OFF_MISC + 1024;
   static constexpr int SBUF = 2;                                 // buffers of S and P
   static constexpr int TMEM = D == 256 ? 512 : 256, TMEM_S = D, TMEM_Q = TMEM_S + SBUF * kKeys;      // columns; O in the first D
@@ -381,7 +383,7 @@ struct Walk {
       x.whole = p.cluster_log == 0;
       x.starts_here = false, x.second = 0, x.parts = 0;
       return x.end > x.begin;
-    }
+    } else {
     while (more) {
       if (at >= t1) {
         more = false;
@@ -410,6 +412,7 @@ struct Walk {
       if (x.end > x.begin) return true;
     }
     return false;
+    }
   }
 };
 
@@ -708,6 +711,15 @@ struct Mma {
   }
 };
 
+__device__ __forceinline__ void st_shared(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // ---- the softmax warps: thread = row
 template <int CACHE, int D, Mode MODE>
 struct Softmax {
@@ -720,50 +732,100 @@ struct Softmax {
 
   __device__ __forceinline__ bool wait(uint64_t& bar, uint32_t parity) { return ok = ok && wait_all(bar, parity, &misc->abort, p.status); }
 
-  // This row's query to where the MMAs take it, times the sign of the scale; returns by what its scores are scaled
-  // besides (8-bit caches: its power of two). The whole warp together; rows that are not live become zero.
-  __device__ __forceinline__ float put_query(const uint16_t* row, uint32_t mine, bool live) {
-    const int r = warp * 32 + lane;
+  // Queries and results are read and written 128 bytes of a row by eight lanes, four rows an instruction: place k of a lane is row
+  // 4 k + lane / 8 of its warp. (A row to a lane made 32 lines of every instruction.) They pass through 4 KB of shared memory, 128 bytes of
+  // each of the warp's 32 rows, 16-byte units swizzled: unit u of this lane's row, and of its places, as addresses.
+  __device__ __forceinline__ uint32_t stage() const { return smem_u32(smem) + warp * 4096; }
+  __device__ __forceinline__ uint32_t own(uint32_t base, int u) const { return (base + lane * 128 + ((lane & 7) << 4)) ^ (u << 4); }
+  __device__ __forceinline__ uint32_t placed(uint32_t base, int k) const {
+    return base + lane / 8 * 128 + (((lane % 8) ^ (lane / 8) ^ (4 * (k & 1))) << 4) + k * 512;
+  }
+  // Elements from a tensor's first to each place's first (rows that are not there: the warp's first row's, so that nothing has to branch).
+  struct Places {
+    int64_t off[8];
+    __device__ __forceinline__ void init(int64_t mine, bool live, int lane) {
+      const int64_t first = __shfl_sync(0xffffffffu, mine, 0);
+      if (!live) mine = first;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) off[k] = __shfl_sync(0xffffffffu, mine, 4 * k + lane / 8) + lane % 8 * 8;
+    }
+  };
+
+  // The warp's queries to where the MMAs take them, times the sign of the scale; returns by what the scores of this lane's row are
+  // scaled besides (8-bit caches: its power of two).
+  __device__ __forceinline__ float put_queries(const Places& places, uint32_t mine) {
+    constexpr int C = D / 64, AHEAD = C < 2 ? C : 2;    // 128-byte columns, and how many are asked for at once
     float up = 1.f, by = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
     const bool narrow = T::F8 && p.q_bf16;
+    // where a column goes: to the stage and on to tensor memory, or to its place
+    auto base = [&](int c) { return T::QT ? stage() : smem_u32(smem) + c * (kTreeRows * 128) + warp * 4096; };
+    auto ask = [&](int c, int k) { return __ldg(reinterpret_cast<const uint4*>(p.q + places.off[k] + 64 * c)); };
     if (narrow) {
       float top = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(row) + i) : make_uint4(0, 0, 0, 0);
-        const uint32_t* const w = &x.x;
+#pragma unroll 1
+      for (int c = 0; c < C; ++c) {
+        uint4 x[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack2<true>(w[j]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        for (int k = 0; k < 8; ++k) x[k] = ask(c, k);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) st_shared(placed(base(0), k), x[k]);
+        __syncwarp();
+#pragma unroll 2
+        for (int u = 0; u < 8; ++u) {
+          const uint4 v = ld_shared(own(base(0), u));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack2<true>(w[j]);
+            top = max3(top, fabsf(f.x), fabsf(f.y));
+          }
         }
+        __syncwarp();
       }
       // 2^e <= top < 2^(e + 1); e is kept where both 2^e and 2^-e are normal (an infinite or NaN q stays one)
       const int e = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, -126), 126);
       up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
       by *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
     }
-#pragma unroll (D == 256 ? 2 : 1)
-    for (int c = 0; c < D / 64; ++c) {                  // 128 bytes of the row at a time
-      uint32_t w[32];
+    // this lane's row of a column, in place
+    auto scale = [&](int c) {
+      if (!narrow && p.scale_log2 > 0.f) return;
+#pragma unroll 1
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t at = own(base(c), u);
+        const uint4 v = ld_shared(at);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(row) + 8 * c + i) : make_uint4(0, 0, 0, 0);
-        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-      }
-      if (by != 1.f || narrow) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float2 f = T::BF16 || p.q_bf16 ? unpack2<true>(w[j]) : unpack2<false>(w[j]);
           w[j] = pack2<T::BF16>(f.x * by, f.y * by);
         }
+        st_shared(at, make_uint4(w[0], w[1], w[2], w[3]));
       }
-      if constexpr (T::QT) {
-        tmem_st_32x32b_x32(mine + T::TMEM_Q + 32 * c, w);
-      } else {
+    };
+#pragma unroll 1
+    for (int c0 = 0; c0 < C; c0 += AHEAD) {
+      uint4 x[AHEAD][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(smem + c * (kTreeRows * 128) + swizzled(r, i)) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      for (int c = 0; c < AHEAD; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[c][k] = ask(c0 + c, k);
+#pragma unroll
+      for (int c = 0; c < AHEAD; ++c) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) st_shared(placed(base(c0 + c), k), x[c][k]);
+        __syncwarp();
+        scale(c0 + c);
+        if constexpr (T::QT) {
+          uint32_t w[32];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint4 v = ld_shared(own(base(0), u));
+            w[4 * u] = v.x, w[4 * u + 1] = v.y, w[4 * u + 2] = v.z, w[4 * u + 3] = v.w;
+          }
+          tmem_st_32x32b_x32(mine + T::TMEM_Q + 32 * (c0 + c), w);
+          __syncwarp();
+        }
       }
     }
     if constexpr (T::QT) {
@@ -871,7 +933,11 @@ struct Softmax {
         vs = __ldg(p.v_scale + x.kvh);
       }
       if (live) mask = static_cast<uint64_t>(__ldg(p.masks + token)) & low_bits(w.r.n);
-      if (busy) sc *= put_query(p.q + token * p.ldq + static_cast<int64_t>(head) * D, mine, live);
+      if (busy) {
+        Places places;
+        places.init(token * p.ldq + static_cast<int64_t>(head) * D, live, lane);
+        sc *= put_queries(places, mine);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&misc->q_full));
       float m = -INFINITY;
@@ -928,8 +994,8 @@ struct Softmax {
         float* const part = MODE == kCluster ? reinterpret_cast<float*>(smem + T::OFF_SLOT)
                                              : p.partials + (static_cast<size_t>(2) * blockIdx.x + x.second) * tree_partial_floats(D);
         const float sum = l.x + l.y, inv = sum == 0.f ? 0.f : vs / sum;
-        uint8_t* const stage = smem + warp * 4096;      // 128 bytes of 32 rows
-        uint16_t* const to = p.out + token * p.ldo + static_cast<int64_t>(head) * D;
+        Places places;
+        if (x.whole) places.init(token * p.ldo + static_cast<int64_t>(head) * D, live, lane);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -955,25 +1021,23 @@ struct Softmax {
                 q[e / 4 * kTreeRows] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
             continue;
           }
-          // 64 channels of 32 rows pass through shared memory, so that eight lanes write 128 bytes of a row
+          const int half = c % 64 / 8;                  // 64 channels of 32 rows pass through shared memory
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float a = __uint_as_float(o[e + 2 * k]) * inv, b = __uint_as_float(o[e + 2 * k + 1]) * inv;
-              v[k] = p.q_bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
+              const float2 f = __fmul2_rn(make_float2(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1])), make_float2(inv, inv));
+              v[k] = T::BF16 ? pack2<true>(f.x, f.y) : !T::F8 ? pack2<false>(f.x, f.y) : p.q_bf16 ? pack2<true>(f.x, f.y) : pack2<false>(f.x, f.y);
             }
-            *reinterpret_cast<uint4*>(stage + swizzled(lane, c % 64 / 8 + e / 8)) = make_uint4(v[0], v[1], v[2], v[3]);
+            st_shared(own(stage(), half + e / 8), make_uint4(v[0], v[1], v[2], v[3]));
           }
-          if (c % 64 == 0) continue;
+          if (half == 0) continue;
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int r = 4 * k + lane / 8, u = lane % 8;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + swizzled(r, u));
-            uint16_t* const at = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), r));
-            if (warp * 32 + r < rows) *reinterpret_cast<uint4*>(at + c - 32 + 8 * u) = v;
+            const uint4 v = ld_shared(placed(stage(), k));
+            if (warp * 32 + 4 * k + lane / 8 < rows) *reinterpret_cast<uint4*>(p.out + places.off[k] + c - 32) = v;
           }
           __syncwarp();
         }
@@ -1057,7 +1121,6 @@ __global__ void __launch_bounds__(Traits<CACHE, D>::THREADS, Traits<CACHE, D>::B
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc<T>* const misc = reinterpret_cast<Misc<T>*>(smem + T::OFF_MISC);
   static_assert(sizeof(Misc<T>) <= 1024, "misc");
-  static_assert(tree_partial_floats(D) * 4 <= T::OFF_MISC - T::OFF_SLOT, "a part fits the ring");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023) != 0) {                  // the swizzle goes by addresses
     if (threadIdx.x == 0) set_status(p.status, TL_ECUDA);
