@@ -90,6 +90,7 @@ constexpr int kKeys = 64;                // keys of a tile
 constexpr int kSegmentCost = 5;          // what a segment costs besides its tiles, in tiles
 constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
 constexpr int kMaxClusterLog = 4;
+constexpr int kLeastShare = 4;           // places of the list to a block: fewer make more parts than their joins are worth
 constexpr long long kReread = 64 << 20;  // bytes of K and V that several row blocks read, from which on they do so together
 
 enum Mode {
@@ -319,7 +320,7 @@ struct Walk {
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      const long long least = attn::divide(total + p.grid - 1, p.grid);
+      const long long least = max(attn::divide(total + p.grid - 1, p.grid), static_cast<long long>(kLeastShare));
       if (least <= share) break;
       if (share == 0) {
         share = least;
@@ -530,16 +531,23 @@ struct Loader {
     }
     cp_async_commit();
     cp_async_wait<0>();
-    constexpr uint32_t E = T::BF16 ? 0x7F807F80u : 0x7C007C00u;
-    bool found = false;
-#pragma unroll 2
+    // an exponent of ones, plus one in its last place, carries into the sign's place
+    constexpr uint32_t E = T::BF16 ? 0x7F807F80u : 0x7C007C00u, ONE = T::BF16 ? 0x00800080u : 0x04000400u;
+    uint32_t any = 0;
+#pragma unroll 8
     for (int i = 0; i < STEPS; ++i) {
-      uint4* const at = reinterpret_cast<uint4*>(smem + off + swizzled(i * RPI + row, chunk % 8));
-      uint4 x = *at;
-      const uint32_t a = __vcmpeq2(x.x & E, E), b = __vcmpeq2(x.y & E, E), c = __vcmpeq2(x.z & E, E), d = __vcmpeq2(x.w & E, E);
-      if ((a | b | c | d) != 0) *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d), found = true;
+      const uint4 x = *reinterpret_cast<const uint4*>(smem + off + swizzled(i * RPI + row, chunk % 8));
+      any |= ((x.x & E) + ONE) | ((x.y & E) + ONE) | ((x.z & E) + ONE) | ((x.w & E) + ONE);
     }
-    if (found) note_odd();
+    if ((any & 0x80008000u) != 0) {
+      note_odd();
+#pragma unroll 1
+      for (int i = 0; i < STEPS; ++i) {
+        uint4* const at = reinterpret_cast<uint4*>(smem + off + swizzled(i * RPI + row, chunk % 8));
+        const uint4 x = *at;
+        *at = make_uint4(x.x & ~__vcmpeq2(x.x & E, E), x.y & ~__vcmpeq2(x.y & E, E), x.z & ~__vcmpeq2(x.z & E, E), x.w & ~__vcmpeq2(x.w & E, E));
+      }
+    }
     fence_proxy_async_smem();
     mbar_arrive(full);
   }
@@ -1294,12 +1302,12 @@ cudaError_t launch(TreeAttnParams& p, int sms, cudaStream_t st) {
   const long long tiles = (keys + kKeys - 1) / kKeys + (p.sinks > 0);
   p.row_blocks = static_cast<int>((nodes * p.group + kTreeRows - 1) / kTreeRows);
   const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.row_blocks;
-  // Few segments of few tiles: a cluster each, of the most blocks that all run at once, while a block has eight tiles at most and
-  // none is without.
+  // Few segments of few tiles: a cluster each, of the most blocks that all run at once, while a block has more than one tile and
+  // ten at most.
   for (int log = kMaxClusterLog; log >= 0; --log) {
     const int c = 1 << log;
-    if (segments > __atomic_load_n(&at_once[dev][log], __ATOMIC_RELAXED) || (log > 0 && tiles <= c / 2)) continue;
-    if (tiles > 8 * c) break;
+    if (segments > __atomic_load_n(&at_once[dev][log], __ATOMIC_RELAXED) || (log > 0 && tiles <= c)) continue;
+    if (tiles > 10 * c) break;
     p.cluster_log = log;
     return launch_pdl_cluster(clusters, dim3(static_cast<unsigned>(segments * c)), dim3(T::THREADS), T::SMEM, st, c, p);
   }
