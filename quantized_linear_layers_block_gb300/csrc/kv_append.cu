@@ -69,7 +69,7 @@ __host__ __device__ constexpr int power_of_two(int n) {
 // lanes = head_dim / 16 threads cover a head; `rows` heads are taken at a time. With NORM they are a power of two of neighbouring
 // lanes of one warp, the last of them idle for other sizes, and add up the squares of their head by shuffles.
 template <bool BF16, bool F8, int THREADS, bool NORM>
-__global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 12 : 20) : THREADS == 256 ? (NORM ? 2 : 4) : 1) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 14 : 20) : THREADS == 256 ? (NORM ? 2 : 4) : 1) kv_append_kernel(const __grid_constant__ AppendParams p) {
   const int lanes = NORM ? power_of_two(p.dim >> 4) : p.dim >> 4;
   const int row = threadIdx.x / lanes, j = threadIdx.x - row * lanes;
   const int rows = blockDim.x / lanes;
@@ -126,8 +126,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 12 : 20) : TH
     cell = page * p.page_stride + (slot - page * p.page_size) * p.token_stride;
   }
   const int heads = p.q_heads + (keep ? 2 * p.kv_heads : 0);
-  float wt[16];                         // norm weights of the thread's channels, of q's heads, then of k's
-  int wt_of = 0;                        // 1: q's, 2: k's
   const unsigned head_lanes = NORM ? (lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1) << ((threadIdx.x & 31) / lanes * lanes)) : 0u;
   const float per_channel = 1.f / static_cast<float>(p.dim);
   auto store = [&](int h, const uint4& v0, const uint4& v1) {
@@ -143,23 +141,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 12 : 20) : TH
       widen8<BF16>(v1, b);
     }
     if (normed) {
-      if (wt_of != 2 - is_q) {
-        wt_of = 2 - is_q;
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 w = idle ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldg(reinterpret_cast<const float4*>(weight + (i < 8 ? c0 + i : c1 + i - 8)));
-          wt[i] = w.x, wt[i + 1] = w.y, wt[i + 2] = w.z, wt[i + 3] = w.w;
-        }
-      }
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += a[i] * a[i] + b[i] * b[i];
-      for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(head_lanes, sum, o);
-      const float inv = __frsqrt_rn(sum * per_channel + p.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = __fmul_rn(__fmul_rn(a[i], inv), wt[i]);
-        b[i] = __fmul_rn(__fmul_rn(b[i], inv), wt[8 + i]);
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) sum += __shfl_xor_sync(head_lanes, sum, o);
+      const float inv = __frsqrt_rn(sum * per_channel + p.eps);
+      // (the weights come from L1 for each head: held in registers they would cost a third of the blocks)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(weight + (idle ? 0 : c0 + i))), x = __ldg(reinterpret_cast<const float4*>(weight + (idle ? 0 : c1 + i)));
+        a[i] *= inv * w.x, a[i + 1] *= inv * w.y, a[i + 2] *= inv * w.z, a[i + 3] *= inv * w.w;
+        b[i] *= inv * x.x, b[i + 1] *= inv * x.y, b[i + 2] *= inv * x.z, b[i + 3] *= inv * x.w;
       }
     }
     if (idle) return;
@@ -206,6 +200,16 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 12 : 20) : TH
       }
     }
   };
+  if constexpr (NORM) {                 // the next head's data are on their way while this one's squares are summed
+#pragma unroll 1
+    for (int h = row; h < heads; h += rows) {
+      uint4 v0, v1;
+      load(h + rows < heads ? h + rows : h, v0, v1);
+      store(h, first0, first1);
+      first0 = v0, first1 = v1;
+    }
+    return;
+  }
   if (row < heads) store(row, first0, first1);
 #pragma unroll 2
   for (int h = row + rows; h < heads; h += rows) {

@@ -444,6 +444,15 @@ __device__ __forceinline__ uint64_t visible(const TreeAttnParams& p, const Reque
   return cached | drafted;
 }
 
+__device__ __forceinline__ void st_shared(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // ---- the loading warps: rows of K and V into the ring's slots. They take the loads in turn, each a whole one: looking the rows' addresses up
 // takes as long as copying them, and all warps together at every load took 3000 cycles for a tile of 256 channels.
 template <int CACHE, int D, Mode MODE>
@@ -561,25 +570,38 @@ struct Loader {
     cp_async_wait<0>();
     wait_empty(n);
     if (!ok) return;
-    bool found = false;
-    uint8_t* const to = smem + T::OFF_SLOT + n % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128);
-#pragma unroll 4
-    for (int i = 0; i < STEPS; ++i) {
-      const int kk = i * RPI + row;
-      uint4 x = *reinterpret_cast<const uint4*>(stage + kk * T::ROW);
-      if (check) {                                      // e4m3 has NaN (0x7F, 0xFF), no infinities
-        constexpr uint32_t N = 0x7F7F7F7Fu;
+    if (check) {                                        // e4m3 has NaN (0x7F, 0xFF), no infinities
+      constexpr uint32_t N = 0x7F7F7F7Fu;
+      bool found = false;
+#pragma unroll 1
+      for (int i = 0; i < STEPS; ++i) {
+        uint4* const at = reinterpret_cast<uint4*>(stage + (i * RPI + row) * T::ROW);
+        const uint4 x = *at;
         const uint32_t a = __vcmpeq4(x.x & N, N), b = __vcmpeq4(x.y & N, N), c = __vcmpeq4(x.z & N, N), d = __vcmpeq4(x.w & N, N);
-        found |= (a | b | c | d) != 0;
-        x = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d);
+        if ((a | b | c | d) != 0) *at = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d), found = true;
       }
-      // (lanes of the two 64-channel blocks write their halves in different order: different banks)
-      const bool turn = chunk & 4;
-      if (turn) x = make_uint4(x.z, x.w, x.x, x.y);
-      *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2 + turn)) = make_uint4(widen_lo(x.x), widen_hi(x.x), widen_lo(x.y), widen_hi(x.y));
-      *reinterpret_cast<uint4*>(to + swizzled(kk, chunk % 4 * 2 + !turn)) = make_uint4(widen_lo(x.z), widen_hi(x.z), widen_lo(x.w), widen_hi(x.w));
+      if (found) note_odd();
     }
-    if (found) note_odd();
+    // Lanes of the two 64-channel blocks write their halves in different order: different banks. (All loads of a batch before its
+    // conversions: one after the other took three times as long.)
+    const bool turn = chunk & 4;
+    const uint32_t from = smem_u32(stage) + row * T::ROW;
+    const uint32_t to = smem_u32(smem) + T::OFF_SLOT + n % T::SLOTS * T::SLOT + chunk / 4 * (kKeys * 128) + row * 128 + (((chunk % 4 * 2 + turn) ^ (row & 7)) << 4);
+    constexpr int BATCH = STEPS < 8 ? STEPS : 8;
+#pragma unroll
+    for (int i0 = 0; i0 < STEPS; i0 += BATCH) {
+      uint4 x[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) x[i] = ld_shared(from + (i0 + i) * (RPI * T::ROW));
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        if (turn) x[i] = make_uint4(x[i].z, x[i].w, x[i].x, x[i].y);
+        const int r = (i0 + i) * RPI;
+        const uint32_t at = (to ^ ((r & 7) << 4)) + r * 128;
+        st_shared(at, make_uint4(widen_lo(x[i].x), widen_hi(x[i].x), widen_lo(x[i].y), widen_hi(x[i].y)));
+        st_shared(at ^ 16, make_uint4(widen_lo(x[i].z), widen_hi(x[i].z), widen_lo(x[i].w), widen_hi(x[i].w)));
+      }
+    }
     fence_proxy_async_smem();
     mbar_arrive(smem_u32(&misc->full[n % T::SLOTS]));
   }
@@ -718,15 +740,6 @@ struct Mma {
     }
   }
 };
-
-__device__ __forceinline__ void st_shared(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 
 // ---- the softmax warps: thread = row
 template <int CACHE, int D, Mode MODE>
