@@ -270,12 +270,13 @@ PyObject* tree_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     on_device(&slots, c->device, "slots");
     const Trees trees(a[2], a[4], a[3], c->device);
     const int64_t T = parents.dim() == 1 ? parents.size(0) : 0;
-    const void* const up = vector(parents, at::kInt, T, "parents");
+    const auto* const up = static_cast<const int32_t*>(vector(parents, at::kInt, T, "parents"));
+    auto* const pm = static_cast<int64_t*>(const_cast<void*>(vector(masks, at::kLong, T, "masks")));
+    auto* const pp = static_cast<int32_t*>(const_cast<void*>(vector(positions, at::kInt, T, "positions")));
+    auto* const ps = static_cast<int64_t*>(const_cast<void*>(vector(slots, at::kLong, T, "slots")));
     const OnDevice guard(c->device);
-    return tl_tree_plan(static_cast<const int32_t*>(up), trees.starts, trees.B, fits(T, "parents"), trees.lens, trees.pages, trees.width,
-                        trees.ldp, c->page_size, c->num_pages, static_cast<int64_t*>(const_cast<void*>(vector(masks, at::kLong, T, "masks"))),
-                        static_cast<int32_t*>(const_cast<void*>(vector(positions, at::kInt, T, "positions"))),
-                        static_cast<int64_t*>(const_cast<void*>(vector(slots, at::kLong, T, "slots"))), stream_of(a[8], parents));
+    return tl_tree_plan(up, trees.starts, trees.B, fits(T, "parents"), trees.lens, trees.pages, trees.width, trees.ldp, c->page_size,
+                        c->num_pages, pm, pp, ps, stream_of(a[8], parents));
   });
 }
 
@@ -307,9 +308,9 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool all = window > INT32_MAX;
     const int tokens = all ? 0 : window < 0 ? -1 : static_cast<int>(window);
     const int first = sinks < 0 ? -1 : all ? 0 : sinks > INT32_MAX ? INT32_MAX : static_cast<int>(sinks);
+    const auto* const pm = static_cast<const int64_t*>(vector(masks, at::kLong, T, "masks"));
     const OnDevice guard(c->device);
-    return tl_tree_attention(c, q.data_ptr(), code, trees.B, fits(T, "q"), fits(heads, "q"), ldq,
-                             static_cast<const int64_t*>(vector(masks, at::kLong, T, "masks")), trees.starts, trees.pages, trees.width,
+    return tl_tree_attention(c, q.data_ptr(), code, trees.B, fits(T, "q"), fits(heads, "q"), ldq, pm, trees.starts, trees.pages, trees.width,
                              trees.ldp, trees.lens, static_cast<float>(scale), tokens, first, out.data_ptr(), ldo, pl, ws.data_ptr(),
                              ws.nbytes(), stream_of(a[12], q));
   });
@@ -338,11 +339,12 @@ PyObject* verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const int B = Trees::requests(starts);
     auto ints = [&](const at::Tensor& t, int64_t size, const char* name) { return static_cast<int32_t*>(const_cast<void*>(vector(t, at::kInt, size, name))); };
+    const int32_t *const pt = ints(tokens, T, "tokens"), *const pp = ints(parents, T, "parents");
+    int32_t *const po = ints(path, T, "path"), *const pc = ints(counts, B, "counts"), *const pn = ints(next, B, "next");
+    const auto* const pu = static_cast<const float*>(vector(uniform, at::kFloat, T, "uniform"));
     const OnDevice guard(device);
-    return tl_verify_tree(static_cast<const float*>(target.data_ptr()), ldt, pd, ldd, fits(vocab, "the vocabulary"), ints(tokens, T, "tokens"),
-                          ints(parents, T, "parents"), static_cast<const int32_t*>(starts.data_ptr()), B, fits(T, "target"),
-                          static_cast<const float*>(vector(uniform, at::kFloat, T, "uniform")), ints(path, T, "path"), ints(counts, B, "counts"),
-                          ints(next, B, "next"), stream_of(a[9], target));
+    return tl_verify_tree(static_cast<const float*>(target.data_ptr()), ldt, pd, ldd, fits(vocab, "the vocabulary"), pt, pp,
+                          static_cast<const int32_t*>(starts.data_ptr()), B, fits(T, "target"), pu, po, pc, pn, stream_of(a[9], target));
   });
 }
 
@@ -354,10 +356,10 @@ PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     on_device(&path, c->device, "path"), on_device(&counts, c->device, "counts");
     const Trees trees(a[3], a[4], a[5], c->device);
     const int64_t T = path.dim() == 1 ? path.size(0) : 0;
-    const void* const nodes = vector(path, at::kInt, T, "path");
+    const auto* const nodes = static_cast<const int32_t*>(vector(path, at::kInt, T, "path"));
+    const auto* const pc = static_cast<const int32_t*>(vector(counts, at::kInt, trees.B, "counts"));
     const OnDevice guard(c->device);
-    return tl_kv_compact(c, static_cast<const int32_t*>(nodes), static_cast<const int32_t*>(vector(counts, at::kInt, trees.B, "counts")),
-                         trees.starts, trees.B, fits(T, "path"), trees.pages, trees.width, trees.ldp, trees.lens, stream_of(a[6], path));
+    return tl_kv_compact(c, nodes, pc, trees.starts, trees.B, fits(T, "path"), trees.pages, trees.width, trees.ldp, trees.lens, stream_of(a[6], path));
   });
 }
 
