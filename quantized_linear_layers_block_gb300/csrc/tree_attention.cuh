@@ -941,10 +941,13 @@ struct Softmax {
     uint32_t tiles = 0, pieces = 0;
     TreeCut cut{};
     const uint32_t mine = misc->tmem + (static_cast<uint32_t>(warp) << 21);      // this warp's 32 lanes
+    // The piece's rows from 32 `first` on are this warp's: where two blocks share an SM, warps w and w + 2 of the second change places, so that
+    // few rows of both keep all four schedulers at work.
+    const int first = warp ^ ((misc->tmem & 0xFFFF) != 0 ? 2 : 0);
     while (ok && w.next(p, x)) {
       const int first_row = x.row_block * kTreeRows, rows = min(kTreeRows, w.r.n * p.group - first_row);
-      const int mr = warp * 32 + lane;
-      const bool busy = warp * 32 < rows, live = mr < rows;
+      const int mr = first * 32 + lane;
+      const bool busy = first * 32 < rows, live = mr < rows;
       const int gr = first_row + (live ? mr : 0), node = static_cast<int>(p.group_div.div(gr)), head = x.kvh * p.group + gr - node * p.group;
       const int64_t token = static_cast<int64_t>(w.r.row0) + node;
       uint64_t mask = 0;
@@ -1058,7 +1061,7 @@ struct Softmax {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint4 v = ld_shared(placed(stage(), k));
-            if (warp * 32 + 4 * k + lane / 8 < rows) *reinterpret_cast<uint4*>(p.out + places.off[k] + c - 32) = v;
+            if (first * 32 + 4 * k + lane / 8 < rows) *reinterpret_cast<uint4*>(p.out + places.off[k] + c - 32) = v;
           }
           __syncwarp();
         }
