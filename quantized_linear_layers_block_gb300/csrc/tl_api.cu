@@ -551,14 +551,16 @@ int tl_verify_tree(const float* target, int64_t ldt, const float* draft, int64_t
                    void* stream) {
   if (B < 0 || T < 0 || vocab <= 0) return TL_EINVAL;
   if (vocab > (1 << 24)) return TL_EUNSUPPORTED;
-  if (B == 0) return TL_OK;
-  if (!starts || !counts || !next || (T > 0 && (!target || !tokens || !parents || !uniform || !path))) return TL_EINVAL;
+  if (B == 0 && T == 0) return TL_OK;
+  if (!starts || (B > 0 && (!counts || !next)) || (T > 0 && (!target || !tokens || !parents || !uniform || !path))) return TL_EINVAL;
   for (const void* x : {static_cast<const void*>(target), static_cast<const void*>(draft), static_cast<const void*>(tokens),
                         static_cast<const void*>(parents), static_cast<const void*>(starts), static_cast<const void*>(uniform),
                         static_cast<const void*>(path), static_cast<const void*>(counts), static_cast<const void*>(next)})
     if (!aligned4(x)) return TL_EINVAL;
   int r;
   if ((r = check_rows(ldt, vocab, T, 1)) != TL_OK || (draft != nullptr && (r = check_rows(ldd, vocab, T, 1)) != TL_OK)) return r;
+  if (B == 0)                                          // all rows are padding
+    return cudaMemsetAsync(path, 0xFF, static_cast<size_t>(T) * sizeof(int32_t), as_stream(stream)) == cudaSuccess ? TL_OK : TL_ECUDA;
   int sms = 0;
   int* status = nullptr;
   if ((r = num_sms(&sms)) != TL_OK || (r = status_ptr(&status)) != TL_OK) return r;

@@ -168,3 +168,30 @@ def test_refusals():
     assert empty.shape == (0, 4, 64)
     assert tl.tl_verify_tree(torch.rand(0, 7, device="cuda"), None, i32([]), i32([]), i32([0, 0]), torch.rand(0, device="cuda"))[1].tolist() == [0]
     assert tl.tl_get_status() == tl.TL_OK
+
+
+def test_all_rows_are_padding():
+    """No request, but rows: the outputs of padding."""
+    kv = tl.PagedKVCache(4, 16, 2, 64)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")       # noqa: E731
+    none, pages = i32([]), torch.zeros((0, 3), dtype=torch.int32, device="cuda")
+    path, counts, after = tl.tl_verify_tree(torch.rand(5, 9, device="cuda"), None, i32([1] * 5), i32([-1] * 5), i32([0]), torch.rand(5, device="cuda"),
+                                            path=i32([7] * 5))
+    assert path.tolist() == [-1] * 5 and counts.numel() == after.numel() == 0
+    masks, positions, slots = kv.plan_tree(i32([-1] * 5), i32([0]), none, pages)
+    assert masks.tolist() == positions.tolist() == [0] * 5 and slots.tolist() == [-1] * 5
+    out = torch.full((5, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    kv.attend_tree(torch.ones_like(out), masks, i32([0]), pages, none, out=out)
+    assert torch.all(out == 3.0)
+    kv.compact(path, counts, i32([0]), pages, none)
+    assert tl.tl_get_status() == tl.TL_OK
+
+
+@pytest.mark.parametrize("hq,hkv,d,cache", [(128, 1, 64, "bf16"), (128, 1, 256, "f8"), (1024, 8, 128, "f16")])
+def test_most_rows(hq, hkv, d, cache):
+    """64 nodes of 128 heads on one: 64 row blocks to a request."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(hq + d)
+    kv = filled(60, 16, hkv, d, cache, gen)
+    qtype = torch.float16 if cache == "f16" else torch.bfloat16
+    same(*chains(kv, [130, 0, 77], 64, hq, gen, qtype))
