@@ -99,6 +99,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 14 : 20) : TH
   // the first head's data wait for neither slot nor angles
   uint4 first0 = make_uint4(0, 0, 0, 0), first1 = first0;
   if (row < p.q_heads + 2 * p.kv_heads) load(row, first0, first1);
+  // Norm weights, by thread of a head: float4 i of thread j at [i][j], where all heads' threads j read it with one wavefront.
+  __shared__ float4 s_w[NORM ? 2 : 1][4][NORM ? 32 : 1];
+  if constexpr (NORM) {
+    for (int i = threadIdx.x; i < 8 * lanes; i += blockDim.x) {
+      const int at = i % lanes, part = i / lanes % 4;
+      const float* const w = i < 4 * lanes ? p.q_norm : p.k_norm;
+      const bool apart = 16 * at < p.rot && !p.interleaved;
+      const int c = apart ? 8 * at + part % 2 * 4 + (part < 2 ? 0 : p.rot >> 1) : 16 * at + 4 * part;
+      if (w != nullptr && 16 * at < p.dim) s_w[i / (4 * lanes)][part][at] = __ldg(reinterpret_cast<const float4*>(w + c));
+    }
+  }
   bool ok = true;
   float cs[8], sn[8];
   if (p.rot > 0) {
@@ -134,8 +145,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 14 : 20) : TH
     uint4 r0 = v0, r1 = v1;
     float a[8], b[8];
     const bool turned = turn && !is_v;
-    const float* const weight = !NORM || is_v ? nullptr : is_q ? p.q_norm : p.k_norm;
-    const bool normed = NORM && weight != nullptr;
+    const bool normed = NORM && !is_v && (is_q ? p.q_norm : p.k_norm) != nullptr;
     if (turned || normed || (F8 && !is_q)) {
       widen8<BF16>(v0, a);
       widen8<BF16>(v1, b);
@@ -148,10 +158,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 14 : 20) : TH
       for (int o = 16; o > 0; o >>= 1)
         if (o < lanes) sum += __shfl_xor_sync(head_lanes, sum, o);
       const float inv = __frsqrt_rn(sum * per_channel + p.eps);
-      // (the weights come from L1 for each head: held in registers they would cost a third of the blocks)
+      const float4(&weight)[4][NORM ? 32 : 1] = s_w[NORM && !is_q];
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(weight + (idle ? 0 : c0 + i))), x = __ldg(reinterpret_cast<const float4*>(weight + (idle ? 0 : c1 + i)));
+        const float4 w = weight[i / 4][NORM ? j : 0], x = weight[2 + i / 4][NORM ? j : 0];
         a[i] *= inv * w.x, a[i + 1] *= inv * w.y, a[i + 2] *= inv * w.z, a[i + 3] *= inv * w.w;
         b[i] *= inv * x.x, b[i + 1] *= inv * x.y, b[i + 2] *= inv * x.z, b[i + 3] *= inv * x.w;
       }
@@ -200,6 +210,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 64 ? (NORM ? 14 : 20) : TH
       }
     }
   };
+  if constexpr (NORM) __syncthreads();
   if constexpr (NORM) {                 // the next head's data are on their way while this one's squares are summed
 #pragma unroll 1
     for (int h = row; h < heads; h += rows) {
