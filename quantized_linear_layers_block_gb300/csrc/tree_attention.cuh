@@ -5,15 +5,17 @@
 // over a request's cached tokens and the nodes of t's mask. All nodes of a request read the same keys, and G = q_heads /
 // kv_heads query heads share a key-value head: n G rows use each cached byte, 2 n G flops a 16-bit element. At 8 nodes and
 // 6 heads that is 48 rows, which mma.sync could just feed; at 26 nodes it could not, so the products run on tcgen05, with 128 rows
-// (node, head) to a tile: S = Q K^T and O += P V with S, P and O in tensor memory. Up to 128 rows HBM bounds, above it the MMAs.
+// (node, head) to a tile: S = Q K^T and O += P V with S, P and O in tensor memory.
 //
-// Work. A (request, key-value head, 128 rows) is a segment; its keys are cut into tiles of 64 and the tiles of all segments form
-// one list, cut into equal shares for the blocks of one resident wave, so that ragged lengths need no plan from the host.
-// A segment inside one block's share is finished there; one that is cut leaves partial (m, l, o) in the workspace, and a second small
-// kernel joins them, in block order.
+// Work. A (request, key-value head, 128 rows) is a segment; its keys are cut into tiles of 64. Where the segments are few and short,
+// each goes to a cluster of blocks that join their parts through shared memory (kCluster). Else the tiles of all segments form
+// one list, cut into equal shares for the blocks of one resident wave, so that ragged lengths need no plan from the
+// host (kList): a segment inside one block's share is finished there; one that is cut leaves partial (m, l, o) in the workspace, and
+// a second small kernel joins them, in block order.
 //
-// Warps. Four (a thread to a row) turn S into P and write results; one issues the MMAs; four load keys and values. Tiles go through a ring
-// of slots in the order in which the MMAs take them: K0, K1, V0, K2, V1, ...
+// Warps. Four (a thread to a row) turn S into P and write results; one issues the MMAs; three or four load keys and values. Tiles go through a
+// ring of slots in the order in which the MMAs take them: K0, K1, V0, K2, V1, ... All of a block's MMAs come from one thread and
+// so run in order, which is what lets S of tile i + 2 overwrite P of tile i without a wait.
 //
 // Softmax. One pass with a running maximum m, sum l and output o; o is rescaled only where m grows by more than 2^8 (bf16) or
 // 2^3 (f16): p just has to stay in range. Probabilities enter the second product as two 16-bit parts (16 bits for bf16, 22
@@ -22,6 +24,13 @@
 // Masks. A key that only some rows see meets the others with p = 0, and 0 V is NaN where V is not finite. So in tiles that not
 // every row sees whole (the nodes, the edge of a window) such values are taken out when they are loaded, and added
 // at the end to the rows that see them. In the others a weight that underflowed makes an infinity NaN: a NaN channel at the end is looked into.
+//
+// Measured (GB300; 24 heads on 4 of 256 channels and bf16 where nothing else is said): one request of 577 tokens, 8 nodes 11.6 us, a
+// chain of latencies (length, page, tile, two products and a softmax, cluster, output); 24 requests of 40 to 9000 tokens and 4 to 26 nodes 54
+// (bytes: 28), tensor pipe 38 % busy: a tile is 2250 cycles of product, softmax, product and the waits between them, and a piece of a
+// segment costs 6 us besides (queries, list, output); 64 nodes on 80001 tokens 147 (flops: 66, 100 with both parts of P), tensor pipe 65 %;
+// 160 requests of 512 to 16384 tokens in 8 bits under a window of 8192, 40 heads on 8 of 128 channels 455 (bytes: 193), tensor pipe 48 %:
+// of a block's 3200 cycles a tile the softmax takes 2700, on two warps (60 rows at most) beside three that widen.
 #pragma once
 
 #include "paged_attention.cuh"
@@ -87,11 +96,12 @@ using attn::widen_hi;
 using attn::widen_lo;
 
 constexpr int kKeys = 64;                // keys of a tile
-constexpr int kSegmentCost = 5;          // what a segment costs besides its tiles, in tiles
 constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kLoadWarp = 5;
 constexpr int kMaxClusterLog = 4;
-constexpr int kLeastShare = 4;           // places of the list to a block: fewer make more parts than their joins are worth
-constexpr long long kReread = 64 << 20;  // bytes of K and V that several row blocks read, from which on they do so together
+// Bytes of K and V that several row blocks read, from which on they do so together, if that leaves no more than an eighth of the places empty.
+// One request, 64 nodes, together and not: 20000 tokens 52.2 and 55.5 us, 40000 80.8 and 96.4, 80001 137 and 166; below, eight of 1000 tokens
+// 45 and 39, 24 of 40 to 9000 62 and 59. Eight of 4000, where padding would add half: 96 and 77.
+constexpr long long kReread = 64 << 20;
 
 enum Mode {
   kList,      // the list of tiles, in equal shares, and a second kernel for the segments that are cut
@@ -111,6 +121,7 @@ struct Traits {
   static constexpr bool QT = D != 128;
   static constexpr int Q = QT ? kSoftmaxWarps * 4096 : kTreeRows * D * 2;        // the results pass through it, 4 KB a warp
   static constexpr int SLOT = kKeys * D * 2, STAGE = F8 ? SLOT / 2 : 0;
+  // (slots, us: 64 channels 8 or 12: 123 or 132 of 64 requests, 128 channels 4 or 5: 99 or 101 of 40, 256 channels 6 or 4: 73 or 76 of 24)
   static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 8) : D == 128 ? (F8 ? 3 : 4) : F8 ? 4 : 6;
   static constexpr int STAGES = F8 ? (D == 64 ? 12 : D == 128 ? 3 : 4) : 0;     // of 8-bit rows on their way, shared out to the loading warps
   static constexpr int PART = kTreeRows * (D + 2) * 4;           // of a cluster's block, in the ring's place
@@ -119,6 +130,9 @@ struct Traits {
   static constexpr int SMEM = OFF_MISC + 1024;
   static constexpr int SBUF = 2;                                 // buffers of S and P
   static constexpr int TMEM = D == 256 ? 512 : 256, TMEM_S = D, TMEM_Q = TMEM_S + SBUF * kKeys;      // columns; O in the first D
+  // What a segment costs besides its tiles (queries, results, the list: some 6 us), in tiles. Against 5 and 8 in turn: 24 requests, 256
+  // channels 58.7 and 54.8 us; 60 requests, 8 bits, 235 and 218; 40 requests, 128 channels 91 and 87, in 8 bits 448 and 454; 64 channels 160 and 165.
+  static constexpr int COST = D == 64 || (D == 128 && F8) ? 5 : 8;
   static constexpr float POFF = BF16 ? 0.f : 12.f;               // p is kept 2^POFF as large (f16: away from the subnormals)
   static constexpr float SLACK = BF16 ? 8.f : 3.f;               // by how much m may lag behind the maximum
   static_assert(SMEM <= (BLOCKS == 1 ? 232448 : 115712) && TMEM_Q + (QT ? D / 2 : 0) <= TMEM, "room");
@@ -244,7 +258,7 @@ __device__ __forceinline__ void read_tmem(uint32_t addr, uint32_t (&v)[32]) {
 // ---- the list of work: every warp goes through its block's share by itself
 struct Request {
   int n, row0, len, first, begin, sinks, sink_tiles, tiles, row_blocks;
-  __device__ __forceinline__ int places(const TreeAttnParams& p) const { return row_blocks == 0 ? 0 : tiles + kSegmentCost; }
+  __device__ __forceinline__ int places(int cost) const { return row_blocks == 0 ? 0 : tiles + cost; }
 };
 
 __device__ __forceinline__ Request request(const TreeAttnParams& p, int b, bool& bad) {
@@ -270,7 +284,7 @@ struct Piece {              // tiles begin .. end - 1 of a segment
   int second, parts;        // which of the block's partials; blocks that share the segment
 };
 
-template <Mode MODE>
+template <Mode MODE, int COST>
 struct Walk {
   Request r;
   int b, seg, segs;         // request, segment of it, its segments
@@ -305,12 +319,12 @@ struct Walk {
       n = row_blocks = 0;
       if (base + lane >= p.B) return;
       const Request x = request(p, base + lane, bad);
-      n = x.places(p), row_blocks = x.row_blocks;
+      n = x.places(COST), row_blocks = x.row_blocks;
     };
     look(0);
     share = 0;
     bool together = false;
-    long long total, again = 0;
+    long long total, again = 0, apart = 0, bare = 0;  // apart, bare: share and total without padding
     for (;;) {              // the least share with which the places fit the blocks, within 3 %
       total = 0;
       for (int base = 0; base < p.B; base += 32) {
@@ -320,10 +334,10 @@ struct Walk {
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      const long long least = max(attn::divide(total + p.grid - 1, p.grid), static_cast<long long>(kLeastShare));
+      const long long least = attn::divide(total + p.grid - 1, p.grid);
       if (least <= share) break;
       if (share == 0) {
-        share = least;
+        share = apart = least, bare = total;
         if (!__any_sync(0xffffffffu, row_blocks > 1 || again > 0)) break;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) again += __shfl_xor_sync(0xffffffffu, again, o);
@@ -331,6 +345,10 @@ struct Walk {
         if (!together) break;
       } else {
         share = max(least, share + share / 32);
+        if (share > apart + apart / 8) {                // too much would stay empty
+          together = false, share = apart, total = bare;
+          break;
+        }
       }
     }
     if (report && bad) set_status(p.status, TL_EDATA);
@@ -366,7 +384,7 @@ struct Walk {
   bool join;                // (of `padded`)
 
   __device__ __forceinline__ void enter(const TreeAttnParams& p) {
-    places = padded(r.places(p), r.row_blocks, join);
+    places = padded(r.places(COST), r.row_blocks, join);
     segs = p.kv_heads * r.row_blocks;
     seg = 0;
   }
@@ -397,7 +415,7 @@ struct Walk {
         continue;
       }
       // (what is left of a whole number of shares stays empty)
-      const long long from = max(t0 - at, 0ll) - kSegmentCost, to = min(t1 - at, static_cast<long long>(r.places(p))) - kSegmentCost;
+      const long long from = max(t0 - at, 0ll) - COST, to = min(t1 - at, static_cast<long long>(r.places(COST))) - COST;
       x.begin = static_cast<int>(max(from, 0ll));
       x.end = static_cast<int>(max(to, 0ll));
       x.kvh = seg / r.row_blocks;
@@ -407,7 +425,7 @@ struct Walk {
       x.second = x.starts_here;
       x.parts = 1;
       if (!x.whole && x.starts_here)
-        x.parts = static_cast<int>(attn::divide(at + kSegmentCost + r.tiles - 1, share)) - static_cast<int>(blockIdx.x) + 1;
+        x.parts = static_cast<int>(attn::divide(at + COST + r.tiles - 1, share)) - static_cast<int>(blockIdx.x) + 1;
       ++seg;
       at += places;
       if (x.end > x.begin) return true;
@@ -607,7 +625,7 @@ struct Loader {
   }
 
   __device__ __forceinline__ void run() {
-    Walk<MODE> w;
+    Walk<MODE, T::COST> w;
     w.init(p, 2 * kKeys * T::ROW, false);
     Piece x;
     uint32_t before = 0;                                // loads of the pieces before
@@ -707,7 +725,7 @@ struct Mma {
   // idle for a third of the time: so the three barriers of a step are asked together.
   __device__ __forceinline__ void run() {
     init();
-    Walk<MODE> w;
+    Walk<MODE, T::COST> w;
     w.init(p, 2 * kKeys * T::ROW, false);
     Piece x;
     uint32_t before = 0, tiles = 0, pieces = 0;
@@ -907,7 +925,7 @@ struct Softmax {
 
   // Infinite and NaN values that the row sees, in 32 of its channels from d on: those that were taken out of tiles that not all rows see
   // whole; and, as a weight that underflowed to 0 makes an infinity NaN, all of them where a channel is NaN.
-  __device__ __noinline__ void add_odd(float* o, int d, const Walk<MODE>& w, const Piece& x, uint64_t mask, bool all) const {
+  __device__ __noinline__ void add_odd(float* o, int d, const Walk<MODE, T::COST>& w, const Piece& x, uint64_t mask, bool all) const {
     for (int c = 0; c < 32; ++c)
       if (o[c] != o[c]) o[c] = 0.f;
     for (int i = x.begin; i < x.end; ++i) {
@@ -935,7 +953,7 @@ struct Softmax {
   }
 
   __device__ __forceinline__ void run() {
-    Walk<MODE> w;
+    Walk<MODE, T::COST> w;
     w.init(p, 2 * kKeys * T::ROW, MODE == kCluster ? warp == 0 : blockIdx.x == 0 && warp == 0);
     Piece x;
     uint32_t tiles = 0, pieces = 0;
@@ -1083,7 +1101,7 @@ struct Softmax {
 
 // The blocks of a cluster join their parts, each some (row, four channels); all threads of all of them.
 template <int CACHE, int D>
-__device__ __forceinline__ void join_cluster(const TreeAttnParams& p, uint8_t* smem, const Walk<kCluster>& w) {
+__device__ __forceinline__ void join_cluster(const TreeAttnParams& p, uint8_t* smem, const Walk<kCluster, Traits<CACHE, D>::COST>& w) {
   using T = Traits<CACHE, D>;
   const int size = 1 << p.cluster_log, rank = blockIdx.x & (size - 1);
   const int kvh = w.seg / p.row_blocks, first_row = (w.seg - kvh * p.row_blocks) * kTreeRows;
@@ -1182,7 +1200,7 @@ __global__ void __launch_bounds__(Traits<CACHE, D>::THREADS, Traits<CACHE, D>::B
   }
   pdl_launch_dependents();
   if (MODE == kCluster && p.cluster_log > 0) {
-    Walk<kCluster> w;
+    Walk<kCluster, T::COST> w;
     w.init(p, 0, false);
     if (w.more) {                                       // the same for all blocks of the cluster
       if (warp < kSoftmaxWarps && (w.r.tiles >> p.cluster_log) == 0) {
@@ -1319,7 +1337,8 @@ cudaError_t launch(TreeAttnParams& p, int sms, cudaStream_t st) {
   p.row_blocks = static_cast<int>((nodes * p.group + kTreeRows - 1) / kTreeRows);
   const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.row_blocks;
   // Few segments of few tiles: a cluster each, of the most blocks that all run at once, while a block has more than one tile and
-  // ten at most.
+  // ten at most. (One request of 577 tokens, 10 tiles: 8 blocks 11.9 us, 16 14.5, the list 22. Above ten tiles to a block the list's
+  // equal shares win.)
   for (int log = kMaxClusterLog; log >= 0; --log) {
     const int c = 1 << log;
     if (segments > __atomic_load_n(&at_once[dev][log], __ATOMIC_RELAXED) || (log > 0 && tiles <= c)) continue;
@@ -1329,7 +1348,7 @@ cudaError_t launch(TreeAttnParams& p, int sms, cudaStream_t st) {
   }
   long long grid = static_cast<long long>(sms) * T::BLOCKS;
   if (grid > kTreeMaxGrid) grid = kTreeMaxGrid;
-  const long long most = segments * (tiles + kSegmentCost);      // places that the list can have
+  const long long most = segments * (tiles + T::COST);    // places that the list can have
   if (grid > most) grid = most;
   p.grid = static_cast<int>(grid);
   e = launch_pdl(tree_attention_kernel<CACHE, D, kList>, dim3(static_cast<unsigned>(grid)), dim3(T::THREADS), T::SMEM, st, p);
