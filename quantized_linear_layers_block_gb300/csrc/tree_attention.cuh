@@ -1337,12 +1337,14 @@ cudaError_t launch(TreeAttnParams& p, int sms, cudaStream_t st) {
   p.row_blocks = static_cast<int>((nodes * p.group + kTreeRows - 1) / kTreeRows);
   const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.row_blocks;
   // Few segments of few tiles: a cluster each, of the most blocks that all run at once, while a block has more than one tile and
-  // ten at most. (One request of 577 tokens, 10 tiles: 8 blocks 11.9 us, 16 14.5, the list 22. Above ten tiles to a block the list's
-  // equal shares win.)
+  // no more than some, where the list's equal shares and its more blocks win; of the up to seven segments that have sixteen blocks the
+  // list makes so many parts that this is later. One request of 577 tokens, 8 nodes: clusters 11.7 us (16 blocks for its 10 tiles: 14.5), the
+  // list 15.1; 4000: 15.6 and 23.1, 64 channels 11.0 and 29.2; 16000: 28.2 and 32.1, 20.1 and 31.4; seven heads of 128 channels, 29000:
+  // 34 and 40, four in 8 bits 38 and 32. Eight requests of 1000: two blocks each 22.4, the list 20.4.
   for (int log = kMaxClusterLog; log >= 0; --log) {
     const int c = 1 << log;
     if (segments > __atomic_load_n(&at_once[dev][log], __ATOMIC_RELAXED) || (log > 0 && tiles <= c)) continue;
-    if (tiles > 10 * c) break;
+    if (tiles > (log < kMaxClusterLog ? 10 : T::F8 ? 20 : 30) * c) break;
     p.cluster_log = log;
     return launch_pdl_cluster(clusters, dim3(static_cast<unsigned>(segments * c)), dim3(T::THREADS), T::SMEM, st, c, p);
   }

@@ -195,3 +195,13 @@ def test_most_rows(hq, hkv, d, cache):
     kv = filled(60, 16, hkv, d, cache, gen)
     qtype = torch.float16 if cache == "f16" else torch.bfloat16
     same(*chains(kv, [130, 0, 77], 64, hq, gen, qtype))
+
+
+@pytest.mark.parametrize("cache,d,tiles", [("bf16", 256, 479), ("bf16", 256, 481), ("f16", 64, 470), ("f8", 128, 319), ("f8", 128, 322)])
+def test_around_the_longest_clusters(cache, d, tiles):
+    """One request on seven heads: sixteen blocks with up to 30 (8 bits: 20) tiles each, and the list beyond."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(tiles)
+    kv = filled(4 * (tiles + 1), 16, 7, d, cache, gen)
+    qtype = torch.float16 if cache == "f16" else torch.bfloat16
+    same(*chains(kv, [64 * tiles - 5], 5, 14, gen, qtype))
