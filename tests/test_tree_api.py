@@ -71,7 +71,7 @@ def test_verify(lib):
         assert call(f, d, **bad) == EINVAL, bad
     for bad in (dict(vocab=(1 << 24) + 1, ldt=1 << 25, ldd=1 << 25), dict(ldt=99), dict(ldd=99)):
         assert call(f, d, **bad) == EUNSUPPORTED, bad
-    assert call(f, d, B=0) == OK
+    assert call(f, d, B=0, T=0) == OK
 
 
 def test_compact(lib):
