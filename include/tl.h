@@ -440,7 +440,8 @@ int tl_paged_attention(const tl_kv_cache* cache, const void* q, int dtype, int B
  *   q_norm, k_norm   fp32 [head_dim], the weights w; NULL: q (k) is not normalised
  *   eps              positive and finite
  * Everything else, rounding included, is tl_kv_append's: sums, norms and rotation are fp32, rounded once
- * to the type that is stored. A head with an infinite or NaN element becomes NaN where the formula does.
+ * to the type that is stored. A head with an infinite or NaN element becomes NaN where the formula does; one whose
+ * squares' sum passes fp32's range (elements of 10^18 and more) becomes 0.
  */
 int tl_kv_append_norm(const tl_kv_cache* cache, const void* q, const void* k, const void* v,
                       int dtype, int T, int q_heads, int64_t ldq, int64_t ldk, int64_t ldv,

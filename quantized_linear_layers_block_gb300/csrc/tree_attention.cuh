@@ -358,6 +358,10 @@ struct Walk {
     if (!more) return;
     long long run = 0;
     for (int base = 0;; base += 32) {
+      if (base >= p.B) {                                // (lengths that change meanwhile: nothing is looked up past the last request)
+        more = false;
+        return;
+      }
       if (p.B > 32) look(base);
       const long long mine = static_cast<long long>(p.kv_heads) * row_blocks * padded(n, row_blocks, together);
       long long incl = mine;
@@ -410,6 +414,10 @@ struct Walk {
       }
       if (seg == segs) {
         bool bad = false;
+        if (b + 1 >= p.B) {
+          more = false;
+          break;
+        }
         r = request(p, ++b, bad);
         enter(p);
         continue;
