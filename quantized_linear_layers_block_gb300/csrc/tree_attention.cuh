@@ -25,12 +25,12 @@
 // every row sees whole (the nodes, the edge of a window) such values are taken out when they are loaded, and added
 // at the end to the rows that see them. In the others a weight that underflowed makes an infinity NaN: a NaN channel at the end is looked into.
 //
-// Measured (GB300; 24 heads on 4 of 256 channels and bf16 where nothing else is said): one request of 577 tokens, 8 nodes 11.6 us, a
+// Measured (GB300; 24 heads on 4 of 256 channels and bf16 where nothing else is said): one request of 577 tokens, 8 nodes 11.5 us, a
 // chain of latencies (length, page, tile, two products and a softmax, cluster, output); 24 requests of 40 to 9000 tokens and 4 to 26 nodes 54
 // (bytes: 28), tensor pipe 38 % busy: a tile is 2250 cycles of product, softmax, product and the waits between them, and a piece of a
-// segment costs 6 us besides (queries, list, output); 64 nodes on 80001 tokens 143 (flops: 66, 100 with both parts of P), tensor pipe 65 %;
-// 160 requests of 512 to 16384 tokens in 8 bits under a window of 8192, 40 heads on 8 of 128 channels 458 (bytes: 193), tensor pipe 48 %:
-// of a block's 3200 cycles a tile the softmax takes 2700, on two warps (60 rows at most) beside three that widen.
+// segment costs 6 us besides (queries, list, output); 64 nodes on 80001 tokens 146 (flops: 66, 100 with both parts of P), tensor pipe 65 %;
+// 160 requests of 512 to 16384 tokens in 8 bits under a window of 8192, 40 heads on 8 of 128 channels 438 (bytes: 193), tensor pipe 48 %:
+// of a block's 3100 cycles a tile the softmax takes 2700, on two warps (60 rows at most) beside three that widen.
 #pragma once
 
 #include "paged_attention.cuh"
