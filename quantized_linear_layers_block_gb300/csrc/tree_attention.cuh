@@ -122,8 +122,8 @@ struct Traits {
   static constexpr int Q = QT ? kSoftmaxWarps * 4096 : kTreeRows * D * 2;        // the results pass through it, 4 KB a warp
   static constexpr int SLOT = kKeys * D * 2, STAGE = F8 ? SLOT / 2 : 0;
   // (slots, us: 64 channels 8 or 12: 123 or 132 of 64 requests, 128 channels 4 or 5: 99 or 101 of 40, 256 channels 6 or 4: 73 or 76 of 24)
-  static constexpr int SLOTS = D == 64 ? (F8 ? 6 : 8) : D == 128 ? (F8 ? 3 : 4) : F8 ? 4 : 6;
-  static constexpr int STAGES = F8 ? (D == 64 ? 12 : D == 128 ? 3 : 4) : 0;     // of 8-bit rows on their way, shared out to the loading warps
+  static constexpr int SLOTS = D == 64 ? 8 : D == 128 ? (F8 ? 3 : 4) : F8 ? 4 : 6;
+  static constexpr int STAGES = F8 ? LOADERS : 0;                // of 8-bit rows on their way, a loading warp's each
   static constexpr int PART = kTreeRows * (D + 2) * 4;           // of a cluster's block, in the ring's place
   static constexpr int OFF_SLOT = Q, OFF_STAGE = OFF_SLOT + SLOTS * SLOT, END = OFF_STAGE + STAGES * STAGE;
   static constexpr int OFF_MISC = END > OFF_SLOT + PART ? END : OFF_SLOT + PART;
@@ -137,7 +137,7 @@ struct Traits {
   static constexpr float SLACK = BF16 ? 8.f : 3.f;               // by how much m may lag behind the maximum
   static_assert(SMEM <= (BLOCKS == 1 ? 232448 : 115712) && TMEM_Q + (QT ? D / 2 : 0) <= TMEM, "room");
   // a piece takes two slots at least, and a loading warp has one load of any LOADERS
-  static_assert(SLOTS / 2 + 3 < kAhead && LOADERS <= 4 && (!F8 || STAGES >= LOADERS), "ahead");
+  static_assert(SLOTS / 2 + 3 < kAhead && LOADERS <= 4, "ahead");
 };
 
 // The small things behind the slots.
