@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tree_kernel(const __grid_c
       a = __ldg(p.target + static_cast<int64_t>(begin + x.parent) * p.ldt + x.token);
       b = p.draft == nullptr ? 1.f : __ldg(p.draft + static_cast<int64_t>(begin + x.parent) * p.ldd + x.token);
     }
+    a = __saturatef(a), b = __saturatef(b);          // below 0 and NaN count as 0, above 1 as 1: here as in the sums
     x.p = fixed(a), x.q = fixed(b), x.first = product_below(u, b, a);
     x.need = tid == 0 ? fixed(u) : times(fixed(u), x.q);
     s.node[tid] = x;
