@@ -64,8 +64,10 @@ struct Node {
 // A row of target sums to no more than this: what a refusal leaves, too.
 constexpr u64 kMost = kOne + (kOne >> 8);
 
-// a b < c, exactly: the product's rounding error decides where the rounded product is c
+// a b < c for numbers in [0, 1], exactly: the product's rounding error decides where the rounded product is c. All by powers of two as
+// large, by which no product that comes near c > 0, nor its error, is subnormal.
 __device__ __forceinline__ bool product_below(float a, float b, float c) {
+  a *= 0x1p60f, b *= 0x1p60f, c *= 0x1p120f;
   const float h = __fmul_rn(a, b);
   return h < c || (h == c && __fmaf_rn(a, b, -h) < 0.f);
 }
