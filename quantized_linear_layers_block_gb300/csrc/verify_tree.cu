@@ -76,7 +76,7 @@ struct Shared {
   Node node[TL_TREE_NODES];
   u64 sum[TL_TREE_NODES + 1];            // S of each refusal at the node where the walk stands
   float2 pair[TL_TREE_NODES + 1];        // the same as two floats
-  int token[TL_TREE_NODES];              // the tokens refused there
+  int token[TL_TREE_NODES];              // the tokens refused there; -1: one outside the vocabulary
   u64 warp_sum[kWarps], step_sum[kWarps];
   int step_last[kWarps];
   u64 block_sum[2][kMaxCluster];         // of every block of the cluster, for two passes in turn
@@ -235,11 +235,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tree_kernel(const __grid_c
     x.token = tid > 0 ? __ldg(p.tokens + begin + tid) : 0;
     const float u = unit(__ldg(p.uniform + begin + tid));
     float a = 0.f, b = 0.f;
-    if (x.parent < -1 || x.parent >= tid || static_cast<unsigned>(x.token) >= static_cast<unsigned>(p.vocab)) {
-      if (rank == 0) set_status(p.status, TL_EDATA);
-      x.parent = -1;                                 // never reached
-    }
-    if (x.parent >= 0) {
+    const bool bad = x.parent < -1 || x.parent >= tid, there = static_cast<unsigned>(x.token) < static_cast<unsigned>(p.vocab);
+    if ((bad || !there) && rank == 0) set_status(p.status, TL_EDATA);
+    if (bad) x.parent = -1;                          // never reached
+    if (!there) x.token = -1;                        // refused: neither distribution gives it any probability
+    if (x.parent >= 0 && there) {
       a = __ldg(p.target + static_cast<int64_t>(begin + x.parent) * p.ldt + x.token);
       b = p.draft == nullptr ? 1.f : __ldg(p.draft + static_cast<int64_t>(begin + x.parent) * p.ldd + x.token);
     }
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tree_kernel(const __grid_c
         const int x = s.token[known];
         bool again = false;
         for (int j = 0; j < known; ++j) again |= s.token[j] == x;
-        next = s.sum[known] - (again ? 0 : fixed(__ldg(p.target + static_cast<int64_t>(begin + at) * p.ldt + x)));
+        next = s.sum[known] - (again || x < 0 ? 0 : fixed(__ldg(p.target + static_cast<int64_t>(begin + at) * p.ldt + x)));
       } else {
         const int all = refused;
         refused = known + 1;
