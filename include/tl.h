@@ -491,6 +491,7 @@ int tl_tree_plan(const int32_t* parents, const int32_t* starts, int B, int T, co
  *   window     0: all cached tokens. Else at least TL_TREE_NODES: how many keys a node sees besides the sinks,
  *              its mask's nodes and the last cached tokens, max(0, window - bits of its mask) of them
  *   sinks      with a window, the first cached tokens that stay visible; 0 without one
+ *   pages      where no node sees a token of a page, and no node's place is in it, its entry may be anything
  *   lse        optional fp32 [T, q_heads]: log sum_j p_j
  *   workspace  ws_bytes >= tl_tree_attention_workspace_size; its contents do not matter. Calls that can overlap on the
  *              GPU must not share one.

@@ -33,6 +33,8 @@
 // of a block's 3100 cycles a tile the softmax takes 2700, on two warps (60 rows at most) beside three that widen.
 #pragma once
 
+#include <climits>
+
 #include "paged_attention.cuh"
 #include "tree.cuh"
 
@@ -148,6 +150,7 @@ struct Misc {
   uint64_t q_full;                                     // a piece's queries are in place
   uint64_t loaded[kAhead];                             // a piece's last rows are, and flag says what was found in them
   int flag[kAhead];                                    // piece + 1 where values were taken out
+  int bad[kAhead];                                     // 0, or of the keys whose page does not exist the last one, plus 1
   uint32_t tmem;
   int abort;
 };
@@ -506,8 +509,8 @@ struct Loader {
   }
   __device__ __forceinline__ int64_t row_of(int key, int page, const Tile& t, int64_t head) const {
     if (key >= t.end) return -1;
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-      set_status(p.status, TL_EDATA);
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {      // (what a window leaves of it is looked into at the piece's end)
+      atomicMax(&misc->bad[pieces % kAhead], key < p.sinks ? INT_MAX : key + (p.runs16 ? 16 : 1));
       return -1;
     }
     return page * p.page_stride + head + static_cast<int64_t>(key - p.page.div(key) * p.page.d) * p.token_stride;
@@ -960,6 +963,14 @@ struct Softmax {
     }
   }
 
+  // Pages up to the key `end` do not exist: an error where a node sees that far back. A window's tiles begin where a row without nodes would; all
+  // nodes may see less, and their pages before that may be gone.
+  __device__ __noinline__ void missing(const Request r, int end) const {
+    int fewest = TL_TREE_NODES;
+    for (int i = 0; i < r.n; ++i) fewest = min(fewest, __popcll(static_cast<uint64_t>(__ldg(p.masks + r.row0 + i)) & low_bits(r.n)));
+    if (p.window == 0 || end > r.len - max(0, p.window - fewest)) set_status(p.status, TL_EDATA);
+  }
+
   __device__ __forceinline__ void run() {
     Walk<MODE, T::COST> w;
     w.init(p, 2 * kKeys * T::ROW, MODE == kCluster ? warp == 0 : blockIdx.x == 0 && warp == 0);
@@ -1037,6 +1048,10 @@ struct Softmax {
       if (!ok) break;
       if (!wait(misc->pv_done[(tiles - 1) % T::SBUF], (tiles - 1) / T::SBUF) || !wait(misc->loaded[pieces % kAhead], pieces / kAhead)) break;
       const bool odd = *const_cast<volatile int*>(&misc->flag[pieces % kAhead]) == static_cast<int>(pieces) + 1;
+      if (warp == 0 && lane == 0) {
+        volatile int* const bad = &misc->bad[pieces % kAhead];
+        if (*bad != 0) missing(w.r, *bad), *bad = 0;
+      }
       ++pieces;
       if (busy) {
         tc_fence_after();
@@ -1184,7 +1199,7 @@ __global__ void __launch_bounds__(Traits<CACHE, D>::THREADS, Traits<CACHE, D>::B
       mbar_init(smem_u32(&misc->pv_done[i]), 1);
     }
     mbar_init(smem_u32(&misc->q_full), kSoftmaxWarps);
-    for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&misc->loaded[i]), T::LOADERS), misc->flag[i] = 0;
+    for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&misc->loaded[i]), T::LOADERS), misc->flag[i] = misc->bad[i] = 0;
     misc->abort = 0;
     fence_barrier_init();
   }
