@@ -454,7 +454,7 @@ int tl_kv_append_norm(const tl_kv_cache* cache, const void* q, const void* k, co
  * of a model. A request's tokens of this pass are the nodes of a tree: node 0 is the last token that is
  * certain (its key is not cached yet), each other node a guess at what follows its parent. The nodes of all requests
  * lie behind each other, in rows starts[b] .. starts[b + 1] - 1 of T rows; a request has at most
- * TL_TREE_NODES of them, or none. Rows from starts[B] on are padding. Node i of a request is cached
+ * TL_TREE_NODES of them, or none. Rows before starts[0] and from starts[B] on are padding. Node i of a request is cached
  * at its place lens[b] + i, whatever its depth, lens[b] being the tokens cached before this pass.
  *
  *   starts   int32 [B + 1], 0 <= starts[0] <= starts[1] <= ... <= starts[B] <= T

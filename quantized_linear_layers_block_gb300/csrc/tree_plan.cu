@@ -21,13 +21,15 @@ __global__ void __launch_bounds__(kWarps * 32) tree_plan_kernel(const __grid_con
   pdl_wait_prior();
   pdl_launch_dependents();
   if (b > p.B) return;
-  if (b == p.B) {            // one warp more, for the rows behind the last request
-    const int begin = __ldg(p.starts + p.B);
+  if (b == p.B) {            // one warp more, for the rows before the first request and behind the last
+    const int first = __ldg(p.starts), begin = __ldg(p.starts + p.B);
     if (begin < 0 || begin > p.T) {
       if (lane == 0) set_status(p.status, TL_EDATA);
       return;
     }
-    for (int64_t t = static_cast<int64_t>(begin) + lane; t < p.T; t += 32) p.masks[t] = 0, p.positions[t] = 0, p.slots[t] = -1;
+    auto pad = [&](int64_t t) { p.masks[t] = 0, p.positions[t] = 0, p.slots[t] = -1; };
+    for (int64_t t = lane; t < min(first, begin); t += 32) pad(t);
+    for (int64_t t = static_cast<int64_t>(begin) + lane; t < p.T; t += 32) pad(t);
     return;
   }
   const int len = __ldg(p.lens + b);

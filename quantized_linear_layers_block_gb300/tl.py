@@ -507,7 +507,7 @@ def tl_tree_plan(cache: PagedKVCache, parents: torch.Tensor, starts: torch.Tenso
                  masks: torch.Tensor | None = None, positions: torch.Tensor | None = None, slots: torch.Tensor | None = None, stream=None):
     """Drafted trees: parents int32 [T] (within the request; -1: root) of the nodes of request b in rows starts[b] .. starts[b + 1] - 1
     (int32 [requests + 1]), lens int32 tokens cached before them, pages int32 [requests, max_pages] -> (masks int64 [T] of each
-    node and its ancestors, positions int32 [T], slots int64 [T] for append). Rows behind the last request are padding: (0, 0, -1)."""
+    node and its ancestors, positions int32 [T], slots int64 [T] for append). Rows of no request are padding: (0, 0, -1)."""
     if masks is None:
         masks = _allocate(torch.empty, parents.shape, torch.int64, parents.device, stream)
     if positions is None:
