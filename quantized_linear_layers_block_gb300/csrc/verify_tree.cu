@@ -223,6 +223,12 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tree_kernel(const __grid_c
     if (end >= 0)
       for (int64_t t = static_cast<int64_t>(end) + tid; t < p.T; t += kThreads) p.path[t] = -1;
   }
+  if (b == 0 && rank == 0 && begin > 0) {            // padding before all requests, in whatever order they are
+    int least = min(begin, p.T);
+    for (int i = lane; i <= p.B; i += 32) least = min(least, __ldg(p.starts + i));
+    least = __reduce_min_sync(0xffffffffu, least);
+    for (int t = tid; t < least; t += kThreads) p.path[t] = -1;
+  }
   if (n == 0) {                                      // the same for all blocks of the cluster
     if (rank == 0 && tid == 0) p.counts[b] = 0, p.next[b] = -1;
     return;

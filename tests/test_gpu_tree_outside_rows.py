@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from quantized_linear_layers_block_gb300 import tl
-from tests.test_gpu_tree import dev
+from tests.test_gpu_tree import dev, draws, expected
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,38 @@ def test_plan_without_requests():
         got = [torch.full((6,), 5, dtype=t, device="cuda") for t in (I64, I32, I64)]
         kv.plan_tree(dev([-1] * 6, I32), dev([start], I32), dev(np.zeros(0), I32), torch.zeros((0, 2), dtype=I32, device="cuda"), *got)
         assert tl.tl_get_status() == tl.TL_OK and [x.tolist() for x in got] == [[0] * 6, [0] * 6, [-1] * 6]
+
+
+@pytest.mark.parametrize("before,behind", [(3, 0), (1, 2), (300, 70)])
+def test_verification_of_rows_before_the_first_request(before, behind):
+    rng = np.random.default_rng(before)
+    nodes = [4, 1, 9]
+    parents, target, draft, tokens, uniform = draws(rng, nodes, 300)
+    T, total = sum(nodes), before + sum(nodes) + behind
+
+    def rows(x, fill):
+        x = np.asarray(x)
+        full = np.full((total,) + x.shape[1:], fill, dtype=x.dtype)
+        full[before:before + T] = x
+        return dev(full)
+
+    path = torch.full((total,), 5, dtype=I32, device="cuda")
+    starts = before + np.concatenate([[0], np.cumsum(nodes)])
+    _, counts, after = tl.tl_verify_tree(rows(target, np.nan), rows(draft, np.nan), rows(tokens.astype(np.int32), 7), rows(np.array(sum(parents, []), dtype=np.int32), 7),
+                                         dev(starts, I32), rows(uniform, 0), path=path)
+    want = expected(parents, target, draft, tokens, uniform, nodes, pad=behind)
+    assert tl.tl_get_status() == tl.TL_OK
+    assert [path.tolist(), counts.tolist(), after.tolist()] == [[-1] * before + want[0]] + want[1:]
+
+
+def test_verification_of_requests_out_of_order():
+    """The first request's start lies behind the second's rows: only those before all of them are padding."""
+    rng = np.random.default_rng(2)
+    parents, target, draft, tokens, uniform = draws(rng, [9], 300)
+    full = [np.concatenate([np.repeat(x[:1], 3, 0), x, np.repeat(x[:1], 4, 0)]) for x in (target, draft, tokens, np.array(parents[0], dtype=np.int32), uniform)]
+    path = torch.full((16,), 5, dtype=I32, device="cuda")
+    t, d, k, p, u = (dev(x) for x in full)
+    _, counts, after = tl.tl_verify_tree(t, d, k.int(), p.int(), dev([7, 3, 12], I32), u, path=path)
+    want = expected(parents, target, draft, tokens, uniform, [9])
+    assert tl.tl_get_status() == tl.TL_EDATA
+    assert [path[:12].tolist(), counts.tolist(), after.tolist()] == [[-1] * 3 + want[0], [0] + want[1], [-1] + want[2]]
