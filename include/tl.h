@@ -475,7 +475,7 @@ int tl_kv_append_norm(const tl_kv_cache* cache, const void* q, const void* k, co
  *   masks      out int64 [T]: bit j is set for node j = i and every ancestor j of i; 0 for padding
  *   positions  out int32 [T]: lens[b] + the node's depth; 0 for padding
  *   slots      out int64 [T]: where tl_kv_append stores the node; -1 for padding, and with TL_EDATA for a place
- *              whose page is outside [0, num_pages)
+ *              whose page is outside [0, num_pages) and for every row of a request whose starts or length are wrong
  */
 int tl_tree_plan(const int32_t* parents, const int32_t* starts, int B, int T, const int32_t* lens,
                  const int32_t* pages, int max_pages, int64_t ldp, int page_size, int num_pages,

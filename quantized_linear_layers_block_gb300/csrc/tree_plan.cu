@@ -21,21 +21,39 @@ __global__ void __launch_bounds__(kWarps * 32) tree_plan_kernel(const __grid_con
   pdl_wait_prior();
   pdl_launch_dependents();
   if (b > p.B) return;
-  if (b == p.B) {            // one warp more, for the rows before the first request and behind the last
-    const int first = __ldg(p.starts), begin = __ldg(p.starts + p.B);
-    if (begin < 0 || begin > p.T) {
+  auto pad = [&](int64_t t) { p.masks[t] = 0, p.positions[t] = 0, p.slots[t] = -1; };
+  // Rows of no request, where starts are not what they have to be: append stores nothing of them.
+  auto pad_others = [&](int64_t from, int64_t to) {
+    for (int64_t t = max(from, int64_t{0}) + lane; t < min(to, static_cast<int64_t>(p.T)); t += 32) {
+      bool taken = false;
+      for (int i = 0; i < p.B && !taken; ++i) {
+        int first, nodes;
+        taken = tree_rows(p.starts, i, p.T, first, nodes) && t >= first && t - first < nodes;
+      }
+      if (!taken) pad(t);
+    }
+  };
+  if (b == p.B) {            // one warp more, for the rows before all requests and behind the last
+    const int first = __ldg(p.starts), last = __ldg(p.starts + p.B);
+    if (first > 0) {
+      int least = min(first, p.T);
+      for (int i = lane; i <= p.B; i += 32) least = min(least, __ldg(p.starts + i));
+      least = __reduce_min_sync(0xffffffffu, least);
+      for (int t = lane; t < least; t += 32) pad(t);
+    }
+    if (last < 0 || last > p.T) {
       if (lane == 0) set_status(p.status, TL_EDATA);
+      if (last < 0) pad_others(0, p.T);
       return;
     }
-    auto pad = [&](int64_t t) { p.masks[t] = 0, p.positions[t] = 0, p.slots[t] = -1; };
-    for (int64_t t = lane; t < min(first, begin); t += 32) pad(t);
-    for (int64_t t = static_cast<int64_t>(begin) + lane; t < p.T; t += 32) pad(t);
+    for (int64_t t = static_cast<int64_t>(last) + lane; t < p.T; t += 32) pad(t);
     return;
   }
   const int len = __ldg(p.lens + b);
   int begin, n;
   if (!tree_rows(p.starts, b, p.T, begin, n)) {
     if (lane == 0) set_status(p.status, TL_EDATA);
+    pad_others(begin, __ldg(p.starts + b + 1));
     return;
   }
   const bool fits = len >= 0 && len <= p.capacity - n;

@@ -1,4 +1,4 @@
-"""Trees of drafted tokens: rows before the first request are padding, as those behind the last are."""
+"""Trees of drafted tokens: rows of no request are padding wherever they lie, and append stores nothing of them."""
 
 import numpy as np
 import pytest
@@ -72,3 +72,22 @@ def test_verification_of_requests_out_of_order():
     want = expected(parents, target, draft, tokens, uniform, [9])
     assert tl.tl_get_status() == tl.TL_EDATA
     assert [path[:12].tolist(), counts.tolist(), after.tolist()] == [[-1] * 3 + want[0], [0] + want[1], [-1] + want[2]]
+
+
+@pytest.mark.parametrize("starts,lens", [([0, 65, 70], [4, 9]), ([0, 90, 70], [4, 9]), ([-3, 65, 70], [4, 9]), ([0, 3, 99], [4, 9]), ([0, 3, 71], [4, 9]),
+                                         ([99, 3, 70], [4, 9]), ([99, 3, 40], [4, 9]), ([50, 3, 60], [4, 9]), ([0, 3, -1], [4, 9]), ([-5, -9, -1], [4, 9]),
+                                         ([0, 3, 67], [-1, 9]), ([0, 3, 67], [2 ** 31 - 1, 9]), ([0, 3, 67], [4, 97])])
+def test_a_refused_request_has_no_places(starts, lens):
+    """What append would store somewhere is left of its rows: nothing that lies there by chance."""
+    kv = tl.PagedKVCache(12, 16, 1, 16)
+    pages = [[11, 10, 9, 8, 7, 6], [0, 1, 2, 3, 4, 5]]
+    _, _, slots = planned(kv, [-1] * 70, starts, lens, pages)
+    assert tl.tl_get_status() == tl.TL_EDATA
+    of = [-1] * 70                                               # who has a row, as far as that is said
+    for b in range(2):
+        if 0 <= starts[b] <= starts[b + 1] <= 70 and starts[b + 1] - starts[b] <= 64:
+            of[starts[b]:starts[b + 1]] = [b] * (starts[b + 1] - starts[b])
+    for t, b in enumerate(of):
+        place = lens[b] + t - starts[b]
+        fits = b >= 0 and 0 <= lens[b] <= 96 - (starts[b + 1] - starts[b])
+        assert slots[t] == (pages[b][place // 16] * 16 + place % 16 if fits else -1), t
