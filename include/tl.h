@@ -464,7 +464,7 @@ int tl_kv_append_norm(const tl_kv_cache* cache, const void* q, const void* k, co
  * A request whose starts are out of order, outside [0, T] or further than TL_TREE_NODES apart, or whose
  * length is negative or does not leave room for its nodes in max_pages * page_size, records
  * TL_EDATA; nothing is read or written out of range for it, and what the call writes for it, or for a row that two
- * requests claim, is unspecified.
+ * requests claim, is unspecified. What a call reads must not change before it is done.
  */
 #define TL_TREE_NODES 64
 

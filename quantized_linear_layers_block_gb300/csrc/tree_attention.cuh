@@ -1225,21 +1225,20 @@ __global__ void __launch_bounds__(Traits<CACHE, D>::THREADS, Traits<CACHE, D>::B
   if (MODE == kCluster && p.cluster_log > 0) {
     Walk<kCluster, T::COST> w;
     w.init(p, 0, false);
-    if (w.more) {                                       // the same for all blocks of the cluster
-      if (warp < kSoftmaxWarps && (w.r.tiles >> p.cluster_log) == 0) {
-        // a block without tiles says so
-        Piece x;
-        if (!w.next(p, x)) {
-          float* const part = reinterpret_cast<float*>(smem + T::OFF_SLOT);
-          part[threadIdx.x] = -INFINITY;
-          part[kTreeRows + threadIdx.x] = 0.f;
-        }
+    if (w.more && warp < kSoftmaxWarps && (w.r.tiles >> p.cluster_log) == 0) {
+      // a block without tiles says so
+      Piece x;
+      if (!w.next(p, x)) {
+        float* const part = reinterpret_cast<float*>(smem + T::OFF_SLOT);
+        part[threadIdx.x] = -INFINITY;
+        part[kTreeRows + threadIdx.x] = 0.f;
       }
-      __syncwarp();
-      cluster_sync();
-      join_cluster<CACHE, D>(p, smem, w);
-      cluster_sync();                                   // no block leaves while another reads its part
+      w.more = true;
     }
+    __syncwarp();
+    cluster_sync();                                     // (all blocks meet, whatever each has read of the request)
+    if (w.more) join_cluster<CACHE, D>(p, smem, w);
+    cluster_sync();                                     // no block leaves while another reads its part
   }
   tc_fence_before();
   __syncthreads();
