@@ -65,20 +65,21 @@ int half_code(const at::Tensor& t, const char* name) {
   refuse("%s must be BFloat16 or Half, got %s", name, type_name(t.scalar_type()));
 }
 
-// [tokens, heads, dim], the heads of a token contiguous and the tokens any distance apart, which is returned
+// [tokens, heads, dim], the heads of a token contiguous and the tokens any distance apart, which is returned. (Without tokens the strides
+// say nothing: torch.tensor of an empty numpy array has zeros.)
 int64_t token_rows(const at::Tensor& t, int64_t heads, int64_t dim, at::ScalarType type, const char* name) {
   want_type(t, type, name);
   const auto size = t.sizes(), stride = t.strides();
   if (size.size() != 3 || size[1] != heads || size[2] != dim)
     refuse("%s must be [tokens, %lld, %lld]", name, static_cast<long long>(heads), static_cast<long long>(dim));
-  if (stride[2] != 1 || (stride[1] != dim && heads > 1)) refuse("%s: the heads of a token must be contiguous", name);
+  if (size[0] > 0 && (stride[2] != 1 || (stride[1] != dim && heads > 1))) refuse("%s: the heads of a token must be contiguous", name);
   return stride[0];
 }
 
 // [rows, cols] with contiguous rows any distance apart, which is returned
 int64_t matrix(const at::Tensor& t, int64_t rows, int64_t cols, const char* name) {
   const auto size = t.sizes(), stride = t.strides();
-  if (size.size() != 2 || size[0] != rows || size[1] != cols || (stride[1] != 1 && cols > 1))
+  if (size.size() != 2 || size[0] != rows || size[1] != cols || (stride[1] != 1 && cols > 1 && rows > 0))
     refuse("%s must be [%lld, %lld] with contiguous rows", name, static_cast<long long>(rows), static_cast<long long>(cols));
   return stride[0];
 }
