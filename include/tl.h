@@ -493,6 +493,8 @@ int tl_tree_plan(const int32_t* parents, const int32_t* starts, int B, int T, co
  *   sinks      with a window, the first cached tokens that stay visible; 0 without one
  *   pages      where no node sees a token of a page, and no node's place is in it, its entry may be anything
  *   lse        optional fp32 [T, q_heads]: log sum_j p_j
+ *   max_pages  also decides, with T, over how many blocks a request is spread, as lengths are read on the GPU: few and
+ *              short requests are fastest with a table that is no wider than they need
  *   workspace  ws_bytes >= tl_tree_attention_workspace_size; its contents do not matter. Calls that can overlap on the
  *              GPU must not share one.
  * Rows outside every request (padding) of out and lse are left as they were. Sizes and the meaning of the rest

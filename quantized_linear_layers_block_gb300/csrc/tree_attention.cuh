@@ -25,7 +25,7 @@
 // every row sees whole (the nodes, the edge of a window) such values are taken out when they are loaded, and added
 // at the end to the rows that see them. In the others a weight that underflowed makes an infinity NaN: a NaN channel at the end is looked into.
 //
-// Measured (GB300; 24 heads on 4 of 256 channels and bf16 where nothing else is said): one request of 577 tokens, 8 nodes 11.5 us, a
+// Measured (GB300; 24 heads on 4 of 256 channels and bf16 where nothing else is said, page tables as wide as the longest request needs): one request of 577 tokens, 8 nodes 11.5 us, a
 // chain of latencies (length, page, tile, two products and a softmax, cluster, output); 24 requests of 40 to 9000 tokens and 4 to 26 nodes 54
 // (bytes: 28), tensor pipe 38 % busy: a tile is 2250 cycles of product, softmax, product and the waits between them, and a piece of a
 // segment costs 6 us besides (queries, list, output); 64 nodes on 80001 tokens 146 (flops: 66, 100 with both parts of P), tensor pipe 65 %;
@@ -1360,7 +1360,9 @@ cudaError_t launch(TreeAttnParams& p, int sms, cudaStream_t st) {
   const long long segments = static_cast<long long>(p.B) * p.kv_heads * p.row_blocks;
   // Few segments of few tiles: a cluster each, of the most blocks that all run at once, while a block has more than one tile and
   // no more than some, where the list's equal shares and its more blocks win; of the up to seven segments that have sixteen blocks the
-  // list makes so many parts that this is later. One request of 577 tokens, 8 nodes: clusters 11.7 us (16 blocks for its 10 tiles: 14.5), the
+  // list makes so many parts that this is later. Lengths lie on the GPU, so keys are counted by the table's width, and nodes by T: a short request
+  // behind a wide table gets what suits a long one (577 tokens, tables of 640, 4096 and from 32768 on: 12.1, 12.7, 16.5; 4000: 17.1, 17.1, 24.6;
+  // 64 channels 8.9, 9.0, 14.0 and 11.5, 11.6, 28.4). One request of 577 tokens, 8 nodes: clusters 11.7 us (16 blocks for its 10 tiles: 14.5), the
   // list 15.1; 4000: 15.6 and 23.1, 64 channels 11.0 and 29.2; 16000: 28.2 and 32.1, 20.1 and 31.4; seven heads of 128 channels, 29000:
   // 34 and 40, four in 8 bits 38 and 32. Eight requests of 1000: two blocks each 22.4, the list 20.4.
   for (int log = kMaxClusterLog; log >= 0; --log) {

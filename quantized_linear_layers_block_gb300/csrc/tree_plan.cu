@@ -4,8 +4,8 @@
 // 2^k steps and p_i the one 2^k steps up,
 //   m_i |= m_{p_i},  p_i = p_{p_i}
 // six times, all by shuffles, instead of a chain of up to 63 dependent steps. A few bytes for each
-// node: bound by the launch and one chain of loads (starts, parents and length, page). GB300: one request of 26 nodes 2.8 us, 500
-// requests of up to 64 2.9.
+// node: bound by the launch and one chain of loads (starts, parents and length, page). GB300: one request of 26 nodes 2.9 us, 500
+// requests of up to 64 3.0.
 #include "tl_internal.cuh"
 
 #include "tree.cuh"

@@ -13,8 +13,8 @@
 // probability (64 requests, 100001 tokens: 211 us). So a thread sums its share as a pair of floats, the sum and what its
 // roundings lost (about 48 bits, a dozen fp32 operations an element), and the threads' sums meet as 64-bit integers in units of 2^-60.
 //
-// GB300: those 64 requests 52 us (rows once from HBM: 8; the request with most refusals makes several passes, one after the other,
-// of some 8 us, of L2's throughput 8 %), a chain of 8 with 131072 tokens 8.2.
+// GB300: those 64 requests 50 to 57 us by their numbers (rows once from HBM: 8; the request with most refusals makes several passes, one
+// after the other, of some 8 us, of L2's throughput 8 %), chosen tokens 28; a chain of 8 with 131072 tokens 8.5, chosen 7.8.
 #include "tl_internal.cuh"
 
 #include "tree.cuh"

@@ -369,7 +369,7 @@ def _filled(device):
 
 
 class PagedKVCache:
-    """The paged key-value cache of one layer, and the two operators on it.
+    """The paged key-value cache of one layer, and the operators on it.
 
     k and v are [num_pages, kv_heads, page_size, head_dim] in bf16, fp16 or
     float8_e4m3fn. They are allocated here (zeros), or passed in with any strides that
@@ -379,7 +379,7 @@ class PagedKVCache:
 
     Which pages belong to which request is the caller's: append() takes a slot
     (page * page_size + row) for each token, attend() a table of pages for each request.
-    append() takes any head_dim that is a multiple of 16 up to 512, attend() 64, 128 and 256.
+    append() and compact() take any head_dim that is a multiple of 16 up to 512, attend() and attend_tree() 64, 128 and 256.
     All tensors of a call lie on the cache's GPU.
 
     The cache keeps one workspace for attend(), which joins requests that several
@@ -531,7 +531,8 @@ def tl_tree_attention(cache: PagedKVCache, q: torch.Tensor, masks: torch.Tensor,
                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [T, q_heads, head_dim] of the nodes over their requests' lens cached tokens and the nodes of their masks int64 [T] -> out of
     q's shape and dtype; lse fp32 [T, q_heads] when given. With a window (64 or more) a node sees that many keys, its own nodes
-    among them, and the first `sinks` cached tokens. Rows of padding are left as they were (in an `out` that is allocated here: zeros).
+    among them, and the first `sinks` cached tokens. Entries of `pages` through which no node sees or is a token may be anything; short
+    requests are fastest behind a table no wider than they need. Rows of padding are left as they were (in an `out` that is allocated here: zeros).
     The workspace is taken from torch's allocator for the call unless it is given (tl_tree_attention_workspace_size bytes)."""
     if out is None:
         out = _allocate(torch.zeros, q.shape, q.dtype, q.device, stream)
